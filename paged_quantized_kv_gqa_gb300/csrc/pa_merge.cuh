@@ -139,12 +139,21 @@ __device__ __forceinline__ void merge_store(const float (&acc)[DV / 32], float M
   const float inv = W > 0.f ? 1.0f / W : 0.f;
   const int64_t o = ((int64_t)token * q_heads + head) * DV + lane * kPer;
   const int e0 = head * DV + lane * kPer;
+  // four elements leave as one store where out's address allows it (the decode
+  // family takes an out of any alignment)
+  const bool vec = (reinterpret_cast<uintptr_t>(out) & (ep.int8_out ? 3 : 7)) == 0;
 #pragma unroll
   for (int k = 0; k < kPer; k += 4) {
     float f[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) f[u] = ep_value(ep, acc[k + u] * inv, e0 + k + u);
-    if (ep.int8_out) {
+    if (!vec) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (ep.int8_out) reinterpret_cast<int8_t*>(out)[o + k + u] = (int8_t)ep_int8(ep, f[u]);
+        else reinterpret_cast<__nv_bfloat16*>(out)[o + k + u] = __float2bfloat16_rn(f[u]);
+      }
+    } else if (ep.int8_out) {
       const uint32_t w = ep_int8(ep, f[0]) | (ep_int8(ep, f[1]) << 8) | (ep_int8(ep, f[2]) << 16) |
                          (ep_int8(ep, f[3]) << 24);
       *reinterpret_cast<uint32_t*>(reinterpret_cast<int8_t*>(out) + o + k) = w;
