@@ -18,7 +18,11 @@
  *     s_j = sm_scale * <q[t][h], k_j>;
  *     out[t][h] = sum_j softmax(s)_j v_j   (bf16, round to nearest even)
  *     lse[t][h] = log sum_j exp(s_j)       (natural log, fp32)
- *   dec() reads a signed int8 byte or an OCP FP8 E4M3 byte.  Split-KV: chunk c
+ *   dec() reads a signed int8 byte, an OCP FP8 E4M3 byte, or a 4-bit code times
+ *   the E4M3 scale of its block of 16 dims.  With causal = PA_MASK_CROSS the
+ *   query tokens are not in the cache: kvtot = seq_lens_kv[b], every position
+ *   j < kvtot is visible, and a row without any (kvtot = 0) gets out = 0 (the
+ *   output epilogue of 0) and lse = -inf.  Split-KV: chunk c
  *   covers [c*chunk_size, min(limit, (c+1)*chunk_size)); each chunk writes a
  *   partial state (o, m, d) and pa_merge combines them by log-sum-exp.
  *
@@ -57,7 +61,8 @@ typedef enum pa_status {
                                problem's bounds (see pa_check)                */
 } pa_status;
 
-enum { PA_KV_INT8 = 0, PA_KV_FP8_E4M3 = 1 };
+enum { PA_KV_INT8 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT4 = 2, PA_KV_FP4_E2M1 = 3 };
+enum { PA_MASK_FULL = 0, PA_MASK_CAUSAL = 1, PA_MASK_CROSS = 2 };   /* pa_problem.causal */
 enum { PA_SCALE_PER_KV_HEAD = 0, PA_SCALE_PER_CHANNEL = 1, PA_SCALE_GLOBAL = 2 };
 enum { PA_LAYOUT_GQA = 0, PA_LAYOUT_MLA = 1 };
 enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
@@ -70,6 +75,17 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *   MLA layout: cache_k uint8 [num_pages][block_size][head_dim_qk] holding one
  *               latent head; V is the first head_dim_v entries of each row, so
  *               cache_v must equal cache_k (XQA mla_sm120.cu's shared K/V).
+ *   4-bit formats (PA_KV_INT4: two's complement; PA_KV_FP4_E2M1: sign, two
+ *               exponent bits, one mantissa bit, i.e. 0 .5 1 1.5 2 3 4 6), GQA
+ *               layout: cache_k and cache_v are uint8 [num_pages][kv_heads][4608],
+ *               a slab being two half pages of 32 positions, 2304 bytes each:
+ *                 K half  codes [32 positions][64], byte i = dims 2i (low nibble)
+ *                         and 2i + 1; then E4M3 scales [32 positions][8]
+ *                 V half  codes [128 dims][16], byte i = positions 2i (low) and
+ *                         2i + 1; then E4M3 scales [8][32 positions]
+ *               real value = code * scale of its 16 dims * k_scale or v_scale.
+ *               Bytes of positions outside a sequence may hold anything; the
+ *               scales of its positions must be finite.
  *   Scales: PER_KV_HEAD  bf16 [kv_heads]              (k_scale and v_scale)
  *           PER_CHANNEL  bf16 [kv_heads * head_dim]   (index kvh * D + d)
  *           GLOBAL       fp32 [1]                     (one value for K and V)
@@ -91,7 +107,7 @@ typedef struct pa_problem {
   int32_t kv_dtype;     /* PA_KV_*     */
   int32_t scale_kind;   /* PA_SCALE_*  */
   int32_t layout;       /* PA_LAYOUT_* */
-  int32_t causal;       /* 0 or 1      */
+  int32_t causal;       /* PA_MASK_*   */
   int32_t chunk_size;
   float sm_scale;       /* softmax scale, e.g. 1/sqrt(head_dim)          */
   int64_t q_stride;
@@ -166,7 +182,7 @@ typedef struct pa_plan_desc {
                                in CTA-major order                            */
   const int32_t* work_indptr;  /* [num_ctas + 1]                              */
   const int32_t* nch_token;    /* [total_q] chunks of each token's tile       */
-  const int32_t* merge_tokens; /* [n_merge] ascending                         */
+  const int32_t* merge_tokens; /* [n_merge] ascending: nch_token != 1         */
   size_t workspace_bytes;
   int64_t kv_bytes;         /* cache bytes read once: visible (page, head) slabs */
   double flops;             /* 2*(Dqk+Dv) per visible (position, query head)  */
@@ -190,7 +206,7 @@ typedef struct pa_plan_desc {
  *   sequence needing more than max_blocks_per_seq pages), PA_ERR_UNSUPPORTED
  *   (shapes without a compiled kernel: GQA needs head_dim 128 and
  *   block_size 64; MLA needs 128 query heads, one kv head, 576/512 and a
- *   global scale).
+ *   global scale, an 8-bit cache and no cross attention).
  */
 pa_status pa_plan(const pa_problem* problem, const int32_t* seq_lens_h,
                   const int32_t* seq_lens_kv_h, const int32_t* cu_seqlens_q_h,
@@ -224,8 +240,9 @@ pa_status pa_plan_upload(const pa_plan_t* plan, void* workspace, void* stream);
 pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, void* stream);
 
 /* Enqueues the log-sum-exp merge of the partial states of split rows into
- * out/lse.  A no-op when the plan has no split rows or merges them inside
- * pa_run (pa_plan_desc.fused_merge). */
+ * out/lse, and writes the rows that see no position (cross attention to an
+ * empty sequence).  A no-op when the plan has neither or merges inside pa_run
+ * (pa_plan_desc.fused_merge). */
 pa_status pa_merge(const pa_plan_t* plan, const pa_args* args, void* workspace, void* stream);
 
 /* Synchronises the stream, then reads the workspace status word.  Returns
@@ -257,6 +274,11 @@ const char* pa_last_error(void);
  *   its scale s (per kv head, per channel kv_head * D + d, or the global fp32
  *   scale), then int8 round-half-even saturated to +-127, or E4M3
  *   round-to-nearest-even saturated to +-448.
+ *   4-bit formats, per block of 16 dims of a position (all in binary32, ties to
+ *   even): a = max |x / s|, block scale e = E4M3(min(a / M, 448)) with M = 7
+ *   (int4) or 6 (FP4), step = e * s, code = nearest code to x / step, saturated
+ *   to +-M (0 where step is 0).  A NaN is stored as 0; the scales s must be
+ *   positive and finite.
  *   k_new, v_new: device bf16, token t's row at t * kv_stride elements, kv head
  *   h at h * D within it (MLA: the 576-wide latent row; v_new unused, may be
  *   NULL).  A packed qkv tensor works with kv_stride = (Hq + 2 Hkv) * D.
@@ -268,6 +290,30 @@ const char* pa_last_error(void);
  */
 pa_status pa_cache_append(const pa_plan_t* plan, const pa_args* args, const void* k_new,
                           const void* v_new, int64_t kv_stride, void* workspace, void* stream);
+
+/*
+ * pa_cache_read: reads cached positions back as bf16 rows, the inverse of
+ * pa_cache_append with the same arguments: position seq_lens_kv[b] + i of
+ * sequence b (i < seq_lens[b]) goes to row cu_seqlens_q[b] + i of k_out and
+ * v_out, token rows kv_stride elements apart, kv head h at h * D within a row
+ * (MLA: the 576-wide latent row in k_out; v_out unused, may be NULL).
+ *   value = bf16(stored * s); 4-bit formats bf16(code * (block scale * s)),
+ *   products in binary32.
+ * The plan gives the batch size and the longest range; the device seq_lens,
+ * seq_lens_kv and cu_seqlens_q of args must be the ones it was built from.
+ * Elements of a row beyond the kv heads are left as they were.  A block_table
+ * entry outside the pool reads as zeros and records PA_ERR_BAD_PAGE.
+ * Neither this call nor pa_cache_append takes a PA_MASK_CROSS plan: encoder
+ * states are written and read with a plan of their own lengths (seq_lens =
+ * encoder lengths, seq_lens_kv = 0).
+ * Asynchronous on stream; no allocation.
+ */
+pa_status pa_cache_read(const pa_plan_t* plan, const pa_args* args, void* k_out, void* v_out,
+                        int64_t kv_stride, void* workspace, void* stream);
+
+/* Bytes of cache_k and of cache_v for a problem's pool (MLA: *v_bytes = 0, V
+ * being part of cache_k's rows). */
+pa_status pa_cache_bytes(const pa_problem* problem, size_t* k_bytes, size_t* v_bytes);
 
 /*
  * pa_run_static: plan upload + pa_run + pa_merge in one call, using a
@@ -299,7 +345,8 @@ pa_status pa_run_static(const pa_plan_t* plan, const pa_args* args, void* stream
  * sequence b, kv head kv_head through the same page lookup the attention
  * kernels use.  dst_k: device uint8 [n][head_dim_qk]; dst_v: device uint8
  * [n][head_dim_v] (one position per row, V un-transposed).  Positions whose
- * page id is outside [0, num_pages) are written as zero bytes.
+ * page id is outside [0, num_pages) are written as zero bytes.  8-bit caches
+ * only (PA_ERR_UNSUPPORTED otherwise).
  */
 pa_status pa_debug_gather(const pa_problem* problem, const pa_args* args, int32_t b,
                           int32_t kv_head, int32_t pos0, int32_t n, void* dst_k, void* dst_v,
@@ -341,7 +388,8 @@ pa_status pa_debug_set_trace(void* device_buf, int32_t ctas, int32_t tiles_per_c
  * Opt-in single-launch path: with on = 1, decode-family plans built
  * afterwards merge their split rows inside pa_run (two warps of each CTA;
  * the CTA that writes a row group's last chunk merges it) and pa_merge does
- * nothing for them.  Default 0: pa_merge's separate kernel is faster on
+ * nothing for them; plans over a 4-bit cache, or with rows that see no
+ * position, keep the separate merge.  Default 0: pa_merge's separate kernel is faster on
  * GB300, because the in-kernel merge's chains of dependent partial-state
  * loads queue behind the attention kernel's own page stream.  Process-wide
  * setting, read by pa_plan.

@@ -15,6 +15,8 @@ Spec:
   rows_cap = 64 (decode), 256 (append: two 128-row query tiles), q_heads
   (mla); tokens per tile tpt = rows_cap // G.  CTAs per item: 2 for mla, else 1; slots = num_sms //
   (CTAs per item).
+  Cross attention (p.cross): lim = seq_lens_kv[b], causal_base = seq_lens_kv[b];
+      a tile with lim = 0 has no items and nch = 0.
   Tiles, sequence-major: for b, for t in 0..ceil(q_len_b / tpt)-1:
       tok0 = t*tpt, tok1 = min(q_len_b, tok0 + tpt),
       lim  = seq_lens_kv[b] + tok1 if causal else seq_lens_kv[b] + q_len_b.
@@ -34,7 +36,8 @@ Spec:
   each CTA runs its items in the order received.  Items are stored CTA-major
   with work_indptr[num_ctas + 1].
   nch_token[t] = nch of token t's tile; max_chunks = max(1, max nch_token);
-  merge_tokens = tokens with nch_token > 1, ascending.
+  merge_tokens = tokens with nch_token != 1, ascending (those with 0 chunks are
+  the rows that see nothing; the merge writes them).
   MLA with chunk_size = -1 replaces the chunk size and the longest-first
   deal by contiguous shares (this library's scheduling choice; the pages fix
   only what an item computes): the tiles' pages, ceil(lim / B) per tile,
@@ -74,6 +77,7 @@ def plan(p, num_sms: int) -> dict:
         family, rows_cap, per_item = "append", APPEND_ROWS, 1
     tpt = rows_cap // G
     slots = max(1, num_sms // per_item)
+    cross = bool(getattr(p, "cross", False))
 
     tiles = []
     for b in range(bsz):
@@ -81,7 +85,7 @@ def plan(p, num_sms: int) -> dict:
         for t in range(math.ceil(ql / tpt)):
             tok0 = t * tpt
             tok1 = min(ql, tok0 + tpt)
-            lim = slkv[b] + tok1 if p.causal else slkv[b] + ql
+            lim = slkv[b] if cross else slkv[b] + tok1 if p.causal else slkv[b] + ql
             tiles.append((b, tok0, tok1, lim))
 
     if family == "mla" and int(p.chunk_size) == -1:
@@ -100,8 +104,8 @@ def plan(p, num_sms: int) -> dict:
     T = cu[-1] if cu else 0
     nch_token = np.zeros(T, dtype=np.int32)
     for (b, tok0, tok1, lim) in tiles:
-        nch = math.ceil(lim / cs) if split else 1
-        base = slkv[b] + tok0 if p.causal else slkv[b] + q_lens[b]
+        nch = math.ceil(lim / cs) if split else min(lim, 1)
+        base = slkv[b] if cross else slkv[b] + tok0 if p.causal else slkv[b] + q_lens[b]
         nch_token[cu[b] + tok0:cu[b] + tok1] = nch
         for kvh in range(p.kv_heads):
             for c in range(nch):
@@ -126,7 +130,7 @@ def plan(p, num_sms: int) -> dict:
         indptr[k + 1] = len(flat)
     arr = np.array([items[i] for i in flat], dtype=np.int64).reshape(-1, 8).astype(np.int32)
     max_chunks = int(max(1, nch_token.max() if T else 1))
-    merge_tokens = np.nonzero(nch_token > 1)[0].astype(np.int32)
+    merge_tokens = np.nonzero(nch_token != 1)[0].astype(np.int32)
     return dict(family=family, chunk=cs, tokens_per_tile=tpt, num_ctas=num_ctas,
                 items=arr, work_indptr=indptr, nch_token=nch_token,
                 max_chunks=max_chunks, merge_tokens=merge_tokens)

@@ -29,7 +29,8 @@ LIB_PATH = os.path.join(_HERE, "libpa_gb300_trace.so" if os.environ.get("PA_GB30
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA = 0, 1, 2, 3
 PA_ERR_DEVICE_TIMEOUT, PA_ERR_BAD_PAGE, PA_ERR_BAD_ITEM = 4, 5, 6
-KV_DTYPES = {"int8": 0, "fp8_e4m3": 1}
+KV_DTYPES = {"int8": 0, "fp8_e4m3": 1, "int4": 2, "fp4_e2m1": 3}
+MASK_FULL, MASK_CAUSAL, MASK_CROSS = 0, 1, 2
 SCALE_KINDS = {"per_kv_head": 0, "per_channel": 1, "global": 2}
 LAYOUTS = {"gqa": 0, "mla": 1}
 FAMILIES = {0: "decode", 1: "append", 2: "mla"}
@@ -91,6 +92,9 @@ def _load():
         "pa_debug_set_trace": ([vp, i32, i32], i32),
         "pa_set_fused_merge": ([i32], i32),
         "pa_cache_append": ([vp, ctypes.POINTER(PaArgs), vp, vp, i64, vp, vp], i32),
+        "pa_cache_read": ([vp, ctypes.POINTER(PaArgs), vp, vp, i64, vp, vp], i32),
+        "pa_cache_bytes": ([ctypes.POINTER(PaProblem), ctypes.POINTER(ctypes.c_size_t),
+                            ctypes.POINTER(ctypes.c_size_t)], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -137,7 +141,11 @@ def _stream(s) -> Optional[int]:
 
 def make_problem(*, bsz, q_heads, kv_heads, head_dim_qk, head_dim_v, block_size,
                  max_blocks_per_seq, num_pages, kv_dtype, scale_kind, layout, causal,
-                 chunk_size, sm_scale, q_stride) -> PaProblem:
+                 chunk_size, sm_scale, q_stride, cross=False) -> PaProblem:
+    """cross=True: cross attention to seq_lens_kv cached states, the query tokens
+    not being in the cache (causal must be False then)."""
+    if cross and causal:
+        raise ValueError("cross attention has no causal mask")
     p = PaProblem()
     p.bsz, p.q_heads, p.kv_heads = bsz, q_heads, kv_heads
     p.head_dim_qk, p.head_dim_v, p.block_size = head_dim_qk, head_dim_v, block_size
@@ -145,7 +153,7 @@ def make_problem(*, bsz, q_heads, kv_heads, head_dim_qk, head_dim_v, block_size,
     p.kv_dtype = KV_DTYPES[kv_dtype] if isinstance(kv_dtype, str) else kv_dtype
     p.scale_kind = SCALE_KINDS[scale_kind] if isinstance(scale_kind, str) else scale_kind
     p.layout = LAYOUTS[layout] if isinstance(layout, str) else layout
-    p.causal = int(bool(causal))
+    p.causal = MASK_CROSS if cross else int(bool(causal))
     p.chunk_size = chunk_size
     p.sm_scale = sm_scale
     p.q_stride = q_stride
@@ -160,7 +168,7 @@ def problem_of(case) -> PaProblem:
                         num_pages=case.num_pages, kv_dtype=case.kv_dtype,
                         scale_kind=case.scale_kind, layout=case.layout, causal=case.causal,
                         chunk_size=case.chunk_size, sm_scale=case.sm_scale,
-                        q_stride=case.q_stride)
+                        q_stride=case.q_stride, cross=getattr(case, "cross", False))
 
 
 class Plan:
@@ -265,6 +273,21 @@ def pa_cache_append(plan: Plan, args: PaArgs, k_new, v_new, kv_stride: int, work
     elements) into the paged cache of args (see include/pa.h)."""
     _check(lib.pa_cache_append(plan.handle, ctypes.byref(args), _ptr(k_new), _ptr(v_new),
                                int(kv_stride), _ptr(workspace), _stream(stream)))
+
+
+def pa_cache_read(plan: Plan, args: PaArgs, k_out, v_out, kv_stride: int, workspace,
+                  stream=None):
+    """Read the plan's position ranges (seq_lens_kv[b] .. + seq_lens[b]) of the
+    cache back as bf16 rows, token stride kv_stride elements (see include/pa.h)."""
+    _check(lib.pa_cache_read(plan.handle, ctypes.byref(args), _ptr(k_out), _ptr(v_out),
+                             int(kv_stride), _ptr(workspace), _stream(stream)))
+
+
+def pa_cache_bytes(problem: PaProblem):
+    """(bytes of cache_k, bytes of cache_v) of the problem's page pool."""
+    k, v = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib.pa_cache_bytes(ctypes.byref(problem), ctypes.byref(k), ctypes.byref(v)))
+    return int(k.value), int(v.value)
 
 
 def pa_debug_set_trace(buf=None, ctas: int = 0, tiles_per_cta: int = 0):

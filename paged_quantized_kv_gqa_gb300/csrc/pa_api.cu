@@ -6,6 +6,8 @@
 // persistent.cuh: per-CTA work lists with work_indptr and kv_start/kv_end per
 // item; XQA mla_sm120.cu: the SM-count-driven sub-sequence split):
 //   family: MLA layout -> MLA; else decode when max(q_len) * G <= 64, else append.
+//   cross attention (causal = PA_MASK_CROSS): lim = kvtot = seq_lens_kv; a tile of an
+//   empty sequence has no items and no chunks, and the merge writes its rows.
 //   tiles of tokens_per_tile = rows_cap / G query tokens (rows_cap 64 decode,
 //   256 append = two 128-row query tiles, q_heads MLA); lim = seq_lens_kv + tok1 (causal) or kvtot.
 //   chunk: >0 as given, 0 none, -1 auto = max(4B, roundup(ceil(W/(4*slots)), B)),
@@ -16,6 +18,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <queue>
 #include <string>
 #include <vector>
@@ -48,13 +51,14 @@ static pa_status check_problem(const pa_problem& p) {
     return fail(PA_ERR_INVALID_ARG, "non-positive shape field in pa_problem");
   if (p.q_heads % p.kv_heads != 0)
     return fail(PA_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
-  if (p.kv_dtype != PA_KV_INT8 && p.kv_dtype != PA_KV_FP8_E4M3)
+  if (p.kv_dtype < PA_KV_INT8 || p.kv_dtype > PA_KV_FP4_E2M1)
     return fail(PA_ERR_INVALID_ARG, "unknown kv_dtype");
   if (p.scale_kind < PA_SCALE_PER_KV_HEAD || p.scale_kind > PA_SCALE_GLOBAL)
     return fail(PA_ERR_INVALID_ARG, "unknown scale_kind");
   if (p.layout != PA_LAYOUT_GQA && p.layout != PA_LAYOUT_MLA)
     return fail(PA_ERR_INVALID_ARG, "unknown layout");
-  if (p.causal != 0 && p.causal != 1) return fail(PA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (p.causal < PA_MASK_FULL || p.causal > PA_MASK_CROSS)
+    return fail(PA_ERR_INVALID_ARG, "causal must be 0, 1 or 2 (PA_MASK_CROSS)");
   if (p.chunk_size < -1) return fail(PA_ERR_INVALID_ARG, "chunk_size must be >= -1");
   if (p.chunk_size > 0 && p.chunk_size % p.block_size != 0)
     return fail(PA_ERR_INVALID_ARG, "chunk_size must be a multiple of block_size");
@@ -69,9 +73,14 @@ static pa_status check_problem(const pa_problem& p) {
       return fail(PA_ERR_UNSUPPORTED, "GQA kernels are built for head_dim 128, block_size 64");
     if (p.scale_kind == PA_SCALE_GLOBAL && p.kv_dtype == PA_KV_INT8)
       ;  // allowed
+    // TMA rows: 128 of 64 bytes per 8-bit V slab, 72 of 64 bytes per 4-bit slab
     if ((int64_t)p.num_pages * p.kv_heads * 128 >= (int64_t)1 << 31)
       return fail(PA_ERR_UNSUPPORTED, "cache too large for 32-bit TMA row coordinates");
   } else {
+    if (p.kv_dtype == PA_KV_INT4 || p.kv_dtype == PA_KV_FP4_E2M1)
+      return fail(PA_ERR_UNSUPPORTED, "4-bit caches hold the GQA layout only");
+    if (p.causal == PA_MASK_CROSS)
+      return fail(PA_ERR_UNSUPPORTED, "cross attention is built for the GQA layout only");
     if (p.kv_heads != 1 || p.q_heads != 128 || p.head_dim_qk != 576 || p.head_dim_v != 512 ||
         p.block_size != 64 || p.scale_kind != PA_SCALE_GLOBAL)
       return fail(PA_ERR_UNSUPPORTED,
@@ -90,13 +99,15 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   const int bsz = prob.bsz;
   const int G = prob.q_heads / prob.kv_heads;
   const int B = prob.block_size;
+  const bool causal = prob.causal == PA_MASK_CAUSAL;
+  const bool cross = prob.causal == PA_MASK_CROSS;
   if (cu[0] != 0) return fail(PA_ERR_INVALID_ARG, "cu_seqlens_q[0] must be 0");
   int max_q = 0;
   for (int b = 0; b < bsz; ++b) {
     if (ql[b] < 0 || slkv[b] < 0) return fail(PA_ERR_INVALID_ARG, "negative sequence length");
     if (cu[b + 1] - cu[b] != ql[b])
       return fail(PA_ERR_INVALID_ARG, "cu_seqlens_q is not the prefix sum of seq_lens");
-    const int64_t kvtot = (int64_t)slkv[b] + ql[b];
+    const int64_t kvtot = (int64_t)slkv[b] + (cross ? 0 : ql[b]);
     if (ceil_div(kvtot, B) > prob.max_blocks_per_seq)
       return fail(PA_ERR_INVALID_ARG, "a sequence needs more pages than max_blocks_per_seq");
     if (kvtot >= (int64_t)1 << 30) return fail(PA_ERR_INVALID_ARG, "sequence too long");
@@ -136,7 +147,7 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     for (int t = 0; t < nt; ++t) {
       const int tok0 = t * tpt;
       const int tok1 = std::min(q, tok0 + tpt);
-      const int64_t lim = prob.causal ? (int64_t)slkv[b] + tok1 : (int64_t)slkv[b] + q;
+      const int64_t lim = (int64_t)slkv[b] + (causal ? tok1 : cross ? 0 : q);
       tiles.push_back({b, tok0, tok1, lim});
     }
   }
@@ -177,7 +188,7 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
         const Tile& t = tiles[i];
         const int64_t kv0 = (std::max(a, first_page[i]) - first_page[i]) * B;
         const int64_t kv1 = std::min<int64_t>(t.lim, (std::min(e, first_page[i + 1]) - first_page[i]) * B);
-        const int64_t base = prob.causal ? (int64_t)slkv[t.b] + t.tok0 : (int64_t)slkv[t.b] + ql[t.b];
+        const int64_t base = (int64_t)slkv[t.b] + (causal ? t.tok0 : ql[t.b]);
         const int32_t rec[kItemWords] = {t.b, 0, cu[t.b] + t.tok0, t.tok1 - t.tok0, (int32_t)base,
                                          (int32_t)kv0, (int32_t)kv1,
                                          (int32_t)(piece[i]++ | (nch[i] << 16))};
@@ -208,9 +219,9 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     std::vector<int32_t> items;
     P.nch_token.assign(P.total_q, 0);
     for (auto& t : tiles) {
-      const int nch = split ? (int)ceil_div(t.lim, cs) : 1;
+      const int nch = split ? (int)ceil_div(t.lim, cs) : t.lim > 0 ? 1 : 0;   // 0: nothing to attend to
       if (nch > 0xFFFF) return fail(PA_ERR_UNSUPPORTED, "too many chunks per row");
-      const int64_t base = prob.causal ? (int64_t)slkv[t.b] + t.tok0 : (int64_t)slkv[t.b] + ql[t.b];
+      const int64_t base = (int64_t)slkv[t.b] + (causal ? t.tok0 : cross ? 0 : ql[t.b]);
       for (int tok = t.tok0; tok < t.tok1; ++tok) P.nch_token[cu[t.b] + tok] = nch;
       for (int kvh = 0; kvh < prob.kv_heads; ++kvh) {
         for (int c = 0; c < nch; ++c) {
@@ -253,9 +264,13 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   }
   P.max_chunks = 1;
   for (int t = 0; t < P.total_q; ++t) P.max_chunks = std::max(P.max_chunks, P.nch_token[t]);
+  // the merge also writes the rows that no item covers (no chunks: out 0, lse -inf)
   P.merge_tokens.clear();
-  for (int t = 0; t < P.total_q; ++t)
-    if (P.nch_token[t] > 1) P.merge_tokens.push_back(t);
+  bool empty_rows = false;
+  for (int t = 0; t < P.total_q; ++t) {
+    if (P.nch_token[t] != 1) P.merge_tokens.push_back(t);
+    empty_rows = empty_rows || P.nch_token[t] == 0;
+  }
 
   // device blob and workspace layout; every array starts on a 16-byte boundary
   // (the kernels read an item record as two 16-byte vectors)
@@ -266,7 +281,8 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   P.off_merge = align4(P.off_nch + P.nch_token.size());
   {
     std::lock_guard<std::mutex> lk(g_fault_mu);
-    P.fused_merge = P.family == PA_FAMILY_DECODE && !P.merge_tokens.empty() && g_faults.fused_merge;
+    P.fused_merge = P.family == PA_FAMILY_DECODE && P.max_chunks > 1 && !empty_rows && !P.four_bit() &&
+                    g_faults.fused_merge;
   }
   P.off_cnt = align4(P.off_merge + P.merge_tokens.size());
   const size_t words = P.off_cnt + (P.fused_merge ? (size_t)P.total_q * prob.kv_heads : 0);
@@ -278,7 +294,7 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   std::copy(P.merge_tokens.begin(), P.merge_tokens.end(), P.blob.begin() + P.off_merge);
   P.plan_bytes = P.blob.size() * sizeof(int32_t);
   size_t off = align_up(kStatusBytes + P.plan_bytes, 256);
-  const size_t slots_part = P.merge_tokens.empty()
+  const size_t slots_part = P.max_chunks == 1
                                 ? 0
                                 : (size_t)P.total_q * P.max_chunks * prob.q_heads;
   P.part_o_off = off;
@@ -293,14 +309,15 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   int64_t pages = 0;
   double pairs = 0.0;
   for (int b = 0; b < bsz; ++b) {
-    const int64_t kvtot = (int64_t)slkv[b] + ql[b];
+    const int64_t kvtot = (int64_t)slkv[b] + (cross ? 0 : ql[b]);
     if (ql[b] == 0) continue;
     pages += ceil_div(kvtot, B);
     const double q = ql[b];
-    pairs += prob.causal ? q * slkv[b] + q * (q + 1) / 2.0 : q * (double)kvtot;
+    pairs += causal ? q * slkv[b] + q * (q + 1) / 2.0 : q * (double)kvtot;
   }
   P.kv_bytes = prob.layout == PA_LAYOUT_MLA
                    ? pages * B * prob.head_dim_qk
+               : P.four_bit() ? pages * 2 * kSlab4 * (int64_t)prob.kv_heads
                    : pages * B * (int64_t)(prob.head_dim_qk + prob.head_dim_v) * prob.kv_heads;
   P.flops = pairs * prob.q_heads * 2.0 * (prob.head_dim_qk + prob.head_dim_v);
   return PA_OK;
@@ -435,8 +452,12 @@ pa_status pa_plan(const pa_problem* problem, const int32_t* seq_lens_h,
   const int32_t zero = 0;
   auto* plan = new (std::nothrow) pa_plan_t();
   if (!plan) return fail(PA_ERR_INVALID_ARG, "out of host memory");
-  s = build_plan(*problem, seq_lens_h, seq_lens_kv_h, cu_seqlens_q_h ? cu_seqlens_q_h : &zero,
-                 num_sms, *plan);
+  try {
+    s = build_plan(*problem, seq_lens_h, seq_lens_kv_h, cu_seqlens_q_h ? cu_seqlens_q_h : &zero,
+                   num_sms, *plan);
+  } catch (const std::exception&) {   // the plan's arrays do not fit into host memory
+    s = fail(PA_ERR_INVALID_ARG, "out of host memory");
+  }
   if (s != PA_OK) {
     delete plan;
     return s;
@@ -538,12 +559,16 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
   if (args->attn_mask) {
     if (plan->family != PA_FAMILY_DECODE)
       return fail(PA_ERR_UNSUPPORTED, "a tree mask is supported for the decode family only");
-    if (!pr.causal) return fail(PA_ERR_INVALID_ARG, "a tree mask needs causal = 1");
+    if (pr.causal != PA_MASK_CAUSAL) return fail(PA_ERR_INVALID_ARG, "a tree mask needs causal = 1");
     if (!args->cu_seqlens_q) return fail(PA_ERR_INVALID_ARG, "a tree mask needs cu_seqlens_q");
   }
 
   cudaError_t e;
-  if (plan->family == PA_FAMILY_DECODE) {
+  if (plan->four_bit()) {
+    if (plan->family == PA_FAMILY_APPEND && reinterpret_cast<uintptr_t>(args->out) % 16)
+      return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
+    e = launch_attn4(*plan, p, args->cache_k, args->cache_v, st);
+  } else if (plan->family == PA_FAMILY_DECODE) {
     CUtensorMap tk, tv;
     const uint64_t heads_total = (uint64_t)pr.num_pages * pr.kv_heads;
     if (plan->max_q * p.group <= kWarpDecodeRows && !plan->fused_merge) {
@@ -634,6 +659,8 @@ pa_status pa_debug_gather(const pa_problem* problem, const pa_args* args, int32_
   if (!problem || !args || !dst_k || !dst_v || !args->cache_k || !args->cache_v ||
       !args->block_table)
     return fail(PA_ERR_INVALID_ARG, "null argument to pa_debug_gather");
+  if (problem->kv_dtype == PA_KV_INT4 || problem->kv_dtype == PA_KV_FP4_E2M1)
+    return fail(PA_ERR_UNSUPPORTED, "pa_debug_gather copies 8-bit caches; use pa_cache_read");
   if (b < 0 || b >= problem->bsz || kv_head < 0 || kv_head >= problem->kv_heads || pos0 < 0 ||
       n < 0 ||
       (int64_t)pos0 + n > (int64_t)problem->max_blocks_per_seq * problem->block_size)
@@ -644,27 +671,65 @@ pa_status pa_debug_gather(const pa_problem* problem, const pa_args* args, int32_
   return PA_OK;
 }
 
-pa_status pa_cache_append(const pa_plan_t* plan, const pa_args* args, const void* k_new,
-                          const void* v_new, int64_t kv_stride, void* workspace, void* stream) {
+pa_status pa_cache_bytes(const pa_problem* problem, size_t* k_bytes, size_t* v_bytes) {
+  if (!problem || !k_bytes || !v_bytes) return fail(PA_ERR_INVALID_ARG, "null argument to pa_cache_bytes");
+  pa_status s = check_problem(*problem);
+  if (s != PA_OK) return s;
+  const size_t n = (size_t)problem->num_pages * problem->kv_heads;
+  if (problem->kv_dtype == PA_KV_INT4 || problem->kv_dtype == PA_KV_FP4_E2M1) {
+    *k_bytes = *v_bytes = n * kSlab4;
+  } else {
+    *k_bytes = n * problem->block_size * problem->head_dim_qk;
+    *v_bytes = problem->layout == PA_LAYOUT_MLA ? 0 : n * problem->block_size * problem->head_dim_v;
+  }
+  return PA_OK;
+}
+
+// What pa_cache_append and pa_cache_read ask of their arguments.
+static pa_status check_rows(const pa_plan_t* plan, const pa_args* args, const void* k_rows,
+                            const void* v_rows, int64_t kv_stride, const void* workspace) {
   if (!plan || !args || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan, args or workspace");
   const pa_problem& pr = plan->prob;
   const bool mla = pr.layout == PA_LAYOUT_MLA;
+  if (pr.causal == PA_MASK_CROSS)
+    return fail(PA_ERR_INVALID_ARG, "a cross-attention plan appends no rows: write and read the "
+                                    "encoder states with a plan of their own lengths");
   if (!args->cache_k || !args->k_scale || !args->block_table || !args->seq_lens ||
-      !args->seq_lens_kv || !args->cu_seqlens_q || !k_new)
-    return fail(PA_ERR_INVALID_ARG, "null device pointer for the cache append");
-  if (!mla && (!args->cache_v || !args->v_scale || !v_new))
-    return fail(PA_ERR_INVALID_ARG, "null V cache, V scale or new V rows");
+      !args->seq_lens_kv || !args->cu_seqlens_q || !k_rows)
+    return fail(PA_ERR_INVALID_ARG, "null device pointer for the cache append or read");
+  if (!mla && (!args->cache_v || !args->v_scale || !v_rows))
+    return fail(PA_ERR_INVALID_ARG, "null V cache, V scale or V rows");
   const int64_t row = mla ? pr.head_dim_qk : (int64_t)pr.kv_heads * pr.head_dim_qk;
   if (kv_stride < row)
     return fail(PA_ERR_INVALID_ARG, "kv_stride smaller than one token's K / V row");
-  if (reinterpret_cast<uintptr_t>(k_new) % 2 || reinterpret_cast<uintptr_t>(v_new) % 2)
-    return fail(PA_ERR_INVALID_ARG, "new K / V rows must be 2-byte aligned (bf16)");
+  if (reinterpret_cast<uintptr_t>(k_rows) % 2 || reinterpret_cast<uintptr_t>(v_rows) % 2)
+    return fail(PA_ERR_INVALID_ARG, "K / V rows must be 2-byte aligned (bf16)");
   if (reinterpret_cast<uintptr_t>(args->cache_k) % 16 || reinterpret_cast<uintptr_t>(args->cache_v) % 16)
     return fail(PA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
-  cudaError_t e = launch_cache_append(*plan, *args, k_new, v_new, kv_stride,
-                                      static_cast<int32_t*>(workspace),
-                                      static_cast<cudaStream_t>(stream));
+  return PA_OK;
+}
+
+pa_status pa_cache_append(const pa_plan_t* plan, const pa_args* args, const void* k_new,
+                          const void* v_new, int64_t kv_stride, void* workspace, void* stream) {
+  pa_status s = check_rows(plan, args, k_new, v_new, kv_stride, workspace);
+  if (s != PA_OK) return s;
+  int32_t* status = static_cast<int32_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = plan->four_bit()
+                            ? launch_cache_append4(*plan, *args, k_new, v_new, kv_stride, status, st)
+                            : launch_cache_append(*plan, *args, k_new, v_new, kv_stride, status, st);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("cache append: ") + cudaGetErrorString(e));
+  return PA_OK;
+}
+
+pa_status pa_cache_read(const pa_plan_t* plan, const pa_args* args, void* k_out, void* v_out,
+                        int64_t kv_stride, void* workspace, void* stream) {
+  pa_status s = check_rows(plan, args, k_out, v_out, kv_stride, workspace);
+  if (s != PA_OK) return s;
+  const cudaError_t e = launch_cache_read(*plan, *args, k_out, v_out, kv_stride,
+                                          static_cast<int32_t*>(workspace),
+                                          static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("cache read: ") + cudaGetErrorString(e));
   return PA_OK;
 }
 

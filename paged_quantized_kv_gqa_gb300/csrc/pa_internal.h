@@ -18,6 +18,7 @@ constexpr int kItemWords = 8;        // b, kvh, token0, n_tok, causal_base, kv0,
 constexpr int kDecodeRows = 64;      // packed (token, head) rows per decode tile
 constexpr int kWarpDecodeRows = 16;  // decode tiles up to this many rows run warp per item
 constexpr int kAppendRows = 256;     // packed rows per append item (two 128-row tiles)
+constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache
 constexpr int kStatusBytes = 256;    // status block at the start of the workspace
 constexpr int64_t kDefaultWaitNs = 2000000000LL;
 constexpr int64_t kMinWaitNs = 1000000LL;      // floor of the test hook's wait limit
@@ -52,6 +53,7 @@ struct Plan {
   size_t part_o_off = 0, part_m_off = 0, part_d_off = 0, ws_bytes = 0;  // byte offsets
   int64_t kv_bytes = 0;
   double flops = 0.0;
+  bool four_bit() const { return prob.kv_dtype == PA_KV_INT4 || prob.kv_dtype == PA_KV_FP4_E2M1; }
   int32_t num_items() const { return (int32_t)(items.size() / kItemWords); }
 };
 
@@ -144,6 +146,14 @@ cudaError_t launch_mla(const Plan& plan, const AttnParams& p, const CUtensorMap&
 cudaError_t launch_cache_append(const Plan& plan, const pa_args& a, const void* k_new,
                                 const void* v_new, int64_t kv_stride, int32_t* status,
                                 cudaStream_t stream);
+// the 4-bit cache: attention, quantise-and-write; every cache: read back as bf16
+cudaError_t launch_attn4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
+                         cudaStream_t stream);
+cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void* k_new,
+                                 const void* v_new, int64_t kv_stride, int32_t* status,
+                                 cudaStream_t stream);
+cudaError_t launch_cache_read(const Plan& plan, const pa_args& a, void* k_out, void* v_out,
+                              int64_t kv_stride, int32_t* status, cudaStream_t stream);
 cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* lse,
                          const OutEpilogue& ep, cudaStream_t stream);
 cudaError_t launch_gather(const pa_problem& prob, const pa_args& a, int32_t b, int32_t kvh,

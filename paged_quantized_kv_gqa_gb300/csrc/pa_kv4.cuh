@@ -1,0 +1,72 @@
+// pa_kv4.cuh - the 4-bit cache: slab layout, code and scale conversions.
+//
+// K and V of one (page, kv head) are a slab each: two half pages of 32
+// positions one after the other, so that a half page (what a warp works on) is
+// one contiguous, 16-byte aligned run of bytes and moves with one bulk copy:
+//   K half  codes  [32 positions][64 bytes]   byte i = dims 2i (low nibble), 2i+1
+//           scales [32 positions][8]          E4M3, one per 16 dims
+//   V half  codes  [128 dims][16 bytes]       byte i = positions 2i (low), 2i+1
+//           scales [8 blocks of 16 dims][32 positions]
+// V is transposed (as in the 8-bit cache) so that an MMA operand's pairs along
+// the positions are neighbours; its scales are transposed with it.
+//
+// A stored value is code * block scale * tensor scale.  code * block scale has
+// at most 3 + 4 significant bits and lies in [2^-10, 3584], so it is exact in
+// fp16: the attention kernels multiply in fp16 without a rounding, and the
+// tensor scale enters where the 8-bit kernels apply theirs (per channel K: into
+// Q'; otherwise into the softmax scale; V: at the output).
+#pragma once
+
+#include <cstdint>
+
+#include "pa_ptx.cuh"
+
+namespace pa {
+
+constexpr int kV4Half = 32;                              // positions per half page
+constexpr int kV4Dim = 128;
+constexpr int kV4Blk = 16;                               // dims per block scale
+constexpr int kV4Nblk = kV4Dim / kV4Blk;
+constexpr int kV4Codes = kV4Half * kV4Dim / 2;           // code bytes of a half page
+constexpr int kV4HalfBytes = kV4Codes + kV4Half * kV4Nblk;
+constexpr int kV4Slab = 2 * kV4HalfBytes;                // one (page, kv head) of K or V
+static_assert(kV4HalfBytes % 16 == 0, "half pages move with bulk copies");
+
+// byte offsets within a slab; pos = position within the page
+__device__ __forceinline__ int k4_code_off(int pos, int dim) {
+  return (pos / kV4Half) * kV4HalfBytes + (pos % kV4Half) * (kV4Dim / 2) + dim / 2;
+}
+__device__ __forceinline__ int k4_scale_off(int pos, int blk) {
+  return (pos / kV4Half) * kV4HalfBytes + kV4Codes + (pos % kV4Half) * kV4Nblk + blk;
+}
+__device__ __forceinline__ int v4_code_off(int pos, int dim) {
+  return (pos / kV4Half) * kV4HalfBytes + dim * (kV4Half / 2) + (pos % kV4Half) / 2;
+}
+__device__ __forceinline__ int v4_scale_off(int pos, int blk) {
+  return (pos / kV4Half) * kV4HalfBytes + kV4Codes + blk * kV4Half + pos % kV4Half;
+}
+
+// E4M3 byte -> fp32 (exact)
+__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(b & 0xFF)));
+  return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFF)));
+}
+
+// a 4-bit code -> fp32 (exact).  FP4: E2M1, sign in bit 3; else two's complement.
+template <int FP4>
+__device__ __forceinline__ float code4_to_f32(uint32_t c) {
+  if constexpr (FP4) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+        : "=r"(h)
+        : "r"(c & 15u));
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFF)));
+  } else {
+    return (float)((int)(c << 28) >> 28);
+  }
+}
+
+}  // namespace pa
