@@ -38,6 +38,16 @@ Spec:
   nch_token[t] = nch of token t's tile; max_chunks = max(1, max nch_token);
   merge_tokens = tokens with nch_token != 1, ascending (those with 0 chunks are
   the rows that see nothing; the merge writes them).
+  A 4-bit cache, decode family, max(q_len) * G <= 16 and chunk_size != 0:
+  shares of equal work per warp (16 warps per CTA).  The tiles' pages are
+  numbered as for MLA below; quota = max(2, ceil(total / max(1, slots * 16 //
+  kv_heads))), at most chunk_size / B if that is positive; share k covers pages
+  [k*quota, (k+1)*quota); its pieces are its overlaps with the tiles, numbered
+  per tile.  Lanes (share, kv head), share-major, are dealt to num_ctas =
+  min(slots, #lanes) CTAs: CTA c takes lanes [c*L // num_ctas, (c+1)*L //
+  num_ctas); its items (lane order, a share's pieces in tile order) are sorted by
+  length descending, ties in that order.  chunk (as reported) = quota * B if
+  some tile has more than one piece, else 0.
   MLA with chunk_size = -1 replaces the chunk size and the longest-first
   deal by contiguous shares (this library's scheduling choice; the pages fix
   only what an item computes): the tiles' pages, ceil(lim / B) per tile,
@@ -88,6 +98,9 @@ def plan(p, num_sms: int) -> dict:
             lim = slkv[b] if cross else slkv[b] + tok1 if p.causal else slkv[b] + ql
             tiles.append((b, tok0, tok1, lim))
 
+    if (p.kv_dtype in ("int4", "fp4_e2m1") and family == "decode" and max_q * G <= 16
+            and int(p.chunk_size) != 0):
+        return _warp_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross)
     if family == "mla" and int(p.chunk_size) == -1:
         return _mla_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B)
 
@@ -134,6 +147,47 @@ def plan(p, num_sms: int) -> dict:
     return dict(family=family, chunk=cs, tokens_per_tile=tpt, num_ctas=num_ctas,
                 items=arr, work_indptr=indptr, nch_token=nch_token,
                 max_chunks=max_chunks, merge_tokens=merge_tokens)
+
+
+def _warp_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross):
+    """Equal shares of the pages per warp (the 4-bit decode rule in the spec above)."""
+    npages = [math.ceil(t[3] / B) for t in tiles]
+    start = [sum(npages[:i]) for i in range(len(tiles))]
+    total = sum(npages)
+    quota = max(2, math.ceil(total / max(1, slots * 16 // p.kv_heads)))
+    if int(p.chunk_size) > 0:
+        quota = min(quota, int(p.chunk_size) // B)
+    shares = math.ceil(total / quota)
+    pieces, count = [], [0] * len(tiles)
+    for k in range(shares):
+        mine = []
+        for i, (b, tok0, tok1, lim) in enumerate(tiles):
+            lo, hi = max(k * quota, start[i]), min((k + 1) * quota, start[i] + npages[i])
+            if lo < hi:
+                base = slkv[b] if cross else slkv[b] + tok0 if p.causal else slkv[b] + q_lens[b]
+                mine.append((i, b, cu[b] + tok0, tok1 - tok0, base, (lo - start[i]) * B,
+                             min(lim, (hi - start[i]) * B), count[i]))
+                count[i] += 1
+        pieces.append(mine)
+    lanes = [(k, h) for k in range(shares) for h in range(p.kv_heads)]
+    L = len(lanes)
+    num_ctas = min(slots, L)
+    rows, indptr = [], np.zeros(num_ctas + 1, dtype=np.int32)
+    for c in range(num_ctas):
+        mine = [(x, h) for k, h in lanes[L * c // num_ctas:L * (c + 1) // num_ctas] for x in pieces[k]]
+        mine.sort(key=lambda y: y[0][5] - y[0][6])          # longest first, stable
+        for (i, b, tok, n, base, kv0, kv1, idx), h in mine:
+            rows.append((b, h, tok, n, base, kv0, kv1, idx | (count[i] << 16)))
+        indptr[c + 1] = len(rows)
+    T = cu[-1] if cu else 0
+    nch_token = np.zeros(T, dtype=np.int32)
+    for i, (b, tok0, tok1, _) in enumerate(tiles):
+        nch_token[cu[b] + tok0:cu[b] + tok1] = count[i]
+    arr = np.array(rows, dtype=np.int64).reshape(-1, 8).astype(np.int32)
+    return dict(family="decode", chunk=quota * B if max(count, default=0) > 1 else 0, tokens_per_tile=tpt,
+                num_ctas=num_ctas, items=arr, work_indptr=indptr, nch_token=nch_token,
+                max_chunks=int(max(1, nch_token.max() if T else 1)),
+                merge_tokens=np.nonzero(nch_token != 1)[0].astype(np.int32))
 
 
 def _mla_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B):

@@ -151,7 +151,73 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       tiles.push_back({b, tok0, tok1, lim});
     }
   }
-  if (P.family == PA_FAMILY_MLA && prob.chunk_size == -1) {
+  const bool warp4 = P.four_bit() && P.family == PA_FAMILY_DECODE && max_q * G <= kWarpDecodeRows;
+  if (warp4 && prob.chunk_size != 0) {
+    // 4-bit decode, one warp per item: the pages of all tiles, tile after tile,
+    // are cut into shares of `quota` pages, about one share per kv head and warp
+    // of the grid, so that every warp has the same work and few partial states
+    // are merged (a chunk size bounds a share).  A share's pieces (its overlaps
+    // with the tiles) are run for every kv head; the (share, kv head) lanes are
+    // dealt to the CTAs in runs of equal length, each CTA's items longest first.
+    std::vector<int64_t> first_page(tiles.size() + 1, 0);
+    for (size_t i = 0; i < tiles.size(); ++i)
+      first_page[i + 1] = first_page[i] + ceil_div(tiles[i].lim, (int64_t)B);
+    const int64_t total = first_page.back();
+    const int64_t groups = std::max<int64_t>(1, (int64_t)slots * kDecode4Warps / prob.kv_heads);
+    int64_t quota = std::max<int64_t>(kDecode4MinPages, ceil_div(total, groups));
+    if (prob.chunk_size > 0) quota = std::min<int64_t>(quota, prob.chunk_size / B);
+    const int64_t shares = ceil_div(total, quota), lanes = shares * prob.kv_heads;
+    if (lanes > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "too many work items");
+    P.num_ctas = (int)std::min<int64_t>(slots, lanes);
+    P.nch_token.assign(P.total_q, 0);
+    std::vector<int32_t> share_pieces, nch(tiles.size(), 0);   // pieces of each share, as item records
+    std::vector<int64_t> share_at(shares + 1, 0);
+    size_t i0 = 0;
+    for (int64_t k = 0; k < shares; ++k) {
+      const int64_t a = k * quota, e = std::min(total, a + quota);
+      while (first_page[i0 + 1] <= a) ++i0;
+      for (size_t i = i0; i < tiles.size() && first_page[i] < e; ++i) {
+        if (first_page[i + 1] <= a || first_page[i + 1] == first_page[i]) continue;
+        const Tile& t = tiles[i];
+        const int64_t kv0 = (std::max(a, first_page[i]) - first_page[i]) * B;
+        const int64_t kv1 = std::min<int64_t>(t.lim, (std::min(e, first_page[i + 1]) - first_page[i]) * B);
+        const int64_t base = (int64_t)slkv[t.b] + (causal ? t.tok0 : cross ? 0 : ql[t.b]);
+        const int32_t rec[kItemWords] = {t.b, (int32_t)i, cu[t.b] + t.tok0, t.tok1 - t.tok0, (int32_t)base,
+                                         (int32_t)kv0, (int32_t)kv1, nch[i]++};
+        share_pieces.insert(share_pieces.end(), rec, rec + kItemWords);
+      }
+      share_at[k + 1] = (int64_t)(share_pieces.size() / kItemWords);
+    }
+    bool any_split = false;
+    for (size_t i = 0; i < tiles.size(); ++i) {
+      if (nch[i] > 0xFFFF) return fail(PA_ERR_UNSUPPORTED, "too many chunks per row");
+      any_split = any_split || nch[i] > 1;
+      for (int tok = tiles[i].tok0; tok < tiles[i].tok1; ++tok) P.nch_token[cu[tiles[i].b] + tok] = nch[i];
+    }
+    P.chunk = any_split ? (int32_t)(quota * B) : 0;
+    P.work_indptr.assign(P.num_ctas + 1, 0);
+    P.items.clear();
+    std::vector<std::pair<int64_t, int32_t>> mine;   // (piece, kv head) of a CTA
+    for (int c = 0; c < P.num_ctas; ++c) {
+      mine.clear();
+      for (int64_t l = lanes * c / P.num_ctas; l < lanes * (c + 1) / P.num_ctas; ++l)
+        for (int64_t s = share_at[l / prob.kv_heads]; s < share_at[l / prob.kv_heads + 1]; ++s)
+          mine.push_back({s, (int32_t)(l % prob.kv_heads)});
+      auto len = [&](const std::pair<int64_t, int32_t>& x) {
+        const int32_t* r = &share_pieces[(size_t)x.first * kItemWords];
+        return r[6] - r[5];
+      };
+      std::stable_sort(mine.begin(), mine.end(), [&](const auto& x, const auto& y) { return len(x) > len(y); });
+      for (const auto& x : mine) {
+        int32_t rec[kItemWords];
+        std::copy_n(&share_pieces[(size_t)x.first * kItemWords], kItemWords, rec);
+        rec[7] |= nch[rec[1]] << 16;
+        rec[1] = x.second;
+        P.items.insert(P.items.end(), rec, rec + kItemWords);
+      }
+      P.work_indptr[c + 1] = (int32_t)(P.items.size() / kItemWords);
+    }
+  } else if (P.family == PA_FAMILY_MLA && prob.chunk_size == -1) {
     // MLA with the planner's choice: contiguous shares.  The pages of all
     // tiles, tile after tile, are cut into shares of `quota` pages; CTA pair k
     // runs the pieces of the tiles that overlap share k, in tile order.  A
@@ -298,7 +364,11 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
                                 ? 0
                                 : (size_t)P.total_q * P.max_chunks * prob.q_heads;
   P.part_o_off = off;
-  off = align_up(off + slots_part * prob.head_dim_v * sizeof(__nv_bfloat16), 256);
+  // partial rows: bf16; fp32 over a 4-bit cache, where a second rounding to bf16
+  // would be the largest error of the result (measured on chunked decode: error
+  // against 64 bits 0.0024 with bf16 partial rows, 0.0017 without)
+  off = align_up(off + slots_part * prob.head_dim_v * (P.four_bit() ? sizeof(float) : sizeof(__nv_bfloat16)),
+                 256);
   P.part_m_off = off;
   off = align_up(off + slots_part * sizeof(float), 256);
   P.part_d_off = off;
@@ -567,7 +637,10 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
   if (plan->four_bit()) {
     if (plan->family == PA_FAMILY_APPEND && reinterpret_cast<uintptr_t>(args->out) % 16)
       return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
-    e = launch_attn4(*plan, p, args->cache_k, args->cache_v, st);
+    if (plan->family == PA_FAMILY_DECODE && plan->max_q * p.group <= kWarpDecodeRows)
+      e = launch_decode4(*plan, p, args->cache_k, args->cache_v, st);
+    else
+      e = launch_attn4(*plan, p, args->cache_k, args->cache_v, st);
   } else if (plan->family == PA_FAMILY_DECODE) {
     CUtensorMap tk, tv;
     const uint64_t heads_total = (uint64_t)pr.num_pages * pr.kv_heads;

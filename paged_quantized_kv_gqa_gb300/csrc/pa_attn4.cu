@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) attn4_kernel(const uint8_t* __restrict__ 
       const float v = o[e] * inv * gv[e];
       const int d = 4 * lane + e;
       if (m.nch > 1) {
-        p.part_o[sp * 128 + d] = __float2bfloat16_rn(v);
+        reinterpret_cast<float*>(p.part_o)[sp * 128 + d] = v;
       } else {
         const float f = ep_value(p.ep, v, head * 128 + d);
         const int64_t oi = ((int64_t)token * p.q_heads + head) * 128 + d;

@@ -180,6 +180,41 @@ __device__ __forceinline__ void ep_store16(const OutEpilogue& e, void* out, int6
   }
 }
 
+// The same for 8 dims at out element offset o; element stores unless `vec`
+// (out 16-byte aligned).
+__device__ __forceinline__ void ep_store8(const OutEpilogue& e, void* out, int64_t o, int idx0,
+                                          const float (&v)[8], bool vec) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = ep_value(e, v[k], idx0 + k);
+  if (e.int8_out) {
+    int8_t* dst = reinterpret_cast<int8_t*>(out) + o;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k >> 2] |= ep_int8(e, f[k]) << (8 * (k & 3));
+    if (vec) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dst[k] = (int8_t)((w[k >> 2] >> (8 * (k & 3))) & 0xFF);
+    }
+  } else {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(out) + o;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+      w[k] = *reinterpret_cast<uint32_t*>(&b2);
+    }
+    if (vec) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dst[k] = __float2bfloat16_rn(f[k]);
+    }
+  }
+}
+
 // lane-0 arrive after the whole warp finished its part
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();

@@ -1,0 +1,590 @@
+// pa_decode4.cu - attention over the 4-bit cache for at most 16 packed query
+// rows per (sequence, kv head) tile: decode with small GQA groups.
+//
+// A warp owns whole work items (sequence, kv head, kv chunk), taken one after
+// the other from its CTA's list, and works on half pages of 32 positions:
+//   * load: K and V of a half page are one contiguous run of 2304 bytes each
+//     (codes and block scales together), so two bulk copies fill a stage of the
+//     warp's ring; the warp issues them itself, kStages half pages ahead;
+//   * S^T = K Q'^T with mma.sync m16n8k16 (M = 16 positions, N = 8 query rows):
+//     lane (g, t) holds dims 32 t .. 32 t + 31 of a position, i.e. 16 bytes of
+//     codes and two block scales, and turns each code pair into fp16 with one
+//     conversion and one multiplication by its block scale (exact); the dims are
+//     dealt to the k steps in whatever order the codes unpack to, Q' following;
+//   * running maximum and sum per row in fp32, P = 2^(x - m) in fp16, moved into
+//     the B operand by movmatrix;
+//   * O^T += V^T P^T: lane (g, t) holds positions 8 t .. 8 t + 7 of 16 dims, a
+//     32-bit word of codes each; a 16-dim MMA block is one scale block, so the
+//     scale pairs of the positions serve both rows of a lane.
+// What bounds it: 144 bytes a position and kv head, and per 32 positions about
+// 460 warp instructions (128 code pairs a lane, a conversion and a product
+// each), three fifths of the issue slots of the time that the bytes take.
+#include <cfloat>
+
+#include "pa_common.cuh"
+#include "pa_kv4.cuh"
+
+#ifndef D4_WARPS
+#define D4_WARPS 16
+#endif
+#ifndef D4_STAGES
+#define D4_STAGES 3
+#endif
+
+namespace pa {
+namespace {
+
+constexpr int kPage = 64;
+constexpr int kRing = 4;               // item records between load and compute cursors
+constexpr int kBtStride = 8;           // block-table entries kept per item (512 positions)
+constexpr int kScaleBytes = 4096;      // preloaded tensor scales (2 KB each for K and V)
+constexpr int kStage4 = 2 * kV4HalfBytes;
+
+template <int NB>
+struct D4Cfg {
+  static constexpr int kWarps = NB == 1 ? D4_WARPS : 8;
+  static constexpr int kStages = D4_STAGES;
+  static constexpr int kItems = 32;    // CTA item records kept in shared memory
+  static constexpr int kScaleOff = kWarps * kStages * kStage4;
+  static constexpr int kItemOff = kScaleOff + kScaleBytes;
+  static constexpr int kBtOff = kItemOff + kItems * kItemWords * 4;
+  static constexpr int kRecOff = kBtOff + kItems * kBtStride * 4;
+  static constexpr int kBarOff = kRecOff + kWarps * kRing * 48;
+  static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
+  static constexpr int kTotal = kMiscOff + 16 + 128;   // + alignment slack
+  static_assert(kTotal <= 232448, "shared memory overflow");
+  static_assert(kStages < kRing, "a record outlives its stages");
+  // the epilogue stages 8 NB rows of 128 fp32 in the item's last stages
+  static constexpr int kStageRows = 8;
+  static_assert(kStageRows * 128 * 4 <= kStage4, "output staging");
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 b16 transpose across the warp
+__device__ __forceinline__ uint32_t movtrans(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Position (0..31 within the half page) of MMA row g (h = 0) or g + 8 (h = 1)
+// of 16-position block b: the positions that lane t's V words unpack to.
+template <int FP4>
+__device__ __forceinline__ int kpos(int b, int g, int h) {
+  return FP4 ? 8 * (g >> 1) + 4 * b + 2 * h + (g & 1) : 8 * (g >> 1) + 2 * b + h + 4 * (g & 1);
+}
+
+}  // namespace
+
+template <int NB, int FP4, bool TREE>
+__global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
+    decode4_kernel(const uint8_t* __restrict__ cache_k, const uint8_t* __restrict__ cache_v,
+                   const AttnParams p) {
+  using C = D4Cfg<NB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int item_begin = p.work_indptr[blockIdx.x];
+  const int item_end = p.work_indptr[blockIdx.x + 1];
+  const uint64_t limit = (uint64_t)p.wait_limit_ns;
+  const int G = p.group;
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * C::kStages;
+  int32_t* items_s = reinterpret_cast<int32_t*>(smem + C::kItemOff);
+  int32_t* bt_s = reinterpret_cast<int32_t*>(smem + C::kBtOff);
+  int32_t* rec_ring = reinterpret_cast<int32_t*>(smem + C::kRecOff) + warp * kRing * 12;
+  int* next_item = reinterpret_cast<int*>(smem + C::kMiscOff);
+  volatile int* abort_any = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  const uint8_t* stage_p = smem + warp * C::kStages * kStage4;
+  const __nv_bfloat16* ks_s = reinterpret_cast<const __nv_bfloat16*>(smem + C::kScaleOff);
+  const __nv_bfloat16* vs_s = ks_s + kScaleBytes / 4;
+
+  const int sc_n = p.scale_kind == PA_SCALE_PER_CHANNEL ? p.kv_heads * kV4Dim
+                   : p.scale_kind == PA_SCALE_PER_KV_HEAD ? p.kv_heads : 0;
+  const bool sc_smem = sc_n > 0 && sc_n * 2 <= kScaleBytes / 2;
+  PA_DEBUG_PROLOGUE(smem, C::kTotal - 128, p, item_begin, item_end);
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < C::kWarps; ++w)
+      for (int s = 0; s < C::kStages; ++s)
+        mbar_init(reinterpret_cast<uint64_t*>(smem + C::kBarOff) + w * C::kStages + s, 1);
+    *next_item = item_begin;
+    *abort_any = 0;
+    fence_mbar_init();
+  }
+  const int n_staged = min(item_end - item_begin, C::kItems);
+  for (int i = threadIdx.x; i < n_staged * kItemWords; i += blockDim.x)
+    items_s[i] = p.items[(int64_t)item_begin * kItemWords + i];
+  if (sc_smem) {
+    __nv_bfloat16* kd = reinterpret_cast<__nv_bfloat16*>(smem + C::kScaleOff);
+    __nv_bfloat16* vd = kd + kScaleBytes / 4;
+    for (int i = threadIdx.x; i < sc_n; i += blockDim.x) {
+      kd[i] = reinterpret_cast<const __nv_bfloat16*>(p.k_scale)[i];
+      vd[i] = reinterpret_cast<const __nv_bfloat16*>(p.v_scale)[i];
+    }
+  }
+  __syncthreads();
+  // page ids of every staged item of at most kBtStride pages
+  for (int idx = threadIdx.x; idx < n_staged * kBtStride; idx += blockDim.x) {
+    const int32_t* rec = items_s + (idx / kBtStride) * kItemWords;
+    const int k = idx % kBtStride;
+    const int kv0 = rec[5];
+    const int np = (rec[6] - kv0 + kPage - 1) / kPage;
+    const int nb = p.max_blocks - kv0 / kPage;
+    bt_s[idx] = k < np && k < nb ? p.block_table[(int64_t)rec[0] * p.max_blocks + kv0 / kPage + k] : -1;
+  }
+  __syncthreads();
+
+  // -------------------------------------------------------------- load side
+  // warp-uniform cursor over this warp's half pages; the next item is taken
+  // when the current one's last half page is issued
+  int cur_it = -1, cur_b = 0, cur_kvh = 0, cur_kv0 = 0, cur_nh = 0, cur_h = 0;
+  int cur_bt = -1, nxt_bt = -1;       // lane k: page id of page 32 * batch + k of the item
+  int pend_it = -1, pend_rec = 0, pend_bt = -1;
+  // Q rows of a taken item, read several half pages before they are needed;
+  // lane (g, t): dims 32 t .. 32 t + 31 of row 8 j + g
+  uint4 qpre[NB][4];
+  int qpre_it = -1;
+  auto load_q_rows = [&](uint4 (&qr)[NB][4], int tok0, int ntok, int kvh) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int row = 8 * j + g;
+      const bool valid = row < ntok * G;
+      const __nv_bfloat16* src = p.q + (int64_t)(tok0 + (valid ? row / G : 0)) * p.q_stride +
+                                 (int64_t)(kvh * G + (valid ? row % G : 0)) * kV4Dim + 32 * t;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        qr[j][k] = make_uint4(0, 0, 0, 0);
+        if (valid) qr[j][k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
+      }
+    }
+  };
+  uint32_t n_load = 0;                // half pages issued by this warp
+  uint32_t k_load = 0;                // items started on the load side
+  const bool skip_hook = p.skip_first_load && blockIdx.x == 0;   // failure-detection test hook
+  uint32_t skipped_n = 0xFFFFFFFFu;
+
+  auto bt_at = [&](int b, int kv0, int pg) -> int {
+    const int np = p.max_blocks - kv0 / kPage;
+    return pg < np ? p.block_table[(int64_t)b * p.max_blocks + kv0 / kPage + pg] : -1;
+  };
+  auto take_pending = [&]() {
+    int it = 0;
+    if (lane == 0) it = atomicAdd(next_item, 1);
+    it = __shfl_sync(0xffffffffu, it, 0);
+    pend_it = it < item_end ? it : -1;
+    if (pend_it >= 0) {
+      const int k = pend_it - item_begin;
+      if (lane < kItemWords)
+        pend_rec = k < n_staged ? items_s[k * kItemWords + lane] : p.items[(int64_t)pend_it * kItemWords + lane];
+      const int b = __shfl_sync(0xffffffffu, pend_rec, 0);
+      const int kv0 = __shfl_sync(0xffffffffu, pend_rec, 5);
+      const int kv1 = __shfl_sync(0xffffffffu, pend_rec, 6);
+      const int np = (kv1 - kv0 + kPage - 1) / kPage;
+      if (k < n_staged && np <= kBtStride) pend_bt = lane < np ? bt_s[k * kBtStride + lane] : -1;
+      else pend_bt = lane < np ? bt_at(b, kv0, lane) : -1;
+      if (qpre_it < 0) {   // the previous prefetch has been used
+        load_q_rows(qpre, __shfl_sync(0xffffffffu, pend_rec, 2), __shfl_sync(0xffffffffu, pend_rec, 3),
+                    __shfl_sync(0xffffffffu, pend_rec, 1));
+        qpre_it = pend_it;
+      }
+    }
+  };
+  // issues the next half page of this warp's sequence
+  auto issue_next = [&]() -> bool {
+    bool skip_copy = false;
+    if (cur_it < 0 || cur_h == cur_nh) {
+      if (pend_it < 0) return false;
+      cur_it = pend_it;
+      cur_b = __shfl_sync(0xffffffffu, pend_rec, 0);
+      cur_kvh = __shfl_sync(0xffffffffu, pend_rec, 1);
+      cur_kv0 = __shfl_sync(0xffffffffu, pend_rec, 5);
+      const int kv1 = __shfl_sync(0xffffffffu, pend_rec, 6);
+      cur_nh = (kv1 - cur_kv0 + kV4Half - 1) / kV4Half;
+      cur_h = 0;
+      cur_bt = pend_bt;
+      nxt_bt = (lane + 32) * 2 < cur_nh ? bt_at(cur_b, cur_kv0, 32 + lane) : -1;
+      int32_t* slot = rec_ring + (k_load % kRing) * 12;   // the record for the compute side
+      if (lane < kItemWords) slot[lane] = pend_rec;
+      if (lane == kItemWords) slot[kItemWords] = cur_it;
+      __syncwarp();
+      ++k_load;
+      skip_copy = skip_hook && cur_it == item_begin;
+      pend_it = -1;
+    } else if ((cur_h & 63) == 0) {
+      cur_bt = nxt_bt;
+      const int pg = (cur_h >> 1) + 32 + lane;
+      nxt_bt = pg * 2 < cur_nh ? bt_at(cur_b, cur_kv0, pg) : -1;
+    }
+    const int page = __shfl_sync(0xffffffffu, cur_bt, (cur_h >> 1) & 31);
+    const int stage = n_load % C::kStages;
+    if (lane == 0 && !skip_copy) {
+      uint64_t* bar = &full[stage];
+      fence_proxy_async_smem();   // this stage's earlier reads before the new writes
+      mbar_arrive_expect_tx(bar, (uint32_t)kStage4);
+      const bool ok = page >= 0 && page < p.num_pages;
+      if (!ok) record_status(p.status, PA_ERR_BAD_PAGE, cur_it);
+      // a bad page id reads page 0 instead (the run's status says so)
+      const int64_t off = ((int64_t)(ok ? page : 0) * p.kv_heads + cur_kvh) * kV4Slab + (cur_h & 1) * kV4HalfBytes;
+      uint8_t* st = smem + (warp * C::kStages + stage) * kStage4;
+      bulk_load(st, cache_k + off, kV4HalfBytes, bar);
+      bulk_load(st + kV4HalfBytes, cache_v + off, kV4HalfBytes, bar);
+    }
+    __syncwarp();
+    if (skip_copy) skipped_n = n_load;
+    ++cur_h;
+    ++n_load;
+    if (cur_h == cur_nh) take_pending();   // the next item, one stage ahead of its use
+    return true;
+  };
+
+  // ------------------------------------------------------------ compute side
+  bool fail = false;
+  take_pending();
+  for (int s = 0; s < C::kStages; ++s)
+    if (!issue_next()) break;
+
+  uint32_t n_comp = 0, k_comp = 0;
+  while (!fail && n_comp < n_load) {
+    const int32_t* slot = rec_ring + (k_comp % kRing) * 12;
+    const Item m = item_from<kV4Half>(*reinterpret_cast<const int4*>(slot), *reinterpret_cast<const int4*>(slot + 4));
+    const int it = slot[kItemWords];
+    const int n_rows = m.ntok * G;
+    const int nh = m.ntiles;   // half pages
+    float c_log2 = p.sm_scale_log2;
+    if (p.scale_kind == PA_SCALE_GLOBAL) c_log2 *= reinterpret_cast<const float*>(p.k_scale)[0];
+    else if (p.scale_kind == PA_SCALE_PER_KV_HEAD)
+      c_log2 *= __bfloat162float(sc_smem ? ks_s[m.kvh] : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)[m.kvh]);
+    int tok0_local = 0, pre_len = 0;
+    const uint8_t* tmask = nullptr;
+    if constexpr (TREE) {
+      tok0_local = m.tok0 - p.cu_seqlens_q[m.b];
+      pre_len = m.cbase - tok0_local;
+      tmask = p.attn_mask + (int64_t)m.b * p.mask_dim * p.mask_dim;
+    }
+
+    // Q' fragments of row 8 j + g: k step ks takes dims 32 t + 8 (ks / 2) + the
+    // pairs that the codes of that word unpack to
+    uint32_t qf[NB][8][2];
+    {
+      uint4 qr[NB][4];
+      if (it == qpre_it) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) qr[j][k] = qpre[j][k];
+        qpre_it = -1;
+      } else {
+        load_q_rows(qr, m.tok0, m.ntok, m.kvh);
+      }
+      const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
+      const __nv_bfloat16* sk = (sc_smem ? ks_s : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)) +
+                                (pc ? m.kvh * kV4Dim + 32 * t : 0);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float sc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sc[e] = pc ? __bfloat162float(sk[8 * w + e]) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const uint32_t u[4] = {qr[j][w].x, qr[j][w].y, qr[j][w].z, qr[j][w].w};
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b2 = *reinterpret_cast<const __nv_bfloat162*>(&u[e]);
+            f[2 * e] = __low2float(b2) * sc[2 * e];
+            f[2 * e + 1] = __high2float(b2) * sc[2 * e + 1];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            qf[j][2 * w + (i >> 1)][i & 1] =
+                FP4 ? pack_half2(f[2 * i], f[2 * i + 1]) : pack_half2(f[i], f[i + 4]);
+        }
+      }
+    }
+
+    float o[NB][8][4];
+    float mrow[NB][2], lrow[NB][2];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][d][e] = 0.f;
+      mrow[j][0] = mrow[j][1] = -INFINITY;
+      lrow[j][0] = lrow[j][1] = 0.f;
+    }
+
+    for (int hp = 0; hp < nh; ++hp) {
+      const int stage = n_comp % C::kStages;
+      if (!wait_or_abort(&full[stage], (n_comp / C::kStages) & 1, limit, abort_any, 32)) {
+        if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, it);
+        *abort_any = 1;
+        fail = true;
+        break;
+      }
+      const uint8_t* kst = stage_p + stage * kStage4;
+      const uint8_t* vst = kst + kV4HalfBytes;
+      const int pos0 = m.kv0 + hp * kV4Half;
+
+      // ---- S^T = K Q'^T for the two 16-position blocks
+      float s[2][NB][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][j][e] = 0.f;
+        uint4 kr[2];
+        uint32_t ksc[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = kpos<FP4>(b, g, h);
+          kr[h] = *reinterpret_cast<const uint4*>(kst + r * (kV4Dim / 2) + 16 * t);
+          scale_pair(*reinterpret_cast<const uint16_t*>(kst + kV4Codes + r * kV4Nblk + 2 * t), ksc[h][0], ksc[h][1]);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a[4], c[4];
+          codes8<FP4>(word_of(kr[0], w), a);
+          codes8<FP4>(word_of(kr[1], w), c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = scaled<FP4>(a[i], ksc[0][w >> 1], i);
+            c[i] = scaled<FP4>(c[i], ksc[1][w >> 1], i);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              mma_16816(s[b][j], a[2 * i], c[2 * i], a[2 * i + 1], c[2 * i + 1], qf[j][2 * w + i][0],
+                        qf[j][2 * w + i][1]);
+        }
+      }
+
+      // ---- scale, mask, running max, P
+      const bool need_mask = (pos0 + kV4Half > m.kv1) || (pos0 + kV4Half - 1 > m.cbase) ||
+                             (TREE && pos0 + kV4Half > pre_len);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int jpos = pos0 + kpos<FP4>(b, g, h);
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = s[b][j][2 * h + e] * c_log2;
+              if (need_mask) {
+                const int r = 8 * j + 2 * t + e;
+                bool vis = jpos < m.kv1 && jpos <= m.cbase + r / G;
+                if (TREE && vis && jpos >= pre_len && r < n_rows) {
+                  const int tl = tok0_local + r / G;
+                  vis = tmask[tl * p.mask_dim + (jpos - pre_len)] != 0;
+                }
+                x = vis ? x : -INFINITY;
+              }
+              s[b][j][2 * h + e] = x;
+            }
+        }
+      uint32_t pb[2][NB][2];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        float al[2], mu[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          const float mn = fmaxf(mrow[j][e], v);
+          al[e] = (mn == mrow[j][e]) ? 1.f : fast_exp2(mrow[j][e] - mn);
+          mrow[j][e] = mn;
+          mu[e] = mn == -INFINITY ? 0.f : mn;
+          lrow[j][e] *= al[e];
+        }
+        if (al[0] != 1.f || al[1] != 1.f) {
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            o[j][d][0] *= al[0];
+            o[j][d][2] *= al[0];
+            o[j][d][1] *= al[1];
+            o[j][d][3] *= al[1];
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float p0 = fast_exp2(s[b][j][0] - mu[0]);
+          const float p1 = fast_exp2(s[b][j][1] - mu[1]);
+          const float p2 = fast_exp2(s[b][j][2] - mu[0]);
+          const float p3 = fast_exp2(s[b][j][3] - mu[1]);
+          lrow[j][0] += p0 + p2;
+          lrow[j][1] += p1 + p3;
+          pb[b][j][0] = movtrans(pack_half2(p0, p1));
+          pb[b][j][1] = movtrans(pack_half2(p2, p3));
+        }
+      }
+
+      // ---- O^T += V^T P^T.  Positions past the chunk's end get scale 0: their
+      // bytes may hold anything, and a code is finite whatever it is.
+      const int nvalid = min(kV4Half, m.kv1 - pos0);
+      uint32_t vm[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p0 = FP4 ? 8 * t + 4 * b + 2 * i : 8 * t + 2 * b + i;
+          vm[b][i] = (p0 < nvalid ? 0x0000FFFFu : 0u) | (p0 + (FP4 ? 1 : 4) < nvalid ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t a[4], c[4], vs[2][2];
+        codes8<FP4>(*reinterpret_cast<const uint32_t*>(vst + (16 * d + g) * (kV4Half / 2) + 4 * t), a);
+        codes8<FP4>(*reinterpret_cast<const uint32_t*>(vst + (16 * d + g + 8) * (kV4Half / 2) + 4 * t), c);
+        const uint2 sw = *reinterpret_cast<const uint2*>(vst + kV4Codes + d * kV4Half + 8 * t);
+        if constexpr (FP4) {
+          e4m3x4_to_f16x4(sw.x, vs[0][0], vs[0][1]);
+          e4m3x4_to_f16x4(sw.y, vs[1][0], vs[1][1]);
+        } else {
+          e4m3x4_to_f16x4(__byte_perm(sw.x, sw.y, 0x5140), vs[0][0], vs[0][1]);
+          e4m3x4_to_f16x4(__byte_perm(sw.x, sw.y, 0x7362), vs[1][0], vs[1][1]);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t x[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t sc = nvalid < kV4Half ? vs[b][i] & vm[b][i] : vs[b][i];
+            x[2 * i] = scaled<FP4>(a[2 * b + i], sc, 2 * b + i);
+            x[2 * i + 1] = scaled<FP4>(c[2 * b + i], sc, 2 * b + i);
+          }
+#pragma unroll
+          for (int j = 0; j < NB; ++j) mma_16816(o[j][d], x[0], x[1], x[2], x[3], pb[b][j][0], pb[b][j][1]);
+        }
+      }
+
+      // the stage is free (the epilogue uses the item's last one)
+      __syncwarp();
+      ++n_comp;
+      if (hp + 1 < nh) issue_next();
+    }
+    if (fail) break;
+
+    // ---- epilogue, 8 rows at a time: O / l as fp32 [8 rows][128 dims] through
+    // the item's last stage (dims of row r XOR 8 ((r >> 1) & 3): no bank
+    // conflicts), out as 16-byte pieces
+    float* stg = reinterpret_cast<float*>(smem + (warp * C::kStages + (n_comp - 1) % C::kStages) * kStage4);
+    const bool final_row = m.nch == 1;
+    const bool per_channel = p.scale_kind == PA_SCALE_PER_CHANNEL;
+    const float vs_head = p.scale_kind == PA_SCALE_GLOBAL ? reinterpret_cast<const float*>(p.v_scale)[0]
+                          : p.scale_kind == PA_SCALE_PER_KV_HEAD
+                              ? __bfloat162float(sc_smem ? vs_s[m.kvh]
+                                                         : reinterpret_cast<const __nv_bfloat16*>(p.v_scale)[m.kvh])
+                              : 1.f;
+    const __nv_bfloat16* vsc = (sc_smem ? vs_s : reinterpret_cast<const __nv_bfloat16*>(p.v_scale)) +
+                               (per_channel ? m.kvh * kV4Dim : 0);
+    const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = lrow[j][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int r = 8 * j + 2 * t + e;
+        const float inv = l > 0.f ? __frcp_rn(l) : 0.f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            stg[(2 * t + e) * kV4Dim + ((16 * d + g + 8 * h) ^ (8 * t))] = o[j][d][2 * h + e] * inv;
+        if (g == 0 && r < n_rows) {
+          const int token = m.tok0 + r / G;
+          const int head = m.kvh * G + r % G;
+          const float ln2 = 0.69314718055994530942f;
+          const float mr = mrow[j][e];
+          if (final_row) {
+            if (p.lse != nullptr)
+              p.lse[(int64_t)token * p.q_heads + head] = l > 0.f ? (mr + __log2f(l)) * ln2 : -INFINITY;
+          } else {
+            const int64_t sp = ((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head;
+            p.part_m[sp] = l > 0.f ? mr * ln2 : -INFINITY;
+            p.part_d[sp] = l;
+          }
+        }
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int idx = lane; idx < min(8, n_rows - 8 * j) * 16; idx += 32) {
+        const int rr = idx >> 4, c = idx & 15;   // row 8 j + rr, dims 8c .. 8c+7
+        const float* src = stg + rr * kV4Dim + ((8 * c) ^ (8 * ((rr >> 1) & 3)));
+        const float4 a = *reinterpret_cast<const float4*>(src);
+        const float4 b = *reinterpret_cast<const float4*>(src + 4);
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= per_channel ? __bfloat162float(vsc[8 * c + k]) : vs_head;
+        const int r = 8 * j + rr;
+        const int token = m.tok0 + r / G;
+        const int head = m.kvh * G + r % G;
+        if (final_row) {
+          ep_store8(p.ep, p.out, ((int64_t)token * p.q_heads + head) * kV4Dim + 8 * c, head * kV4Dim + 8 * c, v, vec);
+        } else {
+          float* dst = reinterpret_cast<float*>(p.part_o) +
+                       (((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head) * kV4Dim + 8 * c;
+          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
+      __syncwarp();   // the staged rows are read before they are overwritten
+    }
+    ++k_comp;
+    issue_next();   // the stage of the item's last half page
+  }
+
+  if (fail || *abort_any) {
+    if (!*abort_any) *abort_any = 1;
+    // every copy this warp issued lands before the CTA's shared memory is released
+    if (lane == 0)
+      for (uint32_t n = n_comp; n < n_load; ++n)
+        if (n != skipped_n) mbar_wait(&full[n % C::kStages], (n / C::kStages) & 1, kDrainNs);
+    __syncwarp();
+  }
+  pdl_launch_dependents();   // the merge grid may be scheduled while the last CTAs finish
+}
+
+template <int NB, int FP4>
+static cudaError_t launch_d4(const Plan& plan, const AttnParams& p, const uint8_t* ck, const uint8_t* cv,
+                             cudaStream_t stream) {
+  auto kern = p.attn_mask != nullptr ? decode4_kernel<NB, FP4, true> : decode4_kernel<NB, FP4, false>;
+  const int smem = D4Cfg<NB>::kTotal;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<plan.num_ctas, D4Cfg<NB>::kWarps * 32, smem, stream>>>(ck, cv, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
+                           cudaStream_t stream) {
+  const bool fp4 = plan.prob.kv_dtype == PA_KV_FP4_E2M1;
+  const uint8_t* k = static_cast<const uint8_t*>(ck);
+  const uint8_t* v = static_cast<const uint8_t*>(cv);
+  const int rows = plan.max_q * (plan.prob.q_heads / plan.prob.kv_heads);
+  if (rows <= 8) return fp4 ? launch_d4<1, 1>(plan, p, k, v, stream) : launch_d4<1, 0>(plan, p, k, v, stream);
+  if (rows <= 16) return fp4 ? launch_d4<2, 1>(plan, p, k, v, stream) : launch_d4<2, 0>(plan, p, k, v, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -18,6 +18,8 @@ constexpr int kItemWords = 8;        // b, kvh, token0, n_tok, causal_base, kv0,
 constexpr int kDecodeRows = 64;      // packed (token, head) rows per decode tile
 constexpr int kWarpDecodeRows = 16;  // decode tiles up to this many rows run warp per item
 constexpr int kAppendRows = 256;     // packed rows per append item (two 128-row tiles)
+constexpr int kDecode4Warps = 16;    // warps of a 4-bit decode CTA (each takes whole items)
+constexpr int kDecode4MinPages = 2;  // smallest share of a warp
 constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache
 constexpr int kStatusBytes = 256;    // status block at the start of the workspace
 constexpr int64_t kDefaultWaitNs = 2000000000LL;
@@ -65,7 +67,7 @@ struct WsView {
   const int32_t* nch_token;
   const int32_t* merge_tokens;
   int32_t* merge_cnt;   // fused merge counters or null
-  __nv_bfloat16* part_o;
+  __nv_bfloat16* part_o;   // fp32 rows for 4-bit plans
   float* part_m;
   float* part_d;
 };
@@ -147,6 +149,8 @@ cudaError_t launch_cache_append(const Plan& plan, const pa_args& a, const void* 
                                 const void* v_new, int64_t kv_stride, int32_t* status,
                                 cudaStream_t stream);
 // the 4-bit cache: attention, quantise-and-write; every cache: read back as bf16
+cudaError_t launch_decode4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
+                           cudaStream_t stream);
 cudaError_t launch_attn4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
                          cudaStream_t stream);
 cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void* k_new,

@@ -69,4 +69,48 @@ __device__ __forceinline__ float code4_to_f32(uint32_t c) {
   }
 }
 
+// Eight codes of a word -> four fp16x2 words, in the order `codes8` defines:
+//   FP4   word i = codes (2i, 2i + 1): one hardware conversion per byte;
+//   int4  word i = codes (i, i + 4), as 1024 + (code + 8) for even i and
+//         64 + (code + 8) for odd i: the nibble, its sign bit flipped, in the
+//         mantissa of that power of two (one logic operation per pair, one
+//         shift per word).
+// scaled() makes code * scale of it, exact in fp16 (see the file comment).
+template <int FP4>
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&o)[4]) {
+  if constexpr (FP4) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+  } else {
+    const uint32_t u = w >> 8;
+    o[0] = (w & 0x000F000Fu) ^ 0x64086408u;
+    o[1] = (w & 0x00F000F0u) ^ 0x54805480u;
+    o[2] = (u & 0x000F000Fu) ^ 0x64086408u;
+    o[3] = (u & 0x00F000F0u) ^ 0x54805480u;
+  }
+}
+
+template <int FP4>
+__device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t s, int i) {
+  uint32_t r;
+  if constexpr (!FP4)   // 1032 and 72
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"((i & 1) ? 0x54805480u : 0x64086408u));
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(s));
+  return r;
+}
+
+// Two E4M3 scales -> each as an fp16x2 word of two equal halves.
+__device__ __forceinline__ void scale_pair(uint16_t b, uint32_t& s0, uint32_t& s1) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
+  s0 = __byte_perm(h, h, 0x1010);
+  s1 = __byte_perm(h, h, 0x3232);
+}
+
 }  // namespace pa

@@ -114,12 +114,87 @@ __global__ void __launch_bounds__(256, DV >= 512 ? 5 : 1) merge_kernel(const int
   merge_store<DV>(acc[0], M[0], W[0], out, lse, ep, token, head, q_heads, lane);
 }
 
+// Rows whose partial states are fp32 (plans over a 4-bit cache), 128 wide: one
+// warp per row, lane l owning dims 4l .. 4l+3 (one 16-byte load per chunk row).
+// The (m, d) of up to 32 chunks sit one per lane; the first eight chunk rows are
+// requested before the weights are known, so that a row of at most eight chunks
+// costs one memory round trip.  A row without chunks comes out as 0 and -inf.
+__global__ void __launch_bounds__(256) merge_f32_kernel(const int32_t* __restrict__ merge_tokens,
+                                                        const int32_t* __restrict__ nch_token, int n_merge,
+                                                        int q_heads, int max_chunks,
+                                                        const float* __restrict__ part_o,
+                                                        const float* __restrict__ part_m,
+                                                        const float* __restrict__ part_d, void* __restrict__ out,
+                                                        float* __restrict__ lse, const OutEpilogue ep) {
+  pdl_wait();   // launched as a programmatic dependent of the attention kernel
+  const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (wid >= (int64_t)n_merge * q_heads) return;
+  const int token = merge_tokens[wid / q_heads];
+  const int head = (int)(wid % q_heads);
+  const int nch = nch_token[token];
+  const int64_t slot0 = (int64_t)token * max_chunks * q_heads + head;
+  constexpr int kU = 8;
+  const float4* rows = reinterpret_cast<const float4*>(part_o) + slot0 * 32 + lane;
+  const int64_t rstride = (int64_t)q_heads * 32;
+  float4 v[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) v[u] = u < nch ? __ldcg(rows + u * rstride) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, m0 = -INFINITY, d0 = 0.f;
+  for (int c = lane; c < nch; c += 32) {
+    const float mc = __ldcg(part_m + slot0 + (int64_t)c * q_heads);
+    if (c == lane) {
+      m0 = mc;
+      d0 = __ldcg(part_d + slot0 + (int64_t)c * q_heads);
+    }
+    M = fmaxf(M, mc);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}}, W = 0.f;
+  if (M != -INFINITY) {
+    for (int c0 = 0; c0 < nch; c0 += 32) {
+      if (c0 > 0) {
+        m0 = -INFINITY;
+        if (c0 + lane < nch) {
+          m0 = __ldcg(part_m + slot0 + (int64_t)(c0 + lane) * q_heads);
+          d0 = __ldcg(part_d + slot0 + (int64_t)(c0 + lane) * q_heads);
+        }
+      }
+      const float w = m0 != -INFINITY ? d0 * __expf(m0 - M) : 0.f;
+      W += w;
+      const int n = min(32, nch - c0);
+      for (int j = 0; j < n; j += kU) {
+        if (c0 + j > 0) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            v[u] = j + u < n ? __ldcg(rows + (c0 + j + u) * rstride) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const float wc = __shfl_sync(0xffffffffu, w, j + u);   // 0 past the last chunk
+          if (wc != 0.f) {
+            acc[0][0] += wc * v[u].x;
+            acc[0][1] += wc * v[u].y;
+            acc[0][2] += wc * v[u].z;
+            acc[0][3] += wc * v[u].w;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+  }
+  merge_store<128>(acc[0], M, W, out, lse, ep, token, head, q_heads, lane);
+}
+
 cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* lse,
                          const OutEpilogue& ep, cudaStream_t stream) {
   const int n_merge = (int)plan.merge_tokens.size();
   if (n_merge == 0) return cudaSuccess;
-  const int warps = n_merge * plan.prob.q_heads;
-  const int blocks = (warps + 7) / 8;
+  const int64_t warps = (int64_t)n_merge * plan.prob.q_heads;
+  if (warps > INT32_MAX) return cudaErrorInvalidValue;
+  const int blocks = (int)((warps + 7) / 8);
   // programmatic dependent launch: the grid is set up while the attention
   // kernel's last CTAs finish, and waits for it in pdl_wait
   cudaLaunchConfig_t cfg = {};
@@ -138,6 +213,9 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const __nv_bfloat16* po = ws.part_o;
   const float* pm = ws.part_m;
   const float* pd = ws.part_d;
+  if (plan.four_bit())
+    return cudaLaunchKernelEx(&cfg, merge_f32_kernel, mt, nt, n_merge, qh, mc,
+                              reinterpret_cast<const float*>(po), pm, pd, out, lse, ep);
   if (plan.prob.head_dim_v == 128)
     return cudaLaunchKernelEx(&cfg, merge_kernel<128>, mt, nt, n_merge, qh, mc, po, pm, pd, out, lse, ep);
   if (plan.prob.head_dim_v == 512)

@@ -74,12 +74,36 @@ def test_single_launch_option_is_not_taken_with_empty_rows_or_4_bits(pa):
         pa.pa_set_fused_merge(False)
 
 
-@pytest.mark.parametrize("kind", KINDS)
-def test_four_bit_plans_match_oracle(pa, kind):
-    p = make(2, seq_lens=[3, 0, 1], seq_lens_kv=[70, 5, 500], q_heads=8, kv_heads=2, kv_dtype=kind, chunk_size=128)
-    d = plan(pa, p).describe()
-    same_plan(d, op.plan(p, 152))
-    assert d["kv_bytes"] == (2 + 8) * 2 * 4608 * 2
+@pytest.mark.parametrize("seed", range(30))
+def test_four_bit_plans_match_oracle(pa, seed):
+    """Every family; decode with at most 16 rows takes equal shares of the pages."""
+    r = np.random.default_rng(100 + seed)
+    bsz, kvh, G = int(r.integers(1, 7)), int(r.choice([1, 3, 8])), int(r.choice([1, 4, 5, 16]))
+    q = r.integers(0, max(1, 16 // G) + 1, bsz) if seed % 3 else r.integers(0, 90, bsz)
+    p = make(seed, seq_lens=q, seq_lens_kv=r.integers(0, 4000, bsz), q_heads=kvh * G, kv_heads=kvh,
+             kv_dtype=KINDS[seed % 2], chunk_size=int(r.choice([0, 64, 512, -1, -1])), causal=bool(r.random() < 0.7),
+             garbage=False)
+    sms = int(r.choice([1, 8, 152]))
+    d = plan(pa, p, sms).describe()
+    same_plan(d, op.plan(p, sms))
+    assert d["kv_bytes"] == sum(-(-int(n) // 64) for n, a in zip(p.held, q) if a) * 2 * 4608 * kvh
+
+
+@pytest.mark.parametrize("chunk", [-1, 128, 4096])
+def test_decode_shares_cover_every_position_once(pa, chunk):
+    p = make(3, seq_lens=[1, 2, 1, 1], seq_lens_kv=[5000, 63, 0, 777], q_heads=12, kv_heads=3, chunk_size=chunk,
+             garbage=False)
+    d = plan(pa, p, 20).describe()
+    pieces = {}
+    for b, h, tok, n, base, lo, hi, c in d["items"].tolist():
+        pieces.setdefault((b, h), []).append((lo, hi, c & 0xFFFF, c >> 16))
+        assert lo < hi and (chunk < 0 or hi - lo <= chunk)
+    for b in range(4):
+        for h in range(3):
+            got = sorted(pieces[b, h])
+            assert [x[0] for x in got] == [0] + [x[1] for x in got[:-1]] and got[-1][1] == p.held[b]
+            assert [x[2] for x in got] == list(range(len(got))) and all(x[3] == len(got) for x in got)
+            assert (d["nch_token"][p.cu_seqlens_q[b]:p.cu_seqlens_q[b + 1]] == len(got)).all()
 
 
 def test_cache_bytes(pa):
