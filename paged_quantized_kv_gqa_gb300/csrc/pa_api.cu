@@ -634,13 +634,17 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
   }
 
   cudaError_t e;
-  if (plan->four_bit()) {
-    if (plan->family == PA_FAMILY_APPEND && reinterpret_cast<uintptr_t>(args->out) % 16)
-      return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
-    if (plan->family == PA_FAMILY_DECODE && plan->max_q * p.group <= kWarpDecodeRows)
+  const uint64_t slabs = (uint64_t)pr.num_pages * pr.kv_heads;
+  if (plan->four_bit() && plan->family == PA_FAMILY_DECODE) {
+    if (plan->max_q * p.group <= kWarpDecodeRows) {
       e = launch_decode4(*plan, p, args->cache_k, args->cache_v, st);
-    else
-      e = launch_attn4(*plan, p, args->cache_k, args->cache_v, st);
+    } else {
+      // a K slab is a box of 72 rows of 64 bytes
+      CUtensorMap tk;
+      s = make_map(&tk, args->cache_k, slabs * (kSlab4 / 64), 64, kSlab4 / 64, CU_TENSOR_MAP_SWIZZLE_64B);
+      if (s != PA_OK) return s;
+      e = launch_decode4_tm(*plan, p, tk, args->cache_v, st);
+    }
   } else if (plan->family == PA_FAMILY_DECODE) {
     CUtensorMap tk, tv;
     const uint64_t heads_total = (uint64_t)pr.num_pages * pr.kv_heads;
@@ -664,18 +668,20 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
     if (reinterpret_cast<uintptr_t>(args->out) % 16)
       return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
     CUtensorMap tk, tv, tq;
-    const uint64_t heads_total = (uint64_t)pr.num_pages * pr.kv_heads;
-    s = make_map(&tk, args->cache_k, heads_total * 64, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (s != PA_OK) return s;
-    s = make_map(&tv, args->cache_v, heads_total * 128, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B);
-    if (s != PA_OK) return s;
+    if (!plan->four_bit()) {
+      s = make_map(&tk, args->cache_k, slabs * 64, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+      if (s != PA_OK) return s;
+      s = make_map(&tv, args->cache_v, slabs * 128, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B);
+      if (s != PA_OK) return s;
+    }
     const int G = pr.q_heads / pr.kv_heads;
     const int box_tok = std::min(plan->tokens_per_tile, plan->total_q);
     s = make_map_q(&tq, args->q, (uint64_t)plan->total_q, (uint64_t)pr.q_heads, pr.q_stride,
                    (uint32_t)G, (uint32_t)box_tok);
     if (s != PA_OK) return s;
     p.q_box_tokens = box_tok;
-    e = launch_append(*plan, p, tk, tv, tq, st);
+    e = plan->four_bit() ? launch_append4(*plan, p, args->cache_k, args->cache_v, tq, st)
+                         : launch_append(*plan, p, tk, tv, tq, st);
   } else {
     // MLA: one latent row of 576 bytes per position, read as 128-byte boxes
     if (reinterpret_cast<uintptr_t>(args->out) % 16)

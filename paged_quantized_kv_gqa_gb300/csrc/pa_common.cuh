@@ -180,6 +180,13 @@ __device__ __forceinline__ void ep_store16(const OutEpilogue& e, void* out, int6
   }
 }
 
+// 16 dims of an fp32 partial row (16-byte aligned).
+__device__ __forceinline__ void store16_f32(float* dst, const float (&v)[16]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    reinterpret_cast<float4*>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+
 // The same for 8 dims at out element offset o; element stores unless `vec`
 // (out 16-byte aligned).
 __device__ __forceinline__ void ep_store8(const OutEpilogue& e, void* out, int64_t o, int idx0,

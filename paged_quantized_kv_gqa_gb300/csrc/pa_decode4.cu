@@ -30,6 +30,9 @@
 #ifndef D4_STAGES
 #define D4_STAGES 3
 #endif
+#ifndef D4_HINT
+#define D4_HINT 32
+#endif
 
 namespace pa {
 namespace {
@@ -39,6 +42,7 @@ constexpr int kRing = 4;               // item records between load and compute 
 constexpr int kBtStride = 8;           // block-table entries kept per item (512 positions)
 constexpr int kScaleBytes = 4096;      // preloaded tensor scales (2 KB each for K and V)
 constexpr int kStage4 = 2 * kV4HalfBytes;
+constexpr float kTau = 8.0f;           // lazy rescale: P stays below 2^8
 
 template <int NB>
 struct D4Cfg {
@@ -172,6 +176,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     }
   };
   uint32_t n_load = 0;                // half pages issued by this warp
+  int st_load = 0;                    // the stage of the next one
   uint32_t k_load = 0;                // items started on the load side
   const bool skip_hook = p.skip_first_load && blockIdx.x == 0;   // failure-detection test hook
   uint32_t skipped_n = 0xFFFFFFFFu;
@@ -229,16 +234,15 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       nxt_bt = pg * 2 < cur_nh ? bt_at(cur_b, cur_kv0, pg) : -1;
     }
     const int page = __shfl_sync(0xffffffffu, cur_bt, (cur_h >> 1) & 31);
-    const int stage = n_load % C::kStages;
     if (lane == 0 && !skip_copy) {
-      uint64_t* bar = &full[stage];
+      uint64_t* bar = &full[st_load];
       fence_proxy_async_smem();   // this stage's earlier reads before the new writes
       mbar_arrive_expect_tx(bar, (uint32_t)kStage4);
       const bool ok = page >= 0 && page < p.num_pages;
       if (!ok) record_status(p.status, PA_ERR_BAD_PAGE, cur_it);
       // a bad page id reads page 0 instead (the run's status says so)
-      const int64_t off = ((int64_t)(ok ? page : 0) * p.kv_heads + cur_kvh) * kV4Slab + (cur_h & 1) * kV4HalfBytes;
-      uint8_t* st = smem + (warp * C::kStages + stage) * kStage4;
+      const int64_t off = (int64_t)((ok ? page : 0) * p.kv_heads + cur_kvh) * kV4Slab + (cur_h & 1) * kV4HalfBytes;
+      uint8_t* st = smem + (warp * C::kStages + st_load) * kStage4;
       bulk_load(st, cache_k + off, kV4HalfBytes, bar);
       bulk_load(st + kV4HalfBytes, cache_v + off, kV4HalfBytes, bar);
     }
@@ -246,6 +250,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     if (skip_copy) skipped_n = n_load;
     ++cur_h;
     ++n_load;
+    if (++st_load == C::kStages) st_load = 0;
     if (cur_h == cur_nh) take_pending();   // the next item, one stage ahead of its use
     return true;
   };
@@ -257,6 +262,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     if (!issue_next()) break;
 
   uint32_t n_comp = 0, k_comp = 0;
+  int st_comp = 0;
+  uint32_t ph_comp = 0;
   while (!fail && n_comp < n_load) {
     const int32_t* slot = rec_ring + (k_comp % kRing) * 12;
     const Item m = item_from<kV4Half>(*reinterpret_cast<const int4*>(slot), *reinterpret_cast<const int4*>(slot + 4));
@@ -316,26 +323,25 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     }
 
     float o[NB][8][4];
-    float mrow[NB][2], lrow[NB][2];
+    float mrow[NB][2], mlim[NB][2], lrow[NB][2];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
 #pragma unroll
       for (int d = 0; d < 8; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][d][e] = 0.f;
-      mrow[j][0] = mrow[j][1] = -INFINITY;
+      mrow[j][0] = mrow[j][1] = mlim[j][0] = mlim[j][1] = -INFINITY;
       lrow[j][0] = lrow[j][1] = 0.f;
     }
 
     for (int hp = 0; hp < nh; ++hp) {
-      const int stage = n_comp % C::kStages;
-      if (!wait_or_abort(&full[stage], (n_comp / C::kStages) & 1, limit, abort_any, 32)) {
+      if (!wait_or_abort(&full[st_comp], ph_comp, limit, abort_any, D4_HINT)) {
         if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, it);
         *abort_any = 1;
         fail = true;
         break;
       }
-      const uint8_t* kst = stage_p + stage * kStage4;
+      const uint8_t* kst = stage_p + st_comp * kStage4;
       const uint8_t* vst = kst + kV4HalfBytes;
       const int pos0 = m.kv0 + hp * kV4Half;
 
@@ -374,6 +380,22 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         }
       }
 
+      uint16_t* vs16 = reinterpret_cast<uint16_t*>(smem + (warp * C::kStages + st_comp) * kStage4);   // [8][32]
+      // V scales as fp16, once per half page, over the K codes (every lane has read
+      // its own): lane (g, t) converts block g's
+      // positions 8t .. 8t+7, stored in the order their codes unpack to.
+      // Positions past the chunk's end get scale 0: their bytes may hold
+      // anything, and a code is finite whatever it is.
+      {
+        uint2 sw = *reinterpret_cast<const uint2*>(vst + kV4Codes + g * kV4Half + 8 * t);
+        const int left = m.kv1 - pos0 - 8 * t;   // valid positions of these eight
+        keep_scales(sw, left);
+        uint32_t f[4];
+        scales8<FP4>(sw, f);
+        __syncwarp();
+        *reinterpret_cast<uint4*>(vs16 + g * kV4Half + 8 * t) = make_uint4(f[0], f[1], f[2], f[3]);
+      }
+
       // ---- scale, mask, running max, P
       const bool need_mask = (pos0 + kV4Half > m.kv1) || (pos0 + kV4Half - 1 > m.cbase) ||
                              (TREE && pos0 + kV4Half > pre_len);
@@ -399,37 +421,48 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
               s[b][j][2 * h + e] = x;
             }
         }
+      // The running maximum moves only when some score exceeds it by 2^kTau (the
+      // vote makes that one decision for the warp); P and the sums stay relative
+      // to it in fp32.
+      bool exceed = false;
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          exceed |= fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e])) > mlim[j][e];
+      if (__any_sync(0xffffffffu, exceed)) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float mo = mrow[j][e], mn = fmaxf(mo, v);
+            // a row without a visible position so far keeps mrow = -inf, O = 0
+            const float al = mo == -INFINITY ? 0.f : fast_exp2(mo - mn);
+            mrow[j][e] = mn;
+            mlim[j][e] = mn == -INFINITY ? -INFINITY : mn + kTau;
+            lrow[j][e] *= al;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              o[j][d][e] *= al;
+              o[j][d][2 + e] *= al;
+            }
+          }
+      }
       uint32_t pb[2][NB][2];
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        float al[2], mu[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float mn = fmaxf(mrow[j][e], v);
-          al[e] = (mn == mrow[j][e]) ? 1.f : fast_exp2(mrow[j][e] - mn);
-          mrow[j][e] = mn;
-          mu[e] = mn == -INFINITY ? 0.f : mn;
-          lrow[j][e] *= al[e];
-        }
-        if (al[0] != 1.f || al[1] != 1.f) {
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            o[j][d][0] *= al[0];
-            o[j][d][2] *= al[0];
-            o[j][d][1] *= al[1];
-            o[j][d][3] *= al[1];
-          }
-        }
+        const float mu0 = mrow[j][0] == -INFINITY ? 0.f : mrow[j][0];
+        const float mu1 = mrow[j][1] == -INFINITY ? 0.f : mrow[j][1];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float p0 = fast_exp2(s[b][j][0] - mu[0]);
-          const float p1 = fast_exp2(s[b][j][1] - mu[1]);
-          const float p2 = fast_exp2(s[b][j][2] - mu[0]);
-          const float p3 = fast_exp2(s[b][j][3] - mu[1]);
+          const float p0 = fast_exp2(s[b][j][0] - mu0);
+          const float p1 = fast_exp2(s[b][j][1] - mu1);
+          const float p2 = fast_exp2(s[b][j][2] - mu0);
+          const float p3 = fast_exp2(s[b][j][3] - mu1);
           lrow[j][0] += p0 + p2;
           lrow[j][1] += p1 + p3;
           pb[b][j][0] = movtrans(pack_half2(p0, p1));
@@ -437,38 +470,21 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         }
       }
 
-      // ---- O^T += V^T P^T.  Positions past the chunk's end get scale 0: their
-      // bytes may hold anything, and a code is finite whatever it is.
-      const int nvalid = min(kV4Half, m.kv1 - pos0);
-      uint32_t vm[2][2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int p0 = FP4 ? 8 * t + 4 * b + 2 * i : 8 * t + 2 * b + i;
-          vm[b][i] = (p0 < nvalid ? 0x0000FFFFu : 0u) | (p0 + (FP4 ? 1 : 4) < nvalid ? 0xFFFF0000u : 0u);
-        }
+      // ---- O^T += V^T P^T
+      __syncwarp();   // the fp16 scales of every lane are in place
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
-        uint32_t a[4], c[4], vs[2][2];
+        uint32_t a[4], c[4];
         codes8<FP4>(*reinterpret_cast<const uint32_t*>(vst + (16 * d + g) * (kV4Half / 2) + 4 * t), a);
         codes8<FP4>(*reinterpret_cast<const uint32_t*>(vst + (16 * d + g + 8) * (kV4Half / 2) + 4 * t), c);
-        const uint2 sw = *reinterpret_cast<const uint2*>(vst + kV4Codes + d * kV4Half + 8 * t);
-        if constexpr (FP4) {
-          e4m3x4_to_f16x4(sw.x, vs[0][0], vs[0][1]);
-          e4m3x4_to_f16x4(sw.y, vs[1][0], vs[1][1]);
-        } else {
-          e4m3x4_to_f16x4(__byte_perm(sw.x, sw.y, 0x5140), vs[0][0], vs[0][1]);
-          e4m3x4_to_f16x4(__byte_perm(sw.x, sw.y, 0x7362), vs[1][0], vs[1][1]);
-        }
+        const uint4 sv = *reinterpret_cast<const uint4*>(vs16 + d * kV4Half + 8 * t);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t x[4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t sc = nvalid < kV4Half ? vs[b][i] & vm[b][i] : vs[b][i];
-            x[2 * i] = scaled<FP4>(a[2 * b + i], sc, 2 * b + i);
-            x[2 * i + 1] = scaled<FP4>(c[2 * b + i], sc, 2 * b + i);
+            x[2 * i] = scaled<FP4>(a[2 * b + i], word_of(sv, 2 * b + i), 2 * b + i);
+            x[2 * i + 1] = scaled<FP4>(c[2 * b + i], word_of(sv, 2 * b + i), 2 * b + i);
           }
 #pragma unroll
           for (int j = 0; j < NB; ++j) mma_16816(o[j][d], x[0], x[1], x[2], x[3], pb[b][j][0], pb[b][j][1]);
@@ -478,6 +494,10 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       // the stage is free (the epilogue uses the item's last one)
       __syncwarp();
       ++n_comp;
+      if (++st_comp == C::kStages) {
+        st_comp = 0;
+        ph_comp ^= 1;
+      }
       if (hp + 1 < nh) issue_next();
     }
     if (fail) break;
@@ -485,7 +505,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     // ---- epilogue, 8 rows at a time: O / l as fp32 [8 rows][128 dims] through
     // the item's last stage (dims of row r XOR 8 ((r >> 1) & 3): no bank
     // conflicts), out as 16-byte pieces
-    float* stg = reinterpret_cast<float*>(smem + (warp * C::kStages + (n_comp - 1) % C::kStages) * kStage4);
+    float* stg = reinterpret_cast<float*>(smem + (warp * C::kStages + (st_comp == 0 ? C::kStages : st_comp) - 1) * kStage4);
     const bool final_row = m.nch == 1;
     const bool per_channel = p.scale_kind == PA_SCALE_PER_CHANNEL;
     const float vs_head = p.scale_kind == PA_SCALE_GLOBAL ? reinterpret_cast<const float*>(p.v_scale)[0]

@@ -151,8 +151,10 @@ cudaError_t launch_cache_append(const Plan& plan, const pa_args& a, const void* 
 // the 4-bit cache: attention, quantise-and-write; every cache: read back as bf16
 cudaError_t launch_decode4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
                            cudaStream_t stream);
-cudaError_t launch_attn4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
-                         cudaStream_t stream);
+cudaError_t launch_decode4_tm(const Plan& plan, const AttnParams& p, const CUtensorMap& tm_k,
+                              const void* cv, cudaStream_t stream);
+cudaError_t launch_append4(const Plan& plan, const AttnParams& p, const void* ck, const void* cv,
+                           const CUtensorMap& tm_q, cudaStream_t stream);
 cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void* k_new,
                                  const void* v_new, int64_t kv_stride, int32_t* status,
                                  cudaStream_t stream);

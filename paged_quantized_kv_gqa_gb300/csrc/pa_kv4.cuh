@@ -19,6 +19,7 @@
 
 #include <cstdint>
 
+#include "pa.h"
 #include "pa_ptx.cuh"
 
 namespace pa {
@@ -103,6 +104,37 @@ __device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t s, int i) {
     asm("sub.f16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"((i & 1) ? 0x54805480u : 0x64086408u));
   asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(s));
   return r;
+}
+
+// The first element of pair i and the distance to its second, in elements, where
+// eight neighbours unpack to four fp16x2 words (8-bit formats: in order).
+template <int KV>
+__host__ __device__ constexpr int pair_first(int i) {
+  return KV == PA_KV_INT4 ? 8 * (i / 4) + i % 4 : 2 * i;
+}
+template <int KV>
+__host__ __device__ constexpr int pair_gap() {
+  return KV == PA_KV_INT4 ? 4 : 1;
+}
+
+// Eight E4M3 scales -> four fp16x2 words in the order of codes8.
+template <int FP4>
+__device__ __forceinline__ void scales8(uint2 w, uint32_t (&o)[4]) {
+  if constexpr (FP4) {
+    e4m3x4_to_f16x4(w.x, o[0], o[1]);
+    e4m3x4_to_f16x4(w.y, o[2], o[3]);
+  } else {
+    e4m3x4_to_f16x4(__byte_perm(w.x, w.y, 0x5140), o[0], o[1]);
+    e4m3x4_to_f16x4(__byte_perm(w.x, w.y, 0x7362), o[2], o[3]);
+  }
+}
+
+// Keeps the first n of eight scale bytes (n may be negative or above 8).
+__device__ __forceinline__ void keep_scales(uint2& w, int n) {
+  if (n < 8) {
+    w.x = n <= 0 ? 0u : n >= 4 ? w.x : w.x & (0xFFFFFFFFu >> (8 * (4 - n)));
+    w.y = n <= 4 ? 0u : w.y & (0xFFFFFFFFu >> (8 * (8 - n)));
+  }
 }
 
 // Two E4M3 scales -> each as an fp16x2 word of two equal halves.
