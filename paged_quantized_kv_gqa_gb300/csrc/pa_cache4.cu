@@ -11,22 +11,23 @@
 // NaN that a masked position could spread); an infinity saturates its block's
 // scale and itself.
 //
-// One warp per (sequence, half page of the appended range, kv head, K or V),
-// each reading its rows once with coalesced 8- or 16-byte loads:
+// One warp per (sequence, unit of 32 or 8 positions of the appended range, kv
+// head, K or V), each reading its rows once with coalesced 8- or 16-byte loads:
 //   K: lane = 8 dims of one row (two lanes per block), codes leave as a 32-bit
 //      word per lane;
-//   V: lane = 4 dims of all 32 positions (four lanes per block), so a dim's 16
-//      code bytes of the half page gather in the lane's registers and leave as
-//      one store; a half page that is written in part keeps the other nibbles
-//      (one warp owns a half page, so nobody else writes its bytes).
+//   V: lane = 4 dims of all the unit's positions (four lanes per block), so a
+//      dim's code bytes of the unit gather in the lane's registers and leave as
+//      one store.
 // The block maximum of uniform scales is taken on the bf16 bits, two elements a
 // step; the lanes of a block then work out a different row's scale each and
 // share them.  Quotients: an approximate reciprocal, and one correction of the
 // quotient by its residual, which gives every quotient that is exactly a border
-// between two codes exactly, and the others to the last bit; blocks out of the
-// common range (a scale that is not a normal E4M3 number, saturated, infinities,
-// NaN) take the division.
-// What bounds it: 2.56 bytes per element against about 8 instructions.
+// between two codes exactly, and the others to the last bit.
+// Rows that are not aligned and blocks out of the common range (a scale that is
+// not a normal E4M3 number or is saturated, infinities, NaN) go position by
+// position with divisions.  Where the range covers a unit in part, the nibbles of
+// other positions stay (one warp owns a unit, so nobody else writes its bytes).
+// What bounds it: 2.56 bytes per element against about 9 instructions.
 #include "pa_common.cuh"
 #include "pa_kv4.cuh"
 
@@ -35,6 +36,9 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kWarps = 8;
+// 64 registers a thread, 32 warps an SM: writing prompts of 33k tokens took 48.6,
+// 50.1, 38.2, 43.3 and 49.2 us with 2 to 6 CTAs an SM
+constexpr int kCtas = 4;
 
 struct Append4Params {
   const __nv_bfloat16* k_new;
@@ -53,9 +57,9 @@ struct Append4Params {
   int32_t num_pages;
   int32_t kv_heads;
   int32_t scale_kind;
-  int32_t units;       // half pages an appended range can touch
+  int32_t units;       // units an appended range can touch
   int32_t vec;         // rows may be read with 16-byte loads
-  uint32_t total;      // (sequence, half page, kv head, side) warps
+  uint32_t total;      // (sequence, unit, kv head, side) warps
 };
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -84,26 +88,20 @@ struct Fmt {
   static constexpr float kTop = FP4 ? 6.0f : 7.0f;
 };
 
-// Block scale from a = max |x / g|: the E4M3 byte.
+// Block scale from max |x / g| / M: the E4M3 byte.
 template <int FP4>
 __device__ __forceinline__ uint32_t block_scale(float a) {
   uint16_t sb;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(__fdiv_rn(a, Fmt<FP4>::kTop)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(a));
   return sb & 0xFFu;
 }
 
-// Whether the short quotients hold for a block: a normal, unsaturated scale and
-// a step far from the ends of the exponent range (false for NaN).
+// Whether the short quotients hold for a block of maximum a = max |x / g|: a
+// normal, unsaturated scale and a step far from the ends of the exponent range
+// (false for NaN).
 template <int FP4>
 __device__ __forceinline__ bool common(float a, float s, float step) {
   return s >= 0.015625f && a < 448.0f * Fmt<FP4>::kTop && step > 1e-30f && step < 1e30f;
-}
-
-// Any block, by division: x (NaN as 0) -> quotient clamped to the code range.
-template <int FP4>
-__device__ __forceinline__ float quot_any(float x, float step) {
-  const float q = step > 0.0f ? __fdiv_rn(x, step) : 0.0f;
-  return fminf(fmaxf(q, -Fmt<FP4>::kTop), Fmt<FP4>::kTop);
 }
 
 // Eight quotients -> eight codes, the first in the lowest nibble.
@@ -136,10 +134,57 @@ __device__ __forceinline__ uint32_t pack8(const float (&q)[8]) {
   return w;
 }
 
-// ---- K: rows of the half page, two at a time per load instruction
-template <int FP4, bool PC>
-__device__ __forceinline__ void write_k(const Append4Params& p, uint8_t* half, int kvh, int64_t row0, int lo, int hi,
-                                        int lane) {
+// ---- any positions, any values: [lo, hi) of the half page, lane = 4 dims
+template <int FP4>
+__device__ __noinline__ void write_any(const __nv_bfloat16* src, int64_t stride, const void* scale, int kind, int kvh,
+                                       uint8_t* half, bool value_side, int lo, int hi, int lane) {
+  constexpr float kTop = Fmt<FP4>::kTop;
+  float g[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    g[e] = load_scale(scale, kind, kind == PA_SCALE_PER_CHANNEL ? kvh * kV4Dim + 4 * lane + e : kvh);
+  src += 4 * lane;
+#pragma unroll 1
+  for (int r = lo; r < hi; ++r, src += stride) {
+    float x[4], a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = __bfloat162float(src[e]);
+      if (x[e] != x[e]) x[e] = 0.0f;
+      a = fmaxf(a, fabsf(__fdiv_rn(x[e], g[e])));
+    }
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    const uint32_t sb = block_scale<FP4>(__fdiv_rn(a, kTop));
+    const float s = e4m3_to_f32(sb);
+    float q[8] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float step = __fmul_rn(s, g[e]);
+      q[e] = fminf(fmaxf(step > 0.0f ? __fdiv_rn(x[e], step) : 0.0f, -kTop), kTop);
+    }
+    const uint32_t w = pack8<FP4>(q);
+    if (value_side) {
+      const int sh = 4 * (r & 1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint8_t* v = half + (4 * lane + e) * (kV4Half / 2) + r / 2;
+        *v = (uint8_t)((*v & (0xF0u >> sh)) | ((w >> (4 * e)) & 15u) << sh);
+      }
+      if ((lane & 3) == 0) half[kV4Codes + (lane >> 2) * kV4Half + r] = (uint8_t)sb;
+    } else {
+      *reinterpret_cast<uint16_t*>(half + r * (kV4Dim / 2) + 2 * lane) = (uint16_t)w;
+      if ((lane & 3) == 0) half[kV4Codes + r * kV4Nblk + (lane >> 2)] = (uint8_t)sb;
+    }
+  }
+}
+
+// ---- K, positions [lo, hi) of the unit of U that starts at `first` of the half
+// page (FULL: all of them); rows: the row of position lo
+template <int FP4, bool PC, int U, bool FULL>
+__device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloat16* rows, uint8_t* half, int kvh,
+                                        int first, int lo, int hi, int lane) {
+  auto in = [&](int r) { return FULL || (r >= lo && r < hi); };
   const int c = lane & 15, r0 = lane >> 4;   // dims 8c .. 8c+7 of rows r0, r0 + 2, ...
   float g[8], rg[8];
 #pragma unroll
@@ -147,113 +192,83 @@ __device__ __forceinline__ void write_k(const Append4Params& p, uint8_t* half, i
     g[e] = load_scale(p.k_scale, p.scale_kind, PC ? kvh * kV4Dim + 8 * c + e : kvh);
     rg[e] = rcp_approx(g[e]);
   }
-  const __nv_bfloat16* src0 = p.k_new + row0 + (int64_t)kvh * kV4Dim + 8 * c;
-  for (int base = lo & ~3; base < hi; base += 4) {
-    uint4 x[2];
-    bool ok[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = base + 2 * i + r0;
-      ok[i] = r >= lo && r < hi;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (ok[i]) {
-        const __nv_bfloat16* src = src0 + (int64_t)(r - lo) * p.kv_stride;
-        if (p.vec) {
-          x[i] = __ldg(reinterpret_cast<const uint4*>(src));
-        } else {
-          const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-          x[i] = make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
-                            h[6] | (uint32_t)h[7] << 16);
-        }
-      }
+  const __nv_bfloat16* src = rows + (FULL ? r0 : r0 - lo) * p.kv_stride + 8 * c;
+  const int64_t s2 = 2 * p.kv_stride;
+  uint8_t* codes = half + (first + r0) * (kV4Dim / 2) + 4 * c;
+  uint8_t* scales = half + kV4Codes + (first + 2 * (lane & 1) + r0) * kV4Nblk + (c >> 1);
+#pragma unroll 1
+  for (int base = 0; base < U; base += 8) {
+    if (!FULL && (base + 8 <= lo || base >= hi)) {
+      src += 4 * s2;
+      continue;
     }
-    float f[2][8];
+    uint4 xs[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int i = 0; i < 4; ++i, src += s2)
+      xs[i] = in(base + 2 * i + r0) ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[i][2 * e] = bf16_lo(w[e]);
-        f[i][2 * e + 1] = bf16_hi(w[e]);
-      }
-    }
-    // the block maxima of both rows; an even lane goes on with row 0's, odd row 1's
-    float a;
-    bool finite = true;
-    {
+    for (int h = 0; h < 2; ++h) {   // rows base + 4h + {0, 2} + r0
+      const uint4* x = xs + 2 * h;
+      float f[2][8];
       uint32_t m[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        m[i] = max_u16x2(max_u16x2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                         max_u16x2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[i][2 * e] = bf16_lo(w[e]);
+          f[i][2 * e + 1] = bf16_hi(w[e]);
+        }
+        m[i] = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                         max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      }
+      // the block maxima of both rows; an even lane goes on with the first row's
       uint32_t mm = max_u16x2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
       mm = max_u16x2(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
       const uint32_t mine = (lane & 1) ? mm >> 16 : mm & 0xFFFFu;
-      finite = mine < 0x7F80u;
+      float a;
       if constexpr (PC) {
         float y[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           y[i] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[i] = fmaxf(y[i], fabsf(__fdiv_rn(f[i][e], g[e])));
+          for (int e = 0; e < 8; ++e) y[i] = fmaxf(y[i], fabsf(quot(f[i][e], g[e], rg[e])));
         }
         const float t = (lane & 1) ? y[0] : y[1];
         a = fmaxf((lane & 1) ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, t, 1));
       } else {
-        a = __fdiv_rn(__uint_as_float(mine << 16), g[0]);
+        a = quot(__uint_as_float(mine << 16), g[0], rg[0]);
       }
-    }
-    uint32_t sb = block_scale<FP4>(a);
-    float s = e4m3_to_f32(sb);
-    const int my_row = base + 2 * (lane & 1) + r0;
-    const bool mine_ok = my_row >= lo && my_row < hi;
-    uint32_t w[2];
-    if (__all_sync(0xffffffffu, !mine_ok || (finite && common<FP4>(a, s, PC ? 1.0f : s * g[0])))) {
-      const float st = PC ? s : s * g[0], rs = rcp_approx(st);
+      const uint32_t sb = block_scale<FP4>(quot(a, Fmt<FP4>::kTop, 1.0f / Fmt<FP4>::kTop));
+      const float s = e4m3_to_f32(sb), st = PC ? s : s * g[0], rs = rcp_approx(st);
+      const bool mine_in = in(base + 4 * h + 2 * (lane & 1) + r0);
+      if (__all_sync(0xffffffffu, !mine_in || (mine < 0x7F80u && common<FP4>(a, s, st)))) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float si = __shfl_sync(0xffffffffu, st, (lane & ~1) | i);
-        const float ri = __shfl_sync(0xffffffffu, rs, (lane & ~1) | i);
-        float q[8];
+        for (int i = 0; i < 2; ++i) {
+          const float si = __shfl_sync(0xffffffffu, st, (lane & ~1) | i);
+          const float ri = __shfl_sync(0xffffffffu, rs, (lane & ~1) | i);
+          float q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = PC ? quot(f[i][e], si * g[e], ri * rg[e]) : quot(f[i][e], si, ri);
-        w[i] = pack8<FP4>(q);
-      }
-    } else {
-      float y[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        y[i] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (f[i][e] != f[i][e]) f[i][e] = 0.0f;
-          y[i] = fmaxf(y[i], fabsf(__fdiv_rn(f[i][e], g[PC ? e : 0])));
+          for (int e = 0; e < 8; ++e) q[e] = PC ? quot(f[i][e], si * g[e], ri * rg[e]) : quot(f[i][e], si, ri);
+          if (in(base + 4 * h + 2 * i + r0))
+            *reinterpret_cast<uint32_t*>(codes + (base + 4 * h + 2 * i) * (kV4Dim / 2)) = pack8<FP4>(q);
         }
-        y[i] = fmaxf(y[i], __shfl_xor_sync(0xffffffffu, y[i], 1));
-      }
-      sb = block_scale<FP4>((lane & 1) ? y[1] : y[0]);
-      s = e4m3_to_f32(sb);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float si = __shfl_sync(0xffffffffu, s, (lane & ~1) | i);
-        float q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = quot_any<FP4>(f[i][e], __fmul_rn(si, g[PC ? e : 0]));
-        w[i] = pack8<FP4>(q);
+        if (mine_in) scales[(base + 4 * h) * kV4Nblk] = (uint8_t)sb;
+      } else {
+        const int a0 = FULL ? base + 4 * h : max(lo, base + 4 * h);
+        write_any<FP4>(rows + (FULL ? a0 : a0 - lo) * p.kv_stride, p.kv_stride, p.k_scale, p.scale_kind, kvh, half,
+                       false, first + a0, first + (FULL ? base + 4 * h + 4 : min(hi, base + 4 * h + 4)), lane);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (ok[i]) *reinterpret_cast<uint32_t*>(half + (base + 2 * i + r0) * (kV4Dim / 2) + 4 * c) = w[i];
-    if (mine_ok) half[kV4Codes + my_row * kV4Nblk + (c >> 1)] = (uint8_t)sb;
   }
 }
 
-// ---- V: four dims of every position per lane, eight positions a step
-template <int FP4, bool PC>
-__device__ __forceinline__ void write_v(const Append4Params& p, uint8_t* half, int kvh, int64_t row0, int lo, int hi,
-                                        int lane) {
+// ---- V, the same: four dims of every position per lane
+template <int FP4, bool PC, int U, bool FULL>
+__device__ __forceinline__ void write_v(const Append4Params& p, const __nv_bfloat16* rows, uint8_t* half, int kvh,
+                                        int first, int lo, int hi, int lane) {
+  auto in = [&](int r) { return FULL || (r >= lo && r < hi); };
   const int sub = lane & 3, blk = lane >> 2;
   float g[4], rg[4];
 #pragma unroll
@@ -261,39 +276,19 @@ __device__ __forceinline__ void write_v(const Append4Params& p, uint8_t* half, i
     g[e] = load_scale(p.v_scale, p.scale_kind, PC ? kvh * kV4Dim + 4 * lane + e : kvh);
     rg[e] = rcp_approx(g[e]);
   }
-  const __nv_bfloat16* src0 = p.v_new + row0 + (int64_t)kvh * kV4Dim + 4 * lane;
-  uint32_t out[4][4];   // [dim][8-position word]
+  const __nv_bfloat16* src = rows - (FULL ? 0 : lo * p.kv_stride) + 4 * lane;
+  uint8_t* scales = half + kV4Codes + blk * kV4Half + first + sub;
+  uint32_t out[4][U / 8];   // [dim][8-position word]
+  bool all_common = true;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d) out[d][k] = 0;
-    if (8 * k + 8 <= lo || 8 * k >= hi) continue;
+  for (int k = 0; k < U / 8; ++k) {
     uint2 x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = 8 * k + j;
-      x[j] = make_uint2(0, 0);
-      if (r >= lo && r < hi) {
-        const __nv_bfloat16* src = src0 + (int64_t)(r - lo) * p.kv_stride;
-        if (p.vec) {
-          x[j] = __ldg(reinterpret_cast<const uint2*>(src));
-        } else {
-          const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-          x[j] = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-        }
-      }
-    }
+    for (int j = 0; j < 8; ++j, src += p.kv_stride)
+      x[j] = in(8 * k + j) ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
     float q[4][8];   // [dim][position]
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // positions 4h .. 4h+3; lane `sub` works out the scale of 4h + sub
-      float f[4][4];   // [position][dim]
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[j][0] = bf16_lo(x[4 * h + j].x);
-        f[j][1] = bf16_hi(x[4 * h + j].x);
-        f[j][2] = bf16_lo(x[4 * h + j].y);
-        f[j][3] = bf16_hi(x[4 * h + j].y);
-      }
       uint32_t m[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -307,6 +302,14 @@ __device__ __forceinline__ void write_v(const Append4Params& p, uint8_t* half, i
       }
       const uint32_t mp = (sub & 2) ? m23 : m01;
       const uint32_t mine = (sub & 1) ? mp >> 16 : mp & 0xFFFFu;
+      float f[4][4];   // [position][dim]
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[j][0] = bf16_lo(x[4 * h + j].x);
+        f[j][1] = bf16_hi(x[4 * h + j].x);
+        f[j][2] = bf16_lo(x[4 * h + j].y);
+        f[j][3] = bf16_hi(x[4 * h + j].y);
+      }
       float a;
       if constexpr (PC) {
         float y[4];
@@ -314,81 +317,64 @@ __device__ __forceinline__ void write_v(const Append4Params& p, uint8_t* half, i
         for (int j = 0; j < 4; ++j) {
           y[j] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[j] = fmaxf(y[j], fabsf(__fdiv_rn(f[j][e], g[e])));
+          for (int e = 0; e < 4; ++e) y[j] = fmaxf(y[j], fabsf(quot(f[j][e], g[e], rg[e])));
           y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 1));
           y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 2));
         }
         a = (sub & 2) ? ((sub & 1) ? y[3] : y[2]) : ((sub & 1) ? y[1] : y[0]);
       } else {
-        a = __fdiv_rn(__uint_as_float(mine << 16), g[0]);
+        a = quot(__uint_as_float(mine << 16), g[0], rg[0]);
       }
-      uint32_t sb = block_scale<FP4>(a);
-      float s = e4m3_to_f32(sb);
-      const int pos = 8 * k + 4 * h + sub;
-      const bool mine_ok = pos >= lo && pos < hi;
-      if (__all_sync(0xffffffffu,
-                     !mine_ok || (mine < 0x7F80u && common<FP4>(a, s, PC ? 1.0f : s * g[0])))) {
-        // (a position outside the range gets finite codes: a word holds several)
-        const float st = !mine_ok ? 1.0f : PC ? s : s * g[0], rs = rcp_approx(st);
+      const uint32_t sb = block_scale<FP4>(quot(a, Fmt<FP4>::kTop, 1.0f / Fmt<FP4>::kTop));
+      // (a position out of the range gets finite codes: a word holds several)
+      const bool mine_in = in(8 * k + 4 * h + sub);
+      const float s = e4m3_to_f32(sb), st = !mine_in ? 1.0f : PC ? s : s * g[0], rs = rcp_approx(st);
+      all_common = all_common && (!mine_in || (mine < 0x7F80u && common<FP4>(a, s, st)));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float sj = __shfl_sync(0xffffffffu, st, (lane & ~3) | j);
-          const float rj = __shfl_sync(0xffffffffu, rs, (lane & ~3) | j);
+      for (int j = 0; j < 4; ++j) {
+        const float sj = __shfl_sync(0xffffffffu, st, (lane & ~3) | j);
+        const float rj = __shfl_sync(0xffffffffu, rs, (lane & ~3) | j);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            q[e][4 * h + j] = PC ? quot(f[j][e], sj * g[e], rj * rg[e]) : quot(f[j][e], sj, rj);
-        }
-      } else {
-        float y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[j] = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (f[j][e] != f[j][e]) f[j][e] = 0.0f;
-            y[j] = fmaxf(y[j], fabsf(__fdiv_rn(f[j][e], g[PC ? e : 0])));
-          }
-          y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 1));
-          y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 2));
-        }
-        sb = block_scale<FP4>((sub & 2) ? ((sub & 1) ? y[3] : y[2]) : ((sub & 1) ? y[1] : y[0]));
-        s = e4m3_to_f32(sb);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float sj = __shfl_sync(0xffffffffu, s, (lane & ~3) | j);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q[e][4 * h + j] = quot_any<FP4>(f[j][e], __fmul_rn(sj, g[PC ? e : 0]));
-        }
+        for (int e = 0; e < 4; ++e)
+          q[e][4 * h + j] = PC ? quot(f[j][e], sj * g[e], rj * rg[e]) : quot(f[j][e], sj, rj);
       }
-      if (mine_ok) half[kV4Codes + blk * kV4Half + pos] = (uint8_t)sb;
+      if (mine_in) scales[8 * k + 4 * h] = (uint8_t)sb;
     }
 #pragma unroll
     for (int d = 0; d < 4; ++d) out[d][k] = pack8<FP4>(q[d]);
   }
-  uint8_t* rows = half + 4 * lane * (kV4Half / 2);
-  if (lo == 0 && hi == kV4Half) {
+  uint8_t* dst = half + 4 * lane * (kV4Half / 2) + first / 2;
+  if (!__all_sync(0xffffffffu, all_common)) {   // the unit again, codes and scales
+    write_any<FP4>(rows, p.kv_stride, p.v_scale, p.scale_kind, kvh, half, true, first + (FULL ? 0 : lo),
+                   first + (FULL ? U : hi), lane);
+  } else if constexpr (!FULL) {
+    // the nibbles of positions out of the range stay
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      reinterpret_cast<uint4*>(rows)[d] = make_uint4(out[d][0], out[d][1], out[d][2], out[d][3]);
-  } else {
-    // part of a half page: the nibbles of other positions stay
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < U / 8; ++k) {
       const int a = max(0, min(8, lo - 8 * k)), b = max(0, min(8, hi - 8 * k));
       const uint32_t mask = (uint32_t)(((1ull << (4 * b)) - 1) & ~((1ull << (4 * a)) - 1));
       if (mask != 0) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(rows + d * (kV4Half / 2)) + k;
+          uint32_t* w = reinterpret_cast<uint32_t*>(dst + d * (kV4Half / 2)) + k;
           *w = mask == 0xFFFFFFFFu ? out[d][k] : (*w & ~mask) | (out[d][k] & mask);
         }
       }
     }
+  } else if constexpr (U == 32) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      reinterpret_cast<uint4*>(dst)[d] = make_uint4(out[d][0], out[d][1], out[d][2], out[d][3]);
+  } else {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int k = 0; k < U / 8; ++k) reinterpret_cast<uint32_t*>(dst + d * (kV4Half / 2))[k] = out[d][k];
   }
 }
 
-template <int FP4, bool PC>
-__global__ void __launch_bounds__(kWarps * 32) cache_append4_kernel(const Append4Params p) {
+template <int FP4, bool PC, int U>
+__global__ void __launch_bounds__(kWarps * 32, kCtas) cache_append4_kernel(const Append4Params p) {
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (id >= p.total) return;
@@ -400,19 +386,48 @@ __global__ void __launch_bounds__(kWarps * 32) cache_append4_kernel(const Append
   const int q = p.seq_lens[b];
   if (q <= 0) return;
   const int start = p.seq_lens_kv[b], end = start + q;
-  const int h0 = (start / kV4Half + u) * kV4Half;       // first position of the half page
-  const int lo = max(h0, start) - h0, hi = min(h0 + kV4Half, end) - h0;
+  const int u0 = (start / U + u) * U;                   // first position of the unit
+  const int lo = max(u0, start), hi = min(u0 + U, end);
   if (lo >= hi) return;
-  const int lp = h0 / kPage;
+  const int lp = u0 / kPage;
   const int page = lp < p.max_blocks ? p.block_table[(int64_t)b * p.max_blocks + lp] : -1;
   if (page < 0 || page >= p.num_pages) {
     if (lane == 0) record_status(p.status, PA_ERR_BAD_PAGE, b);
     return;
   }
-  const int64_t row0 = (int64_t)(p.cu_seqlens_q[b] + (h0 + lo - start)) * p.kv_stride;
-  const int64_t off = ((int64_t)page * p.kv_heads + kvh) * kV4Slab + (h0 % kPage) / kV4Half * kV4HalfBytes;
-  if (side == 0) write_k<FP4, PC>(p, p.cache_k + off, kvh, row0, lo, hi, lane);
-  else write_v<FP4, PC>(p, p.cache_v + off, kvh, row0, lo, hi, lane);
+  const __nv_bfloat16* rows = (side ? p.v_new : p.k_new) +
+                              (int64_t)(p.cu_seqlens_q[b] + (lo - start)) * p.kv_stride + (int64_t)kvh * kV4Dim;
+  uint8_t* half = (side ? p.cache_v : p.cache_k) + ((int64_t)page * p.kv_heads + kvh) * kV4Slab +
+                  (u0 % kPage) / kV4Half * kV4HalfBytes;
+  const int first = u0 % kV4Half;
+  const int a = lo - u0, e = hi - u0;
+  if (!p.vec)
+    write_any<FP4>(rows, p.kv_stride, side ? p.v_scale : p.k_scale, p.scale_kind, kvh, half, side != 0, first + a,
+                   first + e, lane);
+  else if (side == 0)
+    e - a == U ? write_k<FP4, PC, U, true>(p, rows, half, kvh, first, a, e, lane)
+               : write_k<FP4, PC, U, false>(p, rows, half, kvh, first, a, e, lane);
+  else
+    e - a == U ? write_v<FP4, PC, U, true>(p, rows, half, kvh, first, a, e, lane)
+               : write_v<FP4, PC, U, false>(p, rows, half, kvh, first, a, e, lane);
+}
+
+template <int U>
+cudaError_t launch_u(Append4Params& p, const pa_problem& pr, int max_q, cudaStream_t stream) {
+  p.units = (max_q + U - 2) / U + 1;   // at most this many units are touched by a range of max_q positions
+  const double total = 2.0 * pr.bsz * p.units * pr.kv_heads;
+  if (total > (double)INT32_MAX) return cudaErrorInvalidValue;
+  p.total = (uint32_t)total;
+  const dim3 grid((p.total + kWarps - 1) / kWarps), block(kWarps * 32);
+  const bool pc = pr.scale_kind == PA_SCALE_PER_CHANNEL;
+  if (pr.kv_dtype == PA_KV_FP4_E2M1) {
+    if (pc) cache_append4_kernel<1, true, U><<<grid, block, 0, stream>>>(p);
+    else cache_append4_kernel<1, false, U><<<grid, block, 0, stream>>>(p);
+  } else {
+    if (pc) cache_append4_kernel<0, true, U><<<grid, block, 0, stream>>>(p);
+    else cache_append4_kernel<0, false, U><<<grid, block, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -439,24 +454,13 @@ cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void*
   p.num_pages = pr.num_pages;
   p.kv_heads = pr.kv_heads;
   p.scale_kind = pr.scale_kind;
-  // a range of max_q positions touches at most this many half pages
-  p.units = (plan.max_q + kV4Half - 2) / kV4Half + 1;
   p.vec = kv_stride % 8 == 0 && reinterpret_cast<uintptr_t>(k_new) % 16 == 0 &&
           reinterpret_cast<uintptr_t>(v_new) % 16 == 0;
-  const double total = 2.0 * pr.bsz * p.units * pr.kv_heads;
-  if (total > (double)INT32_MAX) return cudaErrorInvalidValue;
-  p.total = (uint32_t)total;
-  const uint32_t blocks = (p.total + kWarps - 1) / kWarps;
-  const bool pc = pr.scale_kind == PA_SCALE_PER_CHANNEL;
-  const dim3 grid(blocks), block(kWarps * 32);
-  if (pr.kv_dtype == PA_KV_FP4_E2M1) {
-    if (pc) cache_append4_kernel<1, true><<<grid, block, 0, stream>>>(p);
-    else cache_append4_kernel<1, false><<<grid, block, 0, stream>>>(p);
-  } else {
-    if (pc) cache_append4_kernel<0, true><<<grid, block, 0, stream>>>(p);
-    else cache_append4_kernel<0, false><<<grid, block, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  // Units of 32 positions; of 8 while those would leave most of the GPU's warps
+  // without one (the time of a small call is one warp's walk through its unit)
+  return 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms
+             ? launch_u<8>(p, pr, plan.max_q, stream)
+             : launch_u<32>(p, pr, plan.max_q, stream);
 }
 
 }  // namespace pa

@@ -4,11 +4,11 @@
 //   value = bf16(stored * scale): 8-bit formats code * scale, 4-bit formats
 //   code * (block scale * tensor scale), products in fp32.
 //
-// One warp per (sequence, half page of 32 positions, kv head, K or V).  K: lane =
+// One warp per (sequence, unit of 32 or 8 positions, kv head, K or V).  K: lane =
 // 8 dims of a row, two rows per load and per store instruction.  V (transposed
-// in the cache): lane = 4 dims, whose 32 positions it loads as 16-byte runs, so
+// in the cache): lane = 4 dims, whose positions it loads as runs of bytes, so
 // that a position's row of 256 bytes leaves as one 8-byte store per lane and no
-// transposition is needed.  MLA rows: lane = 8 of 576 dims, three rounds a row.
+// transposition is needed.  Rows that are not aligned go position by position.  MLA rows: lane = 8 of 576 dims, three rounds a row.
 // What bounds it: the bytes, above all the 2 written per element.
 #include "pa_common.cuh"
 #include "pa_kv4.cuh"
@@ -38,10 +38,10 @@ struct ReadParams {
   int32_t kv_heads;
   int32_t head_dim;
   int32_t scale_kind;
-  int32_t units;       // half pages a range can touch
+  int32_t units;       // units a range can touch
   int32_t sides;       // 2 (K, V) or 1 (MLA)
   int32_t vec;         // rows may be written with 16-byte stores
-  uint32_t total;      // (sequence, half page, kv head, side) warps
+  uint32_t total;      // (sequence, unit, kv head, side) warps
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -49,49 +49,73 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// N / 2 words of bf16 pairs to dst: one store, or elements where it is not aligned
-template <int N>
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t (&w)[N / 2], bool vec) {
-  if (vec) {
-    if constexpr (N == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-      reinterpret_cast<uint16_t*>(dst)[2 * k] = (uint16_t)w[k];
-      reinterpret_cast<uint16_t*>(dst)[2 * k + 1] = (uint16_t)(w[k] >> 16);
-    }
-  }
-}
-
-// Two neighbouring codes (4-bit: one byte; 8-bit: two bytes) as fp32, exact.
+// One stored code as fp32.
 template <int KV>
-__device__ __forceinline__ float2 pair_value(uint32_t b) {
-  if constexpr (KV == PA_KV_FP4_E2M1) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
-        : "=r"(h)
-        : "r"(b));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-  } else if constexpr (KV == PA_KV_INT4) {
-    return make_float2((float)((int)(b << 28) >> 28), (float)((int)(b << 24) >> 28));
-  } else if constexpr (KV == PA_KV_FP8_E4M3) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-  } else {
-    return make_float2((float)(int8_t)b, (float)(int8_t)(b >> 8));
-  }
+__device__ __forceinline__ float one_value(uint32_t b) {
+  if constexpr (KV == PA_KV_INT8) return (float)(int8_t)b;
+  else if constexpr (KV == PA_KV_FP8_E4M3) return e4m3_to_f32(b);
+  else return code4_to_f32<KV == PA_KV_FP4_E2M1>(b & 15u);
 }
 
 template <int KV>
 constexpr bool four() { return KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1; }
 
-template <int KV, bool PC>
-__device__ __forceinline__ void read_k(const ReadParams& p, const uint8_t* slab, int h0, int kvh, int64_t row0, int lo,
-                                       int hi, int lane) {
+// Eight stored codes (4-bit: w[0]; 8-bit: both words) as fp32, in order.
+template <int KV>
+__device__ __forceinline__ void values8(const uint32_t (&w)[2], float (&f)[8]) {
+  uint32_t h[4];
+  if constexpr (four<KV>()) {
+    codes8<KV == PA_KV_FP4_E2M1>(w[0], h);
+    if constexpr (KV == PA_KV_INT4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = scaled<0>(h[i], 0x3C003C00u, i);   // times 1
+    }
+  } else {
+    cvt4<KV == PA_KV_FP8_E4M3>(w[0], h[0], h[1]);
+    cvt4<KV == PA_KV_FP8_E4M3>(w[1], h[2], h[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    f[pair_first<KV>(i)] = v.x;
+    f[pair_first<KV>(i) + pair_gap<KV>()] = v.y;
+  }
+}
+
+// ---- any positions [lo, hi) of the page's half, any alignment: lane = 4 dims
+template <int KV>
+__device__ __noinline__ void read_any(__nv_bfloat16* dst, int64_t stride, const void* scale, int kind, int kvh,
+                                      const uint8_t* slab, int h0, bool value_side, int lo, int hi, int lane) {
+  constexpr bool kFour = four<KV>();
+  float g[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    g[e] = load_scale(scale, kind, kind == PA_SCALE_PER_CHANNEL ? kvh * kV4Dim + 4 * lane + e : kvh);
+  dst += 4 * lane;
+#pragma unroll 1
+  for (int r = h0 + lo; r < h0 + hi; ++r, dst += stride) {
+    float bs = 1.0f;
+    if constexpr (kFour)
+      bs = e4m3_to_f32(slab[value_side ? v4_scale_off(r, lane >> 2) : k4_scale_off(r, lane >> 2)]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = 4 * lane + e;
+      uint32_t b;
+      if constexpr (kFour)
+        b = value_side ? slab[v4_code_off(r, d)] >> (4 * (r & 1)) : slab[k4_code_off(r, d)] >> (4 * (d & 1));
+      else
+        b = slab[value_side ? d * kPage + r : r * kV4Dim + d];
+      dst[e] = __float2bfloat16_rn(one_value<KV>(b) * (bs * g[e]));
+    }
+  }
+}
+
+// ---- K, positions [lo, hi) of the unit of U that starts at `first` of the half
+// page (FULL: all of them; the others' bytes are read, not written); rows: the row
+// of position lo
+template <int KV, bool PC, int U, bool FULL>
+__device__ __forceinline__ void read_k(const ReadParams& p, __nv_bfloat16* rows, const uint8_t* slab, int h0, int kvh,
+                                       int first, int lo, int hi, int lane) {
   constexpr bool kFour = four<KV>();
   const int c = lane & 15, r0 = lane >> 4;   // dims 8c .. 8c+7 of rows r0, r0 + 2, ...
   float g[8];
@@ -99,86 +123,102 @@ __device__ __forceinline__ void read_k(const ReadParams& p, const uint8_t* slab,
   for (int e = 0; e < (PC ? 8 : 1); ++e)
     g[e] = load_scale(p.k_scale, p.scale_kind, PC ? kvh * kV4Dim + 8 * c + e : kvh);
   const uint8_t* half = slab + (kFour ? h0 / kHalf * kV4HalfBytes : h0 * kV4Dim);
-  __nv_bfloat16* dst0 = p.k_out + row0 + (int64_t)kvh * kV4Dim + 8 * c;
-#pragma unroll 4
-  for (int base = lo & ~1; base < hi; base += 2) {
-    const int r = base + r0;
-    if (r < lo || r >= hi) continue;
-    uint32_t w[2] = {0, 0};   // four codes of 8 bits or eight of 4 bits a word
-    float bs = 1.0f;
-    if constexpr (kFour) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(half + r * (kV4Dim / 2)) + c);
-      bs = e4m3_to_f32(__ldg(half + kV4Codes + r * kV4Nblk + (c >> 1)));
-    } else {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(half + r * kV4Dim) + c);
-      w[0] = x.x;
-      w[1] = x.y;
-    }
-    uint32_t o[4];
-    const float step = bs * g[0];
+  const uint8_t* codes = half + (first + r0) * (kFour ? kV4Dim / 2 : kV4Dim) + (kFour ? 4 : 8) * c;
+  const uint8_t* scales = half + kV4Codes + (first + r0) * kV4Nblk + (c >> 1);
+  __nv_bfloat16* dst = rows + (FULL ? r0 : r0 - lo) * p.kv_stride + 8 * c;
+  constexpr int kB = 4;   // rows in flight per lane
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 v = pair_value<KV>(kFour ? (w[0] >> (8 * k)) & 0xFFu : (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-      o[k] = bf16_pair(v.x * (PC ? bs * g[2 * k] : step), v.y * (PC ? bs * g[2 * k + 1] : step));
+  for (int base = 0; base < U; base += 2 * kB) {
+    uint32_t w[kB][2], sb[kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int r = base + 2 * i;
+      if constexpr (kFour) {
+        w[i][0] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * (kV4Dim / 2)));
+        sb[i] = __ldg(scales + r * kV4Nblk);
+      } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes + r * kV4Dim));
+        w[i][0] = x.x;
+        w[i][1] = x.y;
+      }
     }
-    store_row<8>(dst0 + (int64_t)(r - lo) * p.kv_stride, o, p.vec);
+#pragma unroll
+    for (int i = 0; i < kB; ++i, dst += 2 * p.kv_stride) {
+      const float bs = kFour ? e4m3_to_f32(sb[i]) : 1.0f, step = bs * g[0];
+      float f[8];
+      values8<KV>(w[i], f);
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = bf16_pair(f[2 * k] * (PC ? bs * g[2 * k] : step), f[2 * k + 1] * (PC ? bs * g[2 * k + 1] : step));
+      const int r = base + 2 * i + r0;
+      if (FULL || (r >= lo && r < hi)) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
-template <int KV, bool PC>
-__device__ __forceinline__ void read_v(const ReadParams& p, const uint8_t* slab, int h0, int kvh, int64_t row0, int lo,
-                                       int hi, int lane) {
+// ---- V, the same
+template <int KV, bool PC, int U, bool FULL>
+__device__ __forceinline__ void read_v(const ReadParams& p, __nv_bfloat16* rows, const uint8_t* slab, int h0, int kvh,
+                                       int first, int lo, int hi, int lane) {
   constexpr bool kFour = four<KV>();
-  constexpr int kRun = kFour ? 32 : 16;   // positions per 16-byte run of a dim
   float g[4];
 #pragma unroll
   for (int e = 0; e < (PC ? 4 : 1); ++e)
     g[e] = load_scale(p.v_scale, p.scale_kind, PC ? kvh * kV4Dim + 4 * lane + e : kvh);
-  __nv_bfloat16* dst0 = p.v_out + row0 + (int64_t)kvh * kV4Dim + 4 * lane;
+  const uint8_t* half = slab + h0 / kHalf * kV4HalfBytes;   // 4-bit
+  // 16 positions a step where the unit has them (8-bit: a 16-byte run), else 8
+  constexpr int kN = U >= 16 ? 16 : 8;
+  __nv_bfloat16* dst = rows - (FULL ? 0 : lo * p.kv_stride) + 4 * lane;
 #pragma unroll
-  for (int run = 0; run < kHalf / kRun; ++run) {
-    const int q0 = run * kRun;   // first position of the run within the half page
-    if (q0 >= hi || q0 + kRun <= lo) continue;
-    uint4 x[4], s[2];
+  for (int q0 = 0; q0 < U; q0 += kN) {
+    constexpr int kW = kFour ? kN / 8 : kN / 4;   // words of a dim
+    uint32_t w[4][kW], sc[kN / 4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      x[d] = __ldg(reinterpret_cast<const uint4*>(
-          kFour ? slab + h0 / kHalf * kV4HalfBytes + (4 * lane + d) * (kV4Half / 2)
-                : slab + (4 * lane + d) * kPage + h0 + q0));
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          kFour ? half + (4 * lane + d) * (kV4Half / 2) + (first + q0) / 2
+                : slab + (4 * lane + d) * kPage + h0 + first + q0);
+      if constexpr (kW == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+        w[d][0] = x.x, w[d][1] = x.y, w[d][2] = x.z, w[d][3] = x.w;
+      } else if constexpr (kW == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        w[d][0] = x.x, w[d][1] = x.y;
+      } else {
+        w[d][0] = __ldg(src);
+      }
+    }
     if constexpr (kFour) {
-      const uint8_t* sp = slab + h0 / kHalf * kV4HalfBytes + kV4Codes + (lane >> 2) * kV4Half;
-      s[0] = __ldg(reinterpret_cast<const uint4*>(sp));
-      s[1] = __ldg(reinterpret_cast<const uint4*>(sp) + 1);
+      const uint8_t* sp = half + kV4Codes + (lane >> 2) * kV4Half + first + q0;
+#pragma unroll
+      for (int k = 0; k < kN / 8; ++k) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(sp) + k);
+        sc[2 * k] = x.x;
+        sc[2 * k + 1] = x.y;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kRun / 2; ++j) {   // positions q0 + 2j, + 1
-      const int pos = q0 + 2 * j;
-      if (pos + 1 < lo || pos >= hi) continue;
-      float bs[2] = {1.0f, 1.0f};
-      if constexpr (kFour) {
-        const uint4& sv = s[j >> 3];
-        const int wi = (j >> 1) & 3;
-        const uint32_t sw = (wi == 0 ? sv.x : wi == 1 ? sv.y : wi == 2 ? sv.z : sv.w) >> (16 * (j & 1));
-        const float2 b2 = pair_value<PA_KV_FP8_E4M3>(sw & 0xFFFFu);
-        bs[0] = b2.x;
-        bs[1] = b2.y;
-      }
-      float2 v[4];
+    for (int k = 0; k < kN / 8; ++k) {   // eight positions
+      float f[4][8], bs[8];
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        const int byte = kFour ? j : 2 * j;   // of the 16
-        const uint32_t w = (byte >> 2) == 0 ? x[d].x : (byte >> 2) == 1 ? x[d].y : (byte >> 2) == 2 ? x[d].z : x[d].w;
-        v[d] = pair_value<KV>((w >> (8 * (byte & 3))) & (kFour ? 0xFFu : 0xFFFFu));
+        const uint32_t x[2] = {w[d][kFour ? k : 2 * k], w[d][kFour ? k : 2 * k + 1]};
+        values8<KV>(x, f[d]);
+      }
+      if constexpr (kFour) {
+        const uint32_t x[2] = {sc[2 * k], sc[2 * k + 1]};
+        values8<PA_KV_FP8_E4M3>(x, bs);
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (pos + e < lo || pos + e >= hi) continue;
-        const float step = bs[e] * g[0];
-        float f[4];
+      for (int j = 0; j < 8; ++j, dst += p.kv_stride) {
+        const float b = kFour ? bs[j] : 1.0f, step = b * g[0];
+        float o[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) f[d] = (e ? v[d].y : v[d].x) * (PC ? bs[e] * g[d] : step);
-        const uint32_t o[2] = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
-        store_row<4>(dst0 + (int64_t)(pos + e - lo) * p.kv_stride, o, p.vec);
+        for (int d = 0; d < 4; ++d) o[d] = f[d][j] * (PC ? b * g[d] : step);
+        const int r = q0 + 8 * k + j;
+        if (FULL || (r >= lo && r < hi))
+          *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]));
       }
     }
   }
@@ -186,26 +226,29 @@ __device__ __forceinline__ void read_v(const ReadParams& p, const uint8_t* slab,
 
 // MLA: latent rows of head_dim bytes (a multiple of 8), one scale
 template <int KV>
-__device__ __forceinline__ void read_latent(const ReadParams& p, const uint8_t* page, int h0, int64_t row0, int lo,
-                                            int hi, int lane) {
+__device__ __forceinline__ void read_latent(const ReadParams& p, __nv_bfloat16* rows, const uint8_t* codes, int n,
+                                            int lane) {
   const float g = load_scale(p.k_scale, PA_SCALE_GLOBAL, 0);
 #pragma unroll 4
-  for (int r = lo; r < hi; ++r) {
+  for (int r = 0; r < n; ++r) {
     for (int c = lane; c < p.head_dim / 8; c += 32) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(page + (int64_t)(h0 + r) * p.head_dim) + c);
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes + r * p.head_dim) + c);
       const uint32_t w[2] = {x.x, x.y};
-      uint32_t o[4];
+      float f[8];
+      values8<KV>(w, f);
+      __nv_bfloat16* dst = rows + r * p.kv_stride + 8 * c;
+      if (p.vec) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(bf16_pair(f[0] * g, f[1] * g), bf16_pair(f[2] * g, f[3] * g),
+                                                    bf16_pair(f[4] * g, f[5] * g), bf16_pair(f[6] * g, f[7] * g));
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = pair_value<KV>((w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-        o[k] = bf16_pair(v.x * g, v.y * g);
+        for (int e = 0; e < 8; ++e) dst[e] = __float2bfloat16_rn(f[e] * g);
       }
-      store_row<8>(p.k_out + row0 + (int64_t)(r - lo) * p.kv_stride + 8 * c, o, p.vec);
     }
   }
 }
 
-template <int KV, bool PC>
+template <int KV, bool PC, int U>
 __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const ReadParams p) {
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -218,34 +261,59 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const ReadParam
   const int q = p.seq_lens[b];
   if (q <= 0) return;
   const int start = p.seq_lens_kv[b], end = start + q;
-  const int first = (start / kHalf + u) * kHalf;        // first position of the half page
-  const int lo = max(first, start) - first, hi = min(first + kHalf, end) - first;
+  const int u0 = (start / U + u) * U;                   // first position of the unit
+  const int lo = max(u0, start), hi = min(u0 + U, end);
   if (lo >= hi) return;
-  const int lp = first / kPage, h0 = first % kPage;
+  const int lp = u0 / kPage;
   const int page = lp < p.max_blocks ? p.block_table[(int64_t)b * p.max_blocks + lp] : -1;
-  const int64_t row0 = (int64_t)(p.cu_seqlens_q[b] + (first + lo - start)) * p.kv_stride;
+  __nv_bfloat16* rows = (side ? p.v_out : p.k_out) + (int64_t)(p.cu_seqlens_q[b] + (lo - start)) * p.kv_stride +
+                        (int64_t)kvh * p.head_dim;
   if (page < 0 || page >= p.num_pages) {
     if (lane == 0) record_status(p.status, PA_ERR_BAD_PAGE, b);
-    __nv_bfloat16* dst = (side ? p.v_out : p.k_out) + row0 + (int64_t)kvh * p.head_dim;
     for (int r = 0; r < hi - lo; ++r)
-      for (int d = lane; d < p.head_dim; d += 32) dst[(int64_t)r * p.kv_stride + d] = __float2bfloat16_rn(0.0f);
+      for (int d = lane; d < p.head_dim; d += 32) rows[r * p.kv_stride + d] = __float2bfloat16_rn(0.0f);
     return;
   }
   if constexpr (!four<KV>()) {
     if (p.sides == 1) {
-      read_latent<KV>(p, p.cache_k + (int64_t)page * kPage * p.head_dim, h0, row0, lo, hi, lane);
+      read_latent<KV>(p, rows, p.cache_k + ((int64_t)page * kPage + lo % kPage) * p.head_dim, hi - lo, lane);
       return;
     }
   }
-  const int64_t off = ((int64_t)page * p.kv_heads + kvh) * (four<KV>() ? kV4Slab : kPage * kV4Dim);
-  if (side == 0) read_k<KV, PC>(p, p.cache_k + off, h0, kvh, row0, lo, hi, lane);
-  else read_v<KV, PC>(p, p.cache_v + off, h0, kvh, row0, lo, hi, lane);
+  const uint8_t* slab = (side ? p.cache_v : p.cache_k) +
+                        ((int64_t)page * p.kv_heads + kvh) * (four<KV>() ? kV4Slab : kPage * kV4Dim);
+  const int h0 = u0 % kPage / kHalf * kHalf, first = u0 % kHalf;
+  const int a = lo - u0, e = hi - u0;
+  if (!p.vec)
+    read_any<KV>(rows, p.kv_stride, side ? p.v_scale : p.k_scale, p.scale_kind, kvh, slab, h0, side != 0, first + a,
+                 first + e, lane);
+  else if (side == 0)
+    e - a == U ? read_k<KV, PC, U, true>(p, rows, slab, h0, kvh, first, a, e, lane)
+               : read_k<KV, PC, U, false>(p, rows, slab, h0, kvh, first, a, e, lane);
+  else
+    e - a == U ? read_v<KV, PC, U, true>(p, rows, slab, h0, kvh, first, a, e, lane)
+               : read_v<KV, PC, U, false>(p, rows, slab, h0, kvh, first, a, e, lane);
 }
 
+template <int KV, int U>
+cudaError_t launch_u(ReadParams& p, const pa_problem& pr, int max_q, cudaStream_t stream) {
+  p.units = (max_q + U - 2) / U + 1;   // at most this many units are touched by a range of max_q positions
+  const double total = (double)p.sides * pr.bsz * p.units * pr.kv_heads;
+  if (total > (double)INT32_MAX) return cudaErrorInvalidValue;
+  p.total = (uint32_t)total;
+  const uint32_t blocks = (p.total + kWarps - 1) / kWarps;
+  if (p.scale_kind == PA_SCALE_PER_CHANNEL) cache_read_kernel<KV, true, U><<<blocks, kWarps * 32, 0, stream>>>(p);
+  else cache_read_kernel<KV, false, U><<<blocks, kWarps * 32, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// Units of 32 positions; of 8 while those would leave most of the GPU's warps
+// without one (the time of a small call is one warp's walk through its unit).
 template <int KV>
-static void launch_kv(const ReadParams& p, uint32_t blocks, cudaStream_t stream) {
-  if (p.scale_kind == PA_SCALE_PER_CHANNEL) cache_read_kernel<KV, true><<<blocks, kWarps * 32, 0, stream>>>(p);
-  else cache_read_kernel<KV, false><<<blocks, kWarps * 32, 0, stream>>>(p);
+cudaError_t launch_kv(ReadParams& p, const Plan& plan, cudaStream_t stream) {
+  return (double)p.sides * plan.total_q * plan.prob.kv_heads / 32 < 4.0 * kWarps * plan.num_sms
+             ? launch_u<KV, 8>(p, plan.prob, plan.max_q, stream)
+             : launch_u<KV, 32>(p, plan.prob, plan.max_q, stream);
 }
 
 }  // namespace
@@ -274,21 +342,14 @@ cudaError_t launch_cache_read(const Plan& plan, const pa_args& a, void* k_out, v
   p.head_dim = pr.head_dim_qk;
   p.scale_kind = pr.scale_kind;
   p.sides = mla ? 1 : 2;
-  // a range of max_q positions touches at most this many half pages
-  p.units = (plan.max_q + kHalf - 2) / kHalf + 1;
   p.vec = kv_stride % 8 == 0 && reinterpret_cast<uintptr_t>(k_out) % 16 == 0 &&
           reinterpret_cast<uintptr_t>(p.v_out) % 16 == 0;
-  const double total = (double)p.sides * pr.bsz * p.units * pr.kv_heads;
-  if (total > (double)INT32_MAX) return cudaErrorInvalidValue;
-  p.total = (uint32_t)total;
-  const uint32_t blocks = (p.total + kWarps - 1) / kWarps;
   switch (pr.kv_dtype) {
-    case PA_KV_INT8: launch_kv<PA_KV_INT8>(p, blocks, stream); break;
-    case PA_KV_FP8_E4M3: launch_kv<PA_KV_FP8_E4M3>(p, blocks, stream); break;
-    case PA_KV_INT4: launch_kv<PA_KV_INT4>(p, blocks, stream); break;
-    default: launch_kv<PA_KV_FP4_E2M1>(p, blocks, stream); break;
+    case PA_KV_INT8: return launch_kv<PA_KV_INT8>(p, plan, stream);
+    case PA_KV_FP8_E4M3: return launch_kv<PA_KV_FP8_E4M3>(p, plan, stream);
+    case PA_KV_INT4: return launch_kv<PA_KV_INT4>(p, plan, stream);
+    default: return launch_kv<PA_KV_FP4_E2M1>(p, plan, stream);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace pa
