@@ -90,10 +90,9 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *           PER_CHANNEL  bf16 [kv_heads * head_dim]   (index kvh * D + d)
  *           GLOBAL       fp32 [1]                     (one value for K and V)
  *   chunk_size > 0 splits the KV range into chunks of that many positions (a
- *   multiple of block_size); 0 never splits; -1 lets the planner choose.  Over a
- *   4-bit cache with at most 16 packed rows per kv head (max(q_len) * G <= 16) a
- *   positive chunk_size is the most that one piece covers: the planner cuts
- *   shares of equal work.
+ *   multiple of block_size); 0 never splits; -1 lets the planner choose.  Plans
+ *   of the decode family over a 4-bit cache take any other value than 0 as -1:
+ *   the planner cuts pieces of equal work.
  *   q_stride is the distance in elements between consecutive tokens of q
  *   (>= q_heads * head_dim_qk; FastDeploy's packed qkv uses
  *   (q_heads + 2 * kv_heads) * head_dim).

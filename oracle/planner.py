@@ -38,10 +38,11 @@ Spec:
   nch_token[t] = nch of token t's tile; max_chunks = max(1, max nch_token);
   merge_tokens = tokens with nch_token != 1, ascending (those with 0 chunks are
   the rows that see nothing; the merge writes them).
-  A 4-bit cache, decode family, max(q_len) * G <= 16 and chunk_size != 0:
-  shares of equal work per warp (16 warps per CTA).  The tiles' pages are
-  numbered as for MLA below; quota = max(2, ceil(total / max(1, slots * 16 //
-  kv_heads))), at most chunk_size / B if that is positive; share k covers pages
+  A 4-bit cache, decode family and chunk_size != 0: shares of equal work per
+  worker, w workers per CTA: 16 warps if max(q_len) * G <= 16, else the smallest
+  w in 1 .. 4 with slots * w divisible by kv_heads (4 if none).  The tiles' pages
+  are numbered as for MLA below; quota = max(2 (warps) or 8, ceil(total / max(1,
+  slots * w // kv_heads))); share k covers pages
   [k*quota, (k+1)*quota); its pieces are its overlaps with the tiles, numbered
   per tile.  Lanes (share, kv head), share-major, are dealt to num_ctas =
   min(slots, #lanes) CTAs: CTA c takes lanes [c*L // num_ctas, (c+1)*L //
@@ -98,9 +99,8 @@ def plan(p, num_sms: int) -> dict:
             lim = slkv[b] if cross else slkv[b] + tok1 if p.causal else slkv[b] + ql
             tiles.append((b, tok0, tok1, lim))
 
-    if (p.kv_dtype in ("int4", "fp4_e2m1") and family == "decode" and max_q * G <= 16
-            and int(p.chunk_size) != 0):
-        return _warp_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross)
+    if p.kv_dtype in ("int4", "fp4_e2m1") and family == "decode" and int(p.chunk_size) != 0:
+        return _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, max_q * G <= 16)
     if family == "mla" and int(p.chunk_size) == -1:
         return _mla_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B)
 
@@ -149,14 +149,13 @@ def plan(p, num_sms: int) -> dict:
                 max_chunks=max_chunks, merge_tokens=merge_tokens)
 
 
-def _warp_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross):
-    """Equal shares of the pages per warp (the 4-bit decode rule in the spec above)."""
+def _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, warps):
+    """Equal shares of the pages per worker (the 4-bit decode rule in the spec above)."""
+    w = 16 if warps else next((k for k in (1, 2, 3) if slots * k % p.kv_heads == 0), 4)
     npages = [math.ceil(t[3] / B) for t in tiles]
     start = [sum(npages[:i]) for i in range(len(tiles))]
     total = sum(npages)
-    quota = max(2, math.ceil(total / max(1, slots * 16 // p.kv_heads)))
-    if int(p.chunk_size) > 0:
-        quota = min(quota, int(p.chunk_size) // B)
+    quota = max(2 if warps else 8, math.ceil(total / max(1, slots * w // p.kv_heads)))
     shares = math.ceil(total / quota)
     pieces, count = [], [0] * len(tiles)
     for k in range(shares):

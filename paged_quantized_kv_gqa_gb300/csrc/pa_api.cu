@@ -151,21 +151,27 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       tiles.push_back({b, tok0, tok1, lim});
     }
   }
-  const bool warp4 = P.four_bit() && P.family == PA_FAMILY_DECODE && max_q * G <= kWarpDecodeRows;
-  if (warp4 && prob.chunk_size != 0) {
-    // 4-bit decode, one warp per item: the pages of all tiles, tile after tile,
-    // are cut into shares of `quota` pages, about one share per kv head and warp
-    // of the grid, so that every warp has the same work and few partial states
-    // are merged (a chunk size bounds a share).  A share's pieces (its overlaps
-    // with the tiles) are run for every kv head; the (share, kv head) lanes are
-    // dealt to the CTAs in runs of equal length, each CTA's items longest first.
+  if (P.four_bit() && P.family == PA_FAMILY_DECODE && prob.chunk_size != 0) {
+    // 4-bit decode: the pages of all tiles, tile after tile, are cut into shares
+    // of `quota` pages, so that every worker of the grid has the same work and few
+    // partial states are merged.  A worker is a warp (at most 16 rows: a warp takes
+    // whole items) or a CTA (the tensor-memory kernel, where every new item costs
+    // about three tiles: 5064 items of 1024 positions took 450 us, 430 shares 327).
+    // A share's pieces (its overlaps with the tiles) are run for every kv head;
+    // the (share, kv head) lanes are dealt to the CTAs in runs of equal length,
+    // each CTA's items longest first.
+    const bool by_warp = max_q * G <= kWarpDecodeRows;
+    // CTA workers: lanes per CTA, so that the kv heads divide the lanes (else 4)
+    int per_cta = kDecode4Warps;
+    if (!by_warp)
+      for (per_cta = 1; per_cta < 4 && slots * per_cta % prob.kv_heads != 0;) ++per_cta;
     std::vector<int64_t> first_page(tiles.size() + 1, 0);
     for (size_t i = 0; i < tiles.size(); ++i)
       first_page[i + 1] = first_page[i] + ceil_div(tiles[i].lim, (int64_t)B);
     const int64_t total = first_page.back();
-    const int64_t groups = std::max<int64_t>(1, (int64_t)slots * kDecode4Warps / prob.kv_heads);
-    int64_t quota = std::max<int64_t>(kDecode4MinPages, ceil_div(total, groups));
-    if (prob.chunk_size > 0) quota = std::min<int64_t>(quota, prob.chunk_size / B);
+    const int64_t groups = std::max<int64_t>(1, (int64_t)slots * per_cta / prob.kv_heads);
+    const int64_t quota = std::max<int64_t>(by_warp ? kDecode4MinPages : kDecode4MinTiles * 2,
+                                            ceil_div(total, groups));
     const int64_t shares = ceil_div(total, quota), lanes = shares * prob.kv_heads;
     if (lanes > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "too many work items");
     P.num_ctas = (int)std::min<int64_t>(slots, lanes);

@@ -20,6 +20,7 @@ constexpr int kWarpDecodeRows = 16;  // decode tiles up to this many rows run wa
 constexpr int kAppendRows = 256;     // packed rows per append item (two 128-row tiles)
 constexpr int kDecode4Warps = 16;    // warps of a 4-bit decode CTA (each takes whole items)
 constexpr int kDecode4MinPages = 2;  // smallest share of a warp
+constexpr int kDecode4MinTiles = 4;  // smallest share of a tensor-memory CTA, 128-position tiles
 constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache
 constexpr int kStatusBytes = 256;    // status block at the start of the workspace
 constexpr int64_t kDefaultWaitNs = 2000000000LL;
