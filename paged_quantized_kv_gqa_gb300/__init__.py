@@ -125,15 +125,34 @@ def _ptr(x) -> Optional[int]:
     return int(x.data_ptr())
 
 
+# torch's current-stream lookup, resolved at the first call that needs it (None:
+# torch is absent or has no CUDA device).  torch.cuda.is_available() and a Stream
+# object a call cost more host time than a small launch.
+_current_raw_stream = False
+
+
+def _resolve_current_stream():
+    global _current_raw_stream
+    try:
+        import torch
+        if not torch.cuda.is_available():
+            _current_raw_stream = None
+            return
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        torch.cuda.current_stream()     # initialises torch's CUDA state
+        if raw is not None:
+            _current_raw_stream = lambda: int(raw(dev()))
+        else:
+            _current_raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)
+    except Exception:  # pragma: no cover - torch without CUDA
+        _current_raw_stream = None
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return int(torch.cuda.current_stream().cuda_stream)
-        except Exception:  # pragma: no cover - torch without CUDA
-            pass
-        return None
+        if _current_raw_stream is False:
+            _resolve_current_stream()
+        return _current_raw_stream() if _current_raw_stream else None
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
