@@ -77,9 +77,16 @@ constexpr int kSlot4 = 5120;                     // 4-bit: a slab's place in a s
 constexpr int kVs16Warp = 2 * kTileTok * 2;      // 4-bit: a CV warp's V scales as fp16 [2 blocks][128]
 static_assert(kSlot4 >= kV4Slab && kSlot4 % 512 == 0 && 2 * kSlot4 <= 2 * kSlab, "4-bit stage layout");
 constexpr float kTau = 8.0f;                     // lazy-rescale threshold (log2 units)
-constexpr int kThreads = 512;                    // four warpgroups
-constexpr int kWarpTma = 12;
-constexpr int kWarpMma = 13;
+// 8-bit: four warpgroups.  4-bit: the fourth converts V while the third converts
+// K (one group for both is the longest stage of the pipeline: a code needs more
+// steps than a byte), and a fifth warpgroup issues the copies and the MMAs.
+template <int KV>
+struct Roles {
+  static constexpr bool kFour = KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1;
+  static constexpr int kThreads = kFour ? 640 : 512;
+  static constexpr int kWarpTma = kFour ? 16 : 12;
+  static constexpr int kWarpMma = kFour ? 17 : 13;
+};
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPBufs = 4;                        // P^T ring depth
 // P^T buffer: [128 positions][64 rows] fp16, MN-major (rows contiguous),
@@ -249,10 +256,11 @@ struct TileCursor {
 
 // KV: PA_KV_*; cv: the 4-bit V cache (tm_v is unused then)
 template <int NR, int KV, bool TREE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const uint8_t* __restrict__ cv, const AttnParams p) {
-  constexpr bool kFour = KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1;
+  constexpr bool kFour = Roles<KV>::kFour;
+  constexpr int kThreads = Roles<KV>::kThreads;
   constexpr int FP4 = KV == PA_KV_FP4_E2M1, FP8 = KV == PA_KV_FP8_E4M3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int wg = warp >> 2;         // warpgroup: 0, 1 softmax; 2 CV; 3 IO
+  const int wg = warp >> 2;         // warpgroup: 0, 1 softmax; 2 CV; 3 IO (4-bit: 3 CV of V; 4 IO)
   const int item_begin = p.work_indptr[blockIdx.x];
   const int item_end = p.work_indptr[blockIdx.x + 1];
   const uint64_t limit = (uint64_t)p.wait_limit_ns;
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);
+      mbar_init(&empty[s], kFour ? 8 : 4);   // the warps that read a stage
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(&kready[j], 4);
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this warp's TMEM lane quarter (a warp may only touch lanes 32*(warp%4) ..)
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
-  if (warp == kWarpTma) {
+  if (warp == Roles<KV>::kWarpTma) {
     // ================================================================ TMA
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kStages; ++s)   // every issued load lands before exit
         if (issued_g[s] >= 0) mbar_wait(&full[s], ((uint32_t)issued_g[s] / kStages) & 1, kDrainNs);
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp == Roles<KV>::kWarpMma) {
     // ================================================================ MMA issue
     // the whole warp runs the polling loop (warp-uniform operands); one
     // elected lane issues the MMAs and commits
@@ -474,12 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kPBufs; ++j)
         if (pv_commits[j]) mbar_wait(&pvdone[j], (pv_commits[j] - 1) & 1, kDrainNs);
     }
-  } else if (wg == 3) {
+  } else if (kFour && wg == 4) {
+    // warps 18, 19: no role (they complete the fifth warpgroup)
+  } else if (!kFour && wg == 3) {
     // ================================================================ fused merge
     // warps 14 and 15 take alternate items; once all eight softmax warps have
     // finished an item's epilogue, its row group's counter is raised and the
     // CTA that completes the count merges the group and resets the counter
-    if (!kFour && p.merge_cnt != nullptr) {
+    if (p.merge_cnt != nullptr) {
       bool ok = true;
       for (int it = item_begin + (warp - 14); it < item_end && ok; it += 2) {
         const int li = it - item_begin;
@@ -936,6 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // hardware's default time rather than re-probing every 32 ns (fewer issue
     // slots taken from the softmax warps on the same sub-partitions).
     const int d = tid & 127;  // TMEM lane: K position / V head dim / output dim
+    const bool do_k = !kFour || wg == 2, do_v = !kFour || wg == 3;   // (both in the 8-bit kernels)
     uint32_t g = 0;
     bool fail = false;
     auto note_fail = [&](int it) {
@@ -1004,11 +1015,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage = g % kStages;
         // K buffer g&1 was last read by S_{g-2}; Q' buffer li&1 by the S of item
         // li-2, whose last tile is at most g-2
-        if (g >= 2 && !wait_or_abort(&sfull[g & 1], ((g - 2) >> 1) & 1, limit, abort_any)) {
+        if (do_k && g >= 2 && !wait_or_abort(&sfull[g & 1], ((g - 2) >> 1) & 1, limit, abort_any)) {
           note_fail(it);
           break;
         }
-        if (i == 0) {
+        if (do_k && i == 0) {
           if (q_ahead != it) load_q(m, q_s + (li & 1) * NR * 256);
           // the next item's query rows into L2 now; its Q' is written at this
           // item's second tile (below), so that no item boundary waits for it
@@ -1022,15 +1033,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (i == 1 && it + 1 < item_end) {
+        if (do_k && i == 1 && it + 1 < item_end) {
           // Q' buffer (li + 1) & 1 was last read by the S of item li - 1, whose
           // last tile is g - 2 or earlier
           load_q(isrc.at(it + 1), q_s + ((li + 1) & 1) * NR * 256);
           q_ahead = it + 1;
         }
         if (!wait_or_abort(&full[stage], (g / kStages) & 1, limit, abort_any)) { note_fail(it); break; }
-        if (d == 0) trace_ev(p, g, 1);
-        if constexpr (kFour) {
+        if (do_k && d == 0) trace_ev(p, g, 1);
+        if (!do_k) {
+          // this warpgroup converts V only
+        } else if constexpr (kFour) {
           // position d: code row 36 (half page) + row of its page's box, its eight
           // block scales in one of the rows behind the half's codes
           const uint32_t kbase = s_base + stage * kStageBytes + (d >> 6) * kSlot4;
@@ -1078,9 +1091,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        tc_fence_before();
-        warp_arrive(&kready[g & 1], lane);
-        if (d == 0) trace_ev(p, g, 2);
+        if (do_k) {
+          if constexpr (kFour) warp_arrive(&empty[stage], lane);
+          tc_fence_before();
+          warp_arrive(&kready[g & 1], lane);
+          if (d == 0) trace_ev(p, g, 2);
+        }
+        if (!do_v) continue;
         // V buffer g&1 was last read by PV_{g-2}
         if (g >= 2 && !wait_or_abort(&pvdone[(g - 2) & 3], ((g - 2) >> 2) & 1, limit, abort_any)) {
           note_fail(it);
