@@ -28,7 +28,7 @@
 #define D4_WARPS 16
 #endif
 #ifndef D4_STAGES
-#define D4_STAGES 3
+#define D4_STAGES 2
 #endif
 #ifndef D4_HINT
 #define D4_HINT 32
@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   const int item_end = p.work_indptr[blockIdx.x + 1];
   const uint64_t limit = (uint64_t)p.wait_limit_ns;
   const int G = p.group;
+  const uint32_t g_magic = (65536u + (uint32_t)G - 1u) / (uint32_t)G;   // r / G = (r * g_magic) >> 16 for r < 64
+  auto div_g = [&](int r) { return (int)(((uint32_t)r * g_magic) >> 16); };
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * C::kStages;
   int32_t* items_s = reinterpret_cast<int32_t*>(smem + C::kItemOff);
@@ -166,8 +168,9 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     for (int j = 0; j < NB; ++j) {
       const int row = 8 * j + g;
       const bool valid = row < ntok * G;
-      const __nv_bfloat16* src = p.q + (int64_t)(tok0 + (valid ? row / G : 0)) * p.q_stride +
-                                 (int64_t)(kvh * G + (valid ? row % G : 0)) * kV4Dim + 32 * t;
+      const int tok = valid ? div_g(row) : 0;
+      const __nv_bfloat16* src = p.q + (tok0 + tok) * p.q_stride + (kvh * G + (valid ? row - tok * G : 0)) * kV4Dim +
+                                 32 * t;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         qr[j][k] = make_uint4(0, 0, 0, 0);
@@ -274,6 +277,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     if (p.scale_kind == PA_SCALE_GLOBAL) c_log2 *= reinterpret_cast<const float*>(p.k_scale)[0];
     else if (p.scale_kind == PA_SCALE_PER_KV_HEAD)
       c_log2 *= __bfloat162float(sc_smem ? ks_s[m.kvh] : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)[m.kvh]);
+    const float c_abs = fabsf(c_log2), sgn = c_log2 < 0.f ? -1.f : 1.f;   // a sign goes into Q'
+    const float c_inv = __fdividef(1.f, c_abs);
     int tok0_local = 0, pre_len = 0;
     const uint8_t* tmask = nullptr;
     if constexpr (TREE) {
@@ -299,11 +304,22 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
       const __nv_bfloat16* sk = (sc_smem ? ks_s : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)) +
                                 (pc ? m.kvh * kV4Dim + 32 * t : 0);
+      const bool sk16 = pc && (reinterpret_cast<uintptr_t>(sk) & 15) == 0;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         float sc[8];
+        if (sk16) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + 8 * w);
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc[e] = pc ? __bfloat162float(sk[8 * w + e]) : 1.0f;
+          for (int e = 0; e < 4; ++e) {
+            sc[2 * e] = __uint_as_float(x[e] << 16) * sgn;
+            sc[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u) * sgn;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sc[e] = pc ? __bfloat162float(sk[8 * w + e]) * sgn : sgn;
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           const uint32_t u[4] = {qr[j][w].x, qr[j][w].y, qr[j][w].z, qr[j][w].w};
@@ -341,6 +357,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         fail = true;
         break;
       }
+      if (lane == 0 && warp < 4) trace_ev(p, n_comp, 12 + warp);
       const uint8_t* kst = stage_p + st_comp * kStage4;
       const uint8_t* vst = kst + kV4HalfBytes;
       const int pos0 = m.kv0 + hp * kV4Half;
@@ -396,7 +413,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         *reinterpret_cast<uint4*>(vs16 + g * kV4Half + 8 * t) = make_uint4(f[0], f[1], f[2], f[3]);
       }
 
-      // ---- scale, mask, running max, P
+      // ---- mask, running max, P (scores stay unscaled; the scale is in the exponent)
       const bool need_mask = (pos0 + kV4Half > m.kv1) || (pos0 + kV4Half - 1 > m.cbase) ||
                              (TREE && pos0 + kV4Half > pre_len);
 #pragma unroll
@@ -408,17 +425,15 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = s[b][j][2 * h + e] * c_log2;
               if (need_mask) {
                 const int r = 8 * j + 2 * t + e;
-                bool vis = jpos < m.kv1 && jpos <= m.cbase + r / G;
+                bool vis = jpos < m.kv1 && jpos <= m.cbase + div_g(r);
                 if (TREE && vis && jpos >= pre_len && r < n_rows) {
-                  const int tl = tok0_local + r / G;
+                  const int tl = tok0_local + div_g(r);
                   vis = tmask[tl * p.mask_dim + (jpos - pre_len)] != 0;
                 }
-                x = vis ? x : -INFINITY;
+                s[b][j][2 * h + e] = vis ? s[b][j][2 * h + e] : -INFINITY;
               }
-              s[b][j][2 * h + e] = x;
             }
         }
       // The running maximum moves only when some score exceeds it by 2^kTau (the
@@ -439,11 +454,11 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            const float mo = mrow[j][e], mn = fmaxf(mo, v);
+            const float mo = mrow[j][e], mn = fmaxf(mo, v * c_abs);
             // a row without a visible position so far keeps mrow = -inf, O = 0
             const float al = mo == -INFINITY ? 0.f : fast_exp2(mo - mn);
             mrow[j][e] = mn;
-            mlim[j][e] = mn == -INFINITY ? -INFINITY : mn + kTau;
+            mlim[j][e] = mn == -INFINITY ? -INFINITY : (mn + kTau) * c_inv;
             lrow[j][e] *= al;
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
@@ -459,10 +474,10 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         const float mu1 = mrow[j][1] == -INFINITY ? 0.f : mrow[j][1];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float p0 = fast_exp2(s[b][j][0] - mu0);
-          const float p1 = fast_exp2(s[b][j][1] - mu1);
-          const float p2 = fast_exp2(s[b][j][2] - mu0);
-          const float p3 = fast_exp2(s[b][j][3] - mu1);
+          const float p0 = fast_exp2(fmaf(s[b][j][0], c_abs, -mu0));
+          const float p1 = fast_exp2(fmaf(s[b][j][1], c_abs, -mu1));
+          const float p2 = fast_exp2(fmaf(s[b][j][2], c_abs, -mu0));
+          const float p3 = fast_exp2(fmaf(s[b][j][3], c_abs, -mu1));
           lrow[j][0] += p0 + p2;
           lrow[j][1] += p1 + p3;
           pb[b][j][0] = movtrans(pack_half2(p0, p1));
@@ -493,6 +508,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
 
       // the stage is free (the epilogue uses the item's last one)
       __syncwarp();
+      if (lane == 0 && warp < 12) trace_ev(p, n_comp, warp);
       ++n_comp;
       if (++st_comp == C::kStages) {
         st_comp = 0;
@@ -502,10 +518,11 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     }
     if (fail) break;
 
-    // ---- epilogue, 8 rows at a time: O / l as fp32 [8 rows][128 dims] through
-    // the item's last stage (dims of row r XOR 8 ((r >> 1) & 3): no bank
-    // conflicts), out as 16-byte pieces
-    float* stg = reinterpret_cast<float*>(smem + (warp * C::kStages + (st_comp == 0 ? C::kStages : st_comp) - 1) * kStage4);
+    // ---- epilogue.  Partial rows leave as they sit in the accumulators: a store
+    // of the warp writes eight consecutive dims of four rows, whole 32-byte
+    // sectors of fp32.  Final rows (bf16 or int8) go 8 at a time through the
+    // item's last stage as fp32 [8 rows][128 dims] (dims of row r XOR
+    // 8 ((r >> 1) & 3): no bank conflicts) and leave as 16-byte pieces.
     const bool final_row = m.nch == 1;
     const bool per_channel = p.scale_kind == PA_SCALE_PER_CHANNEL;
     const float vs_head = p.scale_kind == PA_SCALE_GLOBAL ? reinterpret_cast<const float*>(p.v_scale)[0]
@@ -515,25 +532,21 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
                               : 1.f;
     const __nv_bfloat16* vsc = (sc_smem ? vs_s : reinterpret_cast<const __nv_bfloat16*>(p.v_scale)) +
                                (per_channel ? m.kvh * kV4Dim : 0);
-    const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+    float inv[NB][2];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
+    for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float l = lrow[j][e];
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
+        inv[j][e] = l > 0.f ? __frcp_rn(l) * vs_head : 0.f;
         const int r = 8 * j + 2 * t + e;
-        const float inv = l > 0.f ? __frcp_rn(l) : 0.f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            stg[(2 * t + e) * kV4Dim + ((16 * d + g + 8 * h) ^ (8 * t))] = o[j][d][2 * h + e] * inv;
         if (g == 0 && r < n_rows) {
-          const int token = m.tok0 + r / G;
-          const int head = m.kvh * G + r % G;
+          const int dt = div_g(r);
+          const int token = m.tok0 + dt;
+          const int head = m.kvh * G + r - dt * G;
           const float ln2 = 0.69314718055994530942f;
           const float mr = mrow[j][e];
           if (final_row) {
@@ -546,29 +559,58 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           }
         }
       }
-      __syncwarp();
-#pragma unroll 1
-      for (int idx = lane; idx < min(8, n_rows - 8 * j) * 16; idx += 32) {
-        const int rr = idx >> 4, c = idx & 15;   // row 8 j + rr, dims 8c .. 8c+7
-        const float* src = stg + rr * kV4Dim + ((8 * c) ^ (8 * ((rr >> 1) & 3)));
-        const float4 a = *reinterpret_cast<const float4*>(src);
-        const float4 b = *reinterpret_cast<const float4*>(src + 4);
-        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (!final_row) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= per_channel ? __bfloat162float(vsc[8 * c + k]) : vs_head;
-        const int r = 8 * j + rr;
-        const int token = m.tok0 + r / G;
-        const int head = m.kvh * G + r % G;
-        if (final_row) {
-          ep_store8(p.ep, p.out, ((int64_t)token * p.q_heads + head) * kV4Dim + 8 * c, head * kV4Dim + 8 * c, v, vec);
-        } else {
-          float* dst = reinterpret_cast<float*>(p.part_o) +
-                       (((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head) * kV4Dim + 8 * c;
-          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * j + 2 * t + e;
+          if (r < n_rows) {
+            const int dt = div_g(r);
+            float* dst = reinterpret_cast<float*>(p.part_o) +
+                         (((int64_t)(m.tok0 + dt) * p.max_chunks + m.chunk) * p.q_heads + m.kvh * G + r - dt * G) *
+                             kV4Dim + g;
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v = o[j][d][2 * h + e] * inv[j][e];
+                if (per_channel) v *= __bfloat162float(vsc[16 * d + 8 * h + g]);
+                dst[16 * d + 8 * h] = v;
+              }
+          }
         }
+    } else {
+      float* stg = reinterpret_cast<float*>(smem + (warp * C::kStages + (st_comp == 0 ? C::kStages : st_comp) - 1) * kStage4);
+      const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              stg[(2 * t + e) * kV4Dim + ((16 * d + g + 8 * h) ^ (8 * t))] = o[j][d][2 * h + e] * inv[j][e];
+        __syncwarp();
+#pragma unroll 1
+        for (int idx = lane; idx < min(8, n_rows - 8 * j) * 16; idx += 32) {
+          const int rr = idx >> 4, c = idx & 15;   // row 8 j + rr, dims 8c .. 8c+7
+          const float* src = stg + rr * kV4Dim + ((8 * c) ^ (8 * ((rr >> 1) & 3)));
+          const float4 a = *reinterpret_cast<const float4*>(src);
+          const float4 b = *reinterpret_cast<const float4*>(src + 4);
+          float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          if (per_channel) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= __bfloat162float(vsc[8 * c + k]);
+          }
+          const int dt = div_g(8 * j + rr);
+          const int token = m.tok0 + dt;
+          const int head = m.kvh * G + 8 * j + rr - dt * G;
+          ep_store8(p.ep, p.out, ((int64_t)token * p.q_heads + head) * kV4Dim + 8 * c, head * kV4Dim + 8 * c, v, vec);
+        }
+        __syncwarp();   // the staged rows are read before they are overwritten
       }
-      __syncwarp();   // the staged rows are read before they are overwritten
     }
     ++k_comp;
     issue_next();   // the stage of the item's last half page
