@@ -7,7 +7,7 @@ template <int KV>
 static cudaError_t launch_t(const Plan& plan, const AttnParams& p, const CUtensorMap& tm_k,
                             const CUtensorMap& tm_v, const CUtensorMap& tm_q, cudaStream_t stream) {
   auto kern = append_kernel<KV>;
-  const int smem = Smem::kTotal;
+  const int smem = Smem<false>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<plan.num_ctas, kThreads, smem, stream>>>(tm_k, tm_v, tm_q, nullptr, nullptr, p);

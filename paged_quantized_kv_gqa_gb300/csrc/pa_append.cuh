@@ -72,9 +72,12 @@ constexpr int kWarpMmaS = 13;                    // issues S = Q' K^T of both qu
 constexpr int kWarpMmaPV = 14;                   // issues O += P V of both query tiles
 constexpr uint32_t kTmemCols = 512;
 
+template <bool kFour>
 struct Smem {
+  static constexpr int kStage = kFour ? 2 * kV4Slab : kStageBytes;
+  static constexpr int kVOff = kStage / 2;                    // V slab within a stage
   static constexpr int kRaw = 0;                              // [kStages][K slab | V slab]
-  static constexpr int kQ = kStages * kStageBytes;            // [2 k-halves][256 rows][128 B]
+  static constexpr int kQ = kStages * kStage;                 // [2 k-halves][256 rows][128 B]
   static constexpr int kK16 = kQ + kRows * 256;               // [2 buffers]
   static constexpr int kV16 = kK16 + 2 * kK16Bytes;           // [2 buffers]
   static constexpr int kBars = kV16 + 2 * kV16Bytes;
@@ -84,6 +87,7 @@ struct Smem {
   static constexpr int kMisc = kBars + kNumBars * 8;          // tmem address, abort flag
   static constexpr int kTotal = kMisc + 16 + 1024;            // + alignment slack
   static_assert(kTotal <= 232448, "shared memory overflow");
+  static_assert(kQ % 1024 == 0, "swizzled operands start on 1 KB");
 };
 
 // Shared-memory descriptor of k-step kk (16 elements) of a K-major SW128
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  using SM = Smem;
+  using SM = Smem<kFour>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBars);
   uint64_t* full = bars;
   uint64_t* empty = full + kStages;
@@ -213,13 +217,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.skip_first_load && g == 0) continue;  // failure-detection test hook
           mbar_arrive_expect_tx(&full[stage], kLoadBytes);
           issued_g[stage] = (int)g;
-          uint8_t* st = smem + SM::kRaw + stage * kStageBytes;
+          uint8_t* st = smem + SM::kRaw + stage * SM::kStage;
           if constexpr (kFour) {
             const bool in_pool = page >= 0 && page < p.num_pages;
             if (!in_pool) record_status(p.status, PA_ERR_BAD_PAGE, it);   // reads page 0 instead
             const int64_t off = (int64_t)((in_pool ? page : 0) * p.kv_heads + m.kvh) * kV4Slab;
             bulk_load(st, ck + off, kV4Slab, &full[stage]);
-            bulk_load(st + kSlab, cv + off, kV4Slab, &full[stage]);
+            bulk_load(st + SM::kVOff, cv + off, kV4Slab, &full[stage]);
             trace_ev(p, g, 0);
             continue;
           }
@@ -374,6 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = r / G;
       const float c_log2 = p.sm_scale_log2 *
           (p.scale_kind == PA_SCALE_PER_CHANNEL ? 1.0f : load_scale(p.k_scale, p.scale_kind, m.kvh));
+      const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
+      // (4-bit: read here, a memory round trip away from its use at the item's end)
+      const float vs_early = kFour && !pc ? load_scale(p.v_scale, p.scale_kind, m.kvh) : 1.0f;
       // positions < vis_lim are visible to this row (prefix rule; cbase is the
       // causal base, or kvtot without a causal mask)
       const int vis_lim = min(m.kv1, m.cbase + tok + 1);
@@ -470,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const float inv_l = l > 0.0f ? __frcp_rn(l) : 0.0f;
-      const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
-      const float vs = pc ? 1.0f : load_scale(p.v_scale, p.scale_kind, m.kvh);
+      const float vs = kFour ? vs_early : pc ? 1.0f : load_scale(p.v_scale, p.scale_kind, m.kvh);
       const int token = m.tok0 + tok;
       const int head = m.kvh * G + (r - tok * G);
       // one chunk: the final row (output epilogue applied); several: the
@@ -483,8 +489,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const OutEpilogue ep_none{nullptr, nullptr, 0, 1.0f, 0.0f, 0.0f};
       const __nv_bfloat16* vsc =
           reinterpret_cast<const __nv_bfloat16*>(p.v_scale) + m.kvh * kHeadDim;
+      // 4-bit: plain bf16 rows leave without the steps of the general epilogue (an
+      // item's rows took 6.4 us, 0.6 us so)
+      const bool plain = kFour && final_row && !pc && p.ep.shift == nullptr && p.ep.smooth == nullptr &&
+                         !p.ep.int8_out;
+      if (plain) {
+        const float f = inv_l * vs;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16], w[8];
+          tmem_ld16(o_tm + 16 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+            w[k] = *reinterpret_cast<uint32_t*>(&b2);
+          }
+          if (row_ok) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + obase + 16 * c);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
+        if (plain) break;
         uint32_t o[16];
         tmem_ld16(o_tm + 16 * c, o);
         tmem_wait_ld();
@@ -544,33 +574,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e) sc[e] = __bfloat162float(sv[e]);
       }
       if (!wait_or_abort(qfull, li & 1, limit, abort_any)) { note_fail(it); break; }
-      // Q' = bf16 Q (times the per-channel K scale) -> fp16, in place
-      for (int task = t; task < kRows * 16; task += 128) {
-        const int row = task >> 4, ch = task & 15;
-        const int kb = ch >> 3, cc = ch & 7;
-        const uint32_t addr = q_s + kb * kRows * 128 + row * 128 + ((cc ^ (row & 7)) << 4);
-        const uint4 raw = ld_shared_v4(addr);
-        const __nv_bfloat16* hv = reinterpret_cast<const __nv_bfloat16*>(&raw);
-        float f[8];
+      // Q' = bf16 Q (times the per-channel K scale) -> fp16, in place.  A thread's
+      // pieces are rows t / 16 + 8 k: one place of the swizzle pattern, 1 KB apart
+      const int ch = t & 15;
+      const uint32_t qaddr = q_s + (ch >> 3) * kRows * 128 + (t >> 4) * 128 + (((ch & 7) ^ ((t >> 4) & 7)) << 4);
+#pragma unroll 1
+      for (int k0 = 0; k0 < kRows / 8; k0 += 4) {
+        uint4 raw[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __bfloat162float(hv[e]);
-        if (pc) {
+        for (int k = 0; k < 4; ++k) raw[k] = ld_shared_v4(qaddr + (k0 + k) * 1024);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= sc[e];
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(u[e] << 16);
+            f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+          }
+          if (pc) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= sc[e];
+          }
+          constexpr int kG = pair_gap<KV>();
+          st_shared_v4(qaddr + (k0 + k) * 1024,
+                       make_uint4(pack_half2(f[pair_first<KV>(0)], f[pair_first<KV>(0) + kG]),
+                                  pack_half2(f[pair_first<KV>(1)], f[pair_first<KV>(1) + kG]),
+                                  pack_half2(f[pair_first<KV>(2)], f[pair_first<KV>(2) + kG]),
+                                  pack_half2(f[pair_first<KV>(3)], f[pair_first<KV>(3) + kG])));
         }
-        uint4 packed;
-        constexpr int kG = pair_gap<KV>();
-        packed.x = pack_half2(f[pair_first<KV>(0)], f[pair_first<KV>(0) + kG]);
-        packed.y = pack_half2(f[pair_first<KV>(1)], f[pair_first<KV>(1) + kG]);
-        packed.z = pack_half2(f[pair_first<KV>(2)], f[pair_first<KV>(2) + kG]);
-        packed.w = pack_half2(f[pair_first<KV>(3)], f[pair_first<KV>(3) + kG]);
-        st_shared_v4(addr, packed);
       }
       fence_proxy_async_smem();
       warp_arrive(qready, lane);
       for (int i = 0; i < m.ntiles; ++i, ++g) {
         const int stage = g % kStages;
-        const uint32_t st = s_base + SM::kRaw + stage * kStageBytes;
+        const uint32_t st = s_base + SM::kRaw + stage * SM::kStage;
         if (!wait_or_abort(&full[stage], (g / kStages) & 1, limit, abort_any)) { note_fail(it); break; }
         const int nvalid = min(kTile, m.kv1 - (m.kv0 + i * kTile));
         // ---- K: thread t converts position t & 63, dims 64 (t >> 6) .. +63,
@@ -643,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = v16 + (g & 1) * kV16Bytes + t * 128;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t src = st + kSlab + h * kV4HalfBytes;
+            const uint32_t src = st + SM::kVOff + h * kV4HalfBytes;
             const uint4 r4 = ld_shared_v4(src + t * (kV4Half / 2));
             const uint32_t w[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll

@@ -7,7 +7,7 @@ template <int KV>
 static cudaError_t launch_t(const Plan& plan, const AttnParams& p, const uint8_t* ck, const uint8_t* cv,
                             const CUtensorMap& tm_q, cudaStream_t stream) {
   auto kern = append_kernel<KV>;
-  const int smem = Smem::kTotal;
+  const int smem = Smem<true>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<plan.num_ctas, kThreads, smem, stream>>>(tm_q, tm_q, tm_q, ck, cv, p);   // tm_k, tm_v unused
