@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           }
         }
     } else {
+      const bool plain = p.ep.shift == nullptr && p.ep.smooth == nullptr && !p.ep.int8_out;
       float* stg = reinterpret_cast<float*>(smem + (warp * C::kStages + (st_comp == 0 ? C::kStages : st_comp) - 1) * kStage4);
       const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 #pragma unroll
@@ -607,7 +608,18 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           const int dt = div_g(8 * j + rr);
           const int token = m.tok0 + dt;
           const int head = m.kvh * G + 8 * j + rr - dt * G;
-          ep_store8(p.ep, p.out, ((int64_t)token * p.q_heads + head) * kV4Dim + 8 * c, head * kV4Dim + 8 * c, v, vec);
+          const int64_t oi = ((int64_t)token * p.q_heads + head) * kV4Dim + 8 * c;
+          if (plain && vec) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+              w[k] = *reinterpret_cast<uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(p.out + oi) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            ep_store8(p.ep, p.out, oi, head * kV4Dim + 8 * c, v, vec);
+          }
         }
         __syncwarp();   // the staged rows are read before they are overwritten
       }

@@ -114,11 +114,13 @@ __global__ void __launch_bounds__(256, DV >= 512 ? 5 : 1) merge_kernel(const int
   merge_store<DV>(acc[0], M[0], W[0], out, lse, ep, token, head, q_heads, lane);
 }
 
-// Rows whose partial states are fp32 (plans over a 4-bit cache), 128 wide: one
-// warp per row, lane l owning dims 4l .. 4l+3 (one 16-byte load per chunk row).
-// The (m, d) of up to 32 chunks sit one per lane; the first eight chunk rows are
-// requested before the weights are known, so that a row of at most eight chunks
-// costs one memory round trip.  A row without chunks comes out as 0 and -inf.
+// Rows whose partial states are fp32 (plans over a 4-bit cache), 128 wide: WPR
+// warps per row, lane l owning dims 4l .. 4l+3 (one 16-byte load per chunk row).
+// Warp w of a row takes chunks 8 w .. 8 w + 7, then those 8 WPR further on; its
+// first eight rows are requested before the weights are known, so that a row of
+// at most 8 WPR chunks costs one memory round trip after the plan's lookup.  The
+// warps' sums meet in shared memory.  A row without chunks comes out as 0, -inf.
+template <int WPR>
 __global__ void __launch_bounds__(256) merge_f32_kernel(const int32_t* __restrict__ merge_tokens,
                                                         const int32_t* __restrict__ nch_token, int n_merge,
                                                         int q_heads, int max_chunks,
@@ -126,66 +128,75 @@ __global__ void __launch_bounds__(256) merge_f32_kernel(const int32_t* __restric
                                                         const float* __restrict__ part_m,
                                                         const float* __restrict__ part_d, void* __restrict__ out,
                                                         float* __restrict__ lse, const OutEpilogue ep) {
-  pdl_wait();   // launched as a programmatic dependent of the attention kernel
-  const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (wid >= (int64_t)n_merge * q_heads) return;
-  const int token = merge_tokens[wid / q_heads];
-  const int head = (int)(wid % q_heads);
-  const int nch = nch_token[token];
-  const int64_t slot0 = (int64_t)token * max_chunks * q_heads + head;
   constexpr int kU = 8;
+  __shared__ float4 sums[8][32];
+  __shared__ float weights[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+  const uint32_t row = blockIdx.x * (8 / WPR) + warp / WPR;
+  const bool valid = row < (uint32_t)n_merge * (uint32_t)q_heads;
+  // (the plan's arrays were there before the attention kernel started)
+  const int token = valid ? merge_tokens[row / (uint32_t)q_heads] : 0;
+  const int head = valid ? (int)(row % (uint32_t)q_heads) : 0;
+  const int nch = valid ? nch_token[token] : 0;
+  pdl_wait();   // launched as a programmatic dependent of the attention kernel
+  const int64_t slot0 = (int64_t)token * max_chunks * q_heads + head;
   const float4* rows = reinterpret_cast<const float4*>(part_o) + slot0 * 32 + lane;
   const int64_t rstride = (int64_t)q_heads * 32;
   float4 v[kU];
 #pragma unroll
-  for (int u = 0; u < kU; ++u) v[u] = u < nch ? __ldcg(rows + u * rstride) : make_float4(0.f, 0.f, 0.f, 0.f);
-  float M = -INFINITY, m0 = -INFINITY, d0 = 0.f;
-  for (int c = lane; c < nch; c += 32) {
-    const float mc = __ldcg(part_m + slot0 + (int64_t)c * q_heads);
-    if (c == lane) {
-      m0 = mc;
-      d0 = __ldcg(part_d + slot0 + (int64_t)c * q_heads);
-    }
-    M = fmaxf(M, mc);
+  for (int u = 0; u < kU; ++u) {
+    const int c = kU * sub + u;
+    v[u] = c < nch ? __ldcg(rows + c * rstride) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float M = -INFINITY;
+  for (int c = lane; c < nch; c += 32) M = fmaxf(M, __ldcg(part_m + slot0 + (int64_t)c * q_heads));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}}, W = 0.f;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, W = 0.f;
   if (M != -INFINITY) {
-    for (int c0 = 0; c0 < nch; c0 += 32) {
-      if (c0 > 0) {
-        m0 = -INFINITY;
-        if (c0 + lane < nch) {
-          m0 = __ldcg(part_m + slot0 + (int64_t)(c0 + lane) * q_heads);
-          d0 = __ldcg(part_d + slot0 + (int64_t)(c0 + lane) * q_heads);
-        }
+    for (int c0 = kU * sub; c0 < nch; c0 += kU * WPR) {
+      if (c0 != kU * sub) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          v[u] = c0 + u < nch ? __ldcg(rows + (c0 + u) * rstride) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      const float w = m0 != -INFINITY ? d0 * __expf(m0 - M) : 0.f;
+      float w = 0.f;   // lane u: weight of chunk c0 + u
+      if (lane < kU && c0 + lane < nch) {
+        const float m = __ldcg(part_m + slot0 + (int64_t)(c0 + lane) * q_heads);
+        if (m != -INFINITY) w = __ldcg(part_d + slot0 + (int64_t)(c0 + lane) * q_heads) * __expf(m - M);
+      }
       W += w;
-      const int n = min(32, nch - c0);
-      for (int j = 0; j < n; j += kU) {
-        if (c0 + j > 0) {
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
-            v[u] = j + u < n ? __ldcg(rows + (c0 + j + u) * rstride) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const float wc = __shfl_sync(0xffffffffu, w, j + u);   // 0 past the last chunk
-          if (wc != 0.f) {
-            acc[0][0] += wc * v[u].x;
-            acc[0][1] += wc * v[u].y;
-            acc[0][2] += wc * v[u].z;
-            acc[0][3] += wc * v[u].w;
-          }
+      for (int u = 0; u < kU; ++u) {
+        const float wc = __shfl_sync(0xffffffffu, w, u);
+        if (wc != 0.f) {
+          acc[0] += wc * v[u].x;
+          acc[1] += wc * v[u].y;
+          acc[2] += wc * v[u].z;
+          acc[3] += wc * v[u].w;
         }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+    for (int o = 4; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+    W = __shfl_sync(0xffffffffu, W, 0);
   }
-  merge_store<128>(acc[0], M, W, out, lse, ep, token, head, q_heads, lane);
+  if constexpr (WPR > 1) {
+    sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) weights[warp] = W;
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      const float4 t = sums[warp + k][lane];
+      acc[0] += t.x;
+      acc[1] += t.y;
+      acc[2] += t.z;
+      acc[3] += t.w;
+      W += weights[warp + k];
+    }
+  }
+  if (valid) merge_store<128>(acc, M, W, out, lse, ep, token, head, q_heads, lane);
 }
 
 cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* lse,
@@ -193,7 +204,7 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const int n_merge = (int)plan.merge_tokens.size();
   if (n_merge == 0) return cudaSuccess;
   const int64_t warps = (int64_t)n_merge * plan.prob.q_heads;
-  if (warps > INT32_MAX) return cudaErrorInvalidValue;
+  if (warps > INT32_MAX / 8) return cudaErrorInvalidValue;
   const int blocks = (int)((warps + 7) / 8);
   // programmatic dependent launch: the grid is set up while the attention
   // kernel's last CTAs finish, and waits for it in pdl_wait
@@ -213,9 +224,16 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const __nv_bfloat16* po = ws.part_o;
   const float* pm = ws.part_m;
   const float* pd = ws.part_d;
-  if (plan.four_bit())
-    return cudaLaunchKernelEx(&cfg, merge_f32_kernel, mt, nt, n_merge, qh, mc,
-                              reinterpret_cast<const float*>(po), pm, pd, out, lse, ep);
+  if (plan.four_bit()) {
+    // one warp per eight chunks of the longest row, up to a whole block
+    const float* pf = reinterpret_cast<const float*>(po);
+    const int wpr = mc <= 8 ? 1 : mc <= 16 ? 2 : mc <= 32 ? 4 : 8;
+    cfg.gridDim = dim3((unsigned)((warps * wpr + 7) / 8));
+    if (wpr == 1) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<1>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    if (wpr == 2) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<2>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    if (wpr == 4) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<4>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    return cudaLaunchKernelEx(&cfg, merge_f32_kernel<8>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+  }
   if (plan.prob.head_dim_v == 128)
     return cudaLaunchKernelEx(&cfg, merge_kernel<128>, mt, nt, n_merge, qh, mc, po, pm, pd, out, lse, ep);
   if (plan.prob.head_dim_v == 512)
