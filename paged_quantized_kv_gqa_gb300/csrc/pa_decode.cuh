@@ -77,15 +77,16 @@ constexpr int kSlot4 = 5120;                     // 4-bit: a slab's place in a s
 constexpr int kVs16Warp = 2 * kTileTok * 2;      // 4-bit: a CV warp's V scales as fp16 [2 blocks][128]
 static_assert(kSlot4 >= kV4Slab && kSlot4 % 512 == 0 && 2 * kSlot4 <= 2 * kSlab, "4-bit stage layout");
 constexpr float kTau = 8.0f;                     // lazy-rescale threshold (log2 units)
-// 8-bit: four warpgroups.  4-bit: the fourth converts V while the third converts
-// K (one group for both is the longest stage of the pipeline: a code needs more
-// steps than a byte), and a fifth warpgroup issues the copies and the MMAs.
+// Warpgroups: two softmax, CV, IO.  4-bit: one CV warpgroup for K and one for V (a
+// code needs more steps than a byte, and one group for both held the pipeline up),
+// and S and PV are issued from a warp each.  (A softmax warpgroup for every 16 rows
+// instead of two for all measured slower, 334 against 319 us on 48 rows.)
 template <int KV>
 struct Roles {
   static constexpr bool kFour = KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1;
   static constexpr int kThreads = kFour ? 640 : 512;
   static constexpr int kWarpTma = kFour ? 16 : 12;
-  static constexpr int kWarpMma = kFour ? 17 : 13;
+  static constexpr int kWarpMma = kWarpTma + 1;    // 4-bit: this one S, the next PV
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPBufs = 4;                        // P^T ring depth
@@ -259,8 +260,9 @@ template <int NR, int KV, bool TREE>
 __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const uint8_t* __restrict__ cv, const AttnParams p) {
-  constexpr bool kFour = Roles<KV>::kFour;
-  constexpr int kThreads = Roles<KV>::kThreads;
+  using R = Roles<KV>;
+  constexpr bool kFour = R::kFour;
+  constexpr int kThreads = R::kThreads;
   constexpr int FP4 = KV == PA_KV_FP4_E2M1, FP8 = KV == PA_KV_FP8_E4M3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int wg = warp >> 2;         // warpgroup: 0, 1 softmax; 2 CV; 3 IO (4-bit: 3 CV of V; 4 IO)
+  const int wg = warp >> 2;         // warpgroup: 0, 1 softmax; 2 CV; 3 IO (4-bit: 2, 3 CV of K, V; 4 IO)
   const int item_begin = p.work_indptr[blockIdx.x];
   const int item_end = p.work_indptr[blockIdx.x + 1];
   const uint64_t limit = (uint64_t)p.wait_limit_ns;
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
   // this warp's TMEM lane quarter (a warp may only touch lanes 32*(warp%4) ..)
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
-  if (warp == Roles<KV>::kWarpTma) {
+  if (warp == R::kWarpTma) {
     // ================================================================ TMA
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
@@ -405,7 +407,56 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
       for (int s = 0; s < kStages; ++s)   // every issued load lands before exit
         if (issued_g[s] >= 0) mbar_wait(&full[s], ((uint32_t)issued_g[s] / kStages) & 1, kDrainNs);
     }
-  } else if (warp == Roles<KV>::kWarpMma) {
+  } else if (kFour && (warp == R::kWarpMma || warp == R::kWarpMma + 1)) {
+    // ================================================================ MMA issue, 4-bit
+    // S and PV each have a warp that sleeps on its barriers: one warp polling both
+    // queues took issue slots from the converters on its sub-partition
+    const bool is_s = warp == R::kWarpMma;
+    auto mwait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, limit, abort_any, 100); };
+    const uint32_t idesc = is_s ? idesc_f16_f32(128, NR) : idesc_f16_f32_bmn(128, NR);
+    TileCursor c;
+    c.init(isrc, item_begin, item_end);
+    uint32_t g = 0, commits[kPBufs] = {0, 0, 0, 0};
+    bool ok = true;
+    for (; c.valid(); c.advance(), ++g) {
+      if (is_s) {
+        if (!mwait(&kready[g & 1], (g >> 1) & 1) ||
+            (g >= 2 && !mwait(&sfree[g & 1], ((g - 2) >> 1) & 1))) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t qb = q_s + ((c.it - item_begin) & 1) * NR * 256;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + TM::S0 + (g & 1) * NR, tmem + TM::K0 + (g & 1) * 64 + 8 * kk,
+                   sdesc_k128(qb + (kk >> 2) * NR * 128 + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+          tc_commit(&sfull[g & 1]);
+        }
+        ++commits[g & 1];
+        if (lane == 0) trace_ev(p, g, 8);
+      } else {
+        if (!mwait(&pready[g & 3], (g >> 2) & 1) || !mwait(&vready[g & 1], (g >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t pb = p_s + (g & 3) * kPBufBytes;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)   // positions 16kk .. 16kk+15: two 8-position swizzle atoms of 1 KB
+            mma_ts(tmem + TM::O0 + ((c.it - item_begin) & 1) * NR, tmem + TM::V0 + (g & 1) * 64 + 8 * kk,
+                   sdesc_mn128(pb + kk * 2048, kPBufBytes, 1024), idesc, (c.i > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(&pvdone[g & 3]);
+        }
+        ++commits[g & 3];
+        if (lane == 0) trace_ev(p, g, 9);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) {
+      if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, item_begin);
+      *abort_any = 1;
+    }
+    // drain: every MMA this warp issued completes before TMEM is released
+    for (int j = 0; j < kPBufs; ++j)
+      if (commits[j]) mbar_wait(is_s ? &sfull[j] : &pvdone[j], (commits[j] - 1) & 1, kDrainNs);
+  } else if (!kFour && warp == R::kWarpMma) {
     // ================================================================ MMA issue
     // the whole warp runs the polling loop (warp-uniform operands); one
     // elected lane issues the MMAs and commits
@@ -483,7 +534,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         if (pv_commits[j]) mbar_wait(&pvdone[j], (pv_commits[j] - 1) & 1, kDrainNs);
     }
   } else if (kFour && wg == 4) {
-    // warps 18, 19: no role (they complete the fifth warpgroup)
+    // the last warp has no role (it completes the warpgroup)
   } else if (!kFour && wg == 3) {
     // ================================================================ fused merge
     // warps 14 and 15 take alternate items; once all eight softmax warps have
