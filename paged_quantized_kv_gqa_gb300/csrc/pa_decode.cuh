@@ -1101,15 +1101,15 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
           const int hrow = ((d >> 5) & 1) * (kV4HalfBytes / 64), r = hrow + (d & 31);
           const int rs = hrow + kV4Half + ((d & 31) >> 3);
           const uint2 sw = ld_shared_v2(kbase + rs * 64 + ((((d & 7) >> 1) ^ ((rs >> 1) & 3)) << 4) + 8 * (d & 1));
-          uint4 raw[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) raw[c] = ld_shared_v4(kbase + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+          uint4 nx = ld_shared_v4(kbase + r * 64 + (((r >> 1) & 3) << 4));
           const uint32_t dst = t_lane + TM::K0 + (g & 1) * 64;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {   // dims 32c .. 32c+31
             uint32_t s0, s1, x[16];
             scale_pair((uint16_t)((c < 2 ? sw.x : sw.y) >> (16 * (c & 1))), s0, s1);
-            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+            const uint4 rc = nx;
+            nx = ld_shared_v4(kbase + r * 64 + ((((c + 1) & 3) ^ ((r >> 1) & 3)) << 4));
+            const uint32_t w[4] = {rc.x, rc.y, rc.z, rc.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t y[4];
