@@ -91,8 +91,9 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *           GLOBAL       fp32 [1]                     (one value for K and V)
  *   chunk_size > 0 splits the KV range into chunks of that many positions (a
  *   multiple of block_size); 0 never splits; -1 lets the planner choose.  Plans
- *   of the decode family over a 4-bit cache take any other value than 0 as -1:
- *   the planner cuts pieces of equal work.
+ *   of the decode family over a 4-bit cache ignore it: the planner keeps ranges of
+ *   at most 512 positions whole and otherwise cuts pieces of equal work, so
+ *   pa_merge always belongs after pa_run there.
  *   q_stride is the distance in elements between consecutive tokens of q
  *   (>= q_heads * head_dim_qk; FastDeploy's packed qkv uses
  *   (q_heads + 2 * kv_heads) * head_dim).
@@ -119,7 +120,8 @@ typedef struct pa_problem {
  * Device buffers of one call (all device pointers, caller-owned).
  *   q            bf16  [T][q_stride], T = cu_seqlens_q[bsz]
  *   cache_k/v    uint8 (layouts above); 16-byte aligned
- *   k_scale/v_scale  as the scale kind says
+ *   k_scale/v_scale  as the scale kind says; per-channel K scales 16-byte aligned
+ *                (any bf16 address where max(q_len) * G <= 16)
  *   block_table  int32 [bsz][max_blocks_per_seq]; only the first
  *                ceil(kvtot_b / block_size) entries of row b are read
  *   out          bf16  [T][q_heads][head_dim_v]

@@ -38,7 +38,8 @@ Spec:
   nch_token[t] = nch of token t's tile; max_chunks = max(1, max nch_token);
   merge_tokens = tokens with nch_token != 1, ascending (those with 0 chunks are
   the rows that see nothing; the merge writes them).
-  A 4-bit cache, decode family and chunk_size != 0: shares of equal work per
+  A 4-bit cache, decode family: chunk_size is ignored; no split while the largest
+  lim is at most 8 * B, else shares of equal work per
   worker, w workers per CTA: 16 warps if max(q_len) * G <= 16, else the smallest
   w in 1 .. 4 with slots * w divisible by kv_heads (4 if none).  The tiles' pages
   are numbered as for MLA below; quota = max(2 (warps) or 8, ceil(total / max(1,
@@ -99,12 +100,13 @@ def plan(p, num_sms: int) -> dict:
             lim = slkv[b] if cross else slkv[b] + tok1 if p.causal else slkv[b] + ql
             tiles.append((b, tok0, tok1, lim))
 
-    if p.kv_dtype in ("int4", "fp4_e2m1") and family == "decode" and int(p.chunk_size) != 0:
+    decode4 = p.kv_dtype in ("int4", "fp4_e2m1") and family == "decode"
+    if decode4 and max((t[3] for t in tiles), default=0) > 8 * B:
         return _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, max_q * G <= 16)
     if family == "mla" and int(p.chunk_size) == -1:
         return _mla_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B)
 
-    cs = int(p.chunk_size)
+    cs = 0 if decode4 else int(p.chunk_size)
     if cs == -1:
         W = p.kv_heads * sum(t[3] for t in tiles)
         target = 4 * slots

@@ -151,7 +151,10 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       tiles.push_back({b, tok0, tok1, lim});
     }
   }
-  if (P.four_bit() && P.family == PA_FAMILY_DECODE && prob.chunk_size != 0) {
+  int64_t longest = 0;
+  for (const auto& t : tiles) longest = std::max(longest, t.lim);
+  const bool decode4 = P.four_bit() && P.family == PA_FAMILY_DECODE;
+  if (decode4 && longest > (int64_t)kDecode4WholePages * B) {
     // 4-bit decode: the pages of all tiles, tile after tile, are cut into shares
     // of `quota` pages, so that every worker of the grid has the same work and few
     // partial states are merged.  A worker is a warp (at most 16 rows: a warp takes
@@ -269,7 +272,7 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       P.work_indptr[k + 1] = (int32_t)(P.items.size() / kItemWords);
     }
   } else {
-    int64_t cs = prob.chunk_size;
+    int64_t cs = decode4 ? 0 : prob.chunk_size;
     if (cs == -1) {
       if (tiles.empty()) {
         cs = 0;
@@ -482,6 +485,12 @@ static OutEpilogue epilogue_of(const pa_args& a) {
   return e;
 }
 
+// Scale arrays are read as their elements (bf16, or fp32 when global).
+static bool scales_aligned(const pa_problem& pr, const pa_args* a) {
+  const uintptr_t n = pr.scale_kind == PA_SCALE_GLOBAL ? 4 : 2;
+  return reinterpret_cast<uintptr_t>(a->k_scale) % n == 0 && reinterpret_cast<uintptr_t>(a->v_scale) % n == 0;
+}
+
 static pa_status check_args(const Plan& P, const pa_args* a, bool need_cache) {
   if (!a) return fail(PA_ERR_INVALID_ARG, "null pa_args");
   if (!a->out) return fail(PA_ERR_INVALID_ARG, "null out");
@@ -500,6 +509,12 @@ static pa_status check_args(const Plan& P, const pa_args* a, bool need_cache) {
     if (reinterpret_cast<uintptr_t>(a->q) % 16 || reinterpret_cast<uintptr_t>(a->cache_k) % 16 ||
         reinterpret_cast<uintptr_t>(a->cache_v) % 16)
       return fail(PA_ERR_INVALID_ARG, "q and caches must be 16-byte aligned");
+    if (!scales_aligned(P.prob, a)) return fail(PA_ERR_INVALID_ARG, "misaligned scale array");
+    // all kernels but the warp-per-item ones read a head's K scales as 16-byte vectors
+    const bool by_warp = P.family == PA_FAMILY_DECODE && !P.fused_merge &&
+                         P.max_q * (P.prob.q_heads / P.prob.kv_heads) <= kWarpDecodeRows;
+    if (P.prob.scale_kind == PA_SCALE_PER_CHANNEL && !by_warp && reinterpret_cast<uintptr_t>(a->k_scale) % 16)
+      return fail(PA_ERR_INVALID_ARG, "per-channel K scales must be 16-byte aligned");
     if (P.prob.layout == PA_LAYOUT_MLA && a->cache_k != a->cache_v)
       return fail(PA_ERR_INVALID_ARG, "MLA layout: cache_v must equal cache_k");
   }
@@ -789,6 +804,7 @@ static pa_status check_rows(const pa_plan_t* plan, const pa_args* args, const vo
     return fail(PA_ERR_INVALID_ARG, "kv_stride smaller than one token's K / V row");
   if (reinterpret_cast<uintptr_t>(k_rows) % 2 || reinterpret_cast<uintptr_t>(v_rows) % 2)
     return fail(PA_ERR_INVALID_ARG, "K / V rows must be 2-byte aligned (bf16)");
+  if (!scales_aligned(pr, args)) return fail(PA_ERR_INVALID_ARG, "misaligned scale array");
   if (reinterpret_cast<uintptr_t>(args->cache_k) % 16 || reinterpret_cast<uintptr_t>(args->cache_v) % 16)
     return fail(PA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
   return PA_OK;

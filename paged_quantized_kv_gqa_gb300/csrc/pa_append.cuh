@@ -376,8 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_rows = m.ntok * G;
       const bool row_ok = r < n_rows;
       const int tok = r / G;
+      // (a negative K scale's sign is in Q': the running maximum needs a positive factor)
       const float c_log2 = p.sm_scale_log2 *
-          (p.scale_kind == PA_SCALE_PER_CHANNEL ? 1.0f : load_scale(p.k_scale, p.scale_kind, m.kvh));
+          (p.scale_kind == PA_SCALE_PER_CHANNEL ? 1.0f : fabsf(load_scale(p.k_scale, p.scale_kind, m.kvh)));
       const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
       // (4-bit: read here, a memory round trip away from its use at the item's end)
       const float vs_early = kFour && !pc ? load_scale(p.v_scale, p.scale_kind, m.kvh) : 1.0f;
@@ -574,6 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e) sc[e] = __bfloat162float(sv[e]);
       }
       if (!wait_or_abort(qfull, li & 1, limit, abort_any)) { note_fail(it); break; }
+      const uint32_t flip =
+          !pc && load_scale(p.k_scale, p.scale_kind, m.kvh) < 0.0f ? 0x80008000u : 0u;   // the K scale's sign
       // Q' = bf16 Q (times the per-channel K scale) -> fp16, in place.  A thread's
       // pieces are rows t / 16 + 8 k: one place of the swizzle pattern, 1 KB apart
       const int ch = t & 15;
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k) raw[k] = ld_shared_v4(qaddr + (k0 + k) * 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          const uint32_t u[4] = {raw[k].x ^ flip, raw[k].y ^ flip, raw[k].z ^ flip, raw[k].w ^ flip};
           float f[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

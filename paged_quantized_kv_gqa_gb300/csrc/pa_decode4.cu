@@ -24,16 +24,6 @@
 #include "pa_common.cuh"
 #include "pa_kv4.cuh"
 
-#ifndef D4_WARPS
-#define D4_WARPS 16
-#endif
-#ifndef D4_STAGES
-#define D4_STAGES 2
-#endif
-#ifndef D4_HINT
-#define D4_HINT 32
-#endif
-
 namespace pa {
 namespace {
 
@@ -46,8 +36,13 @@ constexpr float kTau = 8.0f;           // lazy rescale: P stays below 2^8
 
 template <int NB>
 struct D4Cfg {
-  static constexpr int kWarps = NB == 1 ? D4_WARPS : 8;
-  static constexpr int kStages = D4_STAGES;
+  // Up to 8 rows: 16 warps of 128 registers, two stages each.  On 8 sequences of
+  // 33k-131k positions (64 / 8 heads, FP4) 8, 12 and 16 warps took 185, 162 and 158
+  // us, three stages instead of two 158; on 24 of up to 3k positions 21.1, 20.5 and
+  // 19.8 us, three stages 21.9 (they put more copies before a warp's first).
+  // 9 to 16 rows need twice the accumulators: 8 warps.
+  static constexpr int kWarps = NB == 1 ? kDecode4Warps : 8;
+  static constexpr int kStages = NB == 1 ? 2 : 3;
   static constexpr int kItems = 32;    // CTA item records kept in shared memory
   static constexpr int kScaleOff = kWarps * kStages * kStage4;
   static constexpr int kItemOff = kScaleOff + kScaleBytes;
@@ -351,7 +346,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     }
 
     for (int hp = 0; hp < nh; ++hp) {
-      if (!wait_or_abort(&full[st_comp], ph_comp, limit, abort_any, D4_HINT)) {
+      if (!wait_or_abort(&full[st_comp], ph_comp, limit, abort_any, 32)) {
         if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, it);
         *abort_any = 1;
         fail = true;

@@ -18,10 +18,10 @@ constexpr int kItemWords = 8;        // b, kvh, token0, n_tok, causal_base, kv0,
 constexpr int kDecodeRows = 64;      // packed (token, head) rows per decode tile
 constexpr int kWarpDecodeRows = 16;  // decode tiles up to this many rows run warp per item
 constexpr int kAppendRows = 256;     // packed rows per append item (two 128-row tiles)
-#ifndef D4_WARPS
-#define D4_WARPS 16
-#endif
-constexpr int kDecode4Warps = D4_WARPS;    // warps of a 4-bit decode CTA (each takes whole items)
+constexpr int kDecode4Warps = 16;    // warps of a 4-bit decode CTA (each takes whole items)
+// 4-bit decode plans keep their tiles whole while none is longer: up to there the
+// merge's launch costs more than the split saves
+constexpr int kDecode4WholePages = 8;
 constexpr int kDecode4MinPages = 2;  // smallest share of a warp
 constexpr int kDecode4MinTiles = 4;  // smallest share of a tensor-memory CTA, 128-position tiles
 constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache

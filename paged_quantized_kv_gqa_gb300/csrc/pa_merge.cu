@@ -5,6 +5,7 @@
 // One warp per (token, query head); the partial states of a token sit at
 // slot (token * max_chunks + c) * q_heads + head.  HBM-bound, CUDA cores:
 // the row reads of all chunks are issued before they are summed.
+#include <algorithm>
 #include <cfloat>
 
 #include "pa_common.cuh"
@@ -121,18 +122,18 @@ __global__ void __launch_bounds__(256, DV >= 512 ? 5 : 1) merge_kernel(const int
 // at most 8 WPR chunks costs one memory round trip after the plan's lookup.  The
 // warps' sums meet in shared memory.  A row without chunks comes out as 0, -inf.
 template <int WPR>
-__global__ void __launch_bounds__(256) merge_f32_kernel(const int32_t* __restrict__ merge_tokens,
+__global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(const int32_t* __restrict__ merge_tokens,
                                                         const int32_t* __restrict__ nch_token, int n_merge,
                                                         int q_heads, int max_chunks,
                                                         const float* __restrict__ part_o,
                                                         const float* __restrict__ part_m,
                                                         const float* __restrict__ part_d, void* __restrict__ out,
                                                         float* __restrict__ lse, const OutEpilogue ep) {
-  constexpr int kU = 8;
-  __shared__ float4 sums[8][32];
-  __shared__ float weights[8];
+  constexpr int kU = 8, kBlockWarps = WPR <= 8 ? 8 : WPR;
+  __shared__ float4 sums[kBlockWarps][32];
+  __shared__ float weights[kBlockWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
-  const uint32_t row = blockIdx.x * (8 / WPR) + warp / WPR;
+  const uint32_t row = blockIdx.x * (kBlockWarps / WPR) + warp / WPR;
   const bool valid = row < (uint32_t)n_merge * (uint32_t)q_heads;
   // (the plan's arrays were there before the attention kernel started)
   const int token = valid ? merge_tokens[row / (uint32_t)q_heads] : 0;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(256) merge_f32_kernel(const int32_t* __restric
     if (lane == 0) weights[warp] = W;
     __syncthreads();
     if (sub != 0) return;
-#pragma unroll
+#pragma unroll 4
     for (int k = 1; k < WPR; ++k) {
       const float4 t = sums[warp + k][lane];
       acc[0] += t.x;
@@ -204,7 +205,7 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const int n_merge = (int)plan.merge_tokens.size();
   if (n_merge == 0) return cudaSuccess;
   const int64_t warps = (int64_t)n_merge * plan.prob.q_heads;
-  if (warps > INT32_MAX / 8) return cudaErrorInvalidValue;
+  if (warps > INT32_MAX / 32) return cudaErrorInvalidValue;
   const int blocks = (int)((warps + 7) / 8);
   // programmatic dependent launch: the grid is set up while the attention
   // kernel's last CTAs finish, and waits for it in pdl_wait
@@ -225,14 +226,18 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const float* pm = ws.part_m;
   const float* pd = ws.part_d;
   if (plan.four_bit()) {
-    // one warp per eight chunks of the longest row, up to a whole block
+    // one warp per eight chunks of the longest row, up to 32
     const float* pf = reinterpret_cast<const float*>(po);
-    const int wpr = mc <= 8 ? 1 : mc <= 16 ? 2 : mc <= 32 ? 4 : 8;
-    cfg.gridDim = dim3((unsigned)((warps * wpr + 7) / 8));
+    const int wpr = mc <= 8 ? 1 : mc <= 16 ? 2 : mc <= 32 ? 4 : mc <= 64 ? 8 : mc <= 128 ? 16 : 32;
+    const int block_warps = std::max(8, wpr);
+    cfg.gridDim = dim3((unsigned)((warps * wpr + block_warps - 1) / block_warps));
+    cfg.blockDim = dim3(32 * block_warps);
     if (wpr == 1) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<1>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
     if (wpr == 2) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<2>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
     if (wpr == 4) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<4>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
-    return cudaLaunchKernelEx(&cfg, merge_f32_kernel<8>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    if (wpr == 8) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<8>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    if (wpr == 16) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<16>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    return cudaLaunchKernelEx(&cfg, merge_f32_kernel<32>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
   }
   if (plan.prob.head_dim_v == 128)
     return cudaLaunchKernelEx(&cfg, merge_kernel<128>, mt, nt, n_merge, qh, mc, po, pm, pd, out, lse, ep);

@@ -163,6 +163,13 @@ def test_run_rejects_bad_arguments_before_launch(pa):
     with pytest.raises(pa.PaError) as e:
         pa.pa_run(plan(pa, x), fake_args(pa, attn_mask=256), 256, None)
     assert e.value.status == pa.PA_ERR_INVALID_ARG
+    with pytest.raises(pa.PaError) as e:
+        pa.pa_run(pl, fake_args(pa, k_scale=257), 256, None)
+    assert e.value.status == pa.PA_ERR_INVALID_ARG
+    z = make(1, seq_lens=[40], seq_lens_kv=[10], q_heads=8, kv_heads=2, scale_kind="per_channel")
+    with pytest.raises(pa.PaError) as e:
+        pa.pa_run(plan(pa, z), fake_args(pa, k_scale=264), 256, None)
+    assert e.value.status == pa.PA_ERR_INVALID_ARG and "per-channel" in pa.pa_last_error()
     y = make(1, seq_lens=[40], seq_lens_kv=[10], q_heads=8, kv_heads=2)
     with pytest.raises(pa.PaError) as e:
         pa.pa_run(plan(pa, y), fake_args(pa, attn_mask=256), 256, None)
@@ -177,7 +184,7 @@ def test_row_calls_reject_bad_arguments_before_launch(pa, call):
     f = getattr(pa, call)
     p = make(1, seq_lens=[1], seq_lens_kv=[10], q_heads=8, kv_heads=2)
     pl = plan(pa, p)
-    bad = [dict(cache_k=None), dict(cache_v=None), dict(k_scale=None), dict(v_scale=None), dict(block_table=None),
+    bad = [dict(v_scale=255), dict(cache_k=None), dict(cache_v=None), dict(k_scale=None), dict(v_scale=None), dict(block_table=None),
            dict(seq_lens=None), dict(seq_lens_kv=None), dict(cu_seqlens_q=None), dict(cache_k=264)]
     for kw in bad:
         with pytest.raises(pa.PaError) as e:

@@ -63,6 +63,93 @@ def test_attention_without_causal_mask(kw):
     check(p, out, lse)
 
 
+LONG = [
+    dict(seq_lens=[1], seq_lens_kv=[20000], q_heads=2, kv_heads=1),                  # 157 pieces, 32 warps merge a row
+    dict(seq_lens=[1, 1], seq_lens_kv=[9000, 513], q_heads=10, kv_heads=2),          # 16 warps
+    dict(seq_lens=[2, 1], seq_lens_kv=[3700, 511], q_heads=8, kv_heads=1),           # 16 rows, pieces of one sequence
+    dict(seq_lens=[6, 2], seq_lens_kv=[6000, 30], q_heads=16, kv_heads=2),           # 48 rows
+    dict(seq_lens=[3], seq_lens_kv=[5000], q_heads=21, kv_heads=3),                  # 21 rows, odd head count
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kw", LONG)
+def test_long_contexts_in_pieces(kw, kind):
+    p = make(24, kv_dtype=kind, scale_kind="per_channel", **kw)
+    out, lse, _, plan = run(p)
+    check(p, out, lse)
+    assert plan.describe()["max_chunks"] > 1
+
+
+def test_per_channel_scales_at_an_odd_address():
+    """At most 16 rows: the scales may start at any bf16 address."""
+    p = make(28, scale_kind="per_channel", **DECODE[3])
+    d = device(p)
+    for n in ("k_scale", "v_scale"):
+        whole = torch.zeros(d[n].numel() + 1, dtype=torch.bfloat16, device="cuda")
+        whole[1:] = d[n]
+        d[n] = whole[1:]
+    out, lse, *_ = run(p, d)
+    check(p, out, lse)
+
+
+@pytest.mark.parametrize("kw", [DECODE[3], VERIFY[1], APPEND[0]])
+def test_negative_tensor_scales(kw):
+    """The sign of a tensor scale is part of the value."""
+    p = make(25, **kw)
+    p.k_scale, p.v_scale = p.k_scale ^ 0x8000, p.v_scale ^ 0x8000
+    out, lse, *_ = run(p)
+    check(p, out, lse)
+
+
+@pytest.mark.parametrize("kw", [DECODE[2], VERIFY[0], APPEND[0]])
+def test_workspace_of_one_plan_in_two_graphs(pa, kw):
+    """Two captured graphs share a plan's workspace: replayed one after the other,
+    each gives its own queries' result."""
+    p = make(26, **kw)
+    ds = [device(p), device(p)]
+    other = bf16_bits(np.random.default_rng(3).standard_normal(p.q_bits.shape))
+    ds[1]["q"].copy_(torch.from_numpy(other.view(np.int16)).view(torch.bfloat16))
+    plan = plan_of(pa, p)
+    ws = workspace(plan)
+    pa.pa_plan_upload(plan, ws)
+    graphs = []
+    for d in ds:
+        args = args_of(pa, d)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.pa_run(plan, args, ws)
+            pa.pa_merge(plan, args, ws)
+        graphs.append(g)
+    for k in (0, 1, 1, 0):
+        graphs[k].replay()
+    assert pa.pa_check(plan, ws)[0] == 0
+    for d, q in zip(ds, (p.q_bits, other)):
+        p.q_bits = q
+        check(p, d["out"].float().cpu().numpy().astype(np.float64), d["lse"].cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("kw", [DECODE[2], VERIFY[0], APPEND[0]])
+def test_bounded_wait_times_out_and_context_survives(pa, kw):
+    """The test hook skips the first copy: the waits run out, the run reports it, and
+    the next run is right."""
+    p = make(27, **kw)
+    d = device(p)
+    plan = plan_of(pa, p)
+    ws, args = workspace(plan), args_of(pa, d)
+    pa.pa_plan_upload(plan, ws)
+    pa.pa_debug_set_faults(wait_limit_ns=5_000_000, skip_first_load=True)
+    try:
+        pa.pa_run(plan, args, ws)
+        st, _ = pa.pa_check(plan, ws)
+    finally:
+        pa.pa_debug_set_faults(0, False)
+    assert st == pa.PA_ERR_DEVICE_TIMEOUT
+    out, lse, *_ = run(p, d)
+    check(p, out, lse)
+
+
 @pytest.mark.parametrize("sms", [1, 5])
 @pytest.mark.parametrize("kw", [DECODE[3], DECODE[6], VERIFY[0], APPEND[0]])
 def test_few_ctas_take_many_items(kw, sms):
@@ -106,8 +193,9 @@ def test_single_launch_option_leaves_4_bit_plans_alone(pa, kw):
     check(p, out, lse)
 
 
-@pytest.mark.parametrize("kw", [dict(seq_lens=[3, 4], seq_lens_kv=[61, 200], q_heads=4, kv_heads=2, chunk_size=64),
-                                dict(seq_lens=[6, 1], seq_lens_kv=[127, 0], q_heads=16, kv_heads=2)])
+@pytest.mark.parametrize("kw", [dict(seq_lens=[3, 4], seq_lens_kv=[61, 1150], q_heads=4, kv_heads=2),
+                                dict(seq_lens=[6, 1], seq_lens_kv=[127, 0], q_heads=16, kv_heads=2),
+                                dict(seq_lens=[6, 5], seq_lens_kv=[1021, 63], q_heads=16, kv_heads=2)])
 def test_tree_mask_with_rows_that_see_nothing_of_their_chunk(kw):
     p = make(18, **kw)
     M = int(p.seq_lens.max())
