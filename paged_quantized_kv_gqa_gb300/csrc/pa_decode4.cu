@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     const int it = slot[kItemWords];
     const int n_rows = m.ntok * G;
     const int nh = m.ntiles;   // half pages
-    float c_log2 = p.sm_scale_log2;
+    float c_log2 = p.sm_scale_log2 * kFold8<FP4>;
     if (p.scale_kind == PA_SCALE_GLOBAL) c_log2 *= reinterpret_cast<const float*>(p.k_scale)[0];
     else if (p.scale_kind == PA_SCALE_PER_KV_HEAD)
       c_log2 *= __bfloat162float(sc_smem ? ks_s[m.kvh] : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)[m.kvh]);
@@ -366,12 +366,13 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[b][j][e] = 0.f;
         uint4 kr[2];
-        uint32_t ksc[2][2];
+        uint32_t ksc[2][2], koff[2][2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = kpos<FP4>(b, g, h);
           kr[h] = *reinterpret_cast<const uint4*>(kst + r * (kV4Dim / 2) + 16 * t);
-          scale_pair(*reinterpret_cast<const uint16_t*>(kst + kV4Codes + r * kV4Nblk + 2 * t), ksc[h][0], ksc[h][1]);
+          scale_pair_fold8<FP4>(*reinterpret_cast<const uint16_t*>(kst + kV4Codes + r * kV4Nblk + 2 * t), ksc[h],
+                                koff[h]);
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -380,8 +381,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           codes8<FP4>(word_of(kr[1], w), c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            a[i] = scaled<FP4>(a[i], ksc[0][w >> 1], i);
-            c[i] = scaled<FP4>(c[i], ksc[1][w >> 1], i);
+            a[i] = scaled_fold8<FP4>(a[i], ksc[0][w >> 1], koff[0][w >> 1][i & 1]);
+            c[i] = scaled_fold8<FP4>(c[i], ksc[1][w >> 1], koff[1][w >> 1][i & 1]);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -404,7 +405,18 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         keep_scales(sw, left);
         uint32_t f[4];
         scales8<FP4>(sw, f);
-        __syncwarp();
+        if constexpr (!FP4) {
+          uint32_t e0, e2, unused;
+          fold8(f[0], f[0], e0, unused);
+          fold8(f[2], f[2], e2, unused);
+          uint32_t o1, o3;
+          fold8(f[1], f[1], unused, o1);
+          fold8(f[3], f[3], unused, o3);
+          __syncwarp();
+          *reinterpret_cast<uint4*>(vs16 + kV4Nblk * kV4Half + g * kV4Half + 8 * t) = make_uint4(e0, o1, e2, o3);
+        } else {
+          __syncwarp();
+        }
         *reinterpret_cast<uint4*>(vs16 + g * kV4Half + 8 * t) = make_uint4(f[0], f[1], f[2], f[3]);
       }
 
@@ -488,13 +500,15 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         codes8<FP4>(*reinterpret_cast<const uint32_t*>(vst + (16 * d + g) * (kV4Half / 2) + 4 * t), a);
         codes8<FP4>(*reinterpret_cast<const uint32_t*>(vst + (16 * d + g + 8) * (kV4Half / 2) + 4 * t), c);
         const uint4 sv = *reinterpret_cast<const uint4*>(vs16 + d * kV4Half + 8 * t);
+        uint4 nv = sv;
+        if constexpr (!FP4) nv = *reinterpret_cast<const uint4*>(vs16 + kV4Nblk * kV4Half + d * kV4Half + 8 * t);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t x[4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            x[2 * i] = scaled<FP4>(a[2 * b + i], word_of(sv, 2 * b + i), 2 * b + i);
-            x[2 * i + 1] = scaled<FP4>(c[2 * b + i], word_of(sv, 2 * b + i), 2 * b + i);
+            x[2 * i] = scaled_fold8<FP4>(a[2 * b + i], word_of(sv, 2 * b + i), word_of(nv, 2 * b + i));
+            x[2 * i + 1] = scaled_fold8<FP4>(c[2 * b + i], word_of(sv, 2 * b + i), word_of(nv, 2 * b + i));
           }
 #pragma unroll
           for (int j = 0; j < NB; ++j) mma_16816(o[j][d], x[0], x[1], x[2], x[3], pb[b][j][0], pb[b][j][1]);
@@ -520,11 +534,11 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     // 8 ((r >> 1) & 3): no bank conflicts) and leave as 16-byte pieces.
     const bool final_row = m.nch == 1;
     const bool per_channel = p.scale_kind == PA_SCALE_PER_CHANNEL;
-    const float vs_head = p.scale_kind == PA_SCALE_GLOBAL ? reinterpret_cast<const float*>(p.v_scale)[0]
+    const float vs_head = kFold8<FP4> * (p.scale_kind == PA_SCALE_GLOBAL ? reinterpret_cast<const float*>(p.v_scale)[0]
                           : p.scale_kind == PA_SCALE_PER_KV_HEAD
                               ? __bfloat162float(sc_smem ? vs_s[m.kvh]
                                                          : reinterpret_cast<const __nv_bfloat16*>(p.v_scale)[m.kvh])
-                              : 1.f;
+                              : 1.f);
     const __nv_bfloat16* vsc = (sc_smem ? vs_s : reinterpret_cast<const __nv_bfloat16*>(p.v_scale)) +
                                (per_channel ? m.kvh * kV4Dim : 0);
     float inv[NB][2];

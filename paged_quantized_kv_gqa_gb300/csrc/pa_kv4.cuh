@@ -145,4 +145,51 @@ __device__ __forceinline__ void scale_pair(uint16_t b, uint32_t& s0, uint32_t& s
   s1 = __byte_perm(h, h, 0x3232);
 }
 
+// One instruction instead of scaled()'s two, where a scale serves enough codes to
+// pay for its constants: (2^k + code + 8) * (s / 8) - (2^k + 8) * (s / 8) as one
+// fused multiply-add.  Exact for int4: the offset's product is 129 s or 9 s, at
+// most 11 significant bits below 57800, and the result is code * s / 8.  The
+// caller multiplies what it sums by kFold8.
+template <int FP4>
+constexpr float kFold8 = FP4 ? 1.f : 8.f;
+
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// f16x2 of scales -> s / 8 and the offsets of codes8's even and odd words
+__device__ __forceinline__ void fold8(uint32_t h, uint32_t& s, uint32_t& n_even, uint32_t& n_odd) {
+  s = mul_h2(h, 0x30003000u);        // 1 / 8
+  n_even = mul_h2(h, 0xD808D808u);   // -129
+  n_odd = mul_h2(h, 0xC880C880u);    // -9
+}
+
+template <int FP4>
+__device__ __forceinline__ uint32_t scaled_fold8(uint32_t x, uint32_t s, uint32_t n) {
+  if constexpr (FP4) return mul_h2(x, s);
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(s), "r"(n));
+  return r;
+}
+
+// Two E4M3 scales -> per scale, as words of two equal halves: what scaled_fold8
+// takes (FP4: the scale alone).
+template <int FP4>
+__device__ __forceinline__ void scale_pair_fold8(uint16_t b, uint32_t (&s)[2], uint32_t (&n)[2][2]) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
+  if constexpr (!FP4) {
+    uint32_t e, o;
+    fold8(h, h, e, o);
+    n[0][0] = __byte_perm(e, e, 0x1010);
+    n[0][1] = __byte_perm(o, o, 0x1010);
+    n[1][0] = __byte_perm(e, e, 0x3232);
+    n[1][1] = __byte_perm(o, o, 0x3232);
+  }
+  s[0] = __byte_perm(h, h, 0x1010);
+  s[1] = __byte_perm(h, h, 0x3232);
+}
+
 }  // namespace pa
