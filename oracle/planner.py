@@ -39,17 +39,19 @@ Spec:
   merge_tokens = tokens with nch_token != 1, ascending (those with 0 chunks are
   the rows that see nothing; the merge writes them).
   A 4-bit cache, decode family: chunk_size is ignored; no split while the largest
-  lim is at most 8 * B, else shares of equal work per
+  lim is at most 8 * B, else shares of about equal cost per
   worker, w workers per CTA: 16 warps if max(q_len) * G <= 16, else the smallest
-  w in 1 .. 4 with slots * w divisible by kv_heads (4 if none).  The tiles' pages
-  are numbered as for MLA below; quota = max(2 (warps) or 8, ceil(total / max(1,
-  slots * w // kv_heads))); share k covers pages
-  [k*quota, (k+1)*quota); its pieces are its overlaps with the tiles, numbered
-  per tile.  Lanes (share, kv head), share-major, are dealt to num_ctas =
+  w in 1 .. 4 with slots * w divisible by kv_heads (4 if none).  A piece (a range
+  of one tile's positions) costs its half pages (B / 2 positions) plus a start: 2
+  for warps, which cut at half pages, 12 for CTAs, which cut at pages.  Shares are
+  filled in tile order: a new one begins where less than start + 2 is left of the
+  quota; a piece takes what the tile and the quota have left.  The quota is the
+  least, from start + 4 (warps) or start + 16 on, found by bisection, that gives at
+  most max(1, slots * w // kv_heads) shares.  Pieces are numbered per tile.  Lanes (share, kv head), share-major, are dealt to num_ctas =
   min(slots, #lanes) CTAs: CTA c takes lanes [c*L // num_ctas, (c+1)*L //
   num_ctas); its items (lane order, a share's pieces in tile order) are sorted by
-  length descending, ties in that order.  chunk (as reported) = quota * B if
-  some tile has more than one piece, else 0.
+  length descending, ties in that order.  chunk (as reported) = the longest piece
+  (in whole units of the cut) if some tile has more than one, else 0.
   MLA with chunk_size = -1 replaces the chunk size and the longest-first
   deal by contiguous shares (this library's scheduling choice; the pages fix
   only what an item computes): the tiles' pages, ceil(lim / B) per tile,
@@ -152,23 +154,45 @@ def plan(p, num_sms: int) -> dict:
 
 
 def _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, warps):
-    """Equal shares of the pages per worker (the 4-bit decode rule in the spec above)."""
+    """Shares of about equal cost per worker (the 4-bit decode rule in the spec above)."""
     w = 16 if warps else next((k for k in (1, 2, 3) if slots * k % p.kv_heads == 0), 4)
-    npages = [math.ceil(t[3] / B) for t in tiles]
-    start = [sum(npages[:i]) for i in range(len(tiles))]
-    total = sum(npages)
-    quota = max(2 if warps else 8, math.ceil(total / max(1, slots * w // p.kv_heads)))
-    shares = math.ceil(total / quota)
+    groups = max(1, slots * w // p.kv_heads)
+    unit, per_unit, start, least = (B // 2, 1, 2, 4) if warps else (B, 2, 12, 16)
+
+    def fill(quota):
+        """Shares as lists of (tile, first position, end), each of cost <= quota."""
+        out, used = [], quota
+        for i, t in enumerate(tiles):
+            at = 0
+            while at < t[3]:
+                if quota - used < start + 2:
+                    out.append([])
+                    used = 0
+                n = min(math.ceil((t[3] - at) / unit), (quota - used - start) // per_unit)
+                out[-1].append((i, at, min(t[3], at + n * unit)))
+                used += start + per_unit * n
+                at += n * unit
+        return out
+
+    low = start + least
+    high = low + sum(start + per_unit * math.ceil(t[3] / unit) for t in tiles)
+    while low < high:                      # the least quota with enough workers
+        mid = low + (high - low) // 2
+        if len(fill(mid)) <= groups:
+            high = mid
+        else:
+            low = mid + 1
+    cut = fill(low)
+    shares = len(cut)
+    longest = max((math.ceil((e - a) / unit) * unit for m in cut for _, a, e in m), default=0)
     pieces, count = [], [0] * len(tiles)
-    for k in range(shares):
+    for m in cut:
         mine = []
-        for i, (b, tok0, tok1, lim) in enumerate(tiles):
-            lo, hi = max(k * quota, start[i]), min((k + 1) * quota, start[i] + npages[i])
-            if lo < hi:
-                base = slkv[b] if cross else slkv[b] + tok0 if p.causal else slkv[b] + q_lens[b]
-                mine.append((i, b, cu[b] + tok0, tok1 - tok0, base, (lo - start[i]) * B,
-                             min(lim, (hi - start[i]) * B), count[i]))
-                count[i] += 1
+        for i, a, e in m:
+            b, tok0, tok1, _ = tiles[i]
+            base = slkv[b] if cross else slkv[b] + tok0 if p.causal else slkv[b] + q_lens[b]
+            mine.append((i, b, cu[b] + tok0, tok1 - tok0, base, a, e, count[i]))
+            count[i] += 1
         pieces.append(mine)
     lanes = [(k, h) for k in range(shares) for h in range(p.kv_heads)]
     L = len(lanes)
@@ -185,7 +209,7 @@ def _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, warps):
     for i, (b, tok0, tok1, _) in enumerate(tiles):
         nch_token[cu[b] + tok0:cu[b] + tok1] = count[i]
     arr = np.array(rows, dtype=np.int64).reshape(-1, 8).astype(np.int32)
-    return dict(family="decode", chunk=quota * B if max(count, default=0) > 1 else 0, tokens_per_tile=tpt,
+    return dict(family="decode", chunk=longest if max(count, default=0) > 1 else 0, tokens_per_tile=tpt,
                 num_ctas=num_ctas, items=arr, work_indptr=indptr, nch_token=nch_token,
                 max_chunks=int(max(1, nch_token.max() if T else 1)),
                 merge_tokens=np.nonzero(nch_token != 1)[0].astype(np.int32))

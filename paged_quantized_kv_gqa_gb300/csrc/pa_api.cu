@@ -156,10 +156,11 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   const bool decode4 = P.four_bit() && P.family == PA_FAMILY_DECODE;
   if (decode4 && longest > (int64_t)kDecode4WholePages * B) {
     // 4-bit decode: the pages of all tiles, tile after tile, are cut into shares
-    // of `quota` pages, so that every worker of the grid has the same work and few
-    // partial states are merged.  A worker is a warp (at most 16 rows: a warp takes
+    // of about equal cost, so that every worker of the grid has the same work and
+    // few partial states are merged.  A worker is a warp (at most 16 rows: a warp takes
     // whole items) or a CTA (the tensor-memory kernel, where every new item costs
-    // about three tiles: 5064 items of 1024 positions took 450 us, 430 shares 327).
+    // about three tiles: cut every 1024 positions, 32 prefixes of up to 32k took a
+    // third longer than in shares).
     // A share's pieces (its overlaps with the tiles) are run for every kv head;
     // the (share, kv head) lanes are dealt to the CTAs in runs of equal length,
     // each CTA's items longest first.
@@ -168,42 +169,61 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     int per_cta = kDecode4Warps;
     if (!by_warp)
       for (per_cta = 1; per_cta < 4 && slots * per_cta % prob.kv_heads != 0;) ++per_cta;
-    std::vector<int64_t> first_page(tiles.size() + 1, 0);
-    for (size_t i = 0; i < tiles.size(); ++i)
-      first_page[i + 1] = first_page[i] + ceil_div(tiles[i].lim, (int64_t)B);
-    const int64_t total = first_page.back();
     const int64_t groups = std::max<int64_t>(1, (int64_t)slots * per_cta / prob.kv_heads);
-    const int64_t quota = std::max<int64_t>(by_warp ? kDecode4MinPages : kDecode4MinTiles * 2,
-                                            ceil_div(total, groups));
-    const int64_t shares = ceil_div(total, quota), lanes = shares * prob.kv_heads;
+    // A piece costs its half pages and its start and end.  The shares are filled in
+    // order up to a cost of `quota`, the least that needs no more shares than there
+    // are workers.  Warps cut at half pages, CTAs at pages.
+    const int64_t unit = by_warp ? B / 2 : B, per_unit = by_warp ? 1 : 2;
+    const int64_t start = by_warp ? kDecode4ItemCost : kDecode4TileCost;
+    std::vector<int32_t> share_pieces, nch;   // pieces of each share, as item records
+    std::vector<int64_t> share_at;
+    int64_t longest_piece = 0;
+    auto fill = [&](int64_t quota, bool emit) -> int64_t {
+      int64_t shares = 0, used = quota;
+      for (size_t i = 0; i < tiles.size(); ++i) {
+        const Tile& t = tiles[i];
+        const int64_t n = ceil_div(t.lim, unit);
+        for (int64_t u0 = 0; u0 < n;) {
+          if (quota - used < start + 2) {   // no room for a page
+            if (emit) share_at.push_back((int64_t)(share_pieces.size() / kItemWords));
+            ++shares;
+            used = 0;
+          }
+          const int64_t u1 = std::min(n, u0 + (quota - used - start) / per_unit);
+          if (emit) {
+            const int64_t base = (int64_t)slkv[t.b] + (causal ? t.tok0 : cross ? 0 : ql[t.b]);
+            const int32_t rec[kItemWords] = {t.b, (int32_t)i, cu[t.b] + t.tok0, t.tok1 - t.tok0, (int32_t)base,
+                                             (int32_t)(u0 * unit), (int32_t)std::min(t.lim, u1 * unit), nch[i]++};
+            share_pieces.insert(share_pieces.end(), rec, rec + kItemWords);
+            longest_piece = std::max(longest_piece, (u1 - u0) * unit);
+          }
+          used += start + per_unit * (u1 - u0);
+          u0 = u1;
+        }
+      }
+      return shares;
+    };
+    int64_t quota = start + 2 * (by_warp ? kDecode4MinPages : kDecode4MinTiles * 2);
+    int64_t enough = quota;   // one share
+    for (const auto& t : tiles) enough += start + per_unit * ceil_div(t.lim, unit);
+    while (quota < enough) {
+      const int64_t mid = quota + (enough - quota) / 2;
+      if (fill(mid, false) <= groups) enough = mid;
+      else quota = mid + 1;
+    }
+    nch.assign(tiles.size(), 0);
+    const int64_t shares = fill(quota, true), lanes = shares * prob.kv_heads;
+    share_at.push_back((int64_t)(share_pieces.size() / kItemWords));
     if (lanes > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "too many work items");
     P.num_ctas = (int)std::min<int64_t>(slots, lanes);
     P.nch_token.assign(P.total_q, 0);
-    std::vector<int32_t> share_pieces, nch(tiles.size(), 0);   // pieces of each share, as item records
-    std::vector<int64_t> share_at(shares + 1, 0);
-    size_t i0 = 0;
-    for (int64_t k = 0; k < shares; ++k) {
-      const int64_t a = k * quota, e = std::min(total, a + quota);
-      while (first_page[i0 + 1] <= a) ++i0;
-      for (size_t i = i0; i < tiles.size() && first_page[i] < e; ++i) {
-        if (first_page[i + 1] <= a || first_page[i + 1] == first_page[i]) continue;
-        const Tile& t = tiles[i];
-        const int64_t kv0 = (std::max(a, first_page[i]) - first_page[i]) * B;
-        const int64_t kv1 = std::min<int64_t>(t.lim, (std::min(e, first_page[i + 1]) - first_page[i]) * B);
-        const int64_t base = (int64_t)slkv[t.b] + (causal ? t.tok0 : cross ? 0 : ql[t.b]);
-        const int32_t rec[kItemWords] = {t.b, (int32_t)i, cu[t.b] + t.tok0, t.tok1 - t.tok0, (int32_t)base,
-                                         (int32_t)kv0, (int32_t)kv1, nch[i]++};
-        share_pieces.insert(share_pieces.end(), rec, rec + kItemWords);
-      }
-      share_at[k + 1] = (int64_t)(share_pieces.size() / kItemWords);
-    }
     bool any_split = false;
     for (size_t i = 0; i < tiles.size(); ++i) {
       if (nch[i] > 0xFFFF) return fail(PA_ERR_UNSUPPORTED, "too many chunks per row");
       any_split = any_split || nch[i] > 1;
       for (int tok = tiles[i].tok0; tok < tiles[i].tok1; ++tok) P.nch_token[cu[tiles[i].b] + tok] = nch[i];
     }
-    P.chunk = any_split ? (int32_t)(quota * B) : 0;
+    P.chunk = any_split ? (int32_t)longest_piece : 0;
     P.work_indptr.assign(P.num_ctas + 1, 0);
     P.items.clear();
     std::vector<std::pair<int64_t, int32_t>> mine;   // (piece, kv head) of a CTA

@@ -141,17 +141,17 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   for (int idx = threadIdx.x; idx < n_staged * kBtStride; idx += blockDim.x) {
     const int32_t* rec = items_s + (idx / kBtStride) * kItemWords;
     const int k = idx % kBtStride;
-    const int kv0 = rec[5];
-    const int np = (rec[6] - kv0 + kPage - 1) / kPage;
-    const int nb = p.max_blocks - kv0 / kPage;
-    bt_s[idx] = k < np && k < nb ? p.block_table[(int64_t)rec[0] * p.max_blocks + kv0 / kPage + k] : -1;
+    const int pg0 = rec[5] / kPage;
+    const int np = (rec[6] + kPage - 1) / kPage - pg0;
+    const int nb = p.max_blocks - pg0;
+    bt_s[idx] = k < np && k < nb ? p.block_table[(int64_t)rec[0] * p.max_blocks + pg0 + k] : -1;
   }
   __syncthreads();
 
   // -------------------------------------------------------------- load side
   // warp-uniform cursor over this warp's half pages; the next item is taken
   // when the current one's last half page is issued
-  int cur_it = -1, cur_b = 0, cur_kvh = 0, cur_kv0 = 0, cur_nh = 0, cur_h = 0;
+  int cur_it = -1, cur_b = 0, cur_kvh = 0, cur_pg0 = 0, cur_nh = 0, cur_h = 0;   // from page cur_pg0 on
   int cur_bt = -1, nxt_bt = -1;       // lane k: page id of page 32 * batch + k of the item
   int pend_it = -1, pend_rec = 0, pend_bt = -1;
   // Q rows of a taken item, read several half pages before they are needed;
@@ -179,9 +179,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   const bool skip_hook = p.skip_first_load && blockIdx.x == 0;   // failure-detection test hook
   uint32_t skipped_n = 0xFFFFFFFFu;
 
-  auto bt_at = [&](int b, int kv0, int pg) -> int {
-    const int np = p.max_blocks - kv0 / kPage;
-    return pg < np ? p.block_table[(int64_t)b * p.max_blocks + kv0 / kPage + pg] : -1;
+  auto bt_at = [&](int b, int pg0, int pg) -> int {
+    return pg < p.max_blocks - pg0 ? p.block_table[(int64_t)b * p.max_blocks + pg0 + pg] : -1;
   };
   auto take_pending = [&]() {
     int it = 0;
@@ -193,11 +192,11 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       if (lane < kItemWords)
         pend_rec = k < n_staged ? items_s[k * kItemWords + lane] : p.items[(int64_t)pend_it * kItemWords + lane];
       const int b = __shfl_sync(0xffffffffu, pend_rec, 0);
-      const int kv0 = __shfl_sync(0xffffffffu, pend_rec, 5);
+      const int pg0 = __shfl_sync(0xffffffffu, pend_rec, 5) / kPage;
       const int kv1 = __shfl_sync(0xffffffffu, pend_rec, 6);
-      const int np = (kv1 - kv0 + kPage - 1) / kPage;
+      const int np = (kv1 + kPage - 1) / kPage - pg0;
       if (k < n_staged && np <= kBtStride) pend_bt = lane < np ? bt_s[k * kBtStride + lane] : -1;
-      else pend_bt = lane < np ? bt_at(b, kv0, lane) : -1;
+      else pend_bt = lane < np ? bt_at(b, pg0, lane) : -1;
       if (qpre_it < 0) {   // the previous prefetch has been used
         load_q_rows(qpre, __shfl_sync(0xffffffffu, pend_rec, 2), __shfl_sync(0xffffffffu, pend_rec, 3),
                     __shfl_sync(0xffffffffu, pend_rec, 1));
@@ -213,12 +212,13 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       cur_it = pend_it;
       cur_b = __shfl_sync(0xffffffffu, pend_rec, 0);
       cur_kvh = __shfl_sync(0xffffffffu, pend_rec, 1);
-      cur_kv0 = __shfl_sync(0xffffffffu, pend_rec, 5);
+      const int kv0 = __shfl_sync(0xffffffffu, pend_rec, 5);
       const int kv1 = __shfl_sync(0xffffffffu, pend_rec, 6);
-      cur_nh = (kv1 - cur_kv0 + kV4Half - 1) / kV4Half;
-      cur_h = 0;
+      cur_pg0 = kv0 / kPage;
+      cur_nh = (kv1 + kV4Half - 1) / kV4Half - 2 * cur_pg0;
+      cur_h = kv0 / kV4Half - 2 * cur_pg0;   // a piece may begin with a second half
       cur_bt = pend_bt;
-      nxt_bt = (lane + 32) * 2 < cur_nh ? bt_at(cur_b, cur_kv0, 32 + lane) : -1;
+      nxt_bt = (lane + 32) * 2 < cur_nh ? bt_at(cur_b, cur_pg0, 32 + lane) : -1;
       int32_t* slot = rec_ring + (k_load % kRing) * 12;   // the record for the compute side
       if (lane < kItemWords) slot[lane] = pend_rec;
       if (lane == kItemWords) slot[kItemWords] = cur_it;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     } else if ((cur_h & 63) == 0) {
       cur_bt = nxt_bt;
       const int pg = (cur_h >> 1) + 32 + lane;
-      nxt_bt = pg * 2 < cur_nh ? bt_at(cur_b, cur_kv0, pg) : -1;
+      nxt_bt = pg * 2 < cur_nh ? bt_at(cur_b, cur_pg0, pg) : -1;
     }
     const int page = __shfl_sync(0xffffffffu, cur_bt, (cur_h >> 1) & 31);
     if (lane == 0 && !skip_copy) {

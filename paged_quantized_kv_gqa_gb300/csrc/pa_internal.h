@@ -24,6 +24,14 @@ constexpr int kDecode4Warps = 16;    // warps of a 4-bit decode CTA (each takes 
 constexpr int kDecode4WholePages = 8;
 constexpr int kDecode4MinPages = 2;  // smallest share of a warp
 constexpr int kDecode4MinTiles = 4;  // smallest share of a tensor-memory CTA, 128-position tiles
+// What starting and ending a piece costs, in half pages of a warp and of a CTA.
+// With shares of equal pages (cost 0) the warps with the most pieces finished last:
+// 24 sequences of up to 3k positions 22.0 us, at 2 to 4 20.6; 57 of up to 2k (one
+// row, int4) 44.5, at 2 and 3 40.5, at 4 42.9; 64 of up to 4k 49.3, at 2 47.0, at 3
+// and 4 49.3 (the cuts fall badly); CTAs: 6 drafts after 32 prefixes of up to 32k
+// positions 311.6, at 8 308.9, at 12 and 16 308.0.
+constexpr int kDecode4ItemCost = 2;
+constexpr int kDecode4TileCost = 12;
 constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache
 constexpr int kStatusBytes = 256;    // status block at the start of the workspace
 constexpr int64_t kDefaultWaitNs = 2000000000LL;

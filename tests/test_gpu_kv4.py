@@ -158,6 +158,17 @@ def test_few_ctas_take_many_items(kw, sms):
     check(p, out, lse)
 
 
+@pytest.mark.parametrize("kv_heads, kv", [(4, [9001, 4032]), (8, [90, 9170])])
+def test_pieces_begin_with_a_second_half_page(kv_heads, kv):
+    """One CTA, so that the pieces run over more pages than a warp looks up at once."""
+    p = make(31, seq_lens=[1, 1], seq_lens_kv=kv, q_heads=16, kv_heads=kv_heads)
+    out, lse, _, plan = run(p, sms=1)
+    it = np.asarray(plan.describe()["items"])
+    odd = it[it[:, 5] % 64 == 32]
+    assert len(odd) and (odd[:, 6] - odd[:, 5]).max() > 32 * 64
+    check(p, out, lse)
+
+
 def test_more_items_than_a_cta_keeps_records_of():
     """One CTA, 700 items of one or two pages, and one of 40 pages."""
     p = make(14, seq_lens=[1] * 351, seq_lens_kv=[2500] + [70] * 350, q_heads=4, kv_heads=2)
