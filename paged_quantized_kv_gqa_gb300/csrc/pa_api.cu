@@ -168,7 +168,7 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     // CTA workers: lanes per CTA, so that the kv heads divide the lanes (else 4)
     int per_cta = kDecode4Warps;
     if (!by_warp)
-      for (per_cta = 1; per_cta < 4 && slots * per_cta % prob.kv_heads != 0;) ++per_cta;
+      for (per_cta = 1; per_cta < 4 && (int64_t)slots * per_cta % prob.kv_heads != 0;) ++per_cta;
     const int64_t groups = std::max<int64_t>(1, (int64_t)slots * per_cta / prob.kv_heads);
     // A piece costs its half pages and its start and end.  The shares are filled in
     // order up to a cost of `quota`, the least that needs no more shares than there

@@ -1,5 +1,9 @@
 """GPU parity of the 4-bit cache with the float64 oracle: attention of every
 family, cross attention, quantise-and-write, and reading back."""
+import importlib.util
+import os
+import subprocess
+import sys
 import types
 
 import numpy as np
@@ -15,6 +19,8 @@ from kv4_helpers import (KINDS, SCALES, args_of, bf16_bits, check, device, make,
                          workspace)
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -509,3 +515,17 @@ def test_built_in_workspace(pa):
     d = device(p)
     pa.pa_run_static(plan_of(pa, p), args_of(pa, d), check=True)
     check(p, d["out"].float().cpu().numpy().astype(np.float64), d["lse"].cpu().numpy().astype(np.float64))
+
+
+def test_debug_library_cases():
+    spec = importlib.util.spec_from_file_location(
+        "pa_build_for_kv4_debug_test", os.path.join(ROOT, "paged_quantized_kv_gqa_gb300", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.build(debug=True)
+    env = dict(os.environ, PA_GB300_DEBUG="1")
+    env.pop("PA_GB300_TRACE", None)
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "tests", "debug_kv4_cases.py")], env=env,
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-4000:]
+    assert "all 4-bit cases passed" in r.stdout
