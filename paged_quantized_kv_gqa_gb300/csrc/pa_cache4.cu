@@ -57,7 +57,7 @@ struct Append4Params {
   int32_t num_pages;
   int32_t kv_heads;
   int32_t scale_kind;
-  int32_t units;       // units an appended range can touch
+  RowUnits units;
   int32_t vec;         // rows may be read with 16-byte loads
   uint32_t total;      // (sequence, unit, kv head, side) warps
 };
@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_append4_kernel(const
   const int side = id & 1;
   const uint32_t bu = (id >> 1) / (uint32_t)p.kv_heads;
   const int kvh = (int)((id >> 1) - bu * p.kv_heads);
-  const int b = (int)(bu / (uint32_t)p.units), u = (int)(bu % (uint32_t)p.units);
+  int b, u;
+  find_unit<U>(p.units, p.cu_seqlens_q, bu, lane, b, u);
   const int q = p.seq_lens[b];
   if (q <= 0) return;
   const int start = p.seq_lens_kv[b], end = start + q;
@@ -413,9 +414,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_append4_kernel(const
 }
 
 template <int U>
-cudaError_t launch_u(Append4Params& p, const pa_problem& pr, int max_q, cudaStream_t stream) {
-  p.units = (max_q + U - 2) / U + 1;   // at most this many units are touched by a range of max_q positions
-  const double total = 2.0 * pr.bsz * p.units * pr.kv_heads;
+cudaError_t launch_u(Append4Params& p, const Plan& plan, cudaStream_t stream) {
+  const pa_problem& pr = plan.prob;
+  p.units = row_units<U>(pr.bsz, plan.max_q, plan.total_q);
+  const double total = 2.0 * p.units.count * pr.kv_heads;
   if (total > (double)INT32_MAX) return cudaErrorInvalidValue;
   p.total = (uint32_t)total;
   const dim3 grid((p.total + kWarps - 1) / kWarps), block(kWarps * 32);
@@ -459,8 +461,8 @@ cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void*
   // Units of 32 positions; of 8 while those would leave most of the GPU's warps
   // without one (the time of a small call is one warp's walk through its unit)
   return 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms
-             ? launch_u<8>(p, pr, plan.max_q, stream)
-             : launch_u<32>(p, pr, plan.max_q, stream);
+             ? launch_u<8>(p, plan, stream)
+             : launch_u<32>(p, plan, stream);
 }
 
 }  // namespace pa

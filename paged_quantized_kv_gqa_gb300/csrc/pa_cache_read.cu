@@ -38,7 +38,7 @@ struct ReadParams {
   int32_t kv_heads;
   int32_t head_dim;
   int32_t scale_kind;
-  int32_t units;       // units a range can touch
+  RowUnits units;
   int32_t sides;       // 2 (K, V) or 1 (MLA)
   int32_t vec;         // rows may be written with 16-byte stores
   uint32_t total;      // (sequence, unit, kv head, side) warps
@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const ReadParam
   const int side = (int)(id - rest * p.sides);
   const uint32_t bu = rest / (uint32_t)p.kv_heads;
   const int kvh = (int)(rest - bu * p.kv_heads);
-  const int b = (int)(bu / (uint32_t)p.units), u = (int)(bu % (uint32_t)p.units);
+  int b, u;
+  find_unit<U>(p.units, p.cu_seqlens_q, bu, lane, b, u);
   const int q = p.seq_lens[b];
   if (q <= 0) return;
   const int start = p.seq_lens_kv[b], end = start + q;
@@ -296,9 +297,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const ReadParam
 }
 
 template <int KV, int U>
-cudaError_t launch_u(ReadParams& p, const pa_problem& pr, int max_q, cudaStream_t stream) {
-  p.units = (max_q + U - 2) / U + 1;   // at most this many units are touched by a range of max_q positions
-  const double total = (double)p.sides * pr.bsz * p.units * pr.kv_heads;
+cudaError_t launch_u(ReadParams& p, const Plan& plan, cudaStream_t stream) {
+  p.units = row_units<U>(plan.prob.bsz, plan.max_q, plan.total_q);
+  const double total = (double)p.sides * p.units.count * plan.prob.kv_heads;
   if (total > (double)INT32_MAX) return cudaErrorInvalidValue;
   p.total = (uint32_t)total;
   const uint32_t blocks = (p.total + kWarps - 1) / kWarps;
@@ -312,8 +313,8 @@ cudaError_t launch_u(ReadParams& p, const pa_problem& pr, int max_q, cudaStream_
 template <int KV>
 cudaError_t launch_kv(ReadParams& p, const Plan& plan, cudaStream_t stream) {
   return (double)p.sides * plan.total_q * plan.prob.kv_heads / 32 < 4.0 * kWarps * plan.num_sms
-             ? launch_u<KV, 8>(p, plan.prob, plan.max_q, stream)
-             : launch_u<KV, 32>(p, plan.prob, plan.max_q, stream);
+             ? launch_u<KV, 8>(p, plan, stream)
+             : launch_u<KV, 32>(p, plan, stream);
 }
 
 }  // namespace

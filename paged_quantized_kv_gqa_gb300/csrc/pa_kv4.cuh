@@ -70,6 +70,49 @@ __device__ __forceinline__ float code4_to_f32(uint32_t c) {
   }
 }
 
+// The units of U positions that ranges of rows touch, for kernels with one warp per
+// unit (and kv head, and side).  Numbering them as bsz rectangles of the longest
+// range's count leaves most warps without work when one prompt is written beside
+// many single tokens (8192 rows beside 255 of 1, 8 kv heads: 418 us, with the other
+// numbering 18.2), but needs no search (writing 16 prompts of up to 4k rows: 67.7 us
+// for the pair of calls, 68.0 with it), so it is used up to twice the numbers of the
+// other.  That gives sequence b the numbers from cu[b] / U + 2 b on: a range of q
+// rows touches at most q / U + 2 units, whatever its start.  A warp finds its
+// sequence by a search of 32 ways a step (one step up to 32 sequences, two up to 1024).
+struct RowUnits {
+  int32_t per_seq;   // units of a rectangle; 0: by search
+  int32_t bsz;
+  int64_t count;     // numbers given out
+};
+
+template <int U>
+inline RowUnits row_units(int bsz, int max_q, int64_t total_q) {
+  const int per_seq = (max_q + U - 2) / U + 1;   // touched at most by a range of max_q rows
+  const int64_t rect = (int64_t)bsz * per_seq, by_rows = total_q / U + 2 * (int64_t)bsz;
+  return rect <= 2 * by_rows ? RowUnits{per_seq, bsz, rect} : RowUnits{0, bsz, by_rows};
+}
+
+// Unit number n -> sequence and unit of its range (a number may be past the range's
+// last unit); the whole warp calls it.
+template <int U>
+__device__ __forceinline__ void find_unit(const RowUnits& ru, const int32_t* cu, uint32_t n, int lane, int& b, int& u) {
+  if (ru.per_seq > 0) {
+    b = (int)(n / (uint32_t)ru.per_seq);
+    u = (int)(n - (uint32_t)b * (uint32_t)ru.per_seq);
+    return;
+  }
+  auto first = [&](int k) { return (uint32_t)cu[k] / U + 2u * (uint32_t)k; };
+  int lo = 0, hi = ru.bsz;   // first(lo) <= n < first(hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, k = lo + lane * step;
+    const int at = __popc(__ballot_sync(0xffffffffu, k < hi && first(k) <= n));   // true for the first lanes
+    lo += (max(at, 1) - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  b = lo;
+  u = (int)(n - first(lo));
+}
+
 // Eight codes of a word -> four fp16x2 words, in the order `codes8` defines:
 //   FP4   word i = codes (2i, 2i + 1): one hardware conversion per byte;
 //   int4  word i = codes (i, i + 4), as 1024 + (code + 8) for even i and

@@ -353,6 +353,10 @@ def placed(rows, how):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("kw", ROWS)
 def test_written_bytes_are_the_oracles(pa, kw, kind, scale_kind, how):
+    check_written(pa, kw, kind, scale_kind, how)
+
+
+def check_written(pa, kw, kind, scale_kind, how, sms=None):
     p = make(41, q_heads=kw["kv_heads"], kv_dtype=kind, scale_kind=scale_kind, **kw)
     p.k_new[0, 0, :4] = bf16_bits([np.nan, np.inf, -np.inf, 1.0])
     p.v_new[-1, -1, 16:20] = bf16_bits([np.nan, 3e38, 1e-38, -0.0])
@@ -360,7 +364,7 @@ def test_written_bytes_are_the_oracles(pa, kw, kind, scale_kind, how):
     d = device(p)
     k, stride, _ = placed(d["k_new"], how)
     v, _, _ = placed(d["v_new"], how)
-    plan = plan_of(pa, p)
+    plan = plan_of(pa, p, sms)
     ws = workspace(plan)
     pa.pa_plan_upload(plan, ws)
     pa.pa_cache_append(plan, args_of(pa, d), k, v, stride, ws)
@@ -376,11 +380,15 @@ def test_written_bytes_are_the_oracles(pa, kw, kind, scale_kind, how):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("kw", ROWS)
 def test_rows_read_back(pa, kw, kind, scale_kind, how):
+    check_read(pa, kw, kind, scale_kind, how)
+
+
+def check_read(pa, kw, kind, scale_kind, how, sms=None):
     p = make(42, q_heads=kw["kv_heads"], kv_dtype=kind, scale_kind=scale_kind, **kw)
     d = device(p)
     k, stride, kw_ = placed(torch.full_like(d["k_new"], 9.0), how)
     v, _, vw_ = placed(torch.full_like(d["v_new"], 9.0), how)
-    plan = plan_of(pa, p)
+    plan = plan_of(pa, p, sms)
     ws = workspace(plan)
     pa.pa_plan_upload(plan, ws)
     pa.pa_cache_read(plan, args_of(pa, d), k, v, stride, ws)
@@ -395,6 +403,24 @@ def test_rows_read_back(pa, kw, kind, scale_kind, how):
             assert bool((got[:, n:] == 9).all()) and bool((whole[:whole.numel() - got.numel()] == 9).all())
 
 
+# A plan for one SM takes units of 32 positions at these sizes; the first two sets number
+# their units by search (a long range beside single rows, empty ranges, more than 32).
+LONG_ROWS = [
+    dict(seq_lens=[1, 700, 0] + [1] * 40, seq_lens_kv=[5, 33, 7] + [29 + 3 * i for i in range(40)], kv_heads=2),
+    dict(seq_lens=[0] * 40 + [2, 600, 0, 31, 1], seq_lens_kv=[1] * 40 + [31, 0, 5, 32, 63], kv_heads=1),
+    dict(seq_lens=[200, 64, 97], seq_lens_kv=[0, 64, 31], kv_heads=4),
+]
+
+
+@pytest.mark.parametrize("sms", [1, None])
+@pytest.mark.parametrize("scale_kind", ["per_kv_head", "per_channel"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kw", LONG_ROWS)
+def test_long_and_mixed_rows(pa, kw, kind, scale_kind, sms):
+    check_written(pa, kw, kind, scale_kind, "plain", sms)
+    check_read(pa, kw, kind, scale_kind, "packed", sms)
+
+
 @pytest.mark.parametrize("kw", [
     dict(q_heads=8, kv_heads=2), dict(q_heads=8, kv_heads=2, scale_kind="per_channel"),
     dict(q_heads=8, kv_heads=2, kv_dtype="fp8_e4m3"),
@@ -403,9 +429,24 @@ def test_rows_read_back(pa, kw, kind, scale_kind, how):
     dict(q_heads=128, kv_heads=1, head_dim_qk=576, head_dim_v=512, layout="mla", scale_kind="global"),
 ])
 def test_8_bit_rows_read_back(pa, kw):
-    c = synth.make_case(name="r", seed=43, seq_lens=[70, 1, 0, 20], seq_lens_kv=[10, 63, 5, 0], **kw)
+    check_8_bit_read(pa, kw, [70, 1, 0, 20], [10, 63, 5, 0], 152)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_heads=8, kv_heads=2, scale_kind="per_channel"), dict(q_heads=8, kv_heads=2, kv_dtype="fp8_e4m3"),
+    dict(q_heads=128, kv_heads=1, head_dim_qk=576, head_dim_v=512, layout="mla", kv_dtype="fp8_e4m3",
+         scale_kind="global"),
+])
+@pytest.mark.parametrize("sms", [1, 152])
+def test_8_bit_long_and_mixed_rows_read_back(pa, kw, sms):
+    check_8_bit_read(pa, kw, [1, 700, 0] + [1] * 40, [5, 33, 7] + [29 + 3 * i for i in range(40)], sms)
+    check_8_bit_read(pa, kw, [300, 364], [0, 31], sms)
+
+
+def check_8_bit_read(pa, kw, q, kv, sms):
+    c = synth.make_case(name="r", seed=43, seq_lens=q, seq_lens_kv=kv, **kw)
     d = to_device(c)
-    plan = pa.pa_plan(pa.problem_of(c), c.seq_lens, c.seq_lens_kv, c.cu_seqlens_q, 152)
+    plan = pa.pa_plan(pa.problem_of(c), c.seq_lens, c.seq_lens_kv, c.cu_seqlens_q, sms)
     ws = workspace(plan)
     pa.pa_plan_upload(plan, ws)
     mla = c.layout == "mla"
