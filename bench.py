@@ -115,9 +115,9 @@ NCU_TRAFFIC = {
     # captured on the first 16 of the 128 sequences (726.5 MB of the 5443 MB
     # cache) and scaled by the KV-bytes ratio 7.4922: pages read and partial
     # states written both grow per sequence
-    "spec-verify-4": (("pa_decode.cu", "pa_index.cuh", "pa_merge.cuh"), "3545fe789aae18a8",
+    "spec-verify-4": (("pa_decode.cu", "pa_decode.cuh", "pa_index.cuh", "pa_kv4.cuh", "pa_merge.cuh"), "3545fe789aae18a8",
                       (729.481728e6 + 31.898112e6) * 7.492152264116904),
-    "append-3": (("pa_append.cu",), "a9cbfbb7a3133fa5", 72.280576e6 + 2.418432e6),
+    "append-3": (("pa_append.cu", "pa_append.cuh", "pa_kv4.cuh"), "a9cbfbb7a3133fa5", 72.280576e6 + 2.418432e6),
     "mla-5": (("pa_mla.cu",), "bdf0753cd25ebc74", 224.310784e6 + 6.930432e6),
 }
 

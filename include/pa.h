@@ -92,8 +92,9 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *   chunk_size > 0 splits the KV range into chunks of that many positions (a
  *   multiple of block_size); 0 never splits; -1 lets the planner choose.  Plans
  *   of the decode family over a 4-bit cache ignore it: the planner keeps ranges of
- *   at most 512 positions whole and otherwise cuts pieces of equal work, so
- *   pa_merge always belongs after pa_run there.
+ *   at most 512 positions whole and otherwise cuts pieces of equal cost, so
+ *   pa_merge always belongs after pa_run there (pa_workspace_size grows with the
+ *   query tokens times the pieces of the longest sequence).
  *   q_stride is the distance in elements between consecutive tokens of q
  *   (>= q_heads * head_dim_qk; FastDeploy's packed qkv uses
  *   (q_heads + 2 * kv_heads) * head_dim).

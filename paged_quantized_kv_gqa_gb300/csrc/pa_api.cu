@@ -74,7 +74,8 @@ static pa_status check_problem(const pa_problem& p) {
     if (p.scale_kind == PA_SCALE_GLOBAL && p.kv_dtype == PA_KV_INT8)
       ;  // allowed
     // TMA rows: 128 of 64 bytes per 8-bit V slab, 72 of 64 bytes per 4-bit slab
-    if ((int64_t)p.num_pages * p.kv_heads * 128 >= (int64_t)1 << 31)
+    const bool four = p.kv_dtype == PA_KV_INT4 || p.kv_dtype == PA_KV_FP4_E2M1;
+    if ((int64_t)p.num_pages * p.kv_heads * (four ? kSlab4 / 64 : 128) >= (int64_t)1 << 31)
       return fail(PA_ERR_UNSUPPORTED, "cache too large for 32-bit TMA row coordinates");
   } else {
     if (p.kv_dtype == PA_KV_INT4 || p.kv_dtype == PA_KV_FP4_E2M1)

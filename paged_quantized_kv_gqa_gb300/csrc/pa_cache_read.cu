@@ -8,8 +8,10 @@
 // 8 dims of a row, two rows per load and per store instruction.  V (transposed
 // in the cache): lane = 4 dims, whose positions it loads as runs of bytes, so
 // that a position's row of 256 bytes leaves as one 8-byte store per lane and no
-// transposition is needed.  Rows that are not aligned go position by position.  MLA rows: lane = 8 of 576 dims, three rounds a row.
-// What bounds it: the bytes, above all the 2 written per element.
+// transposition is needed.  Rows that are not aligned go position by position.  MLA rows:
+// lane = 8 of 576 dims, three rounds a row.
+// What bounds it: the bytes, above all the 2 written per element (88k rows of 8
+// heads, FP4, in 74.0 us: 0.92 of the copy bandwidth).
 #include "pa_common.cuh"
 #include "pa_kv4.cuh"
 

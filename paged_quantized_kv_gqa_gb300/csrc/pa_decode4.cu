@@ -16,9 +16,12 @@
 //   * O^T += V^T P^T: lane (g, t) holds positions 8 t .. 8 t + 7 of 16 dims, a
 //     32-bit word of codes each; a 16-dim MMA block is one scale block, so the
 //     scale pairs of the positions serve both rows of a lane.
-// What bounds it: 144 bytes a position and kv head, and per 32 positions about
-// 460 warp instructions (128 code pairs a lane, a conversion and a product
-// each), three fifths of the issue slots of the time that the bytes take.
+// A piece (a work item) may begin and end inside a page, at a half page.
+// What bounds it: 144 bytes a position and kv head, and per 32 positions about 600
+// (FP4) or 690 (int4) warp instructions for 128 code pairs a lane.  Long caches run
+// at four fifths of the copy bandwidth, held by the issue slots (two thirds of them
+// taken, the rest lost to dependences within four warps a scheduler); short ones by
+// what comes before a warp's first half page (item, page ids, copies: about 8 us).
 #include <cfloat>
 
 #include "pa_common.cuh"
@@ -37,9 +40,9 @@ constexpr float kTau = 8.0f;           // lazy rescale: P stays below 2^8
 template <int NB>
 struct D4Cfg {
   // Up to 8 rows: 16 warps of 128 registers, two stages each.  On 8 sequences of
-  // 33k-131k positions (64 / 8 heads, FP4) 8, 12 and 16 warps took 185, 162 and 158
-  // us, three stages instead of two 158; on 24 of up to 3k positions 21.1, 20.5 and
-  // 19.8 us, three stages 21.9 (they put more copies before a warp's first).
+  // 33k-131k positions (64 / 8 heads, FP4) 8, 12, 14 and 16 warps took 188, 164, 173
+  // and 157 us, one stage 177, 12 warps of three stages 161; on 24 of up to 3k
+  // positions 20.6, 18.0, 19.4 and 17.8 us, one stage 18.0, 12 warps of three 18.3.
   // 9 to 16 rows need twice the accumulators: 8 warps.
   static constexpr int kWarps = NB == 1 ? kDecode4Warps : 8;
   static constexpr int kStages = NB == 1 ? 2 : 3;
@@ -395,8 +398,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
 
       uint16_t* vs16 = reinterpret_cast<uint16_t*>(smem + (warp * C::kStages + st_comp) * kStage4);   // [8][32]
       // V scales as fp16, once per half page, over the K codes (every lane has read
-      // its own): lane (g, t) converts block g's
-      // positions 8t .. 8t+7, stored in the order their codes unpack to.
+      // its own): lane (g, t) converts block g's positions 8t .. 8t+7, stored in the
+      // order their codes unpack to (int4: a plane of offsets behind the scales).
       // Positions past the chunk's end get scale 0: their bytes may hold
       // anything, and a code is finite whatever it is.
       {

@@ -120,7 +120,7 @@ def test_cache_bytes(pa):
 
 @pytest.mark.parametrize("field,value,status", [
     ("kv_dtype", 4, 1), ("kv_dtype", -1, 1), ("causal", 3, 1), ("causal", -1, 1), ("head_dim_qk", 64, 2),
-    ("block_size", 32, 1), ("layout", 1, 2), ("num_pages", 1 << 23, 2), ("chunk_size", 96, 1),
+    ("block_size", 32, 1), ("layout", 1, 2), ("num_pages", 1 << 24, 2), ("chunk_size", 96, 1),
 ])
 def test_invalid_problems_rejected(pa, field, value, status):
     p = make(1, seq_lens=[2], seq_lens_kv=[10], q_heads=8, kv_heads=2)
@@ -131,6 +131,20 @@ def test_invalid_problems_rejected(pa, field, value, status):
     with pytest.raises(pa.PaError) as e:
         pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, 152)
     assert e.value.status == status
+
+
+def test_pools_up_to_the_tma_row_limit(pa):
+    """72 rows of 64 bytes a slab; 8-bit caches 128."""
+    p = make(1, seq_lens=[2], seq_lens_kv=[10], q_heads=8, kv_heads=2)
+    prob = problem(pa, p)
+    prob.num_pages = ((1 << 31) - 1) // (2 * 72)
+    pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, 152)
+    prob.num_pages += 1
+    with pytest.raises(pa.PaError):
+        pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, 152)
+    prob.num_pages, prob.kv_dtype = (1 << 31) // (2 * 128), pa.KV_DTYPES["int8"]
+    with pytest.raises(pa.PaError):
+        pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, 152)
 
 
 def test_mla_refuses_four_bits_and_cross(pa):

@@ -486,6 +486,51 @@ def test_row_calls_report_a_bad_page(pa, call):
         assert torch.equal(d["cache_k"], before)
 
 
+def far_pool(p, d):
+    """The case's pages at the end of a pool whose offsets pass 32 bits."""
+    slabs = (1 << 32) // 4608 + 1000
+    first = slabs // p.kv_heads - p.num_pages
+    for n in ("cache_k", "cache_v"):
+        pool = torch.empty((first + p.num_pages, p.kv_heads, 4608), dtype=torch.uint8, device="cuda")
+        pool[first:] = d[n].view(p.num_pages, p.kv_heads, 4608)
+        d[n] = pool
+    bt = d["block_table"]
+    d["block_table"] = torch.where(bt >= 0, bt + first, bt)
+    return first
+
+
+@pytest.mark.parametrize("kw", [DECODE[3], DECODE[6], VERIFY[0], APPEND[0]])
+def test_attention_over_a_pool_past_32_bits(kw):
+    p = make(32, **kw)
+    d = device(p)
+    p.num_pages += far_pool(p, d)
+    out, lse, *_ = run(p, d)
+    check(p, out, lse)
+
+
+def test_rows_of_a_pool_past_32_bits(pa):
+    p = make(33, seq_lens=[70, 3], seq_lens_kv=[40, 100], q_heads=8, kv_heads=2, kv_dtype="int4")
+    d = device(p)
+    n, first = p.num_pages, far_pool(p, d)
+    p.num_pages += first
+    plan = plan_of(pa, p)
+    ws = workspace(plan)
+    pa.pa_plan_upload(plan, ws)
+    pa.pa_cache_append(plan, args_of(pa, d), d["k_new"], d["v_new"], 256, ws)
+    rk, rv = kv4.append(p, p.k_new, p.v_new, p.cache_k, p.cache_v)
+    assert np.array_equal(d["cache_k"][first:].cpu().numpy().reshape(rk.shape), rk)
+    assert np.array_equal(d["cache_v"][first:].cpu().numpy().reshape(rv.shape), rv)
+    k, v = torch.zeros_like(d["k_new"]), torch.zeros_like(d["v_new"])
+    pa.pa_cache_read(plan, args_of(pa, d), k, v, 256, ws)
+    assert pa.pa_check(plan, ws)[0] == 0
+    p.cache_k, p.cache_v, p.num_pages = rk, rv, n
+    for got, w in ((k, "k"), (v, "v")):
+        want = np.concatenate([np.stack([kv4.read_back(p, w, b, h, int(p.seq_lens_kv[b]), int(p.seq_lens[b]))
+                                         for h in range(p.kv_heads)], 1) for b in range(p.bsz)])
+        bits = got.reshape(p.total_q, 256).view(torch.int16).cpu().numpy().view(np.uint16)
+        assert np.array_equal(bits, want.reshape(bits.shape)), w
+
+
 # ---------------------------------------------------------------- together
 def serve(pa, p, d, plan, ws, args, read):
     pa.pa_cache_append(plan, args, d["k_new"], d["v_new"], p.kv_heads * 128, ws)
