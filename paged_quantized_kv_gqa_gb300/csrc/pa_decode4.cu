@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     if (p.scale_kind == PA_SCALE_GLOBAL) c_log2 *= reinterpret_cast<const float*>(p.k_scale)[0];
     else if (p.scale_kind == PA_SCALE_PER_KV_HEAD)
       c_log2 *= __bfloat162float(sc_smem ? ks_s[m.kvh] : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)[m.kvh]);
-    const float c_abs = fabsf(c_log2), sgn = c_log2 < 0.f ? -1.f : 1.f;   // a sign goes into Q'
+    // a sign goes into Q'; a scale of 0 becomes one too small to matter (-inf * 0 is NaN)
+    const float c_abs = fmaxf(fabsf(c_log2), 1e-30f), sgn = c_log2 < 0.f ? -1.f : 1.f;
     const float c_inv = __fdividef(1.f, c_abs);
     int tok0_local = 0, pre_len = 0;
     const uint8_t* tmask = nullptr;

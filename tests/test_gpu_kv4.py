@@ -108,6 +108,18 @@ def test_negative_tensor_scales(kw):
     check(p, out, lse)
 
 
+@pytest.mark.parametrize("scale_kind", SCALES)
+@pytest.mark.parametrize("kw", [DECODE[3], DECODE[6], VERIFY[1], APPEND[0]])
+def test_zero_tensor_scales(kw, scale_kind):
+    """A K scale of 0 makes every visible position equal; a V scale of 0 the output 0."""
+    p = make(26, scale_kind=scale_kind, **kw)
+    n = max(1, len(p.k_scale) // 2)
+    p.k_scale[:n] = 0
+    p.v_scale[n:] = 0
+    out, lse, *_ = run(p)
+    check(p, out, lse)
+
+
 @pytest.mark.parametrize("kw", [DECODE[2], VERIFY[0], APPEND[0]])
 def test_workspace_of_one_plan_in_two_graphs(pa, kw):
     """Two captured graphs share a plan's workspace: replayed one after the other,
