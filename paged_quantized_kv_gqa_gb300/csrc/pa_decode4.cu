@@ -53,7 +53,9 @@ struct D4Cfg {
   static constexpr int kRecOff = kBtOff + kItems * kBtStride * 4;
   static constexpr int kBarOff = kRecOff + kWarps * kRing * 48;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
-  static constexpr int kTotal = kMiscOff + 16 + 128;   // + alignment slack
+  static constexpr int kQloOff = kMiscOff + 16;        // low parts of Q' (LO = 1, below)
+  static constexpr int kBase = kQloOff + 128;          // + alignment slack
+  static constexpr int kTotal = kBase + kWarps * NB * 2048;
   static_assert(kTotal <= 232448, "shared memory overflow");
   static_assert(kStages < kRing, "a record outlives its stages");
   // the epilogue stages 8 NB rows of 128 fp32 in the item's last stages
@@ -89,11 +91,18 @@ __device__ __forceinline__ int kpos(int b, int g, int h) {
 
 }  // namespace
 
-template <int NB, int FP4, bool TREE>
+// LO > 0: per-channel K scales.  A product of a bf16 query and a bf16 scale has 16
+// significant bits; rounded to fp16 it moved the lse by up to 2e-4 (relative error
+// 4.6e-6, without it 5e-8).  So Q' is the sum of two fp16 numbers there.  LO = 2, at
+// most 4 rows: the low parts are MMA columns 4 to 7, which have no rows (batch of 64
+// sequences, 4 rows: 45.4 -> 46.4 us; as LO = 1 57.4).  LO = 1: they wait in shared
+// memory and go through MMAs of their own (24 sequences, 5 rows: 20.5 -> 23.1 us).
+template <int NB, int FP4, bool TREE, int LO>
 __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
     decode4_kernel(const uint8_t* __restrict__ cache_k, const uint8_t* __restrict__ cache_v,
                    const AttnParams p) {
   using C = D4Cfg<NB>;
+  constexpr bool PC = LO != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
   const int warp = threadIdx.x >> 5;
@@ -113,13 +122,14 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   int* next_item = reinterpret_cast<int*>(smem + C::kMiscOff);
   volatile int* abort_any = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
   const uint8_t* stage_p = smem + warp * C::kStages * kStage4;
+  uint2* qlo = reinterpret_cast<uint2*>(smem + C::kQloOff) + warp * NB * 256 + lane;   // [row block][k step][lane]
   const __nv_bfloat16* ks_s = reinterpret_cast<const __nv_bfloat16*>(smem + C::kScaleOff);
   const __nv_bfloat16* vs_s = ks_s + kScaleBytes / 4;
 
   const int sc_n = p.scale_kind == PA_SCALE_PER_CHANNEL ? p.kv_heads * kV4Dim
                    : p.scale_kind == PA_SCALE_PER_KV_HEAD ? p.kv_heads : 0;
   const bool sc_smem = sc_n > 0 && sc_n * 2 <= kScaleBytes / 2;
-  PA_DEBUG_PROLOGUE(smem, C::kTotal - 128, p, item_begin, item_end);
+  PA_DEBUG_PROLOGUE(smem, (LO == 1 ? C::kTotal : C::kBase) - 128, p, item_begin, item_end);
   if (threadIdx.x == 0) {
     for (int w = 0; w < C::kWarps; ++w)
       for (int s = 0; s < C::kStages; ++s)
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   auto load_q_rows = [&](uint4 (&qr)[NB][4], int tok0, int ntok, int kvh) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const int row = 8 * j + g;
+      const int row = LO == 2 ? g & 3 : 8 * j + g;
       const bool valid = row < ntok * G;
       const int tok = valid ? div_g(row) : 0;
       const __nv_bfloat16* src = p.q + (tok0 + tok) * p.q_stride + (kvh * G + (valid ? row - tok * G : 0)) * kV4Dim +
@@ -300,10 +310,9 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       } else {
         load_q_rows(qr, m.tok0, m.ntok, m.kvh);
       }
-      const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
       const __nv_bfloat16* sk = (sc_smem ? ks_s : reinterpret_cast<const __nv_bfloat16*>(p.k_scale)) +
-                                (pc ? m.kvh * kV4Dim + 32 * t : 0);
-      const bool sk16 = pc && (reinterpret_cast<uintptr_t>(sk) & 15) == 0;
+                                (PC ? m.kvh * kV4Dim + 32 * t : 0);
+      const bool sk16 = PC && (reinterpret_cast<uintptr_t>(sk) & 15) == 0;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         float sc[8];
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sc[e] = pc ? __bfloat162float(sk[8 * w + e]) * sgn : sgn;
+          for (int e = 0; e < 8; ++e) sc[e] = PC ? __bfloat162float(sk[8 * w + e]) * sgn : sgn;
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
@@ -330,9 +339,20 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
             f[2 * e + 1] = __high2float(b2) * sc[2 * e + 1];
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            qf[j][2 * w + (i >> 1)][i & 1] =
-                FP4 ? pack_half2(f[2 * i], f[2 * i + 1]) : pack_half2(f[i], f[i + 4]);
+          for (int i = 0; i < 4; ++i) {
+            const int e0 = FP4 ? 2 * i : i, e1 = FP4 ? 2 * i + 1 : i + 4;
+            const uint32_t hi = pack_half2(f[e0], f[e1]);
+            qf[j][2 * w + (i >> 1)][i & 1] = hi;
+            if constexpr (LO == 2) {
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              if (g >= 4) qf[j][2 * w + (i >> 1)][i & 1] = pack_half2(f[e0] - h.x, f[e1] - h.y);
+            }
+            if constexpr (LO == 1) {
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              reinterpret_cast<uint32_t*>(qlo + (8 * j + 2 * w + (i >> 1)) * 32)[i & 1] =
+                  pack_half2(f[e0] - h.x, f[e1] - h.y);
+            }
+          }
         }
       }
     }
@@ -369,6 +389,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
         for (int j = 0; j < NB; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[b][j][e] = 0.f;
+        float sl[NB][4] = {};   // the low parts' sums, a chain of their own
         uint4 kr[2];
         uint32_t ksc[2][2], koff[2][2][2];
 #pragma unroll
@@ -391,9 +412,24 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
+            for (int j = 0; j < NB; ++j) {
               mma_16816(s[b][j], a[2 * i], c[2 * i], a[2 * i + 1], c[2 * i + 1], qf[j][2 * w + i][0],
                         qf[j][2 * w + i][1]);
+              if constexpr (LO == 1) {
+                const uint2 lo = qlo[(8 * j + 2 * w + i) * 32];
+                mma_16816(sl[j], a[2 * i], c[2 * i], a[2 * i + 1], c[2 * i + 1], lo.x, lo.y);
+              }
+            }
+        }
+        if constexpr (LO == 1) {
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[b][j][e] += sl[j][e];
+        }
+        if constexpr (LO == 2) {   // (columns 4 to 7 end up as copies of 0 to 3, not stored)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][0][e] += __shfl_xor_sync(0xffffffffu, s[b][0][e], 2);
         }
       }
 
@@ -652,11 +688,11 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   pdl_launch_dependents();   // the merge grid may be scheduled while the last CTAs finish
 }
 
-template <int NB, int FP4>
+template <int NB, int FP4, int LO>
 static cudaError_t launch_d4(const Plan& plan, const AttnParams& p, const uint8_t* ck, const uint8_t* cv,
                              cudaStream_t stream) {
-  auto kern = p.attn_mask != nullptr ? decode4_kernel<NB, FP4, true> : decode4_kernel<NB, FP4, false>;
-  const int smem = D4Cfg<NB>::kTotal;
+  auto kern = p.attn_mask != nullptr ? decode4_kernel<NB, FP4, true, LO> : decode4_kernel<NB, FP4, false, LO>;
+  const int smem = LO == 1 ? D4Cfg<NB>::kTotal : D4Cfg<NB>::kBase;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<plan.num_ctas, D4Cfg<NB>::kWarps * 32, smem, stream>>>(ck, cv, p);
@@ -669,9 +705,14 @@ cudaError_t launch_decode4(const Plan& plan, const AttnParams& p, const void* ck
   const uint8_t* k = static_cast<const uint8_t*>(ck);
   const uint8_t* v = static_cast<const uint8_t*>(cv);
   const int rows = plan.max_q * (plan.prob.q_heads / plan.prob.kv_heads);
-  if (rows <= 8) return fp4 ? launch_d4<1, 1>(plan, p, k, v, stream) : launch_d4<1, 0>(plan, p, k, v, stream);
-  if (rows <= 16) return fp4 ? launch_d4<2, 1>(plan, p, k, v, stream) : launch_d4<2, 0>(plan, p, k, v, stream);
-  return cudaErrorInvalidValue;
+  const bool pc = plan.prob.scale_kind == PA_SCALE_PER_CHANNEL;
+  if (rows > 16) return cudaErrorInvalidValue;
+  auto launch = rows <= 8 ? (!pc ? (fp4 ? launch_d4<1, 1, 0> : launch_d4<1, 0, 0>)
+                             : rows <= 4 ? (fp4 ? launch_d4<1, 1, 2> : launch_d4<1, 0, 2>)
+                                         : (fp4 ? launch_d4<1, 1, 1> : launch_d4<1, 0, 1>))
+                          : (pc ? (fp4 ? launch_d4<2, 1, 1> : launch_d4<2, 0, 1>)
+                                : (fp4 ? launch_d4<2, 1, 0> : launch_d4<2, 0, 0>));
+  return launch(plan, p, k, v, stream);
 }
 
 }  // namespace pa

@@ -101,7 +101,9 @@ def reference(p, rows=None):
             q = kv4.bf16_to_f64(p.q_bits[t0:t1, h * G * 128:(h + 1) * G * 128]).reshape(t1 - t0, G, 128)
             V = rows("v", b, h, L)
             o, l, absv, mag = kv4.attend(q, rows("k", b, h, L), V, seen, p.sm_scale)
-            c = (2.0 ** -11 if p.scale_kind == "per_channel" else 0.0) + 2.0 ** -14
+            # up to 16 rows over a 4-bit cache Q' times a per-channel scale is two fp16 numbers
+            one_fp16 = p.scale_kind == "per_channel" and (int(max(p.seq_lens)) * G > 16 or p.kv_dtype not in KINDS)
+            c = (2.0 ** -11 if one_fp16 else 0.0) + 2.0 ** -14
             d = p.sm_scale * c * mag + 2.0 ** -20
             sl = np.s_[t0:t1, h * G:(h + 1) * G]
             out[sl], lse[sl] = o, l
