@@ -116,8 +116,8 @@ NCU_TRAFFIC = {
     # cache) and scaled by the KV-bytes ratio 7.4922: pages read and partial
     # states written both grow per sequence
     "spec-verify-4": (("pa_decode.cu", "pa_decode.cuh", "pa_index.cuh", "pa_kv4.cuh", "pa_merge.cuh"),
-                      "ed836fdbe7ca3c72", (729.497600e6 + 31.870464e6) * 7.492152264116904),
-    "append-3": (("pa_append.cu", "pa_append.cuh", "pa_kv4.cuh"), "1f64180585ea8063", 72.230912e6 + 1.651200e6),
+                      "174c34d94909932f", (729.497600e6 + 31.870464e6) * 7.492152264116904),
+    "append-3": (("pa_append.cu", "pa_append.cuh", "pa_kv4.cuh"), "491ab168a2a29099", 72.230912e6 + 1.651200e6),
     "mla-5": (("pa_mla.cu",), "0876c4e8f2a38132", 224.198656e6 + 7.294464e6),
 }
 

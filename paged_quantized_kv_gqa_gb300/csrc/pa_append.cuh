@@ -36,7 +36,8 @@
 //     completed; K16 / V16 buffer b and Q' are rewritten only after the
 //     MMAs that read them completed (tcgen05.commit of the issuing thread).
 //   * Per-kv-head / global K scales fold into the softmax scale, V scales into
-//     the epilogue, per-channel K scales into Q'.
+//     the epilogue, per-channel K scales into Q' (rounded to fp16 as one number: the
+//     lse moves by up to 2e-4; two would double S's MMAs, which bound the kernel).
 //   * 4-bit cache (KV = int4, FP4): a page's K and V slabs (codes and block
 //     scales together) arrive by one bulk copy each, 9 KB instead of 16 KB; CV
 //     multiplies each code pair by its block scale (exact in fp16).  int4 codes

@@ -44,7 +44,10 @@
 //     operand.  Q' (bf16 query times the per-channel K scale, fp16) and P^T
 //     (fp16) are K-major 128B-swizzled shared-memory B operands.
 //   * Per-kv-head / global K scales fold into the softmax scale, V scales into
-//     the epilogue, per-channel K scales into Q'.
+//     the epilogue, per-channel K scales into Q' (the product of two bf16 numbers
+//     rounded to fp16: it moves the lse by up to 2e-4; a second fp16 number per
+//     element, as in the warp kernel of the 4-bit cache, would need 16 MMAs for S
+//     instead of 8 and shared memory that 64 rows do not leave).
 //   * 4-bit cache (KV = int4, FP4): a page's K slab arrives as a 72-row box of 64
 //     bytes with 64B swizzle (a thread reads one position's 64 code bytes: without
 //     the swizzle eight neighbours would share banks), its V slab by a bulk copy
