@@ -688,6 +688,9 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
       e = launch_decode4_tm(*plan, p, tk, args->cache_v, st);
     }
   } else if (plan->family == PA_FAMILY_DECODE) {
+    // the in-kernel merge stores four elements at once
+    if (plan->fused_merge && reinterpret_cast<uintptr_t>(args->out) % (args->out_int8 ? 4 : 8))
+      return fail(PA_ERR_INVALID_ARG, "single-launch plans need an out aligned to four elements");
     CUtensorMap tk, tv;
     const uint64_t heads_total = (uint64_t)pr.num_pages * pr.kv_heads;
     if (plan->max_q * p.group <= kWarpDecodeRows && !plan->fused_merge) {

@@ -1,65 +1,27 @@
-// pa_decode.cuh - paged int8 / FP8-E4M3 / 4-bit KV attention for few packed query rows
-// (decode and speculative verify: q_len * G <= 64), tcgen05 + TMA, sm_103a.
+// pa_decode.cuh - the tensor-memory decode kernel of the 4-bit cache: 17 to 64 packed
+// query rows (decode and speculative verify), tcgen05 + TMA, sm_103a.
 //
-// Operation: FastDeploy append_attention_c8_impl.cuh,
-// multi_query_append_attention_c8_warp1_4_kernel (one CTA row per
-// (sequence, kv head, kv chunk), the query rows of a GQA group packed as
-// (token, head-in-group), chunk bounds [c*chunk, min(kv_len, (c+1)*chunk)),
-// direct write when the sequence has one chunk, else partial o plus tmp_m /
-// tmp_d).  The sm80 design there (cp.async + mma.sync with dequant in
-// registers, all warps doing every step) is replaced by:
-//
-//   * Swap-AB orientation.  The 128 TMEM lanes hold 128 KV positions, the
-//     packed query rows are the MMA's N (16..64):  S^T = K * Q'^T and
-//     O^T += V^T * P^T, so queries are never padded to M = 128.
-//   * Warp specialisation, one persistent CTA of four warpgroups per SM:
-//       SM0, SM1  online softmax, each on half of the packed rows (lane =
-//                 position): running max (lazy, vote per half), row sums in
-//                 registers, P^T to shared memory, the rare rescale of its
-//                 columns of O, and the epilogue of its rows (one tile after
-//                 the item's last PV was queued).  When every item's rows fit
-//                 in the first half (e.g. one token of a group of 4), SM1 has
-//                 only padding rows and leaves at once;
-//       CV        Q' of each item, K rows (lane = position) and V^T rows (lane
-//                 = head dim) dequantised straight into TMEM;
-//       IO        one TMA warp ((page, kv head) K slab [64 x 128] with 128B
-//                 swizzle and V slab [128 x 64] with 64B swizzle per page),
-//                 one MMA warp issuing S = K Q'^T and O += V^T P^T, polling
-//                 both queues and issuing whichever is ready, and two merge
-//                 warps, active only in the opt-in single-launch mode: for
-//                 split rows the CTA that wrote a row group's last chunk
-//                 merges the group's partial states (a per-group counter in
-//                 the workspace, as the pages' "last CTA merges" semaphore).
-//                 Off by default: those merges' dependent loads queue behind
-//                 the kernel's own page stream, and the separate merge kernel
-//                 is faster.
-//     The roles meet only at mbarriers: K, V and S are double-buffered, P^T
-//     four-deep, Q' and O double-buffered per item (the epilogue of an item
-//     runs during the next item), so dequantisation, softmax, tensor-core work
-//     and page loads of neighbouring tiles and items overlap.
-//   * tcgen05.mma with M = 128 costs about the same for any N <= 64, so the
-//     kernel issues the minimum: 8 MMAs for S and 8 for PV per 128-position
-//     tile; row sums are accumulated by the softmax warps.
-//   * Converted K / V never return to shared memory: they are the TMEM A
-//     operand.  Q' (bf16 query times the per-channel K scale, fp16) and P^T
-//     (fp16) are K-major 128B-swizzled shared-memory B operands.
-//   * Per-kv-head / global K scales fold into the softmax scale, V scales into
-//     the epilogue, per-channel K scales into Q' (the product of two bf16 numbers
-//     rounded to fp16: it moves the lse by up to 2e-4; a second fp16 number per
-//     element, as in the warp kernel of the 4-bit cache, would need 16 MMAs for S
+// The method is pa_decode.cu's (swap-AB: 128 KV positions on the TMEM lanes, the packed
+// rows as the MMA's N; S^T = K Q'^T, O^T += V^T P^T; softmax warpgroups of half of the
+// rows each; K, V and S double-buffered, P^T four-deep, Q' and O per item).  What
+// differs, and why the two are separate sources (one template for both moved the 8-bit
+// kernel's register allocation: 1.52 -> 1.56 to 1.65 ms on spec-verify-4):
+//   * a page's K slab arrives as a 72-row box of 64 bytes with 64B swizzle (a thread
+//     reads one position's 64 code bytes: without the swizzle eight neighbours would
+//     share banks), its V slab by a bulk copy (a thread reads 16 bytes of its dim);
+//   * 640 threads: a converter warpgroup each for K and V, which multiply code pairs by
+//     their block scales (exact in fp16; int4 K with the code offset and 1/8 in the
+//     same instruction, 307.1 -> 303.1 us on 48 rows; doing V so too needs a second
+//     read of scales per word: 305.2); V's scales are converted once per warp and read
+//     back as fp16.  S and PV are issued by a warp each that sleeps on its barriers;
+//   * int4 codes unpack in the order 0 4 1 5 2 6 3 7 of each eight: the dims of Q' take
+//     the same order, and a P^T row is written at its position's place in that order;
+//   * partial rows are fp32, merged by the separate kernel only;
+//   * per-channel K scales go into Q', rounded to fp16 as one number (the lse moves by
+//     up to 2e-4; a second number, as in the warp kernel, would need 16 MMAs for S
 //     instead of 8 and shared memory that 64 rows do not leave).
-//   * 4-bit cache (KV = int4, FP4): a page's K slab arrives as a 72-row box of 64
-//     bytes with 64B swizzle (a thread reads one position's 64 code bytes: without
-//     the swizzle eight neighbours would share banks), its V slab by a bulk copy
-//     (a thread reads 16 bytes of its dim).  CV multiplies code pairs by their
-//     block scales (exact in fp16; int4 K with the code offset and 1/8 in the same
-//     instruction, 307.1 -> 303.1 us on 48 rows; doing V so too needs a second read
-//     of scales per word: 305.2); V's scales are converted once per warp and
-//     read back as fp16.  int4 codes unpack in the order 0 4 1 5 2 6 3 7 of each
-//     eight: the dims of Q' take the same order, and a P^T row is written at its
-//     position's place in that order.
 //
-// Included by pa_decode.cu (8-bit) and pa_decode4_tm.cu (4-bit).
+// Included by pa_decode4_tm.cu.
 #pragma once
 
 #include <cfloat>
@@ -86,13 +48,9 @@ constexpr float kTau = 8.0f;                     // lazy-rescale threshold (log2
 // code needs more steps than a byte, and one group for both held the pipeline up),
 // and S and PV are issued from a warp each.  (A softmax warpgroup for every 16 rows
 // instead of two for all measured slower, 334 against 319 us on 48 rows.)
-template <int KV>
-struct Roles {
-  static constexpr bool kFour = KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1;
-  static constexpr int kThreads = kFour ? 640 : 512;
-  static constexpr int kWarpTma = kFour ? 16 : 12;
-  static constexpr int kWarpMma = kWarpTma + 1;    // 4-bit: this one S, the next PV
-};
+constexpr int kThreads = 640;
+constexpr int kWarpTma = 16;
+constexpr int kWarpS = 17;                       // issues S, the next warp PV
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPBufs = 4;                        // P^T ring depth
 // P^T buffer: [128 positions][64 rows] fp16, MN-major (rows contiguous),
@@ -262,13 +220,10 @@ struct TileCursor {
 
 // KV: PA_KV_*; cv: the 4-bit V cache (tm_v is unused then)
 template <int NR, int KV, bool TREE>
-__global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const uint8_t* __restrict__ cv, const AttnParams p) {
-  using R = Roles<KV>;
-  constexpr bool kFour = R::kFour;
-  constexpr int kThreads = R::kThreads;
-  constexpr int FP4 = KV == PA_KV_FP4_E2M1, FP8 = KV == PA_KV_FP8_E4M3;
+  constexpr int FP4 = KV == PA_KV_FP4_E2M1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -306,12 +261,12 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
   const int item_end = p.work_indptr[blockIdx.x + 1];
   const uint64_t limit = (uint64_t)p.wait_limit_ns;
   const int G = p.group;
-  PA_DEBUG_PROLOGUE(smem, SM::kTotal - 1024, p, item_begin, item_end);
+  PA_DEBUG_PROLOGUE(smem, (SM::kTotal) - 1024, p, item_begin, item_end);
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kFour ? 8 : 4);   // the warps that read a stage
+      mbar_init(&empty[s], 8);   // the warps that read a stage
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(&kready[j], 4);
@@ -353,11 +308,10 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
   // this warp's TMEM lane quarter (a warp may only touch lanes 32*(warp%4) ..)
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
-  if (warp == R::kWarpTma) {
+  if (warp == kWarpTma) {
     // ================================================================ TMA
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
-      if constexpr (!kFour) tma_prefetch_desc(&tm_v);
       uint32_t g = 0;
       int issued_g[kStages];
       for (int s = 0; s < kStages; ++s) issued_g[s] = -1;
@@ -381,30 +335,16 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
             break;
           }
           if (p.skip_first_load && g == 0) continue;  // failure-detection test hook
-          mbar_arrive_expect_tx(&full[stage], (uint32_t)(npg * 2 * (kFour ? kV4Slab : kSlab)));
+          mbar_arrive_expect_tx(&full[stage], (uint32_t)(npg * 2 * kV4Slab));
           issued_g[stage] = (int)g;
           uint8_t* st = smem + stage * kStageBytes;
           for (int pg = 0; pg < npg; ++pg) {
             const int page = pages[pg];
-            if constexpr (kFour) {
-              const bool in_pool = page >= 0 && page < p.num_pages;
-              if (!in_pool) record_status(p.status, PA_ERR_BAD_PAGE, it);   // reads page 0 instead
-              const int slab = (in_pool ? page : 0) * p.kv_heads + m.kvh;
-              tma_load_2d(st + pg * kSlot4, &tm_k, &full[stage], 0, slab * (kV4Slab / 64));
-              bulk_load(st + 2 * kSlab + pg * kSlot4, cv + (int64_t)slab * kV4Slab, kV4Slab, &full[stage]);
-              continue;
-            }
-            int yk, yv;
-            if (page < 0 || page >= p.num_pages) {
-              record_status(p.status, PA_ERR_BAD_PAGE, it);
-              yk = p.num_pages * p.kv_heads * kPage;       // past the end: TMA fills zeros
-              yv = p.num_pages * p.kv_heads * kHeadDim;
-            } else {
-              yk = (page * p.kv_heads + m.kvh) * kPage;
-              yv = (page * p.kv_heads + m.kvh) * kHeadDim;
-            }
-            tma_load_2d(st + pg * kSlab, &tm_k, &full[stage], 0, yk);
-            tma_load_2d(st + 2 * kSlab + pg * kSlab, &tm_v, &full[stage], 0, yv);
+            const bool in_pool = page >= 0 && page < p.num_pages;
+            if (!in_pool) record_status(p.status, PA_ERR_BAD_PAGE, it);   // reads page 0 instead
+            const int slab = (in_pool ? page : 0) * p.kv_heads + m.kvh;
+            tma_load_2d(st + pg * kSlot4, &tm_k, &full[stage], 0, slab * (kV4Slab / 64));
+            bulk_load(st + 2 * kSlab + pg * kSlot4, cv + (int64_t)slab * kV4Slab, kV4Slab, &full[stage]);
           }
           trace_ev(p, g, 0);
         }
@@ -412,11 +352,11 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
       for (int s = 0; s < kStages; ++s)   // every issued load lands before exit
         if (issued_g[s] >= 0) mbar_wait(&full[s], ((uint32_t)issued_g[s] / kStages) & 1, kDrainNs);
     }
-  } else if (kFour && (warp == R::kWarpMma || warp == R::kWarpMma + 1)) {
-    // ================================================================ MMA issue, 4-bit
+  } else if (warp == kWarpS || warp == kWarpS + 1) {
+    // ================================================================ MMA issue
     // S and PV each have a warp that sleeps on its barriers: one warp polling both
     // queues took issue slots from the converters on its sub-partition
-    const bool is_s = warp == R::kWarpMma;
+    const bool is_s = warp == kWarpS;
     auto mwait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, limit, abort_any, 100); };
     const uint32_t idesc = is_s ? idesc_f16_f32(128, NR) : idesc_f16_f32_bmn(128, NR);
     TileCursor c;
@@ -461,144 +401,8 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     // drain: every MMA this warp issued completes before TMEM is released
     for (int j = 0; j < kPBufs; ++j)
       if (commits[j]) mbar_wait(is_s ? &sfull[j] : &pvdone[j], (commits[j] - 1) & 1, kDrainNs);
-  } else if (!kFour && warp == R::kWarpMma) {
-    // ================================================================ MMA issue
-    // the whole warp runs the polling loop (warp-uniform operands); one
-    // elected lane issues the MMAs and commits
-    {
-      const uint32_t idesc = idesc_f16_f32(128, NR);
-      const uint32_t idesc_pv = idesc_f16_f32_bmn(128, NR);   // B = P^T, MN-major
-      TileCursor cs, cp;       // next S to issue, next PV to issue
-      cs.init(isrc, item_begin, item_end);
-      cp.init(isrc, item_begin, item_end);
-      uint32_t gs = 0, gp = 0;
-      uint32_t s_commits[2] = {0, 0}, pv_commits[kPBufs] = {0, 0, 0, 0};
-      bool ok = true;
-      uint64_t t_idle = 0;
-      while (cp.valid()) {
-        bool progressed = false;
-        if (cs.valid() && mbar_test_wait(&kready[gs & 1], (gs >> 1) & 1) &&
-            (gs < 2 || mbar_test_wait(&sfree[gs & 1], ((gs - 2) >> 1) & 1))) {
-          tc_fence_after();
-          const uint32_t kb = TM::K0 + (gs & 1) * 64;
-          const uint32_t sd = TM::S0 + (gs & 1) * NR;
-          const uint32_t qb = q_s + ((cs.it - item_begin) & 1) * NR * 256;
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + sd, tmem + kb + 8 * kk,
-                     sdesc_k128(qb + (kk >> 2) * NR * 128 + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
-            tc_commit(&sfull[gs & 1]);
-          }
-          __syncwarp();
-          ++s_commits[gs & 1];
-          if (lane == 0) trace_ev(p, gs, 8);
-          ++gs;
-          cs.advance();
-          progressed = true;
-        }
-        if (gp < gs && mbar_test_wait(&pready[gp & 3], (gp >> 2) & 1) &&
-            mbar_test_wait(&vready[gp & 1], (gp >> 1) & 1)) {
-          tc_fence_after();
-          const uint32_t vb = TM::V0 + (gp & 1) * 64;
-          const uint32_t pb = p_s + (gp & 3) * kPBufBytes;
-          const uint32_t od = TM::O0 + ((cp.it - item_begin) & 1) * NR;
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              // positions 16kk .. 16kk+15: two 8-position swizzle atoms of 1 KB
-              const uint64_t bd = sdesc_mn128(pb + kk * 2048, kPBufBytes, 1024);
-              mma_ts(tmem + od, tmem + vb + 8 * kk, bd, idesc_pv, (cp.i > 0 || kk > 0) ? 1u : 0u);
-            }
-            tc_commit(&pvdone[gp & 3]);
-          }
-          __syncwarp();
-          ++pv_commits[gp & 3];
-          if (lane == 0) trace_ev(p, gp, 9);
-          ++gp;
-          cp.advance();
-          progressed = true;
-        }
-        if (progressed) {
-          t_idle = 0;
-        } else {
-          if (*abort_any) { ok = false; break; }
-          const uint64_t now = globaltimer();
-          if (t_idle == 0) t_idle = now;
-          else if (now - t_idle > limit) { ok = false; break; }
-        }
-      }
-      if (!ok && lane == 0) {
-        if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, item_begin);
-        *abort_any = 1;
-      }
-      // drain: every issued MMA completes before TMEM is released
-      for (int j = 0; j < 2; ++j)
-        if (s_commits[j]) mbar_wait(&sfull[j], (s_commits[j] - 1) & 1, kDrainNs);
-      for (int j = 0; j < kPBufs; ++j)
-        if (pv_commits[j]) mbar_wait(&pvdone[j], (pv_commits[j] - 1) & 1, kDrainNs);
-    }
-  } else if (kFour && wg == 4) {
+  } else if (wg == 4) {
     // the last warp has no role (it completes the warpgroup)
-  } else if (!kFour && wg == 3) {
-    // ================================================================ fused merge
-    // warps 14 and 15 take alternate items; once all eight softmax warps have
-    // finished an item's epilogue, its row group's counter is raised and the
-    // CTA that completes the count merges the group and resets the counter
-    if (p.merge_cnt != nullptr) {
-      bool ok = true;
-      for (int it = item_begin + (warp - 14); it < item_end && ok; it += 2) {
-        const int li = it - item_begin;
-        const uint64_t t0 = globaltimer();
-        while (true) {
-          const bool done = lane >= 4 * p.softmax_wgs || ep_done[lane] > li;
-          if (__all_sync(0xffffffffu, done)) break;
-          const bool give_up = *abort_any || globaltimer() - t0 > limit;
-          if (__shfl_sync(0xffffffffu, give_up, 0)) { ok = false; break; }
-          __nanosleep(128);
-        }
-        if (!ok) break;
-        __threadfence_block();   // acquire the epilogue's partial-state writes
-        const Item m = isrc.at(it);
-        if (m.nch <= 1) continue;
-        int32_t* cnt = p.merge_cnt + (int64_t)m.tok0 * p.kv_heads + m.kvh;
-        int prev = 0;
-        if (lane == 0) {
-          __threadfence();        // this CTA's partial states before its count
-          prev = atomicAdd(cnt, 1);
-        }
-        prev = __shfl_sync(0xffffffffu, prev, 0);
-        if (prev != m.nch - 1) continue;
-        __threadfence();          // every chunk's partial states after the last count
-        const int rows = m.ntok * G;
-        for (int r0 = 0; r0 < rows; r0 += kMergeRows) {
-          int64_t slot0[kMergeRows];
-          bool valid[kMergeRows];
-          int tok[kMergeRows], head[kMergeRows];
-#pragma unroll
-          for (int r = 0; r < kMergeRows; ++r) {
-            const int rr = min(r0 + r, rows - 1);
-            valid[r] = r0 + r < rows;
-            tok[r] = m.tok0 + rr / G;
-            head[r] = m.kvh * G + rr % G;
-            slot0[r] = (int64_t)tok[r] * p.max_chunks * p.q_heads + head[r];
-          }
-          float acc[kMergeRows][kHeadDim / 32], M[kMergeRows], W[kMergeRows];
-          merge_rows<kHeadDim, kMergeRows, 4>(p.part_o, p.part_m, p.part_d, slot0, valid, p.q_heads, m.nch,
-                                  lane, acc, M, W);
-#pragma unroll
-          for (int r = 0; r < kMergeRows; ++r)
-            if (valid[r])
-              merge_store<kHeadDim>(acc[r], M[r], W[r], p.out, p.lse, p.ep, tok[r], head[r],
-                                    p.q_heads, lane);
-        }
-        if (lane == 0) *cnt = 0;  // the group is done: ready for the next launch
-      }
-      if (!ok && lane == 0) {
-        if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, item_begin);
-        *abort_any = 1;
-      }
-    }
   } else if (wg == 1 && p.softmax_wgs == 1) {
     // every item's rows are in the first half: this warpgroup has no rows
   } else if (wg < 2) {
@@ -691,14 +495,10 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
             }
           } else {
             const int64_t sp = ((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head;
-            if constexpr (kFour) {
+            {
               float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.part_o) + sp * kHeadDim + 8 * c);
               dst[0] = make_float4(f[0], f[1], f[2], f[3]);
               dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-            } else {
-              *reinterpret_cast<uint4*>(p.part_o + sp * kHeadDim + 8 * c) =
-                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                             pack_bf16x2(f[6], f[7]));
             }
           }
         }
@@ -716,14 +516,6 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         bar_sync(bar_id, 128);
         write_rows(kP0, NH - kP0);
       }
-      if (!kFour && p.merge_cnt != nullptr) {
-        // publish: this warp's rows of item li are written (release to the merge warps)
-        __syncwarp();
-        if (lane == 0) {
-          __threadfence_block();
-          ep_done[warp] = li + 1;
-        }
-      }
       if (tid == 0) trace_ev(p, gl, 10);
       return true;
     };
@@ -735,7 +527,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
       const Item cur = isrc.at(it);
       const int li = it - item_begin;
       const int n_rows = cur.ntok * G;
-      const float c_log2 = p.sm_scale_log2 * (kFour ? kFold8<FP4> : 1.f) *
+      const float c_log2 = p.sm_scale_log2 * kFold8<FP4> *
           (p.scale_kind == PA_SCALE_PER_CHANNEL ? 1.0f : kscale(cur.kvh));
       const uint32_t o_col = TM::O0 + (li & 1) * NR + r_lo;
       // speculative tree mask: the item's first token within its sequence and
@@ -1002,7 +794,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     // hardware's default time rather than re-probing every 32 ns (fewer issue
     // slots taken from the softmax warps on the same sub-partitions).
     const int d = tid & 127;  // TMEM lane: K position / V head dim / output dim
-    const bool do_k = !kFour || wg == 2, do_v = !kFour || wg == 3;   // (both in the 8-bit kernels)
+    const bool do_k = wg == 2, do_v = wg == 3;
     uint32_t g = 0;
     bool fail = false;
     auto note_fail = [&](int it) {
@@ -1099,7 +891,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         if (do_k && d == 0) trace_ev(p, g, 1);
         if (!do_k) {
           // this warpgroup converts V only
-        } else if constexpr (kFour) {
+        } else {
           // position d: code row 36 (half page) + row of its page's box, its eight
           // block scales in one of the rows behind the half's codes
           const uint32_t kbase = s_base + stage * kStageBytes + (d >> 6) * kSlot4;
@@ -1125,30 +917,9 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
             tmem_st16(dst + 16 * c, x);
           }
           tmem_wait_st();
-        } else {
-          const int box = d >> 6, row = d & 63;
-          const uint32_t kbase = s_base + stage * kStageBytes + box * kSlab + row * 128;
-          uint4 raw[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) raw[c] = ld_shared_v4(kbase + ((c ^ (row & 7)) << 4));
-          const uint32_t dst = t_lane + TM::K0 + (g & 1) * 64;
-#pragma unroll
-          for (int c2 = 0; c2 < 4; ++c2) {
-            uint32_t w[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 r4 = raw[c2 * 2 + h];
-              cvt4<FP8>(r4.x, w[8 * h + 0], w[8 * h + 1]);
-              cvt4<FP8>(r4.y, w[8 * h + 2], w[8 * h + 3]);
-              cvt4<FP8>(r4.z, w[8 * h + 4], w[8 * h + 5]);
-              cvt4<FP8>(r4.w, w[8 * h + 6], w[8 * h + 7]);
-            }
-            tmem_st16(dst + 16 * c2, w);
-          }
-          tmem_wait_st();
         }
         if (do_k) {
-          if constexpr (kFour) warp_arrive(&empty[stage], lane);
+          warp_arrive(&empty[stage], lane);
           tc_fence_before();
           warp_arrive(&kready[g & 1], lane);
           if (d == 0) trace_ev(p, g, 2);
@@ -1161,7 +932,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         }
         tc_fence_after();
         if (d == 0) trace_ev(p, g, 5);
-        if constexpr (kFour) {
+        {
           // V^T row d of tile g.  The warp's two scale blocks (32 dims) are turned
           // into fp16 once: lane (b, k) takes positions 8k .. 8k+7 of block b; 0
           // past kv1, where the bytes may hold anything.
@@ -1197,42 +968,6 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
           }
           tmem_wait_st();
           __syncwarp();   // every lane has read the scales before the next tile writes them
-        } else {
-          // V^T row d of tile g -> TMEM V buffer g&1 (positions past kv1 zeroed)
-          const int tpos0 = m.kv0 + i * kTileTok;
-          const int nvalid = min(kTileTok, m.kv1 - tpos0);
-          const uint32_t vbase = s_base + stage * kStageBytes + 2 * kSlab + d * 64;
-          uint4 raw[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            raw[c] = ld_shared_v4(vbase + (c >> 2) * kSlab + (((c & 3) ^ ((d >> 1) & 3)) << 4));
-          const uint32_t dst = t_lane + TM::V0 + (g & 1) * 64;
-#pragma unroll
-          for (int box = 0; box < 2; ++box) {
-            uint32_t w[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 r4 = raw[box * 4 + c];
-              cvt4<FP8>(r4.x, w[8 * c + 0], w[8 * c + 1]);
-              cvt4<FP8>(r4.y, w[8 * c + 2], w[8 * c + 3]);
-              cvt4<FP8>(r4.z, w[8 * c + 4], w[8 * c + 5]);
-              cvt4<FP8>(r4.w, w[8 * c + 6], w[8 * c + 7]);
-            }
-            if (nvalid < kTileTok) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const int tok = box * 64 + 2 * k;
-                if (tok >= nvalid) w[k] = 0u;
-                else if (tok + 1 >= nvalid) w[k] &= 0x0000FFFFu;
-              }
-            }
-            uint32_t lo[16], hi[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) { lo[k] = w[k]; hi[k] = w[16 + k]; }
-            tmem_st16(dst + box * 32, lo);
-            tmem_st16(dst + box * 32 + 16, hi);
-          }
-          tmem_wait_st();
         }
         warp_arrive(&empty[stage], lane);
         if (d == 0) trace_ev(p, g, 6);

@@ -1,5 +1,5 @@
-// pa_decode4_tm.cu - the 4-bit instantiations of the tensor-memory decode kernel
-// (pa_decode.cuh); tiles of at most 16 rows run in pa_decode4.cu.
+// pa_decode4_tm.cu - the instantiations of the tensor-memory decode kernel of the 4-bit
+// cache (pa_decode.cuh); tiles of at most 16 rows run in pa_decode4.cu.
 #include "pa_decode.cuh"
 
 namespace pa {
@@ -11,7 +11,7 @@ static cudaError_t launch_t(const Plan& plan, const AttnParams& p, const CUtenso
   const int smem = Smem<NR>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<plan.num_ctas, Roles<KV>::kThreads, smem, stream>>>(tm_k, tm_k, cv, p);   // tm_v unused
+  kern<<<plan.num_ctas, kThreads, smem, stream>>>(tm_k, tm_k, cv, p);   // tm_v unused
   return cudaGetLastError();
 }
 

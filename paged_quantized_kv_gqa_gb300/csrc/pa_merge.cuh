@@ -129,8 +129,10 @@ __device__ __forceinline__ void merge_rows(const __nv_bfloat16* __restrict__ par
   }
 }
 
-// Final output of a merged row (output epilogue applied) and its lse.
-template <int DV>
+// Final output of a merged row (output epilogue applied) and its lse.  kAnyOut: out may
+// have any alignment.  The in-kernel merge refuses an unaligned out instead: the element
+// stores' code in that kernel moved its registers (1.52 -> 1.56 ms on spec-verify-4).
+template <int DV, bool kAnyOut = true>
 __device__ __forceinline__ void merge_store(const float (&acc)[DV / 32], float M, float W,
                                             void* __restrict__ out, float* __restrict__ lse,
                                             const OutEpilogue& ep, int token, int head,
@@ -141,7 +143,7 @@ __device__ __forceinline__ void merge_store(const float (&acc)[DV / 32], float M
   const int e0 = head * DV + lane * kPer;
   // four elements leave as one store where out's address allows it (the decode
   // family takes an out of any alignment)
-  const bool vec = (reinterpret_cast<uintptr_t>(out) & (ep.int8_out ? 3 : 7)) == 0;
+  const bool vec = !kAnyOut || (reinterpret_cast<uintptr_t>(out) & (ep.int8_out ? 3 : 7)) == 0;
 #pragma unroll
   for (int k = 0; k < kPer; k += 4) {
     float f[4];

@@ -147,6 +147,21 @@ def test_pools_up_to_the_tma_row_limit(pa):
         pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, 152)
 
 
+def test_single_launch_plans_refuse_an_unaligned_out(pa):
+    """The in-kernel merge stores four elements at once (8-bit plans with split rows)."""
+    c = synth.make_case(name="f", seed=1, seq_lens=[1], seq_lens_kv=[300], q_heads=8, kv_heads=2, chunk_size=64)
+    pa.pa_set_fused_merge(True)
+    try:
+        pl = pa.pa_plan(pa.problem_of(c), c.seq_lens, c.seq_lens_kv, c.cu_seqlens_q, 152)
+    finally:
+        pa.pa_set_fused_merge(False)
+    assert pl.describe()["fused_merge"]
+    for out in (258, 260):
+        with pytest.raises(pa.PaError) as e:
+            pa.pa_run(pl, fake_args(pa, out=out), 256, None)
+        assert e.value.status == pa.PA_ERR_INVALID_ARG and "aligned" in str(e.value)
+
+
 def test_mla_refuses_four_bits_and_cross(pa):
     kw = dict(bsz=1, q_heads=128, kv_heads=1, head_dim_qk=576, head_dim_v=512, block_size=64, max_blocks_per_seq=1,
               num_pages=1, scale_kind="global", layout="mla", chunk_size=0, sm_scale=0.1, q_stride=128 * 576)
