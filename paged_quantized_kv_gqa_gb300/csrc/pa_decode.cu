@@ -971,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           note_fail(it);
           break;
         }
+        tc_fence_after();   // the K stores below come after the MMAs that read the buffer
         if (i == 0) {
           if (q_ahead != it) load_q(m, q_s + (li & 1) * NR * 256);
           // the next item's query rows into L2 now; its Q' is written at this

@@ -383,6 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fail = true;
           break;
         }
+        tc_fence_after();   // Q's columns: the stores below come after the MMAs that read them
         if (t == 0) trace_ev(p, g, 3);
 #pragma unroll 1
         for (int ph = 0; ph < 6; ++ph) {
