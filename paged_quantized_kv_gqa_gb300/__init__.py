@@ -125,32 +125,33 @@ def _ptr(x) -> Optional[int]:
     return int(x.data_ptr())
 
 
-# torch's current-stream lookup, resolved at the first call that needs it (None:
-# torch is absent or has no CUDA device).  torch.cuda.is_available() and a Stream
-# object a call cost more host time than a small launch.
-_current_raw_stream = False
+# torch's current-stream lookup, kept from the first call that found it
+# (torch.cuda.is_available() and a Stream object a call cost more host time than a
+# small launch).  Only a lookup that worked is kept: without torch or a device every
+# call looks again, and an error of the lookup is raised, since a stream guessed
+# instead of the current one would race with the caller's work.
+_current_raw_stream = None
 
 
 def _resolve_current_stream():
     global _current_raw_stream
     try:
         import torch
-        if not torch.cuda.is_available():
-            _current_raw_stream = None
-            return
-        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
-        torch.cuda.current_stream()     # initialises torch's CUDA state
-        if raw is not None:
-            _current_raw_stream = lambda: int(raw(dev()))
-        else:
-            _current_raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)
-    except Exception:  # pragma: no cover - torch without CUDA
-        _current_raw_stream = None
+    except ImportError:
+        return
+    if not torch.cuda.is_available():
+        return
+    torch.cuda.current_stream()     # initialises torch's CUDA state
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is not None:
+        _current_raw_stream = lambda: int(raw(dev()))
+    else:
+        _current_raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)
 
 
 def _stream(s) -> Optional[int]:
     if s is None:
-        if _current_raw_stream is False:
+        if _current_raw_stream is None:
             _resolve_current_stream()
         return _current_raw_stream() if _current_raw_stream else None
     if isinstance(s, int):

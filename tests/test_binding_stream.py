@@ -1,0 +1,48 @@
+"""Which stream the binding takes when the caller names none, without a GPU."""
+import types
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def pa(monkeypatch):
+    import paged_quantized_kv_gqa_gb300 as m
+    # as in a process that has made no call yet
+    initial = False if m._current_raw_stream is False else None
+    monkeypatch.setattr(m, "_current_raw_stream", initial)
+    return m
+
+
+def with_cuda(monkeypatch, stream):
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 1000 + dev, raising=False)
+
+
+def test_the_current_stream_is_looked_up_at_every_call(pa, monkeypatch):
+    with_cuda(monkeypatch, lambda: types.SimpleNamespace(cuda_stream=7))
+    assert pa._stream(None) == 1003
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 5)
+    pa._current_raw_stream = None
+    assert pa._stream(None) == 1005
+    assert pa._stream(42) == 42 and pa._stream(types.SimpleNamespace(cuda_stream=9)) == 9
+
+
+def test_an_error_of_the_lookup_is_raised_and_not_kept(pa, monkeypatch):
+    """A failed lookup must not turn into the legacy default stream, now or later."""
+    def fails():
+        raise RuntimeError("out of memory")
+    with_cuda(monkeypatch, fails)
+    with pytest.raises(RuntimeError):
+        pa._stream(None)
+    with_cuda(monkeypatch, lambda: types.SimpleNamespace(cuda_stream=7))
+    assert pa._stream(None) == 1003
+
+
+def test_no_device_yet_is_not_kept(pa, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
+    assert pa._stream(None) is None
+    with_cuda(monkeypatch, lambda: types.SimpleNamespace(cuda_stream=7))
+    assert pa._stream(None) == 1003
