@@ -93,8 +93,9 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *   multiple of block_size); 0 never splits; -1 lets the planner choose.  Plans
  *   of the decode family over a 4-bit cache ignore it: the planner keeps ranges of
  *   at most 512 positions whole and otherwise cuts pieces of equal cost, so
- *   pa_merge always belongs after pa_run there (pa_workspace_size grows with the
- *   query tokens times the pieces of the longest sequence).
+ *   pa_merge always belongs after pa_run there.  Over a 4-bit cache the workspace
+ *   holds one fp32 row per piece and query head; over an 8-bit one it grows with the
+ *   query tokens times the chunks of the longest sequence.
  *   q_stride is the distance in elements between consecutive tokens of q
  *   (>= q_heads * head_dim_qk; FastDeploy's packed qkv uses
  *   (q_heads + 2 * kv_heads) * head_dim).

@@ -380,19 +380,43 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     P.fused_merge = P.family == PA_FAMILY_DECODE && P.max_chunks > 1 && !empty_rows && !P.four_bit() &&
                     g_faults.fused_merge;
   }
-  P.off_cnt = align4(P.off_merge + P.merge_tokens.size());
+  P.off_cnt = align4(P.off_merge + P.merge_tokens.size() * (P.four_bit() ? 4 : 1));
   const size_t words = P.off_cnt + (P.fused_merge ? (size_t)P.total_q * prob.kv_heads : 0);
   static_assert(kStatusBytes % 16 == 0, "plan blob must start 16-byte aligned");
   P.blob.assign(std::max<size_t>(words, 1), 0);
   std::copy(P.work_indptr.begin(), P.work_indptr.end(), P.blob.begin() + P.off_indptr);
   std::copy(P.items.begin(), P.items.end(), P.blob.begin() + P.off_items);
   std::copy(P.nch_token.begin(), P.nch_token.end(), P.blob.begin() + P.off_nch);
-  std::copy(P.merge_tokens.begin(), P.merge_tokens.end(), P.blob.begin() + P.off_merge);
+  if (P.four_bit()) {
+    // every token's slots: as many as it has chunks (max_chunks for every token, as the
+    // 8-bit plans have them, is 1210 MB instead of 13 for one sequence of 131k positions
+    // beside 255 of 500: equal shares cut the long one into many)
+    std::vector<int32_t> slot0(P.total_q);
+    P.part_slots = 0;
+    for (int t = 0; t < P.total_q; ++t) {
+      slot0[t] = (int32_t)P.part_slots;
+      if (P.nch_token[t] > 1) P.part_slots += P.nch_token[t];
+      if (P.part_slots > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "too many partial rows");
+    }
+    int32_t* rec = P.blob.data() + P.off_items;
+    for (size_t i = 0; i < P.items.size(); i += kItemWords, rec += kItemWords) {
+      const int32_t nch = (int32_t)((uint32_t)rec[7] >> 16);
+      rec[3] = (int32_t)((uint32_t)rec[3] | (uint32_t)nch << 16);
+      rec[7] = nch > 1 ? slot0[rec[2]] + (rec[7] & 0xFFFF) : 0;
+    }
+    int32_t* row = P.blob.data() + P.off_merge;
+    for (int32_t t : P.merge_tokens) {
+      const int32_t entry[4] = {t, P.nch_token[t], slot0[t], 0};
+      row = std::copy_n(entry, 4, row);
+    }
+  } else {
+    std::copy(P.merge_tokens.begin(), P.merge_tokens.end(), P.blob.begin() + P.off_merge);
+  }
   P.plan_bytes = P.blob.size() * sizeof(int32_t);
   size_t off = align_up(kStatusBytes + P.plan_bytes, 256);
-  const size_t slots_part = P.max_chunks == 1
-                                ? 0
-                                : (size_t)P.total_q * P.max_chunks * prob.q_heads;
+  const size_t slots_part = P.four_bit()         ? (size_t)P.part_slots * prob.q_heads
+                            : P.max_chunks == 1 ? 0
+                                                : (size_t)P.total_q * P.max_chunks * prob.q_heads;
   P.part_o_off = off;
   // partial rows: bf16; fp32 over a 4-bit cache, where a second rounding to bf16
   // would be the largest error of the result (measured on chunked decode: error
@@ -432,6 +456,7 @@ static WsView ws_view(const Plan& P, void* ws) {
   v.items = blob + P.off_items;
   v.nch_token = blob + P.off_nch;
   v.merge_tokens = blob + P.off_merge;
+  v.merge_rows = reinterpret_cast<const int4*>(blob + P.off_merge);
   v.merge_cnt = P.fused_merge
                     ? reinterpret_cast<int32_t*>(base + kStatusBytes) + P.off_cnt : nullptr;
   v.part_o = reinterpret_cast<__nv_bfloat16*>(base + P.part_o_off);
@@ -663,6 +688,8 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
   p.bsz = pr.bsz;
   p.total_q = plan->total_q;
   p.num_items = (int32_t)(plan->items.size() / kItemWords);
+  p.four_bit = plan->four_bit();
+  p.part_slots = (int32_t)plan->part_slots;
   p.sm_scale_log2 = pr.sm_scale * 1.4426950408889634f;
   p.ep = epilogue_of(*args);
   p.cu_seqlens_q = args->cu_seqlens_q;

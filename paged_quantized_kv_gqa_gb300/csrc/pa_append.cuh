@@ -142,6 +142,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t limit = (uint64_t)p.wait_limit_ns;
   const int G = p.group;
 
+  auto item_at = [&](int it) {
+    if constexpr (kFour) return load_item4<kTile>(p.items, it);
+    else return load_item<kTile>(p.items, it);
+  };
+  // slot of the partial rows of an item's token i (4-bit plans number them compactly)
+  auto part_slot = [&](const Item& m, int i) -> int64_t {
+    if constexpr (kFour) return (int64_t)m.chunk + i * (int64_t)m.nch;
+    else return (int64_t)(m.tok0 + i) * p.max_chunks + m.chunk;
+  };
   PA_DEBUG_PROLOGUE(smem, SM::kTotal - 1024, p, item_begin, item_end);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -191,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int q_issued = 0;
       bool ok = true;
       for (int it = item_begin; it < item_end && ok; ++it) {
-        const Item m = load_item<kTile>(p.items, it);
+        const Item m = item_at(it);
         const int li = it - item_begin;
         const int32_t* bt = p.block_table + (int64_t)m.b * p.max_blocks;
         // Q rows of the item (both k-halves); the buffer is free once both
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, gx[2] = {0, 0};
       bool ok = true;
       for (int it = item_begin; it < item_end && ok; ++it) {
-        const Item m = load_item<kTile>(p.items, it);
+        const Item m = item_at(it);
         const int li = it - item_begin;
         const int nq = m.ntok * G > 128 ? 2 : 1;   // query tiles holding rows
         if (!wait_or_abort(qready, li & 1, limit, abort_any)) { ok = false; break; }
@@ -311,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, gx[2] = {0, 0};
       bool ok = true;
       for (int it = item_begin; it < item_end && ok; ++it) {
-        const Item m = load_item<kTile>(p.items, it);
+        const Item m = item_at(it);
         const int nq = m.ntok * G > 128 ? 2 : 1;
         for (int i = 0; i < m.ntiles && ok; ++i, ++g) {
           if (!wait_or_abort(&vready[g & 1], (g >> 1) & 1, limit, abort_any)) { ok = false; break; }
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fail = true;
     };
     for (int it = item_begin; it < item_end && !fail; ++it) {
-      const Item m = load_item<kTile>(p.items, it);
+      const Item m = item_at(it);
       if (!(X == 0 || m.ntok * G > 128)) {   // tile B holds no rows of this item
         gg += m.ntiles;
         continue;
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool final_row = m.nch == 1;
       const int64_t obase = final_row
           ? ((int64_t)token * p.q_heads + head) * kHeadDim
-          : (((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head) * kHeadDim;
+          : (part_slot(m, tok) * p.q_heads + head) * kHeadDim;
       const OutEpilogue ep_none{nullptr, nullptr, 0, 1.0f, 0.0f, 0.0f};
       const __nv_bfloat16* vsc =
           reinterpret_cast<const __nv_bfloat16*>(p.v_scale) + m.kvh * kHeadDim;
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[(int64_t)token * p.q_heads + head] =
                 l > 0.0f ? (m_run + __log2f(l)) * ln2 : -INFINITY;
         } else {
-          const int64_t sp = ((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head;
+          const int64_t sp = part_slot(m, tok) * p.q_heads + head;
           p.part_m[sp] = l > 0.0f ? m_run * ln2 : -INFINITY;
           p.part_d[sp] = l;
         }
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fail = true;
     };
     for (int it = item_begin; it < item_end && !fail; ++it) {
-      const Item m = load_item<kTile>(p.items, it);
+      const Item m = item_at(it);
       const int li = it - item_begin;
       const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
       const __nv_bfloat16* ksc =

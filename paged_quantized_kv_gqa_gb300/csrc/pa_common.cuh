@@ -122,13 +122,37 @@ __device__ __forceinline__ Item load_item(const int32_t* items, int it) {
   return item_from<TILE>(r[0], r[1]);
 }
 
+// The record of a plan over a 4-bit cache: words 3 and 7 hold n_tok | chunks << 16 and
+// the slot of the item's first token among the partial rows; token i of the item is
+// at slot + i * chunks (m.chunk is the slot here).
+template <int TILE>
+__device__ __forceinline__ Item item4_from(const int4 a, const int4 c) {
+  Item m;
+  m.b = a.x; m.kvh = a.y; m.tok0 = a.z; m.ntok = a.w & 0xFFFF;
+  m.cbase = c.x; m.kv0 = c.y; m.kv1 = c.z; m.chunk = c.w; m.nch = (int)((uint32_t)a.w >> 16);
+  m.ntiles = (m.kv1 - m.kv0 + TILE - 1) / TILE;
+  return m;
+}
+
+template <int TILE>
+__device__ __forceinline__ Item load_item4(const int32_t* items, int it) {
+  const int4* r = reinterpret_cast<const int4*>(items + (int64_t)it * kItemWords);
+  return item4_from<TILE>(r[0], r[1]);
+}
+
 #ifdef PA_DEBUG
 // The CTA's items [begin, end) against the problem (all threads call it; the
 // result is the same in every thread, and in both CTAs of an MLA pair).
 static __device__ __noinline__ bool debug_items_ok(const AttnParams& p, int begin, int end) {
   bool bad = begin < 0 || end < begin || end > p.num_items;
   for (int it = begin + (int)threadIdx.x; !bad && it < end; it += (int)blockDim.x) {
-    const Item m = load_item<1>(p.items, it);
+    Item m = load_item<1>(p.items, it);
+    if (p.four_bit) {
+      m = load_item4<1>(p.items, it);
+      // the slots of all the item's tokens lie within the workspace's
+      const bool slots = m.nch == 1 || (m.chunk >= 0 && (int64_t)m.chunk + (int64_t)(m.ntok - 1) * m.nch < p.part_slots);
+      m.chunk = slots ? 0 : -1;
+    }
     const bool ok = m.b >= 0 && m.b < p.bsz && m.kvh >= 0 && m.kvh < p.kv_heads && m.tok0 >= 0 &&
                     m.ntok >= 1 && m.tok0 + m.ntok <= p.total_q && m.cbase >= 0 && m.kv0 >= 0 &&
                     m.kv0 <= m.kv1 && (int64_t)m.kv1 <= (int64_t)p.max_blocks * kDebugPage &&

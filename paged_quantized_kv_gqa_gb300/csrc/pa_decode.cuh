@@ -189,9 +189,9 @@ struct ItemSrc {
     const int k = it - begin;
     if (k < n_cached) {
       const int4* r = reinterpret_cast<const int4*>(cached + k * kItemWords);
-      return item_from<kTileTok>(r[0], r[1]);
+      return item4_from<kTileTok>(r[0], r[1]);
     }
-    return load_item<kTileTok>(items, it);
+    return load_item4<kTileTok>(items, it);
   }
 };
 
@@ -494,12 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 8; ++k) p.out[o + k] = __float2bfloat16_rn(f[k]);
             }
           } else {
-            const int64_t sp = ((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head;
-            {
-              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.part_o) + sp * kHeadDim + 8 * c);
-              dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-              dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-            }
+            const int64_t sp = (int64_t)(m.chunk + (token - m.tok0) * m.nch) * p.q_heads + head;
+            float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.part_o) + sp * kHeadDim + 8 * c);
+            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
           }
         }
       };
@@ -773,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   p.lse[(int64_t)token * p.q_heads + head] =
                       lr > 0.f ? (mr + __log2f(lr)) * ln2 : -INFINITY;
               } else {
-                const int64_t sp = ((int64_t)token * p.max_chunks + cur.chunk) * p.q_heads + head;
+                const int64_t sp = (int64_t)(cur.chunk + (token - cur.tok0) * cur.nch) * p.q_heads + head;
                 p.part_m[sp] = lr > 0.f ? mr * ln2 : -INFINITY;
                 p.part_d[sp] = lr;
               }

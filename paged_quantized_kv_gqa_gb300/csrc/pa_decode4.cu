@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
       if (k < n_staged && np <= kBtStride) pend_bt = lane < np ? bt_s[k * kBtStride + lane] : -1;
       else pend_bt = lane < np ? bt_at(b, pg0, lane) : -1;
       if (qpre_it < 0) {   // the previous prefetch has been used
-        load_q_rows(qpre, __shfl_sync(0xffffffffu, pend_rec, 2), __shfl_sync(0xffffffffu, pend_rec, 3),
+        load_q_rows(qpre, __shfl_sync(0xffffffffu, pend_rec, 2), __shfl_sync(0xffffffffu, pend_rec, 3) & 0xFFFF,
                     __shfl_sync(0xffffffffu, pend_rec, 1));
         qpre_it = pend_it;
       }
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
   uint32_t ph_comp = 0;
   while (!fail && n_comp < n_load) {
     const int32_t* slot = rec_ring + (k_comp % kRing) * 12;
-    const Item m = item_from<kV4Half>(*reinterpret_cast<const int4*>(slot), *reinterpret_cast<const int4*>(slot + 4));
+    const Item m = item4_from<kV4Half>(*reinterpret_cast<const int4*>(slot), *reinterpret_cast<const int4*>(slot + 4));
     const int it = slot[kItemWords];
     const int n_rows = m.ntok * G;
     const int nh = m.ntiles;   // half pages
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
             if (p.lse != nullptr)
               p.lse[(int64_t)token * p.q_heads + head] = l > 0.f ? (mr + __log2f(l)) * ln2 : -INFINITY;
           } else {
-            const int64_t sp = ((int64_t)token * p.max_chunks + m.chunk) * p.q_heads + head;
+            const int64_t sp = (int64_t)(m.chunk + dt * m.nch) * p.q_heads + head;
             p.part_m[sp] = l > 0.f ? mr * ln2 : -INFINITY;
             p.part_d[sp] = l;
           }
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)
           if (r < n_rows) {
             const int dt = div_g(r);
             float* dst = reinterpret_cast<float*>(p.part_o) +
-                         (((int64_t)(m.tok0 + dt) * p.max_chunks + m.chunk) * p.q_heads + m.kvh * G + r - dt * G) *
+                         ((int64_t)(m.chunk + dt * m.nch) * p.q_heads + m.kvh * G + r - dt * G) *
                              kV4Dim + g;
 #pragma unroll
             for (int d = 0; d < 8; ++d)

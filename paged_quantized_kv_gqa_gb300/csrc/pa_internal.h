@@ -60,11 +60,16 @@ struct Plan {
   bool fused_merge = false;
   // device blob = work_indptr | items | nch_token | merge_tokens | merge
   // counters [total_q][kv_heads] (zeros; fused merge only) (int32), at
-  // kStatusBytes; each array starts at a multiple of 4 words (16 bytes)
+  // kStatusBytes; each array starts at a multiple of 4 words (16 bytes).
+  // Plans over a 4-bit cache: item records as item4_from (pa_common.cuh) reads them,
+  // and in place of the merge tokens an entry {token, chunks, its first slot, 0} each.
   std::vector<int32_t> blob;
   size_t off_indptr = 0, off_items = 0, off_nch = 0, off_merge = 0, off_cnt = 0;  // int32 offsets
   size_t plan_bytes = 0;
   size_t part_o_off = 0, part_m_off = 0, part_d_off = 0, ws_bytes = 0;  // byte offsets
+  // 4-bit plans: slots of all partial rows (a slot holds q_heads rows); the chunks of
+  // a token are neighbours, tokens in order, those with one chunk or none left out
+  int64_t part_slots = 0;
   int64_t kv_bytes = 0;
   double flops = 0.0;
   bool four_bit() const { return prob.kv_dtype == PA_KV_INT4 || prob.kv_dtype == PA_KV_FP4_E2M1; }
@@ -79,6 +84,7 @@ struct WsView {
   const int32_t* nch_token;
   const int32_t* merge_tokens;
   int32_t* merge_cnt;   // fused merge counters or null
+  const int4* merge_rows;   // 4-bit plans: entries in place of the merge tokens
   __nv_bfloat16* part_o;   // fp32 rows for 4-bit plans
   float* part_m;
   float* part_d;
@@ -143,6 +149,8 @@ struct AttnParams {
   int32_t bsz;           // bounds of the work items (checked by the debug build)
   int32_t total_q;
   int32_t num_items;
+  int32_t four_bit;      // the items are 4-bit records, with
+  int32_t part_slots;    // so many slots of partial rows (Plan::part_slots)
 };
 
 void set_error(const std::string& msg);

@@ -2,9 +2,11 @@
 //
 // Merge (FastDeploy append_attention_c8_impl.cuh, merge_multi_chunks_*_kernel
 // launched after the split kernel; the arithmetic is in pa_merge.cuh).
-// One warp per (token, query head); the partial states of a token sit at
-// slot (token * max_chunks + c) * q_heads + head.  HBM-bound, CUDA cores:
-// the row reads of all chunks are issued before they are summed.
+// 8-bit plans: one warp per (token, query head); the partial states of a token sit
+// at slot (token * max_chunks + c) * q_heads + head.  4-bit plans: one warp per eight
+// chunks of the longest row; the states at (first slot of the token + c) * q_heads +
+// head, the slots numbered without gaps.  HBM-bound, CUDA cores: the row reads of all
+// chunks are issued before they are summed.
 #include <algorithm>
 #include <cfloat>
 
@@ -119,12 +121,10 @@ __global__ void __launch_bounds__(256, DV >= 512 ? 5 : 1) merge_kernel(const int
 // warps per row, lane l owning dims 4l .. 4l+3 (one 16-byte load per chunk row).
 // Warp w of a row takes chunks 8 w .. 8 w + 7, then those 8 WPR further on; its
 // first eight rows are requested before the weights are known, so that a row of
-// at most 8 WPR chunks costs one memory round trip after the plan's lookup.  The
+// at most 8 WPR chunks costs one memory round trip after its entry's lookup.  The
 // warps' sums meet in shared memory.  A row without chunks comes out as 0, -inf.
 template <int WPR>
-__global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(const int32_t* __restrict__ merge_tokens,
-                                                        const int32_t* __restrict__ nch_token, int n_merge,
-                                                        int q_heads, int max_chunks,
+__global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(const int4* __restrict__ merge_rows, int n_merge, int q_heads,
                                                         const float* __restrict__ part_o,
                                                         const float* __restrict__ part_m,
                                                         const float* __restrict__ part_d, void* __restrict__ out,
@@ -136,11 +136,11 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(co
   const uint32_t row = blockIdx.x * (kBlockWarps / WPR) + warp / WPR;
   const bool valid = row < (uint32_t)n_merge * (uint32_t)q_heads;
   // (the plan's arrays were there before the attention kernel started)
-  const int token = valid ? merge_tokens[row / (uint32_t)q_heads] : 0;
+  const int4 entry = valid ? merge_rows[row / (uint32_t)q_heads] : make_int4(0, 0, 0, 0);
+  const int token = entry.x, nch = entry.y;
   const int head = valid ? (int)(row % (uint32_t)q_heads) : 0;
-  const int nch = valid ? nch_token[token] : 0;
   pdl_wait();   // launched as a programmatic dependent of the attention kernel
-  const int64_t slot0 = (int64_t)token * max_chunks * q_heads + head;
+  const int64_t slot0 = (int64_t)entry.z * q_heads + head;
   const float4* rows = reinterpret_cast<const float4*>(part_o) + slot0 * 32 + lane;
   const int64_t rstride = (int64_t)q_heads * 32;
   float4 v[kU];
@@ -232,12 +232,12 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
     const int block_warps = std::max(8, wpr);
     cfg.gridDim = dim3((unsigned)((warps * wpr + block_warps - 1) / block_warps));
     cfg.blockDim = dim3(32 * block_warps);
-    if (wpr == 1) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<1>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
-    if (wpr == 2) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<2>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
-    if (wpr == 4) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<4>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
-    if (wpr == 8) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<8>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
-    if (wpr == 16) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<16>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
-    return cudaLaunchKernelEx(&cfg, merge_f32_kernel<32>, mt, nt, n_merge, qh, mc, pf, pm, pd, out, lse, ep);
+    if (wpr == 1) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<1>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
+    if (wpr == 2) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<2>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
+    if (wpr == 4) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<4>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
+    if (wpr == 8) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<8>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
+    if (wpr == 16) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<16>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
+    return cudaLaunchKernelEx(&cfg, merge_f32_kernel<32>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
   }
   if (plan.prob.head_dim_v == 128)
     return cudaLaunchKernelEx(&cfg, merge_kernel<128>, mt, nt, n_merge, qh, mc, po, pm, pd, out, lse, ep);

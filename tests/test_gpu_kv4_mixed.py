@@ -1,0 +1,35 @@
+"""GPU parity of long sequences beside many short ones over the 4-bit cache."""
+import numpy as np
+import pytest
+
+from kv4_helpers import KINDS, args_of, check, device, make, plan_of, run
+
+pytestmark = pytest.mark.gpu
+
+MIXED = [
+    dict(seq_lens=[1] * 40, seq_lens_kv=[90 + 13 * i for i in range(39)] + [20000], q_heads=8, kv_heads=2),
+    dict(seq_lens=[1] * 12, seq_lens_kv=[20000, 0, 511, 512, 700] + [1200] * 7, q_heads=10, kv_heads=2),
+    dict(seq_lens=[3, 1, 2, 0, 3], seq_lens_kv=[12000, 40, 513, 9, 600], q_heads=12, kv_heads=3),       # 12 rows
+    dict(seq_lens=[6, 5, 1, 6], seq_lens_kv=[200, 12000, 1500, 0], q_heads=16, kv_heads=2),             # 48 rows
+    dict(seq_lens=[70, 1, 3], seq_lens_kv=[500, 3000, 5], q_heads=8, kv_heads=2, chunk_size=256),       # append
+    dict(seq_lens=[1, 2, 1], seq_lens_kv=[0, 9000, 800], q_heads=4, kv_heads=4, causal=False, cross=True),
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kw", MIXED)
+def test_long_beside_short(kw, kind):
+    p = make(71, kv_dtype=kind, **kw)
+    out, lse, _, plan = run(p)
+    check(p, out, lse)
+    n = plan.describe()["nch_token"]
+    assert n.max() > 8 and n.min() <= 2
+
+
+def test_long_beside_short_in_the_built_in_workspace():
+    """131k positions beside 63 of 500: 5.8 MB of partial rows are written."""
+    import paged_quantized_kv_gqa_gb300 as pa
+    p = make(72, seq_lens=[1] * 64, seq_lens_kv=[131071] + [500] * 63, q_heads=8, kv_heads=1, kv_dtype="int4")
+    d = device(p)
+    pa.pa_run_static(plan_of(pa, p), args_of(pa, d), check=True)
+    check(p, d["out"].float().cpu().numpy().astype(np.float64), d["lse"].cpu().numpy().astype(np.float64))
