@@ -405,9 +405,16 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       rec[7] = nch > 1 ? slot0[rec[2]] + (rec[7] & 0xFFFF) : 0;
     }
     int32_t* row = P.blob.data() + P.off_merge;
-    for (int32_t t : P.merge_tokens) {
-      const int32_t entry[4] = {t, P.nch_token[t], slot0[t], 0};
-      row = std::copy_n(entry, 4, row);
+    for (int c = 0; c < kMergeClasses; ++c) {
+      // chunk counts of the class: (lo, hi]
+      const int hi = c == 0 ? INT32_MAX : 256 >> c, lo = c + 1 == kMergeClasses ? -1 : 128 >> c;
+      P.merge_class[c + 1] = P.merge_class[c];
+      for (int32_t t : P.merge_tokens) {
+        if (P.nch_token[t] <= lo || P.nch_token[t] > hi) continue;
+        const int32_t entry[4] = {t, P.nch_token[t], slot0[t], 0};
+        row = std::copy_n(entry, 4, row);
+        ++P.merge_class[c + 1];
+      }
     }
   } else {
     std::copy(P.merge_tokens.begin(), P.merge_tokens.end(), P.blob.begin() + P.off_merge);

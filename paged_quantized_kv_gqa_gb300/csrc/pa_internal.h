@@ -32,6 +32,9 @@ constexpr int kDecode4MinTiles = 4;  // smallest share of a tensor-memory CTA, 1
 // positions 311.6, at 8 308.9, at 12 and 16 308.0.
 constexpr int kDecode4ItemCost = 2;
 constexpr int kDecode4TileCost = 12;
+// the merge's classes of 4-bit rows: 32, 16, 8, 4, 2, 1 warps a row, for more than 128,
+// 64, 32, 16, 8 chunks and the others
+constexpr int kMergeClasses = 6;
 constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache
 constexpr int kStatusBytes = 256;    // status block at the start of the workspace
 constexpr int64_t kDefaultWaitNs = 2000000000LL;
@@ -62,7 +65,8 @@ struct Plan {
   // counters [total_q][kv_heads] (zeros; fused merge only) (int32), at
   // kStatusBytes; each array starts at a multiple of 4 words (16 bytes).
   // Plans over a 4-bit cache: item records as item4_from (pa_common.cuh) reads them,
-  // and in place of the merge tokens an entry {token, chunks, its first slot, 0} each.
+  // and in place of the merge tokens an entry {token, chunks, its first slot, 0} each,
+  // class by class.
   std::vector<int32_t> blob;
   size_t off_indptr = 0, off_items = 0, off_nch = 0, off_merge = 0, off_cnt = 0;  // int32 offsets
   size_t plan_bytes = 0;
@@ -70,6 +74,7 @@ struct Plan {
   // 4-bit plans: slots of all partial rows (a slot holds q_heads rows); the chunks of
   // a token are neighbours, tokens in order, those with one chunk or none left out
   int64_t part_slots = 0;
+  int32_t merge_class[kMergeClasses + 1] = {};   // first merge entry of each class
   int64_t kv_bytes = 0;
   double flops = 0.0;
   bool four_bit() const { return prob.kv_dtype == PA_KV_INT4 || prob.kv_dtype == PA_KV_FP4_E2M1; }

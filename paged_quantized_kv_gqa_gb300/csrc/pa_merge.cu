@@ -4,9 +4,9 @@
 // launched after the split kernel; the arithmetic is in pa_merge.cuh).
 // 8-bit plans: one warp per (token, query head); the partial states of a token sit
 // at slot (token * max_chunks + c) * q_heads + head.  4-bit plans: one warp per eight
-// chunks of the longest row; the states at (first slot of the token + c) * q_heads +
-// head, the slots numbered without gaps.  HBM-bound, CUDA cores: the row reads of all
-// chunks are issued before they are summed.
+// chunks; the states at (first slot of the token + c) * q_heads + head, the
+// slots numbered without gaps.  HBM-bound, CUDA cores: the row reads of all chunks are
+// issued before they are summed.
 #include <algorithm>
 #include <cfloat>
 
@@ -117,29 +117,33 @@ __global__ void __launch_bounds__(256, DV >= 512 ? 5 : 1) merge_kernel(const int
   merge_store<DV>(acc[0], M[0], W[0], out, lse, ep, token, head, q_heads, lane);
 }
 
-// Rows whose partial states are fp32 (plans over a 4-bit cache), 128 wide: WPR
-// warps per row, lane l owning dims 4l .. 4l+3 (one 16-byte load per chunk row).
-// Warp w of a row takes chunks 8 w .. 8 w + 7, then those 8 WPR further on; its
-// first eight rows are requested before the weights are known, so that a row of
-// at most 8 WPR chunks costs one memory round trip after its entry's lookup.  The
-// warps' sums meet in shared memory.  A row without chunks comes out as 0, -inf.
-template <int WPR>
-__global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(const int4* __restrict__ merge_rows, int n_merge, int q_heads,
-                                                        const float* __restrict__ part_o,
-                                                        const float* __restrict__ part_m,
-                                                        const float* __restrict__ part_d, void* __restrict__ out,
-                                                        float* __restrict__ lse, const OutEpilogue ep) {
-  constexpr int kU = 8, kBlockWarps = WPR <= 8 ? 8 : WPR;
-  __shared__ float4 sums[kBlockWarps][32];
-  __shared__ float weights[kBlockWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
-  const uint32_t row = blockIdx.x * (kBlockWarps / WPR) + warp / WPR;
-  const bool valid = row < (uint32_t)n_merge * (uint32_t)q_heads;
-  // (the plan's arrays were there before the attention kernel started)
-  const int4 entry = valid ? merge_rows[row / (uint32_t)q_heads] : make_int4(0, 0, 0, 0);
+// Rows whose partial states are fp32 (plans over a 4-bit cache), 128 wide, lane l
+// owning dims 4l .. 4l+3 (one 16-byte load per chunk row).  Warp w of a row takes
+// chunks 8 w .. 8 w + 7, then those 8 * (warps of the row) further on; its first eight
+// rows are requested before the weights are known, so that a row of at most eight
+// chunks a warp costs one memory round trip after its entry's lookup.  The warps' sums
+// meet in shared memory.  A row without chunks comes out as 0, -inf.
+//   merge_f32_kernel          every row gets the warps that the longest one takes
+//   merge_f32_classes_kernel  a row gets the warps that its own chunks take.  The plan's
+//                             entries come in classes by their chunks, a block of 32
+//                             warps works on one class.
+// The first is used while all rows are of one class or its warps fit the GPU at once
+// (the lookup of the classes costs 0.6 us).  Beyond that it is what the call waits for:
+// one sequence of 131k positions beside 255 of 500, 64 heads, had 9280 rows merged by
+// 262144 warps, 153 us; by their own 10 us.
+struct MergeGrid {
+  uint32_t block[kMergeClasses + 1];   // first block of each class; the grid's size
+  uint32_t entry[kMergeClasses + 1];   // first entry of each class; their count
+};
+
+// One row by `wpr` warps of the block, of which this is warp `sub` (all of them call it).
+__device__ __forceinline__ void merge_f32_row(const int4 entry, bool valid, int head, int q_heads, int wpr, int sub,
+                                              int warp, int lane, float4 (*sums)[32], float* weights,
+                                              const float* __restrict__ part_o, const float* __restrict__ part_m,
+                                              const float* __restrict__ part_d, void* __restrict__ out,
+                                              float* __restrict__ lse, const OutEpilogue& ep) {
+  constexpr int kU = 8;
   const int token = entry.x, nch = entry.y;
-  const int head = valid ? (int)(row % (uint32_t)q_heads) : 0;
-  pdl_wait();   // launched as a programmatic dependent of the attention kernel
   const int64_t slot0 = (int64_t)entry.z * q_heads + head;
   const float4* rows = reinterpret_cast<const float4*>(part_o) + slot0 * 32 + lane;
   const int64_t rstride = (int64_t)q_heads * 32;
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(co
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, W = 0.f;
   if (M != -INFINITY) {
-    for (int c0 = kU * sub; c0 < nch; c0 += kU * WPR) {
+    for (int c0 = kU * sub; c0 < nch; c0 += kU * wpr) {
       if (c0 != kU * sub) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -182,13 +186,13 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(co
     for (int o = 4; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
     W = __shfl_sync(0xffffffffu, W, 0);
   }
-  if constexpr (WPR > 1) {
+  if (wpr > 1) {   // (the same for the whole block)
     sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     if (lane == 0) weights[warp] = W;
     __syncthreads();
     if (sub != 0) return;
 #pragma unroll 4
-    for (int k = 1; k < WPR; ++k) {
+    for (int k = 1; k < wpr; ++k) {
       const float4 t = sums[warp + k][lane];
       acc[0] += t.x;
       acc[1] += t.y;
@@ -198,6 +202,53 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR) merge_f32_kernel(co
     }
   }
   if (valid) merge_store<128>(acc, M, W, out, lse, ep, token, head, q_heads, lane);
+}
+
+
+template <int WPR>
+__global__ void __launch_bounds__(WPR <= 8 ? 256 : 32 * WPR)
+    merge_f32_kernel(const int4* __restrict__ merge_rows, int n_merge, int q_heads, const float* __restrict__ part_o,
+                     const float* __restrict__ part_m, const float* __restrict__ part_d, void* __restrict__ out,
+                     float* __restrict__ lse, const OutEpilogue ep) {
+  constexpr int kBlockWarps = WPR <= 8 ? 8 : WPR;
+  __shared__ float4 sums[kBlockWarps][32];
+  __shared__ float weights[kBlockWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t row = blockIdx.x * (kBlockWarps / WPR) + warp / WPR;
+  const bool valid = row < (uint32_t)n_merge * (uint32_t)q_heads;
+  // (the plan's arrays were there before the attention kernel started)
+  const int4 entry = valid ? merge_rows[row / (uint32_t)q_heads] : make_int4(0, 0, 0, 0);
+  const int head = valid ? (int)(row % (uint32_t)q_heads) : 0;
+  pdl_wait();   // launched as a programmatic dependent of the attention kernel
+  merge_f32_row(entry, valid, head, q_heads, WPR, warp % WPR, warp, lane, sums, weights, part_o, part_m, part_d, out,
+                lse, ep);
+}
+
+__global__ void __launch_bounds__(1024)
+    merge_f32_classes_kernel(const int4* __restrict__ merge_rows, const MergeGrid grid, int q_heads,
+                             const float* __restrict__ part_o, const float* __restrict__ part_m,
+                             const float* __restrict__ part_d, void* __restrict__ out, float* __restrict__ lse,
+                             const OutEpilogue ep) {
+  __shared__ float4 sums[32][32];
+  __shared__ float weights[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int lw = kMergeClasses - 1;   // 2^lw warps a row in this block's class
+  uint32_t block = blockIdx.x, at = 0, end = grid.entry[1];
+#pragma unroll
+  for (int c = 1; c < kMergeClasses; ++c)
+    if (blockIdx.x >= grid.block[c]) {
+      lw = kMergeClasses - 1 - c;
+      block = blockIdx.x - grid.block[c];
+      at = grid.entry[c];
+      end = grid.entry[c + 1];
+    }
+  const uint32_t row = block * (32u >> lw) + (uint32_t)(warp >> lw);
+  at += row / (uint32_t)q_heads;
+  const bool valid = at < end;
+  const int4 entry = valid ? merge_rows[at] : make_int4(0, 0, 0, 0);
+  pdl_wait();
+  merge_f32_row(entry, valid, (int)(row % (uint32_t)q_heads), q_heads, 1 << lw, warp & ((1 << lw) - 1), warp, lane,
+                sums, weights, part_o, part_m, part_d, out, lse, ep);
 }
 
 cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* lse,
@@ -226,18 +277,36 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const float* pm = ws.part_m;
   const float* pd = ws.part_d;
   if (plan.four_bit()) {
-    // one warp per eight chunks of the longest row, up to 32
     const float* pf = reinterpret_cast<const float*>(po);
-    const int wpr = mc <= 8 ? 1 : mc <= 16 ? 2 : mc <= 32 ? 4 : mc <= 64 ? 8 : mc <= 128 ? 16 : 32;
+    const int32_t* cls = plan.merge_class;
+    int longest = 0;   // its class
+    while (cls[longest] == cls[longest + 1]) ++longest;
+    const int wpr = 1 << (kMergeClasses - 1 - longest);
+    if (cls[longest + 1] < n_merge && warps * wpr > 32 * (int64_t)plan.num_sms) {
+      MergeGrid grid;
+      int64_t total = 0;
+      for (int c = 0; c < kMergeClasses; ++c) {
+        grid.block[c] = (uint32_t)total;
+        grid.entry[c] = (uint32_t)cls[c];
+        const int64_t per_block = 32 >> (kMergeClasses - 1 - c);   // rows
+        total += ((int64_t)(cls[c + 1] - cls[c]) * qh + per_block - 1) / per_block;
+      }
+      grid.block[kMergeClasses] = (uint32_t)total;
+      grid.entry[kMergeClasses] = (uint32_t)n_merge;
+      cfg.gridDim = dim3((unsigned)total);
+      cfg.blockDim = dim3(1024);
+      return cudaLaunchKernelEx(&cfg, merge_f32_classes_kernel, ws.merge_rows, grid, qh, pf, pm, pd, out, lse, ep);
+    }
     const int block_warps = std::max(8, wpr);
     cfg.gridDim = dim3((unsigned)((warps * wpr + block_warps - 1) / block_warps));
     cfg.blockDim = dim3(32 * block_warps);
-    if (wpr == 1) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<1>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
-    if (wpr == 2) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<2>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
-    if (wpr == 4) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<4>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
-    if (wpr == 8) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<8>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
-    if (wpr == 16) return cudaLaunchKernelEx(&cfg, merge_f32_kernel<16>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
-    return cudaLaunchKernelEx(&cfg, merge_f32_kernel<32>, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
+    auto kern = wpr == 1   ? merge_f32_kernel<1>
+                : wpr == 2 ? merge_f32_kernel<2>
+                : wpr == 4 ? merge_f32_kernel<4>
+                : wpr == 8 ? merge_f32_kernel<8>
+                : wpr == 16 ? merge_f32_kernel<16>
+                            : merge_f32_kernel<32>;
+    return cudaLaunchKernelEx(&cfg, kern, ws.merge_rows, n_merge, qh, pf, pm, pd, out, lse, ep);
   }
   if (plan.prob.head_dim_v == 128)
     return cudaLaunchKernelEx(&cfg, merge_kernel<128>, mt, nt, n_merge, qh, mc, po, pm, pd, out, lse, ep);

@@ -33,3 +33,21 @@ def test_long_beside_short_in_the_built_in_workspace():
     d = device(p)
     pa.pa_run_static(plan_of(pa, p), args_of(pa, d), check=True)
     check(p, d["out"].float().cpu().numpy().astype(np.float64), d["lse"].cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("G", [3, 8, 20])
+def test_rows_of_every_chunk_count_are_merged_together(G):
+    """From no chunk at all to more than 128, so that rows taking 1 to 32 warps of the
+    merge stand beside each other.  3 heads: all rows fit the GPU with the longest one's
+    warps; 8 and 20 heads: each gets its own.  20 rows are the tensor-memory kernel's."""
+    kv = [700, 30000, 0, 1500, 7000, 100, 14000, 3000]
+    p = make(73, seq_lens=[1] * 44, seq_lens_kv=kv + [600 + 5 * i for i in range(36)], q_heads=G, kv_heads=1,
+             causal=False, cross=True)
+    out, lse, _, plan = run(p)
+    check(p, out, lse)
+    n = plan.describe()["nch_token"]
+    warps = 1 << sum(int(n.max()) > x for x in (8, 16, 32, 64, 128))
+    assert n[2] == 0 and n[5] == 1 and n[0] > 1
+    assert (int((n != 1).sum()) * G * warps > 32 * 152) == (G > 3)
+    if G < 20:
+        assert {sum(int(x) > y for y in (8, 16, 32, 64, 128)) for x in n} == set(range(6))
