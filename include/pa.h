@@ -91,11 +91,14 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *           GLOBAL       fp32 [1]                     (one value for K and V)
  *   chunk_size > 0 splits the KV range into chunks of that many positions (a
  *   multiple of block_size); 0 never splits; -1 lets the planner choose.  Plans
- *   of the decode family over a 4-bit cache ignore it: the planner keeps ranges of
- *   at most 512 positions whole and otherwise cuts pieces of equal cost, so
- *   pa_merge always belongs after pa_run there.  Over a 4-bit cache the workspace
- *   holds one fp32 row per piece and query head; over an 8-bit one it grows with the
- *   query tokens times the chunks of the longest sequence.
+ *   of the decode family over a 4-bit cache choose by themselves whatever it is:
+ *   ranges of at most 512 positions stay whole, otherwise they are cut into pieces
+ *   of equal cost.  After pa_run of a plan made with chunk_size = 0 every row is
+ *   final: where it has rows for the merge all the same (those pieces, rows of
+ *   cross attention that see nothing), pa_run enqueues the merge too and pa_merge
+ *   does nothing.  Over a 4-bit cache the workspace holds one fp32 row per piece
+ *   and query head; over an 8-bit one it grows with the query tokens times the
+ *   chunks of the longest sequence.
  *   q_stride is the distance in elements between consecutive tokens of q
  *   (>= q_heads * head_dim_qk; FastDeploy's packed qkv uses
  *   (q_heads + 2 * kv_heads) * head_dim).
@@ -240,15 +243,16 @@ pa_status pa_plan_upload(const pa_plan_t* plan, void* workspace, void* stream);
  * persistent.cuh reduction, XQA mla_sm120.cu "last CTA merges" semaphore)
  * and resets the group's counter in the workspace, so the uploaded plan
  * stays valid for the next pa_run; after a failed run (pa_check != PA_OK)
- * upload the plan again.  Other plans need pa_merge afterwards.  The
+ * upload the plan again.  Plans made with chunk_size = 0 leave nothing to
+ * merge; others need pa_merge afterwards.  The
  * workspace must hold this plan (pa_plan_upload).  PA_ERR_UNSUPPORTED for a
  * family whose kernel is not compiled into this build. */
 pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, void* stream);
 
 /* Enqueues the log-sum-exp merge of the partial states of split rows into
  * out/lse, and writes the rows that see no position (cross attention to an
- * empty sequence).  A no-op when the plan has neither or merges inside pa_run
- * (pa_plan_desc.fused_merge). */
+ * empty sequence).  A no-op when the plan has neither, merges inside pa_run
+ * (pa_plan_desc.fused_merge) or was made with chunk_size = 0. */
 pa_status pa_merge(const pa_plan_t* plan, const pa_args* args, void* workspace, void* stream);
 
 /* Synchronises the stream, then reads the workspace status word.  Returns

@@ -544,6 +544,12 @@ static bool scales_aligned(const pa_problem& pr, const pa_args* a) {
   return reinterpret_cast<uintptr_t>(a->k_scale) % n == 0 && reinterpret_cast<uintptr_t>(a->v_scale) % n == 0;
 }
 
+static pa_status enqueue_merge(const Plan& P, const pa_args& a, const WsView& ws, cudaStream_t st) {
+  cudaError_t e = launch_merge(P, ws, a.out, a.lse, epilogue_of(a), st);
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("merge: ") + cudaGetErrorString(e));
+  return PA_OK;
+}
+
 static pa_status check_args(const Plan& P, const pa_args* a, bool need_cache) {
   if (!a) return fail(PA_ERR_INVALID_ARG, "null pa_args");
   if (!a->out) return fail(PA_ERR_INVALID_ARG, "null out");
@@ -652,9 +658,9 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
   if (!plan || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan or workspace");
   pa_status s = check_args(*plan, args, true);
   if (s != PA_OK) return s;
-  if (plan->num_ctas == 0) return PA_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WsView ws = ws_view(*plan, workspace);
+  if (plan->num_ctas == 0) return plan->merge_in_run() ? enqueue_merge(*plan, *args, ws, st) : PA_OK;
   const pa_problem& pr = plan->prob;
   FaultCfg fc;
   {
@@ -772,19 +778,15 @@ pa_status pa_run(const pa_plan_t* plan, const pa_args* args, void* workspace, vo
     e = launch_mla(*plan, p, tc, st);
   }
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("launch: ") + cudaGetErrorString(e));
-  return PA_OK;
+  return plan->merge_in_run() ? enqueue_merge(*plan, *args, ws, st) : PA_OK;
 }
 
 pa_status pa_merge(const pa_plan_t* plan, const pa_args* args, void* workspace, void* stream) {
   if (!plan || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan or workspace");
   pa_status s = check_args(*plan, args, false);
   if (s != PA_OK) return s;
-  if (plan->fused_merge) return PA_OK;   // pa_run merged the split rows
-  const WsView ws = ws_view(*plan, workspace);
-  cudaError_t e = launch_merge(*plan, ws, args->out, args->lse, epilogue_of(*args),
-                               static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("merge: ") + cudaGetErrorString(e));
-  return PA_OK;
+  if (plan->fused_merge || plan->merge_in_run()) return PA_OK;   // pa_run merged the split rows
+  return enqueue_merge(*plan, *args, ws_view(*plan, workspace), static_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_check(const pa_plan_t* plan, const void* workspace, void* stream, int32_t* detail) {

@@ -61,6 +61,10 @@ struct Plan {
   // (the CTA that finishes a row group's last chunk merges it); pa_merge is
   // then a no-op
   bool fused_merge = false;
+  // a plan made with chunk_size 0 promises rows that need no pa_merge: where it has
+  // rows for the merge all the same (4-bit decode, cross attention to nothing), pa_run
+  // enqueues the merge kernel itself and pa_merge is a no-op
+  bool merge_in_run() const { return prob.chunk_size == 0 && !merge_tokens.empty(); }
   // device blob = work_indptr | items | nch_token | merge_tokens | merge
   // counters [total_q][kv_heads] (zeros; fused merge only) (int32), at
   // kStatusBytes; each array starts at a multiple of 4 words (16 bytes).

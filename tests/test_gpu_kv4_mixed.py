@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from kv4_helpers import KINDS, args_of, check, device, make, plan_of, run
+from kv4_helpers import KINDS, args_of, check, device, make, plan_of, reference, run, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,51 @@ def test_rows_of_every_chunk_count_are_merged_together(G):
     assert (int((n != 1).sum()) * G * warps > 32 * 152) == (G > 3)
     if G < 20:
         assert {sum(int(x) > y for y in (8, 16, 32, 64, 128)) for x in n} == set(range(6))
+
+
+def without_merge(pa, p):
+    """Plan, upload, pa_run alone; then pa_merge, which must leave the rows alone."""
+    d = device(p)
+    plan = plan_of(pa, p)
+    ws, args = workspace(plan), args_of(pa, d)
+    pa.pa_plan_upload(plan, ws)
+    pa.pa_run(plan, args, ws)
+    assert pa.pa_check(plan, ws)[0] == 0
+    assert len(plan.describe()["merge_tokens"])
+    got = d["out"].float().cpu().numpy().astype(np.float64), d["lse"].cpu().numpy().astype(np.float64)
+    d["out"].fill_(7)
+    pa.pa_merge(plan, args, ws)
+    assert pa.pa_check(plan, ws)[0] == 0 and bool((d["out"] == 7).all())
+    assert bool((d["out_all"][-1] == 7).all()) and bool((d["lse_all"][-1] == 7).all())
+    return got
+
+
+@pytest.mark.parametrize("kw", [
+    dict(seq_lens=[1, 1, 2], seq_lens_kv=[5000, 30, 700], q_heads=8, kv_heads=2),
+    dict(seq_lens=[6, 1], seq_lens_kv=[4000, 9], q_heads=16, kv_heads=2),
+    dict(seq_lens=[1, 2, 1], seq_lens_kv=[0, 3000, 5], q_heads=4, kv_heads=2, causal=False, cross=True),
+    dict(seq_lens=[2, 1], seq_lens_kv=[0, 0], q_heads=4, kv_heads=2, causal=False, cross=True),
+    dict(seq_lens=[70, 3, 9], seq_lens_kv=[0, 100, 0], q_heads=4, kv_heads=2, causal=False, cross=True),
+])
+def test_rows_of_plans_without_chunks_are_final_after_pa_run(kw):
+    """A program that never splits (chunk_size 0) and does not call pa_merge."""
+    import paged_quantized_kv_gqa_gb300 as pa
+    p = make(74, kv_dtype="int4", chunk_size=0, **kw)
+    check(p, *without_merge(pa, p))
+
+
+def test_8_bit_cross_rows_without_chunks_are_final_after_pa_run():
+    import types
+    import synth
+    from oracle import attention as oa
+    import paged_quantized_kv_gqa_gb300 as pa
+    c = synth.make_case(name="z", seed=75, kv_dtype="int8", causal=False, seq_lens=[1, 2, 1], seq_lens_kv=[0, 200, 64],
+                        q_heads=8, kv_heads=2, chunk_size=0)
+    p = types.SimpleNamespace(**{n: getattr(c, n) for n in (
+        "q_heads", "kv_heads", "kv_dtype", "scale_kind", "layout", "causal", "chunk_size", "sm_scale", "q_stride",
+        "seq_lens", "seq_lens_kv", "bsz", "cu_seqlens_q", "total_q", "num_pages", "max_blocks_per_seq", "block_table",
+        "cache_k", "cache_v", "k_scale", "v_scale", "q_bits")})
+    c.cross = p.cross = True
+    p.held = c.seq_lens_kv
+    ref = reference(p, rows=lambda w, b, h, n: oa.dequant_kv(c, b, h, n)[w == "v"])
+    check(p, *without_merge(pa, p), ref)

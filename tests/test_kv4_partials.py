@@ -61,3 +61,18 @@ def test_plans_without_split_rows_need_no_partial_rows(pa):
     pl = plan(pa, lengths([1] * 9, [400] * 9, 8, 2))
     d = pl.describe()
     assert d["max_chunks"] == 1 and pl.workspace_size <= d["plan_bytes"] + 2 * 256
+
+
+@pytest.mark.parametrize("q,kv,cross,kind", [
+    ([1, 1], [5000, 30], False, "int4"), ([6], [9000], False, "fp4_e2m1"),
+    ([1, 2], [0, 0], True, "int4"), ([70, 3], [0, 100], True, "fp4_e2m1"), ([1, 1], [0, 100], True, "int8"),
+])
+def test_plans_made_without_chunks_leave_nothing_to_merge(pa, q, kv, cross, kind):
+    """chunk_size 0 promises final rows after pa_run: pa_merge does nothing (here it
+    would fail, there being no device memory behind the arguments)."""
+    p = make(1, seq_lens=q, seq_lens_kv=kv, q_heads=16, kv_heads=2, causal=not cross, cross=cross, garbage=False)
+    p.kv_dtype = kind
+    pl = plan(pa, p)
+    assert len(pl.describe()["merge_tokens"])
+    a = dict(q=256, cache_k=256, cache_v=256, k_scale=256, v_scale=256, block_table=256, out=256)
+    pa.pa_merge(pl, pa.make_args(**a), 256, 0)
