@@ -40,8 +40,8 @@ Spec:
   the rows that see nothing; the merge writes them).
   A 4-bit cache, decode family: chunk_size is ignored; no split while the largest
   lim is at most 8 * B, else shares of about equal cost per
-  worker, w workers per CTA: 16 warps if max(q_len) * G <= 16, else the smallest
-  w in 1 .. 4 with slots * w divisible by kv_heads (4 if none).  A piece (a range
+  worker, w workers per CTA: 16 warps if max(q_len) * G <= 8, 8 warps up to 16, else
+  the smallest w in 1 .. 4 with slots * w divisible by kv_heads (4 if none).  A piece (a range
   of one tile's positions) costs its half pages (B / 2 positions) plus a start: 2
   for warps, which cut at half pages, 12 for CTAs, which cut at pages.  Shares are
   filled in tile order: a new one begins where less than start + 2 is left of the
@@ -104,7 +104,7 @@ def plan(p, num_sms: int) -> dict:
 
     decode4 = p.kv_dtype in ("int4", "fp4_e2m1") and family == "decode"
     if decode4 and max((t[3] for t in tiles), default=0) > 8 * B:
-        return _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, max_q * G <= 16)
+        return _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, max_q * G)
     if family == "mla" and int(p.chunk_size) == -1:
         return _mla_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B)
 
@@ -153,9 +153,10 @@ def plan(p, num_sms: int) -> dict:
                 max_chunks=max_chunks, merge_tokens=merge_tokens)
 
 
-def _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, warps):
+def _equal_shares(p, tiles, slots, tpt, q_lens, slkv, cu, B, cross, rows):
     """Shares of about equal cost per worker (the 4-bit decode rule in the spec above)."""
-    w = 16 if warps else next((k for k in (1, 2, 3) if slots * k % p.kv_heads == 0), 4)
+    warps = rows <= 16
+    w = 16 if rows <= 8 else 8 if warps else next((k for k in (1, 2, 3) if slots * k % p.kv_heads == 0), 4)
     groups = max(1, slots * w // p.kv_heads)
     unit, per_unit, start, least = (B // 2, 1, 2, 4) if warps else (B, 2, 12, 16)
 

@@ -167,7 +167,7 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     // each CTA's items longest first.
     const bool by_warp = max_q * G <= kWarpDecodeRows;
     // CTA workers: lanes per CTA, so that the kv heads divide the lanes (else 4)
-    int per_cta = kDecode4Warps;
+    int per_cta = decode4_warps((int)(max_q * G));
     if (!by_warp)
       for (per_cta = 1; per_cta < 4 && (int64_t)slots * per_cta % prob.kv_heads != 0;) ++per_cta;
     const int64_t groups = std::max<int64_t>(1, (int64_t)slots * per_cta / prob.kv_heads);

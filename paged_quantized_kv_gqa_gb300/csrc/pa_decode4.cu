@@ -44,7 +44,7 @@ struct D4Cfg {
   // and 157 us, one stage 177, 12 warps of three stages 161; on 24 of up to 3k
   // positions 20.6, 18.0, 19.4 and 17.8 us, one stage 18.0, 12 warps of three 18.3.
   // 9 to 16 rows need twice the accumulators: 8 warps.
-  static constexpr int kWarps = NB == 1 ? kDecode4Warps : 8;
+  static constexpr int kWarps = decode4_warps(8 * NB);
   static constexpr int kStages = NB == 1 ? 2 : 3;
   static constexpr int kItems = 32;    // CTA item records kept in shared memory
   static constexpr int kScaleOff = kWarps * kStages * kStage4;

@@ -18,7 +18,11 @@ constexpr int kItemWords = 8;        // b, kvh, token0, n_tok, causal_base, kv0,
 constexpr int kDecodeRows = 64;      // packed (token, head) rows per decode tile
 constexpr int kWarpDecodeRows = 16;  // decode tiles up to this many rows run warp per item
 constexpr int kAppendRows = 256;     // packed rows per append item (two 128-row tiles)
-constexpr int kDecode4Warps = 16;    // warps of a 4-bit decode CTA (each takes whole items)
+// Warps of a 4-bit decode CTA (each takes whole items): up to 8 rows, and 9 to 16, which
+// need twice the accumulators.  Plans cut for as many: cut for 16, plans of 9 to 16 rows
+// took 77.5 us (32 sequences of 2-8k, 16 rows, int4; for 8 68.4), 35.6 (24 of up to 3k; 26.0)
+// and 228 (8 of 32k-131k; 219).
+constexpr int decode4_warps(int rows) { return rows <= 8 ? 16 : 8; }
 // 4-bit decode plans keep their tiles whole while none is longer: up to there the
 // merge's launch costs more than the split saves
 constexpr int kDecode4WholePages = 8;

@@ -76,3 +76,12 @@ def test_plans_made_without_chunks_leave_nothing_to_merge(pa, q, kv, cross, kind
     assert len(pl.describe()["merge_tokens"])
     a = dict(q=256, cache_k=256, cache_v=256, k_scale=256, v_scale=256, block_table=256, out=256)
     pa.pa_merge(pl, pa.make_args(**a), 256, 0)
+
+
+@pytest.mark.parametrize("q,G,workers", [(1, 8, 16), (2, 8, 8), (3, 4, 8), (2, 5, 8), (1, 16, 8), (1, 4, 16)])
+def test_decode_is_cut_for_the_warps_that_a_cta_has(pa, q, G, workers):
+    """Pieces: one for every tile and head, and one cut for every worker at most (16
+    warps a CTA up to 8 rows, 8 warps up to 16)."""
+    r = np.random.default_rng(q * G)
+    d = plan(pa, lengths([q] * 32, r.integers(2048, 8192, 32), 8 * G, 8)).describe()
+    assert 152 * workers * 0.9 < d["num_items"] <= 152 * workers + 32 * 8
