@@ -785,6 +785,8 @@ pa_status pa_merge(const pa_plan_t* plan, const pa_args* args, void* workspace, 
   if (!plan || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan or workspace");
   pa_status s = check_args(*plan, args, false);
   if (s != PA_OK) return s;
+  if (plan->family == PA_FAMILY_MLA && reinterpret_cast<uintptr_t>(args->out) % 16)
+    return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
   if (plan->fused_merge || plan->merge_in_run()) return PA_OK;   // pa_run merged the split rows
   return enqueue_merge(*plan, *args, ws_view(*plan, workspace), static_cast<cudaStream_t>(stream));
 }
