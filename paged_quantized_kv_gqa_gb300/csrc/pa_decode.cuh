@@ -17,9 +17,11 @@
 //   * int4 codes unpack in the order 0 4 1 5 2 6 3 7 of each eight: the dims of Q' take
 //     the same order, and a P^T row is written at its position's place in that order;
 //   * partial rows are fp32, merged by the separate kernel only;
-//   * per-channel K scales go into Q', rounded to fp16 as one number (the lse moves by
-//     up to 2e-4; a second number, as in the warp kernel, would need 16 MMAs for S
-//     instead of 8 and shared memory that 64 rows do not leave).
+//   * per-channel K scales go into Q': the product of a bf16 query and a bf16 scale has
+//     16 significant bits and is the sum of two fp16 numbers, as in the warp kernel, with
+//     eight more MMAs a tile for the low parts (PC; 48 rows, int4: 297 -> 321 us, FP4
+//     273 -> 294).  As one number a score moves by up to 2^-11 of its terms' magnitude:
+//     with channel scales near 1e-3 and scores near 10 the lse moved by 2e-3 (now 1e-5).
 //
 // Included by pa_decode4_tm.cu.
 #pragma once
@@ -37,12 +39,12 @@ namespace {
 constexpr int kTileTok = 128;
 constexpr int kHeadDim = 128;
 constexpr int kPage = 64;
-constexpr int kSlab = kPage * kHeadDim;          // bytes of one (page, head) K or V slab
-constexpr int kStageBytes = 4 * kSlab;           // K (2 pages) + V (2 pages)
-constexpr int kSlot4 = 5120;                     // 4-bit: a slab's place in a stage's K or V half
-                                                 // (64B-swizzled boxes start on 512 bytes)
-constexpr int kVs16Warp = 2 * kTileTok * 2;      // 4-bit: a CV warp's V scales as fp16 [2 blocks][128]
-static_assert(kSlot4 >= kV4Slab && kSlot4 % 512 == 0 && 2 * kSlot4 <= 2 * kSlab, "4-bit stage layout");
+constexpr int kSlot4 = 5120;                     // a slab's place in a stage (64B-swizzled boxes
+                                                 // start on 512 bytes)
+constexpr int kVOff = 2 * kSlot4;                // V slabs behind the two K slabs
+constexpr int kStageBytes = 4 * kSlot4;          // K (2 pages) + V (2 pages)
+constexpr int kVs16Warp = 2 * kTileTok * 2;      // a V converter warp's scales as fp16 [2 blocks][128]
+static_assert(kSlot4 >= kV4Slab && kSlot4 % 512 == 0, "stage layout");
 constexpr float kTau = 8.0f;                     // lazy-rescale threshold (log2 units)
 // Warpgroups: two softmax, CV, IO.  4-bit: one CV warpgroup for K and one for V (a
 // code needs more steps than a byte, and one group for both held the pipeline up),
@@ -160,7 +162,8 @@ template <int NR>
 struct Smem {
   static constexpr int kStages = kPageStages;
   static constexpr int kQ = kStages * kStageBytes;         // Q'[2]
-  static constexpr int kP = kQ + 2 * NR * 256;             // P^T ring
+  static constexpr int kQlo = kQ + 2 * NR * 256;           // its low parts [2] (per-channel K scales)
+  static constexpr int kP = kQlo + 2 * NR * 256;           // P^T ring
   static constexpr int kRed = kP + kPBufs * kPBufBytes;    // [4][NR] warp maxima
   static constexpr int kRedL = kRed + 4 * NR * 4;          // [4][NR] warp row sums
   static constexpr int kLsum = kRedL + 4 * NR * 4;         // [2][NR] 1/l per item (by parity)
@@ -177,6 +180,7 @@ struct Smem {
   static constexpr int kTotal = kVs16 + 4 * kVs16Warp + 1024;              // + alignment slack
   static_assert(kVs16 % 16 == 0, "the scales are read as 16-byte vectors");
   static_assert(kItems % 16 == 0, "item records are read as int4");
+  static_assert(kQ % 1024 == 0 && kQlo % 1024 == 0 && kP % 1024 == 0, "swizzled operands start on 1 KB");
   static_assert(kTotal <= 232448, "shared memory overflow");
 };
 
@@ -218,8 +222,8 @@ struct TileCursor {
 
 }  // namespace
 
-// KV: PA_KV_*; cv: the 4-bit V cache (tm_v is unused then)
-template <int NR, int KV, bool TREE>
+// KV: PA_KV_*; PC: per-channel K scales; cv: the 4-bit V cache (tm_v is unused)
+template <int NR, int KV, bool TREE, bool PC>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const uint8_t* __restrict__ cv, const AttnParams p) {
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!in_pool) record_status(p.status, PA_ERR_BAD_PAGE, it);   // reads page 0 instead
             const int slab = (in_pool ? page : 0) * p.kv_heads + m.kvh;
             tma_load_2d(st + pg * kSlot4, &tm_k, &full[stage], 0, slab * (kV4Slab / 64));
-            bulk_load(st + 2 * kSlab + pg * kSlot4, cv + (int64_t)slab * kV4Slab, kV4Slab, &full[stage]);
+            bulk_load(st + kVOff + pg * kSlot4, cv + (int64_t)slab * kV4Slab, kV4Slab, &full[stage]);
           }
           trace_ev(p, g, 0);
         }
@@ -374,6 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 8; ++kk)
             mma_ts(tmem + TM::S0 + (g & 1) * NR, tmem + TM::K0 + (g & 1) * 64 + 8 * kk,
                    sdesc_k128(qb + (kk >> 2) * NR * 128 + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+          if constexpr (PC) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tmem + TM::S0 + (g & 1) * NR, tmem + TM::K0 + (g & 1) * 64 + 8 * kk,
+                     sdesc_k128(qb + SM::kQlo - SM::kQ + (kk >> 2) * NR * 128 + (kk & 3) * 32), idesc, 1u);
+          }
           tc_commit(&sfull[g & 1]);
         }
         ++commits[g & 1];
@@ -836,20 +846,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int r = (d >> 4) + 8 * k;
-        uint4 packed = make_uint4(0, 0, 0, 0);
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};   // lo: PC only
         if (r < n_rows) {
           const __nv_bfloat16* hv = reinterpret_cast<const __nv_bfloat16*>(&raw[k]);
           float f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = __bfloat162float(hv[e]) * sc[e];
-          constexpr int kG = pair_gap<KV>();
-          packed.x = pack_half2(f[pair_first<KV>(0)], f[pair_first<KV>(0) + kG]);
-          packed.y = pack_half2(f[pair_first<KV>(1)], f[pair_first<KV>(1) + kG]);
-          packed.z = pack_half2(f[pair_first<KV>(2)], f[pair_first<KV>(2) + kG]);
-          packed.w = pack_half2(f[pair_first<KV>(3)], f[pair_first<KV>(3) + kG]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = f[pair_first<KV>(e)], b = f[pair_first<KV>(e) + pair_gap<KV>()];
+            hi[e] = pack_half2(a, b);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[e]));
+            if constexpr (PC) lo[e] = pack_half2(a - h.x, b - h.y);
+          }
         }
-        const int kb = ch >> 3, cc = ch & 7;
-        st_shared_v4(qb + kb * NR * 128 + r * 128 + ((cc ^ (r & 7)) << 4), packed);
+        const uint32_t dst = qb + (ch >> 3) * NR * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        st_shared_v4(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        if constexpr (PC)
+          st_shared_v4(dst + SM::kQlo - SM::kQ, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
       fence_proxy_async_smem();
     };
@@ -936,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // into fp16 once: lane (b, k) takes positions 8k .. 8k+7 of block b; 0
           // past kv1, where the bytes may hold anything.
           const int nvalid = min(kTileTok, m.kv1 - (m.kv0 + i * kTileTok));
-          const uint32_t vst = s_base + stage * kStageBytes + 2 * kSlab;
+          const uint32_t vst = s_base + stage * kStageBytes + kVOff;
           const uint32_t scr = s_base + SM::kVs16 + (warp & 3) * kVs16Warp;
           {
             const int blk = lane >> 4, k = lane & 15;   // k: 8-position group of the tile

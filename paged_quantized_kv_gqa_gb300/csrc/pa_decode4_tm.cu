@@ -7,7 +7,9 @@ namespace pa {
 template <int NR, int KV>
 static cudaError_t launch_t(const Plan& plan, const AttnParams& p, const CUtensorMap& tm_k,
                             const uint8_t* cv, cudaStream_t stream) {
-  auto kern = p.attn_mask != nullptr ? decode_kernel<NR, KV, true> : decode_kernel<NR, KV, false>;
+  const bool pc = p.scale_kind == PA_SCALE_PER_CHANNEL;
+  auto kern = p.attn_mask != nullptr ? (pc ? decode_kernel<NR, KV, true, true> : decode_kernel<NR, KV, true, false>)
+                                     : (pc ? decode_kernel<NR, KV, false, true> : decode_kernel<NR, KV, false, false>);
   const int smem = Smem<NR>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
