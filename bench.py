@@ -115,7 +115,7 @@ NCU_TRAFFIC = {
     # captured on the first 16 of the 128 sequences (726.5 MB of the 5443 MB
     # cache) and scaled by the KV-bytes ratio 7.4922: pages read and partial
     # states written both grow per sequence
-    "spec-verify-4": (("pa_decode.cu", "pa_index.cuh", "pa_merge.cuh"),
+    "spec-verify-4": (("pa_decode.cu", "pa_decode_tile.cuh", "pa_index.cuh", "pa_merge.cuh"),
                       "bbd24eded6361848", (729.497600e6 + 31.870464e6) * 7.492152264116904),
     "append-3": (("pa_append.cu", "pa_append.cuh", "pa_kv4.cuh"), "92996fc35da2ffa3", 72.230912e6 + 1.651200e6),
     "mla-5": (("pa_mla.cu",), "a72bfe43cae1f3fd", 224.198656e6 + 7.294464e6),

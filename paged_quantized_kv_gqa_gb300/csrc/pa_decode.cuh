@@ -19,8 +19,8 @@
 //   * partial rows are fp32, merged by the separate kernel only;
 //   * per-channel K scales go into Q': the product of a bf16 query and a bf16 scale has
 //     16 significant bits and is the sum of two fp16 numbers, as in the warp kernel, with
-//     eight more MMAs a tile for the low parts (PC; 48 rows, int4: 297 -> 321 us, FP4
-//     273 -> 294).  As one number a score moves by up to 2^-11 of its terms' magnitude:
+//     eight more MMAs a tile for the low parts (PC; 48 rows, int4: 301 -> 322 us, FP4
+//     278 -> 294).  As one number a score moves by up to 2^-11 of its terms' magnitude:
 //     with channel scales near 1e-3 and scores near 10 the lse moved by 2e-3 (now 1e-5).
 //
 // Included by pa_decode4_tm.cu.
@@ -29,134 +29,25 @@
 #include <cfloat>
 
 #include "pa_common.cuh"
-#include "pa_index.cuh"
+#include "pa_decode_tile.cuh"
 #include "pa_kv4.cuh"
-#include "pa_merge.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kTileTok = 128;
-constexpr int kHeadDim = 128;
-constexpr int kPage = 64;
 constexpr int kSlot4 = 5120;                     // a slab's place in a stage (64B-swizzled boxes
                                                  // start on 512 bytes)
 constexpr int kVOff = 2 * kSlot4;                // V slabs behind the two K slabs
 constexpr int kStageBytes = 4 * kSlot4;          // K (2 pages) + V (2 pages)
 constexpr int kVs16Warp = 2 * kTileTok * 2;      // a V converter warp's scales as fp16 [2 blocks][128]
 static_assert(kSlot4 >= kV4Slab && kSlot4 % 512 == 0, "stage layout");
-constexpr float kTau = 8.0f;                     // lazy-rescale threshold (log2 units)
-// Warpgroups: two softmax, CV, IO.  4-bit: one CV warpgroup for K and one for V (a
-// code needs more steps than a byte, and one group for both held the pipeline up),
-// and S and PV are issued from a warp each.  (A softmax warpgroup for every 16 rows
+// Warpgroups: two softmax, a converter for K and one for V (a code needs more steps
+// than a byte, and one group for both held the pipeline up), and IO, whose warps copy
+// and issue S and PV from a warp each.  (A softmax warpgroup for every 16 rows
 // instead of two for all measured slower, 334 against 319 us on 48 rows.)
 constexpr int kThreads = 640;
 constexpr int kWarpTma = 16;
 constexpr int kWarpS = 17;                       // issues S, the next warp PV
-constexpr uint32_t kTmemCols = 512;
-constexpr int kPBufs = 4;                        // P^T ring depth
-// P^T buffer: [128 positions][64 rows] fp16, MN-major (rows contiguous),
-// 128-byte swizzle; a thread (= position) writes its rows with 16-byte stores
-constexpr int kPBufBytes = kTileTok * 128;
-constexpr int kMergeRows = 2;                    // rows a merge warp combines at once
-// Item records and per-kv-head scales kept in shared memory: every role reads
-// them at each item boundary, where a read from memory would wait behind the
-// kernel's own page stream.
-constexpr int kCachedItems = 160;
-constexpr int kCachedHeads = 64;
-
-// The decode pipeline is latency-bound: its waits re-probe every 32 ns.
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ bool dwait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
-                                      volatile int* abort_any) {
-  return wait_or_abort(bar, parity, limit_ns, abort_any, 32);
-}
-
-// Sums n values per thread (one per row) over the 32 lanes of a warp, all rows
-// at once.  While n is even, each exchange sends half of the rows still held to
-// the partner lane and keeps the other half (the lane with the offset bit set
-// keeps the upper half), so the warp spends n/2 + n/4 + ... shuffles instead of
-// 5 n; once n is odd the remaining offsets exchange everything.  On return v[0
-// .. left) holds the sums of rows row0 .. row0 + left - 1, and the lanes that
-// differ only in the bits of the full exchanges hold the same values.
-template <int N, int O>
-__device__ __forceinline__ void sum_rows_step(float* v, int lane, int& row0) {
-  if constexpr (N % 2 == 0 && N > 1) {
-    constexpr int H = N / 2;
-    const bool up = (lane & O) != 0;
-#pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const float send = up ? v[k] : v[k + H];
-      const float keep = up ? v[k + H] : v[k];
-      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, O);
-    }
-    if (up) row0 += H;
-    if constexpr (O > 1) sum_rows_step<H, O / 2>(v, lane, row0);
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], O);
-    if constexpr (O > 1) sum_rows_step<N, O / 2>(v, lane, row0);
-  }
-}
-
-// The same exchange for the row maxima.  The first step reads the tile's
-// values and writes half as many, so that they stay intact for the softmax.
-template <int N, int O>
-__device__ __forceinline__ void max_rows_step(float* v, int lane, int& row0) {
-  if constexpr (N % 2 == 0 && N > 1) {
-    constexpr int H = N / 2;
-    const bool up = (lane & O) != 0;
-#pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const float send = up ? v[k] : v[k + H];
-      const float keep = up ? v[k + H] : v[k];
-      v[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, O));
-    }
-    if (up) row0 += H;
-    if constexpr (O > 1) max_rows_step<H, O / 2>(v, lane, row0);
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], O));
-    if constexpr (O > 1) max_rows_step<N, O / 2>(v, lane, row0);
-  }
-}
-template <int N>
-__device__ __forceinline__ void max_rows_first(const float* s, float* t, int lane, int& row0) {
-  constexpr int H = N / 2;
-  const bool up = (lane & 16) != 0;
-#pragma unroll
-  for (int k = 0; k < H; ++k) {
-    const float send = up ? s[k] : s[k + H];
-    const float keep = up ? s[k + H] : s[k];
-    t[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
-  }
-  if (up) row0 += H;
-  max_rows_step<H, 8>(t, lane, row0);
-}
-
-// rows one lane holds after sum_rows_step<N, 16>
-template <int N, int O = 16>
-constexpr int sum_rows_left() {
-  if constexpr (O == 0) return N;
-  else if constexpr (N % 2 == 0 && N > 1) return sum_rows_left<N / 2, O / 2>();
-  else return sum_rows_left<N, O / 2>();
-}
-
-// Page-stage ring depth.  Three stages measured faster than four at every
-// row count (48 rows: 1.56-1.65 -> 1.527 ms on spec-verify-4; 32 rows 0.611
-// -> 0.601 ms): the copies still run well ahead of the converter.
-constexpr int kPageStages = 3;
-
-// TMEM columns: K[2] 0/64, V[2] 128/192, S[2] 256/256+NR, O[2] 256+2NR/256+3NR.
-template <int NR>
-struct Tm {
-  static constexpr uint32_t K0 = 0, V0 = 128, S0 = 256, O0 = 256 + 2 * NR;
-  static_assert(256 + 4 * NR <= 512, "TMEM overflow");
-};
 
 template <int NR>
 struct Smem {
@@ -173,10 +64,9 @@ struct Smem {
   // full[S], empty[S], kready[2], sfull[2], sfree[2], pready[4], vready[2], pvdone[4]
   static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2 + kPBufs + 2 + kPBufs;
   static constexpr int kMisc = kBars + kNumBars * 8;       // tmem addr, abort flags
-  static constexpr int kEpDone = kMisc + 32;               // [8] items finished per softmax warp
-  static constexpr int kItems = kEpDone + 32;              // [kCachedItems][8] int32
+  static constexpr int kItems = kMisc + 32;                // [kCachedItems][8] int32
   static constexpr int kScales = kItems + kCachedItems * kItemWords * 4;   // k, v [kCachedHeads] fp32
-  static constexpr int kVs16 = kScales + 2 * kCachedHeads * 4;             // 4-bit: [4 warps] V scales
+  static constexpr int kVs16 = kScales + 2 * kCachedHeads * 4;             // [4 warps] V scales
   static constexpr int kTotal = kVs16 + 4 * kVs16Warp + 1024;              // + alignment slack
   static_assert(kVs16 % 16 == 0, "the scales are read as 16-byte vectors");
   static_assert(kItems % 16 == 0, "item records are read as int4");
@@ -184,49 +74,12 @@ struct Smem {
   static_assert(kTotal <= 232448, "shared memory overflow");
 };
 
-// The CTA's item records: the first kCachedItems from shared memory.
-struct ItemSrc {
-  const int32_t* cached;   // shared memory
-  const int32_t* items;    // global
-  int begin, n_cached;
-  __device__ __forceinline__ Item at(int it) const {
-    const int k = it - begin;
-    if (k < n_cached) {
-      const int4* r = reinterpret_cast<const int4*>(cached + k * kItemWords);
-      return item4_from<kTileTok>(r[0], r[1]);
-    }
-    return load_item4<kTileTok>(items, it);
-  }
-};
-
-// Walks the (item, tile) sequence of one CTA.
-struct TileCursor {
-  int it, end, i, ntiles;
-  ItemSrc src;
-  __device__ __forceinline__ void init(const ItemSrc& s, int begin, int e) {
-    src = s;
-    it = begin;
-    end = e;
-    i = 0;
-    ntiles = it < end ? src.at(it).ntiles : 0;
-  }
-  __device__ __forceinline__ bool valid() const { return it < end; }
-  __device__ __forceinline__ void advance() {
-    if (++i >= ntiles) {
-      ++it;
-      i = 0;
-      ntiles = it < end ? src.at(it).ntiles : 0;
-    }
-  }
-};
-
 }  // namespace
 
-// KV: PA_KV_*; PC: per-channel K scales; cv: the 4-bit V cache (tm_v is unused)
+// KV: PA_KV_*; PC: per-channel K scales; cv: the V cache
 template <int NR, int KV, bool TREE, bool PC>
 __global__ void __launch_bounds__(kThreads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const uint8_t* __restrict__ cv, const AttnParams p) {
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const uint8_t* __restrict__ cv, const AttnParams p) {
   constexpr int FP4 = KV == PA_KV_FP4_E2M1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -247,7 +100,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_any = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
   volatile int* abort_grp = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8);  // [2]
-  volatile int* ep_done = reinterpret_cast<volatile int*>(smem + SM::kEpDone);      // [8]
   float* red = reinterpret_cast<float*>(smem + SM::kRed);
   float* red_l = reinterpret_cast<float*>(smem + SM::kRedL);
   float* lsum_s = reinterpret_cast<float*>(smem + SM::kLsum);
@@ -260,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int wg = warp >> 2;         // warpgroup: 0, 1 softmax; 2 CV; 3 IO (4-bit: 2, 3 CV of K, V; 4 IO)
+  const int wg = warp >> 2;         // warpgroup: 0, 1 softmax; 2, 3 converters of K, V; 4 IO
   const int item_begin = p.work_indptr[blockIdx.x];
   const int item_end = p.work_indptr[blockIdx.x + 1];
   const uint64_t limit = (uint64_t)p.wait_limit_ns;
@@ -285,13 +137,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_any = 0;
     abort_grp[0] = 0;
     abort_grp[1] = 0;
-    for (int w = 0; w < 8; ++w) ep_done[w] = 0;
     fence_mbar_init();
   }
   int32_t* items_s = reinterpret_cast<int32_t*>(smem + SM::kItems);
   float* ks_s = reinterpret_cast<float*>(smem + SM::kScales);
   float* vs_s = ks_s + kCachedHeads;
-  const ItemSrc isrc{items_s, p.items, item_begin, min(item_end - item_begin, kCachedItems)};
+  const ItemSrc<true> isrc{items_s, p.items, item_begin, min(item_end - item_begin, kCachedItems)};
   for (int i = tid; i < isrc.n_cached * kItemWords; i += kThreads)
     items_s[i] = p.items[(int64_t)item_begin * kItemWords + i];
   // per-kv-head or global scales (per-channel ones are read per item)
@@ -363,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_s = warp == kWarpS;
     auto mwait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, limit, abort_any, 100); };
     const uint32_t idesc = is_s ? idesc_f16_f32(128, NR) : idesc_f16_f32_bmn(128, NR);
-    TileCursor c;
+    TileCursor<true> c;
     c.init(isrc, item_begin, item_end);
     uint32_t g = 0, commits[kPBufs] = {0, 0, 0, 0};
     bool ok = true;

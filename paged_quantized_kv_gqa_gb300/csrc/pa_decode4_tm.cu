@@ -13,7 +13,7 @@ static cudaError_t launch_t(const Plan& plan, const AttnParams& p, const CUtenso
   const int smem = Smem<NR>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<plan.num_ctas, kThreads, smem, stream>>>(tm_k, tm_k, cv, p);   // tm_v unused
+  kern<<<plan.num_ctas, kThreads, smem, stream>>>(tm_k, cv, p);
   return cudaGetLastError();
 }
 
