@@ -124,6 +124,8 @@ typedef struct pa_problem {
 /*
  * Device buffers of one call (all device pointers, caller-owned).
  *   q            bf16  [T][q_stride], T = cu_seqlens_q[bsz]
+ *                (the kernels multiply in fp16: |q|, and |q * per-channel K scale|,
+ *                up to 65504)
  *   cache_k/v    uint8 (layouts above); 16-byte aligned
  *   k_scale/v_scale  as the scale kind says; per-channel K scales 16-byte aligned
  *                (any bf16 address where max(q_len) * G <= 16)

@@ -36,8 +36,11 @@
 //     completed; K16 / V16 buffer b and Q' are rewritten only after the
 //     MMAs that read them completed (tcgen05.commit of the issuing thread).
 //   * Per-kv-head / global K scales fold into the softmax scale, V scales into
-//     the epilogue, per-channel K scales into Q' (rounded to fp16 as one number: the
-//     lse moves by up to 2e-4; two would double S's MMAs, which bound the kernel).
+//     the epilogue, per-channel K scales into Q' (rounded to fp16 as one number: a score
+//     moves by up to 2^-11 of sm_scale * sum |q k|, the lse by no more; two numbers would
+//     double S's MMAs, which bound the kernel, and 64 KB for the low parts leave the
+//     rings two stages).  P in fp16 adds at most 2^-11 p|v| a position, about 3 % to the
+//     mean square error of the bf16 rounding of the rows.
 //   * 4-bit cache (KV = int4, FP4): a page's K and V slabs (codes and block
 //     scales together) arrive by one bulk copy each, 9 KB instead of 16 KB; CV
 //     multiplies each code pair by its block scale (exact in fp16).  int4 codes

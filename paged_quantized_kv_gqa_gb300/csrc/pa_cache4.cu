@@ -28,8 +28,12 @@
 // position with divisions.  Where the range covers a unit in part, the nibbles of
 // other positions stay (one warp owns a unit, so nobody else writes its bytes).
 // What bounds it: 2.56 bytes per element against 13 instructions per element and
-// lane; the prompts below are written at 0.63 of the copy bandwidth.  (Requesting
-// the next rows before the current ones are worked on spills, and gained nothing.)
+// lane: 31k rows of 8 heads in 40.4 us (int4) or 38.4 (FP4), 4.0 and 4.2 TB/s; with
+// per-channel scales 64.  (Requesting the next rows before the current ones are worked
+// on spills, and gained nothing.)  That is for blocks of the common range.  A block whose
+// max |x / g| is below M / 64 (its scale is subnormal, or 0 for a block of zeros) sends
+// the four K rows or the V unit that hold it through the divisions: the same rows times
+// 0.03 with g = 1 took 316 us, rows of which every 16th is 0 315.
 #include "pa_common.cuh"
 #include "pa_kv4.cuh"
 
@@ -76,7 +80,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// x / d with r close to 1 / d: the quotient corrected once by its residual
+// x / d with r close to 1 / d: Markstein's correction of a quotient by its residual,
+// which one fused multiply-add gives exactly
 __device__ __forceinline__ float quot(float x, float d, float r) {
   const float q = x * r;
   return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);

@@ -16,7 +16,8 @@
 //     back as fp16.  S and PV are issued by a warp each that sleeps on its barriers;
 //   * int4 codes unpack in the order 0 4 1 5 2 6 3 7 of each eight: the dims of Q' take
 //     the same order, and a P^T row is written at its position's place in that order;
-//   * partial rows are fp32, merged by the separate kernel only;
+//   * partial rows are fp32, merged by the separate kernel only; P is fp16 as there (it
+//     adds about 3 % to the mean square error of the rows' bf16 rounding);
 //   * per-channel K scales go into Q': the product of a bf16 query and a bf16 scale has
 //     16 significant bits and is the sum of two fp16 numbers, as in the warp kernel, with
 //     eight more MMAs a tile for the low parts (PC; 48 rows, int4: 301 -> 322 us, FP4

@@ -17,6 +17,9 @@
 //     32-bit word of codes each; a 16-dim MMA block is one scale block, so the
 //     scale pairs of the positions serve both rows of a lane.
 // A piece (a work item) may begin and end inside a page, at a half page.
+// Roundings: codes times block scales are exact; P in fp16 (relative error at most 2^-11)
+// and the final row.  The mean square error of the outputs is that of the bf16 rounding
+// within 3 %; P as two numbers would double the MMAs of PV.  Partial rows are fp32.
 // What bounds it: 144 bytes a position and kv head, and per 32 positions about 600
 // (FP4) or 690 (int4) warp instructions for 128 code pairs a lane.  Long caches run
 // at four fifths of the copy bandwidth, held by the issue slots (two thirds of them
@@ -58,7 +61,7 @@ struct D4Cfg {
   static constexpr int kTotal = kBase + kWarps * NB * 2048;
   static_assert(kTotal <= 232448, "shared memory overflow");
   static_assert(kStages < kRing, "a record outlives its stages");
-  // the epilogue stages 8 NB rows of 128 fp32 in the item's last stages
+  // the epilogue stages 8 rows of 128 fp32 at a time in the item's last stage
   static constexpr int kStageRows = 8;
   static_assert(kStageRows * 128 * 4 <= kStage4, "output staging");
 };
@@ -92,10 +95,11 @@ __device__ __forceinline__ int kpos(int b, int g, int h) {
 }  // namespace
 
 // LO > 0: per-channel K scales.  A product of a bf16 query and a bf16 scale has 16
-// significant bits; rounded to fp16 it moved the lse by up to 2e-4 (relative error
-// 4.6e-6, without it 5e-8).  So Q' is the sum of two fp16 numbers there.  LO = 2, at
-// most 4 rows: the low parts are MMA columns 4 to 7, which have no rows (batch of 64
-// sequences, 4 rows: 45.4 -> 46.4 us; as LO = 1 57.4).  LO = 1: they wait in shared
+// significant bits; rounded to fp16 it moves a score by up to 2^-11 of sm_scale * sum
+// |q k|, and more where it is subnormal (channel scales near 1e-3 and scores near 10: lse
+// error 1e-3, as two numbers 5e-6 to 1e-5).  So Q' is the sum of two fp16 numbers there.
+// LO = 2, at most 4 rows: the low parts are MMA columns 4 to 7, which have no rows (batch
+// of 64 sequences, 4 rows: 45.4 -> 46.4 us; as LO = 1 57.4).  LO = 1: they wait in shared
 // memory and go through MMAs of their own (24 sequences, 5 rows: 20.5 -> 23.1 us).
 template <int NB, int FP4, bool TREE, int LO>
 __global__ void __launch_bounds__(D4Cfg<NB>::kWarps * 32, 1)

@@ -29,11 +29,12 @@ constexpr int kDecode4WholePages = 8;
 constexpr int kDecode4MinPages = 2;  // smallest share of a warp
 constexpr int kDecode4MinTiles = 4;  // smallest share of a tensor-memory CTA, 128-position tiles
 // What starting and ending a piece costs, in half pages of a warp and of a CTA.
-// With shares of equal pages (cost 0) the warps with the most pieces finished last:
-// 24 sequences of up to 3k positions 22.0 us, at 2 to 4 20.6; 57 of up to 2k (one
-// row, int4) 44.5, at 2 and 3 40.5, at 4 42.9; 64 of up to 4k 49.3, at 2 47.0, at 3
-// and 4 49.3 (the cuts fall badly); CTAs: 6 drafts after 32 prefixes of up to 32k
-// positions 311.6, at 8 308.9, at 12 and 16 308.0.
+// With shares of equal pages (cost 0) the warps with the most pieces finished last
+// (24 sequences of up to 3k positions 22.0 us, at 2 20.6).  Warps: 30 batches of random
+// lengths, five of each of six shapes (16 to 100 sequences of up to 1.5-9k, 1 to 8 rows),
+// took 248.2, 245.5, 246.9 and 249.5 us at costs of 1 to 4, summed over the shapes; a
+// single batch moves by 5 % either way with the cuts.  CTAs: 6 drafts after 32 prefixes
+// of up to 32k positions 311.6, at 8 308.9, at 12 and 16 308.0.
 constexpr int kDecode4ItemCost = 2;
 constexpr int kDecode4TileCost = 12;
 // the merge's classes of 4-bit rows: 32, 16, 8, 4, 2, 1 warps a row, for more than 128,

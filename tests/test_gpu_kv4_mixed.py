@@ -99,3 +99,18 @@ def test_8_bit_cross_rows_without_chunks_are_final_after_pa_run():
     p.held = c.seq_lens_kv
     ref = reference(p, rows=lambda w, b, h, n: oa.dequant_kv(c, b, h, n)[w == "v"])
     check(p, *without_merge(pa, p), ref)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kw", [dict(seq_lens=[4, 2], seq_lens_kv=[61, 1150], q_heads=4, kv_heads=2),      # 8 rows
+                                dict(seq_lens=[4, 2], seq_lens_kv=[61, 1150], q_heads=8, kv_heads=2),      # 16
+                                dict(seq_lens=[3, 2], seq_lens_kv=[127, 1500], q_heads=14, kv_heads=2),    # 21
+                                dict(seq_lens=[6, 5], seq_lens_kv=[1021, 63], q_heads=16, kv_heads=2),     # 48
+                                dict(seq_lens=[8, 5], seq_lens_kv=[900, 0], q_heads=16, kv_heads=2)])      # 64
+def test_tree_masks_over_per_channel_scales(kw, kind):
+    p = make(76, kv_dtype=kind, scale_kind="per_channel", **kw)
+    M = int(p.seq_lens.max())
+    r = np.random.default_rng(6)
+    p.attn_mask = np.tril(r.integers(0, 2, (p.bsz, M, M)), -1).astype(np.uint8) + np.eye(M, dtype=np.uint8)[None]
+    out, lse, *_ = run(p)
+    check(p, out, lse)
