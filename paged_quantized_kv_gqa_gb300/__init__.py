@@ -238,7 +238,11 @@ def make_args(*, q, cache_k, cache_v, k_scale, v_scale, block_table, out, lse=No
               seq_lens=None, seq_lens_kv=None, cu_seqlens_q=None, attn_mask=None,
               shift_bias=None, smooth_weight=None, out_int8=False, in_scale=1.0,
               quant_max_bound=127.0, quant_min_bound=-127.0) -> PaArgs:
+    """The arguments of one call.  Tensors stay alive as long as the returned object;
+    memory behind raw addresses is the caller's to keep."""
     a = PaArgs()
+    a.tensors = [t for t in (q, cache_k, cache_v, k_scale, v_scale, block_table, out, lse, seq_lens, seq_lens_kv,
+                             cu_seqlens_q, attn_mask, shift_bias, smooth_weight) if hasattr(t, "data_ptr")]
     a.q, a.cache_k, a.cache_v = _ptr(q), _ptr(cache_k), _ptr(cache_v)
     a.k_scale, a.v_scale, a.block_table = _ptr(k_scale), _ptr(v_scale), _ptr(block_table)
     a.seq_lens, a.seq_lens_kv, a.cu_seqlens_q = _ptr(seq_lens), _ptr(seq_lens_kv), _ptr(cu_seqlens_q)

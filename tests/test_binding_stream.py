@@ -46,3 +46,24 @@ def test_no_device_yet_is_not_kept(pa, monkeypatch):
     assert pa._stream(None) is None
     with_cuda(monkeypatch, lambda: types.SimpleNamespace(cuda_stream=7))
     assert pa._stream(None) == 1003
+
+
+def test_arguments_keep_their_tensors_alive():
+    """pa_args holds addresses: a tensor that nothing else holds must not be freed under it."""
+    import gc
+    import weakref
+    import paged_quantized_kv_gqa_gb300 as m
+    names = ("q", "cache_k", "cache_v", "k_scale", "v_scale", "block_table", "out", "lse", "seq_lens", "seq_lens_kv",
+             "cu_seqlens_q", "attn_mask", "shift_bias", "smooth_weight")
+    tensors = {n: torch.zeros(4) for n in names}
+    refs = [weakref.ref(t) for t in tensors.values()]
+    args = m.make_args(**tensors)
+    assert [getattr(args, n) for n in names] == [t.data_ptr() for t in tensors.values()]
+    del tensors
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del args
+    gc.collect()
+    assert all(r() is None for r in refs)
+    raw = dict(q=256, cache_k=256, cache_v=256, k_scale=256, v_scale=256, block_table=256, out=256)
+    assert m.make_args(**raw, lse=None).q == 256
