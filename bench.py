@@ -111,14 +111,14 @@ def _peaks(bound: str):
 # version it was taken with.
 NCU_TRAFFIC = {
     # decode-2 runs the warp-per-item kernel (at most 16 packed rows)
-    "decode-2": (("pa_decode_warp.cu", "pa_index.cuh"), "db79655326e15776", 318.198272e6 + 4.333312e6),
+    "decode-2": (("pa_decode_warp.cu", "pa_index.cuh"), "6323b4731a7f60f9", 318.200576e6 + 4.337152e6),
     # captured on the first 16 of the 128 sequences (726.5 MB of the 5443 MB
     # cache) and scaled by the KV-bytes ratio 7.4922: pages read and partial
     # states written both grow per sequence
     "spec-verify-4": (("pa_decode.cu", "pa_decode_tile.cuh", "pa_index.cuh", "pa_merge.cuh"),
-                      "bbd24eded6361848", (729.497600e6 + 31.870464e6) * 7.492152264116904),
-    "append-3": (("pa_append.cu", "pa_append.cuh", "pa_kv4.cuh"), "92996fc35da2ffa3", 72.230912e6 + 1.651200e6),
-    "mla-5": (("pa_mla.cu",), "a72bfe43cae1f3fd", 224.198656e6 + 7.294464e6),
+                      "5a410ba906867b8b", (729.511168e6 + 31.966464e6) * 7.492152264116904),
+    "append-3": (("pa_append.cu", "pa_append.cuh", "pa_kv4.cuh"), "3b2436901272940e", 72.260864e6 + 1.486336e6),
+    "mla-5": (("pa_mla.cu",), "01feea59d87f9468", 224.411648e6 + 7.396608e6),
 }
 
 

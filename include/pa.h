@@ -186,7 +186,7 @@ typedef struct pa_plan_desc {
   int32_t num_items;
   int32_t num_ctas;         /* persistent CTAs (MLA: CTA pairs)               */
   int32_t total_q;          /* T                                              */
-  int32_t max_chunks;       /* partial slots per token                        */
+  int32_t max_chunks;       /* most chunks of a token                          */
   int32_t n_merge;          /* tokens whose rows are split into chunks        */
   const int32_t* items;     /* [num_items][8]: b, kvh, token0, n_tok,
                                causal_base, kv0, kv1, chunk | (n_chunks << 16)

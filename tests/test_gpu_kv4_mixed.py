@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from kv4_helpers import KINDS, args_of, check, device, make, plan_of, reference, run, workspace
+from kv4_helpers import KINDS, args_of, bf16_bits, check, device, make, plan_of, reference, run, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,31 @@ def test_tree_masks_over_per_channel_scales(kw, kind):
     p.attn_mask = np.tril(r.integers(0, 2, (p.bsz, M, M)), -1).astype(np.uint8) + np.eye(M, dtype=np.uint8)[None]
     out, lse, *_ = run(p)
     check(p, out, lse)
+
+
+def test_a_plan_without_chunks_captured_alone_and_in_the_built_in_workspace():
+    """pa_run alone (attention and the merge it enqueues) as a graph that is replayed with
+    other queries, on a side stream; then the same plan through pa_run_static."""
+    import torch
+    import paged_quantized_kv_gqa_gb300 as pa
+    p = make(77, seq_lens=[1, 2, 1], seq_lens_kv=[6000, 700, 3], q_heads=8, kv_heads=2, kv_dtype="int4", chunk_size=0)
+    d = device(p)
+    plan = plan_of(pa, p)
+    ws, args = workspace(plan), args_of(pa, d)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        pa.pa_plan_upload(plan, ws)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            pa.pa_run(plan, args, ws)
+        p.q_bits = bf16_bits(np.random.default_rng(8).standard_normal(p.q_bits.shape))
+        d["q"].copy_(torch.from_numpy(p.q_bits.view(np.int16)).view(torch.bfloat16))
+        for _ in range(2):
+            g.replay()
+        assert pa.pa_check(plan, ws)[0] == 0
+    host = lambda: [d[n].float().cpu().numpy().astype(np.float64) for n in ("out", "lse")]  # noqa: E731
+    check(p, *host())
+    d["out"].fill_(7)
+    pa.pa_run_static(plan, args, check=True)
+    check(p, *host())
