@@ -1,4 +1,5 @@
-"""Which stream the binding takes when the caller names none, without a GPU."""
+"""What the Python binding itself decides, without a GPU: the stream of a call that
+names none, and how long arguments live."""
 import types
 
 import pytest
@@ -8,9 +9,7 @@ import torch
 @pytest.fixture
 def pa(monkeypatch):
     import paged_quantized_kv_gqa_gb300 as m
-    # as in a process that has made no call yet
-    initial = False if m._current_raw_stream is False else None
-    monkeypatch.setattr(m, "_current_raw_stream", initial)
+    monkeypatch.setattr(m, "_current_raw_stream", None)   # as in a process that has made no call yet
     return m
 
 
