@@ -57,8 +57,9 @@ typedef enum pa_status {
   PA_ERR_CUDA = 3,          /* a CUDA runtime/driver call failed              */
   PA_ERR_DEVICE_TIMEOUT = 4,/* a kernel's bounded wait ran out (see pa_check) */
   PA_ERR_BAD_PAGE = 5,      /* a block-table entry outside [0, num_pages)     */
-  PA_ERR_BAD_ITEM = 6       /* debug library only: a work item outside the
+  PA_ERR_BAD_ITEM = 6,      /* debug library only: a work item outside the
                                problem's bounds (see pa_check)                */
+  PA_ERR_BAD_POSITION = 7   /* a position outside the rotation's table        */
 } pa_status;
 
 enum { PA_KV_INT8 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT4 = 2, PA_KV_FP4_E2M1 = 3 };
@@ -322,6 +323,54 @@ pa_status pa_cache_append(const pa_plan_t* plan, const pa_args* args, const void
  */
 pa_status pa_cache_read(const pa_plan_t* plan, const pa_args* args, void* k_out, void* v_out,
                         int64_t kv_stride, void* workspace, void* stream);
+
+/*
+ * Rotary positions.  A pair (a, b) of dims turns by an angle whose cos c and sin s come
+ * from a table: a' = a c - b s, b' = b c + a s, every product and sum rounded to
+ * binary32.  Pair i (i < rot_dim / 2) of a rotated width is dims (i, i + rot_dim / 2)
+ * with PA_ROPE_HALVES, (2i, 2i + 1) with PA_ROPE_ADJACENT.  Row r of the table belongs to
+ * position r, so any scaling of the angles is the table's.
+ *   GQA layout: the first rot_dim of a head's 128 dims turn (rot_dim a multiple of 16,
+ *   up to 128); MLA: the latent row's dims 512 .. 512 + rot_dim - 1 and, in queries of
+ *   192 dims a head, dims 128 .. 128 + rot_dim - 1 (rot_dim up to 64).  Others pass.
+ *   positions == NULL: token i of sequence b stands at seq_lens_kv[b] + i.  Otherwise
+ *   token t (global row) has axes positions positions[a * T + t], T = cu_seqlens_q[bsz],
+ *   and pair i turns by that of axis pair_axis[i] (time, height and width of images and
+ *   video: runs of pairs, or the axes in turn).  Positions turn rows; the cache place of
+ *   a token is seq_lens_kv[b] + i in any case.
+ *   A token with a position outside [0, table_rows) is left unturned and records
+ *   PA_ERR_BAD_POSITION (detail = its row), read with pa_check.
+ */
+enum { PA_ROPE_HALVES = 0, PA_ROPE_ADJACENT = 1 };
+typedef struct pa_rope {
+  const float* cos_sin;      /* device fp32 [table_rows][rot_dim]: the cos of the
+                                rot_dim / 2 pairs, then their sin; 16-byte aligned */
+  const int32_t* positions;  /* device int32 [axes][T] or NULL                     */
+  int32_t table_rows;
+  int32_t rot_dim;
+  int32_t pairs;             /* PA_ROPE_* */
+  int32_t axes;              /* 1 .. 4 */
+  uint8_t pair_axis[64];     /* axis of each pair, < axes */
+} pa_rope;
+
+/*
+ * pa_rope_append: the step before pa_run in one launch.  Rotates the new tokens'
+ * queries into q_out and does what pa_cache_append does with their keys and values, the
+ * keys rotated first: stored K = Q(k' / s) of the rotated binary32 values k' (no rounding
+ * to bf16 between), V as pa_cache_append writes it.
+ *   q_new, q_out: device bf16, token rows q_stride / q_out_stride elements apart, head h
+ *   at h * 128 (GQA) or h * 192 (MLA: 128 dims, then 64 of which rot_dim turn) within
+ *   a row; q_out == q_new with equal strides rotates in place, other overlaps are not
+ *   allowed.  Both NULL: keys and values only.  For GQA, args.q of pa_run is q_out with
+ *   q_stride = q_out_stride; MLA queries go through pa_mla_absorb.
+ *   k_new, v_new, kv_stride, args, workspace: as for pa_cache_append.
+ * Rows must be 16-byte aligned (pointers, and strides multiples of 8 elements).
+ * Asynchronous on stream; no allocation.
+ */
+pa_status pa_rope_append(const pa_plan_t* plan, const pa_args* args, const pa_rope* rope,
+                         const void* q_new, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                         const void* k_new, const void* v_new, int64_t kv_stride,
+                         void* workspace, void* stream);
 
 /* Bytes of cache_k and of cache_v for a problem's pool (MLA: *v_bytes = 0, V
  * being part of cache_k's rows). */

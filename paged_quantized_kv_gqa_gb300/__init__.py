@@ -28,11 +28,12 @@ LIB_PATH = os.path.join(_HERE, "libpa_gb300_trace.so" if os.environ.get("PA_GB30
                         else "libpa_gb300.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA = 0, 1, 2, 3
-PA_ERR_DEVICE_TIMEOUT, PA_ERR_BAD_PAGE, PA_ERR_BAD_ITEM = 4, 5, 6
+PA_ERR_DEVICE_TIMEOUT, PA_ERR_BAD_PAGE, PA_ERR_BAD_ITEM, PA_ERR_BAD_POSITION = 4, 5, 6, 7
 KV_DTYPES = {"int8": 0, "fp8_e4m3": 1, "int4": 2, "fp4_e2m1": 3}
 MASK_FULL, MASK_CAUSAL, MASK_CROSS = 0, 1, 2
 SCALE_KINDS = {"per_kv_head": 0, "per_channel": 1, "global": 2}
 LAYOUTS = {"gqa": 0, "mla": 1}
+ROPE_PAIRS = {"halves": 0, "adjacent": 1}
 FAMILIES = {0: "decode", 1: "append", 2: "mla"}
 
 
@@ -50,6 +51,12 @@ class PaArgs(ctypes.Structure):
         "smooth_weight")] + [("out_int8", ctypes.c_int32), ("in_scale", ctypes.c_float),
                              ("quant_max_bound", ctypes.c_float),
                              ("quant_min_bound", ctypes.c_float)]
+
+
+class PaRope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("table_rows", "rot_dim", "pairs", "axes")] + [
+        ("pair_axis", ctypes.c_uint8 * 64)]
 
 
 class PaPlanDesc(ctypes.Structure):
@@ -93,6 +100,8 @@ def _load():
         "pa_set_fused_merge": ([i32], i32),
         "pa_cache_append": ([vp, ctypes.POINTER(PaArgs), vp, vp, i64, vp, vp], i32),
         "pa_cache_read": ([vp, ctypes.POINTER(PaArgs), vp, vp, i64, vp, vp], i32),
+        "pa_rope_append": ([vp, ctypes.POINTER(PaArgs), ctypes.POINTER(PaRope), vp, i64, vp, i64, vp, vp, i64, vp,
+                            vp], i32),
         "pa_cache_bytes": ([ctypes.POINTER(PaProblem), ctypes.POINTER(ctypes.c_size_t),
                             ctypes.POINTER(ctypes.c_size_t)], i32),
     }
@@ -305,6 +314,34 @@ def pa_cache_read(plan: Plan, args: PaArgs, k_out, v_out, kv_stride: int, worksp
     cache back as bf16 rows, token stride kv_stride elements (see include/pa.h)."""
     _check(lib.pa_cache_read(plan.handle, ctypes.byref(args), _ptr(k_out), _ptr(v_out),
                              int(kv_stride), _ptr(workspace), _stream(stream)))
+
+
+def make_rope(*, cos_sin, table_rows, rot_dim, pairs="halves", positions=None, axes=1, pair_axes=None) -> PaRope:
+    """Rotary positions of pa_rope_append (see include/pa.h): a device fp32 table
+    [table_rows][rot_dim] of cosines, then sines; with several axes, device int32
+    positions [axes][T] and pair_axes, the axis of each of the rot_dim / 2 pairs
+    (pair_axes=None: every pair by the first).  Tensors stay alive with the returned object."""
+    r = PaRope()
+    pair_axes = [int(a) for a in pair_axes] if pair_axes is not None else [0] * max(0, rot_dim // 2)
+    if len(pair_axes) != rot_dim // 2 or len(pair_axes) > 64:
+        raise ValueError("pair_axes needs one axis per pair, rot_dim / 2 of at most 64")
+    if any(a < 0 or a > 255 for a in pair_axes):
+        raise ValueError("an axis is a small non-negative number")
+    r.tensors = [t for t in (cos_sin, positions) if hasattr(t, "data_ptr")]
+    r.cos_sin, r.positions = _ptr(cos_sin), _ptr(positions)
+    r.table_rows, r.rot_dim, r.axes = table_rows, rot_dim, axes
+    r.pairs = ROPE_PAIRS[pairs] if isinstance(pairs, str) else pairs
+    r.pair_axis[:len(pair_axes)] = pair_axes
+    return r
+
+
+def pa_rope_append(plan: Plan, args: PaArgs, rope: PaRope, q_new, q_stride: int, q_out, q_out_stride: int, k_new,
+                   v_new, kv_stride: int, workspace, stream=None):
+    """Rotate the new tokens' queries into q_out (None with q_new=None: no queries) and
+    write their rotated keys and their values into the cache of args (see include/pa.h)."""
+    _check(lib.pa_rope_append(plan.handle, ctypes.byref(args), ctypes.byref(rope), _ptr(q_new), int(q_stride),
+                              _ptr(q_out), int(q_out_stride), _ptr(k_new), _ptr(v_new), int(kv_stride),
+                              _ptr(workspace), _stream(stream)))
 
 
 def pa_cache_bytes(problem: PaProblem):

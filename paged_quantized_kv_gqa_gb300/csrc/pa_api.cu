@@ -808,6 +808,9 @@ pa_status pa_check(const pa_plan_t* plan, const void* workspace, void* stream, i
   if (words[0] == PA_ERR_BAD_PAGE)
     return fail(PA_ERR_BAD_PAGE, "block_table entry outside [0, num_pages) (item " +
                                      std::to_string(words[1]) + ")");
+  if (words[0] == PA_ERR_BAD_POSITION)
+    return fail(PA_ERR_BAD_POSITION, "a position outside the rotation's table (token row " +
+                                         std::to_string(words[1]) + ")");
   return fail((pa_status)words[0], "device status " + std::to_string(words[0]));
 }
 
@@ -882,6 +885,53 @@ pa_status pa_cache_append(const pa_plan_t* plan, const pa_args* args, const void
                             ? launch_cache_append4(*plan, *args, k_new, v_new, kv_stride, status, st)
                             : launch_cache_append(*plan, *args, k_new, v_new, kv_stride, status, st);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("cache append: ") + cudaGetErrorString(e));
+  return PA_OK;
+}
+
+// A row pointer and stride that 16-byte accesses may use.
+static bool rows16(const void* rows, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(rows) % 16 == 0 && stride % 8 == 0;
+}
+
+pa_status pa_rope_append(const pa_plan_t* plan, const pa_args* args, const pa_rope* rope,
+                         const void* q_new, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                         const void* k_new, const void* v_new, int64_t kv_stride,
+                         void* workspace, void* stream) {
+  pa_status s = check_rows(plan, args, k_new, v_new, kv_stride, workspace);
+  if (s != PA_OK) return s;
+  const pa_problem& pr = plan->prob;
+  const bool mla = pr.layout == PA_LAYOUT_MLA;
+  if (!rope || !rope->cos_sin) return fail(PA_ERR_INVALID_ARG, "null pa_rope or cos_sin table");
+  if (rope->rot_dim <= 0 || rope->rot_dim % 16 || rope->rot_dim > (mla ? 64 : 128))
+    return fail(PA_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 up to 128 (MLA: 64)");
+  if (rope->pairs != PA_ROPE_HALVES && rope->pairs != PA_ROPE_ADJACENT)
+    return fail(PA_ERR_INVALID_ARG, "pairs must be PA_ROPE_HALVES or PA_ROPE_ADJACENT");
+  if (rope->table_rows <= 0) return fail(PA_ERR_INVALID_ARG, "table_rows must be positive");
+  if (rope->axes < 1 || rope->axes > 4) return fail(PA_ERR_INVALID_ARG, "axes must be 1 to 4");
+  if (rope->axes > 1 && !rope->positions)
+    return fail(PA_ERR_INVALID_ARG, "positions of several axes must be given");
+  for (int i = 0; i < rope->rot_dim / 2; ++i)
+    if (rope->pair_axis[i] >= rope->axes)
+      return fail(PA_ERR_INVALID_ARG, "pair_axis names an axis that there is not");
+  if (reinterpret_cast<uintptr_t>(rope->cos_sin) % 16 || reinterpret_cast<uintptr_t>(rope->positions) % 4)
+    return fail(PA_ERR_INVALID_ARG, "cos_sin must be 16-byte, positions 4-byte aligned");
+  if ((q_new == nullptr) != (q_out == nullptr))
+    return fail(PA_ERR_INVALID_ARG, "q_new and q_out are given together or not at all");
+  if (q_new) {
+    const int64_t row = (int64_t)pr.q_heads * (mla ? 192 : pr.head_dim_qk);
+    if (q_stride < row || q_out_stride < row)
+      return fail(PA_ERR_INVALID_ARG, "query stride smaller than one token's row");
+    if (q_new == q_out && q_stride != q_out_stride)
+      return fail(PA_ERR_INVALID_ARG, "rotation in place needs equal strides");
+    if (!rows16(q_new, q_stride) || !rows16(q_out, q_out_stride))
+      return fail(PA_ERR_INVALID_ARG, "query rows must be 16-byte aligned");
+  }
+  if (!rows16(k_new, kv_stride) || (!mla && !rows16(v_new, kv_stride)))
+    return fail(PA_ERR_INVALID_ARG, "K / V rows must be 16-byte aligned");
+  const cudaError_t e = launch_rope_append(*plan, *args, *rope, q_new, q_stride, q_out, q_out_stride, k_new, v_new,
+                                           kv_stride, static_cast<int32_t*>(workspace),
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("rope append: ") + cudaGetErrorString(e));
   return PA_OK;
 }
 

@@ -192,6 +192,10 @@ cudaError_t launch_append4(const Plan& plan, const AttnParams& p, const void* ck
 cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void* k_new,
                                  const void* v_new, int64_t kv_stride, int32_t* status,
                                  cudaStream_t stream);
+// queries rotated, K / V rows rotated (K) and written, every cache
+cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope& rope, const void* q,
+                               int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new,
+                               const void* v_new, int64_t kv_stride, int32_t* status, cudaStream_t stream);
 cudaError_t launch_cache_read(const Plan& plan, const pa_args& a, void* k_out, void* v_out,
                               int64_t kv_stride, int32_t* status, cudaStream_t stream);
 cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* lse,

@@ -1,0 +1,511 @@
+// pa_rope.cu - the step before attention in one launch: queries rotated by their
+// positions, new K / V rows rotated (K), quantised and written into the paged cache.
+//
+// Rotation of a pair (a, b) of dims by the angle whose cos c and sin s the table holds,
+// every product and sum rounded to binary32 by itself (no fused multiply-add, so that a
+// stored code is a function of the inputs that another program can reproduce):
+//   a' = a c - b s,  b' = b c + a s.
+// Queries are rounded to bf16 once; K goes to its quantiser in binary32, with the values
+// that pa_cache.cu / pa_cache4.cuh write for a row of such numbers:
+//   8 bits  Q(x / s); 4 bits  per block of 16 dims e = E4M3(min(max |x / g| / M, 448)),
+//   step = e g, code = nearest to x / step.
+// V is written as pa_cache_append writes it.
+//
+// GQA: lane = 8 dims of a row, two rows a step, so that a lane's cos and sin are read
+// once for all heads of its row; the other dim of a pair comes by a shuffle (halves) or
+// is the lane's own (adjacent).  A warp takes a unit of 8 positions and a group of the
+// heads, the queries' first, K's behind them.  V: a warp per (unit, kv head), lane = 4
+// dims of all the unit's positions, whose bytes gather in registers.
+// MLA: 8 lanes hold the 64 rotated dims of a head, 4 query heads a step; a latent row is
+// one warp's.
+#include "pa_cache4.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPage = 64;
+constexpr int kWarps = 8;
+constexpr int kRopeUnit = 8;    // positions of a rotation warp's unit
+constexpr int kMlaRow = 576, kMlaLatent = 512, kMlaQ = 192, kMlaNope = 128;
+
+struct RopeParams {
+  Append4Params a;             // the rows, cache, scales and lengths (units, total: the V warps')
+  const float* cos_sin;
+  const int32_t* positions;    // [axes][total_q] or null
+  const __nv_bfloat16* q;      // or null
+  __nv_bfloat16* q_out;
+  int64_t q_stride, q_out_stride;
+  RowUnits units;              // units of kRopeUnit positions
+  uint32_t rot_warps;          // warps of the rotation; the V warps follow
+  int32_t groups, group_heads; // head groups of a unit
+  int32_t q_heads;             // 0 without queries
+  int32_t table_rows, rot, adjacent, axes, quads;   // quads: four neighbouring pairs share an axis
+  int32_t total_q;
+  uint32_t pair_axis[4];       // two bits a pair
+};
+
+__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// cos and sin (signed for its place in the pair) of a lane's 8 dims
+struct Turn {
+  float c[8], s[8];
+};
+
+// Fills `a` for dims 8 o .. 8 o + 7 of a rotated width of p.rot in row t at position
+// pos; false (and the status recorded) when a position is not a row of the table.
+__device__ __forceinline__ bool load_turn(const RopeParams& p, int64_t t, int pos, int o, Turn& a) {
+  const int half = p.rot / 2;
+  // dims 8 o .. are the first of their pairs in the lower half of `halves`
+  const int pair0 = p.adjacent ? 4 * o : 8 * o % half;
+  int row[4] = {pos, 0, 0, 0};
+  if (p.positions != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < p.axes) row[k] = __ldg(p.positions + (int64_t)k * p.total_q + t);
+  }
+  const int axes = p.positions != nullptr ? p.axes : 1;
+  bool ok = true;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ok = ok && (k >= axes || (row[k] >= 0 && row[k] < p.table_rows));
+  if (!ok) {
+    record_status(p.a.status, PA_ERR_BAD_POSITION, (int)t);
+    return false;
+  }
+  const float* base = p.cos_sin + pair0;
+  auto pick = [&](uint32_t axis) {
+    const int r = axis == 0 ? row[0] : axis == 1 ? row[1] : axis == 2 ? row[2] : row[3];
+    return base + (int64_t)r * p.rot;
+  };
+  const uint32_t ax = axes == 1 ? 0u : p.pair_axis[pair0 >> 4] >> (2 * (pair0 & 15));   // 8 (4) pairs
+  float c[8], s[8];
+  const int n = p.adjacent ? 1 : 2;   // quads of pairs
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h >= n) break;
+    if (axes == 1 || p.quads) {
+      const float* src = pick((ax >> (8 * h)) & 3u) + 4 * h;
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(src + half));
+      c[4 * h] = x.x, c[4 * h + 1] = x.y, c[4 * h + 2] = x.z, c[4 * h + 3] = x.w;
+      s[4 * h] = y.x, s[4 * h + 1] = y.y, s[4 * h + 2] = y.z, s[4 * h + 3] = y.w;
+    } else {
+#pragma unroll
+      for (int e = 4 * h; e < 4 * h + 4; ++e) {
+        const float* src = pick((ax >> (2 * e)) & 3u) + e;
+        c[e] = __ldg(src);
+        s[e] = __ldg(src + half);
+      }
+    }
+  }
+  if (p.adjacent) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a.c[e] = c[e >> 1];
+      a.s[e] = (e & 1) ? s[e >> 1] : -s[e >> 1];
+    }
+  } else {
+    const bool lower = 8 * o < half;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a.c[e] = c[e];
+      a.s[e] = lower ? -s[e] : s[e];
+    }
+  }
+  return true;
+}
+
+// The rotated values of a lane's 8 dims x (bf16), y the 8 dims of the lane that holds
+// the other halves of its pairs.
+__device__ __forceinline__ void turn8(const RopeParams& p, const uint4& x, const uint4& y, const Turn& a, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
+    const float o_lo = p.adjacent ? hi : bf16_lo(v[k]), o_hi = p.adjacent ? lo : bf16_hi(v[k]);
+    f[2 * k] = __fadd_rn(__fmul_rn(lo, a.c[2 * k]), __fmul_rn(o_lo, a.s[2 * k]));
+    f[2 * k + 1] = __fadd_rn(__fmul_rn(hi, a.c[2 * k + 1]), __fmul_rn(o_hi, a.s[2 * k + 1]));
+  }
+}
+
+__device__ __forceinline__ void plain8(const uint4& x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = bf16_lo(w[k]);
+    f[2 * k + 1] = bf16_hi(w[k]);
+  }
+}
+
+__device__ __forceinline__ uint4 shfl4(const uint4& x, int lane) {
+  return make_uint4(__shfl_sync(0xffffffffu, x.x, lane), __shfl_sync(0xffffffffu, x.y, lane),
+                    __shfl_sync(0xffffffffu, x.z, lane), __shfl_sync(0xffffffffu, x.w, lane));
+}
+
+__device__ __forceinline__ uint4 bf16x8_of(const float (&f)[8]) {
+  return make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
+}
+
+template <int KV>
+constexpr bool is_four() { return KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1; }
+
+// One value -> its 8-bit code.
+template <int KV>
+__device__ __forceinline__ uint32_t code8(float x, float s) {
+  const float v = __fdiv_rn(x, s);
+  if constexpr (KV == PA_KV_FP8_E4M3) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+    return r & 0xFFu;
+  } else {
+    return (uint32_t)max(-127, min(127, __float2int_rn(v))) & 0xFFu;
+  }
+}
+
+// A lane's 8 values of a K row -> its codes (and block scale), in place within the slab.
+// The lanes of a block are neighbours; every lane of the warp calls it, those of rows
+// outside the range with in = false.
+template <int KV, bool PC>
+__device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8], uint8_t* slab, int kvh, int off, int c,
+                                        bool in) {
+  float g[8];
+#pragma unroll
+  for (int e = 0; e < (PC ? 8 : 1); ++e)
+    g[e] = load_scale(p.a.k_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 8 * c + e : kvh);
+  if constexpr (!is_four<KV>()) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(f[e], g[PC ? e : 0]) << (8 * (e & 3));
+    if (in) *reinterpret_cast<uint2*>(slab + off * kV4Dim + 8 * c) = make_uint2(w[0], w[1]);
+  } else {
+    constexpr int FP4 = KV == PA_KV_FP4_E2M1;
+    constexpr float kTop = Fmt<FP4>::kTop;
+    float x[8], a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = f[e] != f[e] ? 0.0f : f[e];
+      a = fmaxf(a, PC ? fabsf(__fdiv_rn(x[e], g[e])) : fabsf(x[e]));
+    }
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    if constexpr (!PC) a = fabsf(__fdiv_rn(a, g[0]));   // of the largest: rounding keeps the order
+    const uint32_t sb = block_scale<FP4>(__fdiv_rn(a, kTop));
+    const float s = e4m3_to_f32(sb);
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float step = __fmul_rn(s, g[PC ? e : 0]);
+      q[e] = fminf(fmaxf(step > 0.0f ? __fdiv_rn(x[e], step) : 0.0f, -kTop), kTop);
+    }
+    const uint32_t w = pack8<FP4>(q);
+    if (in) {
+      *reinterpret_cast<uint32_t*>(slab + k4_code_off(off, 8 * c)) = w;
+      if ((c & 1) == 0) slab[k4_scale_off(off, c >> 1)] = (uint8_t)sb;
+    }
+  }
+}
+
+// V of an 8-bit cache: the unit's positions [a, e) of U, lane = 4 dims.
+template <int KV, bool PC, int U>
+__device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat16* rows, uint8_t* slab, int kvh, int off0,
+                                         int a, int e, int lane) {
+  float g[4];
+#pragma unroll
+  for (int d = 0; d < (PC ? 4 : 1); ++d)
+    g[d] = load_scale(p.a.v_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 4 * lane + d : kvh);
+  const __nv_bfloat16* src = rows + 4 * lane - (int64_t)a * p.a.kv_stride;
+  uint8_t* dst = slab + 4 * lane * kPage + off0;
+#pragma unroll
+  for (int k = 0; k < U; k += 8) {
+    uint2 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = k + j >= a && k + j < e ? __ldg(reinterpret_cast<const uint2*>(src + (int64_t)(k + j) * p.a.kv_stride))
+                                     : make_uint2(0, 0);
+    uint32_t w[4][2] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v[4] = {bf16_lo(x[j].x), bf16_hi(x[j].x), bf16_lo(x[j].y), bf16_hi(x[j].y)};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) w[d][j >> 2] |= code8<KV>(v[d], g[PC ? d : 0]) << (8 * (j & 3));
+    }
+    if (a <= k && k + 8 <= e) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) *reinterpret_cast<uint2*>(dst + d * kPage + k) = make_uint2(w[d][0], w[d][1]);
+    } else {   // only the range's own positions
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k + j >= a && k + j < e) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) dst[d * kPage + k + j] = (uint8_t)(w[d][j >> 2] >> (8 * (j & 3)));
+        }
+    }
+  }
+}
+
+// The page of position `pos` of sequence b, or -1 (and the status recorded).
+__device__ __forceinline__ int page_at(const RopeParams& p, int b, int pos, int lane) {
+  const int lp = pos / kPage;
+  const int page = lp < p.a.max_blocks ? p.a.block_table[(int64_t)b * p.a.max_blocks + lp] : -1;
+  if (page >= 0 && page < p.a.num_pages) return page;
+  if (lane == 0) record_status(p.a.status, PA_ERR_BAD_PAGE, b);
+  return -1;
+}
+
+// A unit of U positions: sequence, first position, and the range's part [lo, hi) of it.
+struct UnitAt {
+  int b, u0, lo, hi;
+  int64_t row;   // token row of position lo
+};
+
+template <int U>
+__device__ __forceinline__ bool unit_at(const RopeParams& p, const RowUnits& units, uint32_t n, int lane, UnitAt& m) {
+  int u;
+  find_unit<U>(units, p.a.cu_seqlens_q, n, lane, m.b, u);
+  const int q = p.a.seq_lens[m.b];
+  if (q <= 0) return false;
+  const int start = p.a.seq_lens_kv[m.b], end = start + q;
+  m.u0 = (start / U + u) * U;
+  m.lo = max(m.u0, start);
+  m.hi = min(m.u0 + U, end);
+  m.row = (int64_t)p.a.cu_seqlens_q[m.b] + (m.lo - start);
+  return m.lo < m.hi;
+}
+
+// ---- GQA
+template <int KV, bool PC, int U>
+__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeParams p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  constexpr int kSlabBytes = is_four<KV>() ? kV4Slab : kPage * kV4Dim;
+  UnitAt m;
+  if (id >= p.rot_warps) {   // V
+    const uint32_t n = id - p.rot_warps;
+    if (n >= p.a.total) return;
+    const uint32_t bu = n / (uint32_t)p.a.kv_heads;
+    const int kvh = (int)(n - bu * p.a.kv_heads);
+    if (!unit_at<U>(p, p.a.units, bu, lane, m)) return;
+    const int page = page_at(p, m.b, m.u0, lane);
+    if (page < 0) return;
+    const __nv_bfloat16* rows = p.a.v_new + m.row * p.a.kv_stride + (int64_t)kvh * kV4Dim;
+    uint8_t* slab = p.a.cache_v + ((int64_t)page * p.a.kv_heads + kvh) * kSlabBytes;
+    const int a = m.lo - m.u0, e = m.hi - m.u0;
+    if constexpr (is_four<KV>()) {
+      constexpr int FP4 = KV == PA_KV_FP4_E2M1;
+      uint8_t* half = slab + m.u0 % kPage / kV4Half * kV4HalfBytes;
+      const int first = m.u0 % kV4Half;
+      e - a == U ? write_v<FP4, PC, U, true>(p.a, rows, half, kvh, first, a, e, lane)
+                 : write_v<FP4, PC, U, false>(p.a, rows, half, kvh, first, a, e, lane);
+    } else {
+      store_v8<KV, PC, U>(p, rows, slab, kvh, m.u0 % kPage, a, e, lane);
+    }
+    return;
+  }
+  // rotation: head group fastest, so that neighbouring warps read the same rows
+  const uint32_t bu = id / (uint32_t)p.groups;
+  const int g0 = (int)(id - bu * p.groups) * p.group_heads;
+  const int heads = p.q_heads + p.a.kv_heads, g1 = min(heads, g0 + p.group_heads);
+  if (!unit_at<kRopeUnit>(p, p.units, bu, lane, m)) return;
+  const int page = g1 > p.q_heads ? page_at(p, m.b, m.u0, lane) : -1;
+  const int c = lane & 15, oct = p.rot / 8;
+  const bool turned = c < oct;
+  // the lane whose dims are the other halves of this one's pairs
+  const int other = p.adjacent || !turned ? lane : (lane & 16) | (c < oct / 2 ? c + oct / 2 : c - oct / 2);
+  for (int r = m.lo; r < m.hi; r += 2) {
+    const int pos = r + (lane >> 4);
+    const bool in = pos < m.hi;
+    const int64_t t = m.row + (pos - m.lo);
+    Turn a;
+    const bool turn = in && turned && load_turn(p, t, pos, c, a);
+    for (int h0 = g0; h0 < g1; h0 += 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int h = h0 + k;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (in && h < g1)
+          x[k] = *reinterpret_cast<const uint4*>(
+              h < p.q_heads ? p.q + t * p.q_stride + h * kV4Dim + 8 * c
+                            : p.a.k_new + t * p.a.kv_stride + (h - p.q_heads) * kV4Dim + 8 * c);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int h = h0 + k;
+        if (h >= g1) break;
+        const uint4 y = p.adjacent ? x[k] : shfl4(x[k], other);
+        float f[8];
+        if (turn) turn8(p, x[k], y, a, f);
+        else plain8(x[k], f);
+        if (h < p.q_heads) {
+          if (in) *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * kV4Dim + 8 * c) = bf16x8_of(f);
+        } else if (page >= 0) {
+          const int kvh = h - p.q_heads;
+          store_k<KV, PC>(p, f, p.a.cache_k + ((int64_t)page * p.a.kv_heads + kvh) * kSlabBytes, kvh, pos % kPage, c, in);
+        }
+      }
+    }
+  }
+}
+
+// ---- MLA: groups of query heads, and one more for the latent row
+template <int KV>
+__global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopeParams p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (id >= p.rot_warps) return;
+  const uint32_t bu = id / (uint32_t)p.groups;
+  const int g0 = (int)(id - bu * p.groups) * p.group_heads;
+  UnitAt m;
+  if (!unit_at<kRopeUnit>(p, p.units, bu, lane, m)) return;
+  const int o = lane & 7, oct = p.rot / 8;
+  const bool turned = o < oct;
+  const int other = p.adjacent || !turned ? lane : (lane & 24) | (o < oct / 2 ? o + oct / 2 : o - oct / 2);
+  if (g0 >= p.q_heads) {   // the rows of the cache
+    const int page = page_at(p, m.b, m.u0, lane);
+    if (page < 0) return;
+    const float s = load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0);
+    for (int pos = m.lo; pos < m.hi; ++pos) {
+      const int64_t t = m.row + (pos - m.lo);
+      const __nv_bfloat16* src = p.a.k_new + t * p.a.kv_stride;
+      uint8_t* dst = p.a.cache_k + ((int64_t)page * kPage + pos % kPage) * kMlaRow;
+      uint4 x[3] = {};
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < 2 || lane < 8) x[k] = *reinterpret_cast<const uint4*>(src + 8 * (lane + 32 * k));
+      Turn a;
+      const bool turn = lane < 8 && turned && load_turn(p, t, pos, o, a);
+      const uint4 y = p.adjacent ? x[2] : shfl4(x[2], other);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (k == 2 && lane >= 8) break;
+        float f[8];
+        if (k == 2 && turn) turn8(p, x[2], y, a, f);
+        else plain8(x[k], f);
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(f[e], s) << (8 * (e & 3));
+        *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * k)) = make_uint2(w[0], w[1]);
+      }
+    }
+    return;
+  }
+  const bool copy = p.q_out != p.q;   // dims before the rotated ones; they stay in place
+  const int g1 = min(p.q_heads, g0 + p.group_heads);
+  for (int pos = m.lo; pos < m.hi; ++pos) {
+    const int64_t t = m.row + (pos - m.lo);
+    const __nv_bfloat16* src = p.q + t * p.q_stride;
+    __nv_bfloat16* dst = p.q_out + t * p.q_out_stride;
+    Turn a;
+    const bool turn = turned && load_turn(p, t, pos, o, a);
+    for (int h0 = g0; h0 < g1; h0 += 4) {   // the heads are a multiple of four
+      const int at = (h0 + (lane >> 3)) * kMlaQ + kMlaNope + 8 * o;
+      const int at0 = (h0 + (lane >> 4)) * kMlaQ + 8 * (lane & 15), at1 = at0 + 2 * kMlaQ;
+      const uint4 x = *reinterpret_cast<const uint4*>(src + at);
+      uint4 n0, n1;
+      if (copy) {
+        n0 = *reinterpret_cast<const uint4*>(src + at0);
+        n1 = *reinterpret_cast<const uint4*>(src + at1);
+      }
+      const uint4 y = p.adjacent ? x : shfl4(x, other);
+      float f[8];
+      if (turn) turn8(p, x, y, a, f);
+      else plain8(x, f);
+      *reinterpret_cast<uint4*>(dst + at) = bf16x8_of(f);
+      if (copy) {
+        *reinterpret_cast<uint4*>(dst + at0) = n0;
+        *reinterpret_cast<uint4*>(dst + at1) = n1;
+      }
+    }
+  }
+}
+
+template <int KV, int U>
+cudaError_t launch_gqa(RopeParams& p, const Plan& plan, cudaStream_t stream) {
+  p.a.units = row_units<U>(plan.prob.bsz, plan.max_q, plan.total_q);
+  const double v = (double)p.a.units.count * plan.prob.kv_heads;
+  if (v + p.rot_warps > (double)INT32_MAX) return cudaErrorInvalidValue;
+  p.a.total = (uint32_t)v;
+  const dim3 grid((p.rot_warps + p.a.total + kWarps - 1) / kWarps), block(kWarps * 32);
+  if (p.a.scale_kind == PA_SCALE_PER_CHANNEL) rope_append_kernel<KV, true, U><<<grid, block, 0, stream>>>(p);
+  else rope_append_kernel<KV, false, U><<<grid, block, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int KV>
+cudaError_t launch_kv(RopeParams& p, const Plan& plan, bool small, cudaStream_t stream) {
+  return small ? launch_gqa<KV, 8>(p, plan, stream) : launch_gqa<KV, 32>(p, plan, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope& rope, const void* q,
+                               int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new,
+                               const void* v_new, int64_t kv_stride, int32_t* status, cudaStream_t stream) {
+  const pa_problem& pr = plan.prob;
+  if (pr.bsz == 0 || plan.max_q == 0) return cudaSuccess;
+  RopeParams p{};
+  p.a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.a.kv_stride = kv_stride;
+  p.a.cache_k = static_cast<uint8_t*>(const_cast<void*>(a.cache_k));
+  p.a.cache_v = static_cast<uint8_t*>(const_cast<void*>(a.cache_v));
+  p.a.k_scale = a.k_scale;
+  p.a.v_scale = a.v_scale;
+  p.a.block_table = a.block_table;
+  p.a.seq_lens = a.seq_lens;
+  p.a.seq_lens_kv = a.seq_lens_kv;
+  p.a.cu_seqlens_q = a.cu_seqlens_q;
+  p.a.status = status;
+  p.a.max_blocks = pr.max_blocks_per_seq;
+  p.a.num_pages = pr.num_pages;
+  p.a.kv_heads = pr.kv_heads;
+  p.a.scale_kind = pr.scale_kind;
+  p.a.vec = 1;
+  p.cos_sin = rope.cos_sin;
+  p.positions = rope.positions;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.q_heads = q ? pr.q_heads : 0;
+  p.table_rows = rope.table_rows;
+  p.rot = rope.rot_dim;
+  p.adjacent = rope.pairs == PA_ROPE_ADJACENT;
+  p.axes = rope.axes;
+  p.total_q = plan.total_q;
+  p.quads = 1;
+  for (int i = 0; i < rope.rot_dim / 2; ++i) {
+    p.pair_axis[i >> 4] |= (uint32_t)(rope.pair_axis[i] & 3) << (2 * (i & 15));
+    if (rope.pair_axis[i] != rope.pair_axis[i & ~3]) p.quads = 0;
+  }
+  p.units = row_units<kRopeUnit>(pr.bsz, plan.max_q, plan.total_q);
+  const bool mla = pr.layout == PA_LAYOUT_MLA;
+  const int heads = p.q_heads + (mla ? 0 : pr.kv_heads);
+  // Heads of a warp: enough to use a row's cos and sin often, few while the warps would
+  // not fill the GPU
+  p.group_heads = 16;
+  while (p.group_heads > 4 &&
+         (double)p.units.count * ((heads + p.group_heads - 1) / p.group_heads) < 16.0 * kWarps * plan.num_sms)
+    p.group_heads /= 2;
+  p.groups = (heads + p.group_heads - 1) / p.group_heads + (mla ? 1 : 0);
+  const double rot = (double)p.units.count * p.groups;
+  if (rot > (double)INT32_MAX) return cudaErrorInvalidValue;
+  p.rot_warps = (uint32_t)rot;
+  if (mla) {
+    const dim3 grid((p.rot_warps + kWarps - 1) / kWarps), block(kWarps * 32);
+    if (pr.kv_dtype == PA_KV_FP8_E4M3) rope_latent_kernel<PA_KV_FP8_E4M3><<<grid, block, 0, stream>>>(p);
+    else rope_latent_kernel<PA_KV_INT8><<<grid, block, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  // V's units as pa_cache4.cu takes them
+  const bool small = 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms;
+  switch (pr.kv_dtype) {
+    case PA_KV_INT8: return launch_kv<PA_KV_INT8>(p, plan, small, stream);
+    case PA_KV_FP8_E4M3: return launch_kv<PA_KV_FP8_E4M3>(p, plan, small, stream);
+    case PA_KV_INT4: return launch_kv<PA_KV_INT4>(p, plan, small, stream);
+    default: return launch_kv<PA_KV_FP4_E2M1>(p, plan, small, stream);
+  }
+}
+
+}  // namespace pa
