@@ -372,6 +372,35 @@ pa_status pa_rope_append(const pa_plan_t* plan, const pa_args* args, const pa_ro
                          const void* k_new, const void* v_new, int64_t kv_stride,
                          void* workspace, void* stream);
 
+/*
+ * The products around latent attention.  A head has 256 x 512 bf16 weights, 128 rows W_k
+ * (its keys from a latent row) and 128 rows W_v (its values): one tensor
+ * [heads][256][512] serves all three, w being the first W_k row of head 0 for absorb and
+ * expand, the first W_v row for project, and heads w_head_stride elements apart.  Any
+ * number of heads (a share of a model's) and rows; fp32 sums, outputs rounded to bf16 once.
+ *   pa_mla_absorb   absorbed form, in: q bf16, row t at t * q_stride, head h at h * 192
+ *                   (128 dims, then 64 rotated); out, row t at t * out_stride, head h at
+ *                   h * 576: its 512 dims in the latent space, q W_k, and the rotated 64.
+ *                   With 128 heads, out is args.q of pa_run for the MLA layout.
+ *   pa_mla_project  absorbed form, out: o rows of heads * 512 (out of pa_run and
+ *                   pa_merge); out rows of heads * 128, W_v o.
+ *   pa_mla_expand   expanded form: c bf16, row n's 512 latent dims at n * c_stride (rows of
+ *                   576 as pa_cache_read gives them, or the model's); k_out and v_out, row
+ *                   n at n * kv_stride, head h at h * 128.
+ * Inputs must be finite (a NaN or infinity spreads over its row's outputs, nowhere else).
+ * Pointers 16-byte aligned, strides multiples of 8 elements; outputs do not overlap inputs.
+ * Elements of an output row behind the last head are left as they were.
+ * workspace: device, its first 256 bytes are the status block (of an uploaded plan, or
+ * zeroed), which pa_check(NULL, workspace, ...) reads.  Asynchronous on stream; no allocation.
+ */
+pa_status pa_mla_absorb(int32_t rows, int32_t heads, const void* q, int64_t q_stride, const void* w,
+                        int64_t w_head_stride, void* out, int64_t out_stride, void* workspace, void* stream);
+pa_status pa_mla_project(int32_t rows, int32_t heads, const void* o, int64_t o_stride, const void* w,
+                         int64_t w_head_stride, void* out, int64_t out_stride, void* workspace, void* stream);
+pa_status pa_mla_expand(int32_t rows, int32_t heads, const void* c, int64_t c_stride, const void* w,
+                        int64_t w_head_stride, void* k_out, void* v_out, int64_t kv_stride, void* workspace,
+                        void* stream);
+
 /* Bytes of cache_k and of cache_v for a problem's pool (MLA: *v_bytes = 0, V
  * being part of cache_k's rows). */
 pa_status pa_cache_bytes(const pa_problem* problem, size_t* k_bytes, size_t* v_bytes);
@@ -420,7 +449,7 @@ pa_status pa_debug_gather(const pa_problem* problem, const pa_args* args, int32_
  * waits a millisecond on one barrier).  The waits at a kernel's exit for
  * copies and MMAs it has itself issued keep a fixed 2e9 ns bound, so no limit
  * set here lets shared or tensor memory be released under work in flight.
- * With skip_first_load != 0 the next pa_run's loader skips its first page
+ * With skip_first_load != 0 the loader of the next pa_run or pa_mla_* call skips its first page
  * load so the consumers' bounded wait runs out and the run records
  * PA_ERR_DEVICE_TIMEOUT (read it with pa_check).  Process-wide setting.
  */

@@ -33,6 +33,7 @@ KV_DTYPES = {"int8": 0, "fp8_e4m3": 1, "int4": 2, "fp4_e2m1": 3}
 MASK_FULL, MASK_CAUSAL, MASK_CROSS = 0, 1, 2
 SCALE_KINDS = {"per_kv_head": 0, "per_channel": 1, "global": 2}
 LAYOUTS = {"gqa": 0, "mla": 1}
+PA_STATUS_BYTES = 256     # the status block at the start of a workspace
 ROPE_PAIRS = {"halves": 0, "adjacent": 1}
 FAMILIES = {0: "decode", 1: "append", 2: "mla"}
 
@@ -102,6 +103,9 @@ def _load():
         "pa_cache_read": ([vp, ctypes.POINTER(PaArgs), vp, vp, i64, vp, vp], i32),
         "pa_rope_append": ([vp, ctypes.POINTER(PaArgs), ctypes.POINTER(PaRope), vp, i64, vp, i64, vp, vp, i64, vp,
                             vp], i32),
+        "pa_mla_absorb": ([i32, i32, vp, i64, vp, i64, vp, i64, vp, vp], i32),
+        "pa_mla_project": ([i32, i32, vp, i64, vp, i64, vp, i64, vp, vp], i32),
+        "pa_mla_expand": ([i32, i32, vp, i64, vp, i64, vp, vp, i64, vp, vp], i32),
         "pa_cache_bytes": ([ctypes.POINTER(PaProblem), ctypes.POINTER(ctypes.c_size_t),
                             ctypes.POINTER(ctypes.c_size_t)], i32),
     }
@@ -342,6 +346,30 @@ def pa_rope_append(plan: Plan, args: PaArgs, rope: PaRope, q_new, q_stride: int,
     _check(lib.pa_rope_append(plan.handle, ctypes.byref(args), ctypes.byref(rope), _ptr(q_new), int(q_stride),
                               _ptr(q_out), int(q_out_stride), _ptr(k_new), _ptr(v_new), int(kv_stride),
                               _ptr(workspace), _stream(stream)))
+
+
+def pa_mla_absorb(rows: int, heads: int, q, q_stride: int, w, w_head_stride: int, out, out_stride: int, workspace,
+                  stream=None):
+    """Queries [rows][heads][128 + 64] into the latent space, [rows][heads][512 + 64]
+    (see include/pa.h; workspace: a status block of PA_STATUS_BYTES or more)."""
+    _check(lib.pa_mla_absorb(int(rows), int(heads), _ptr(q), int(q_stride), _ptr(w), int(w_head_stride), _ptr(out),
+                             int(out_stride), _ptr(workspace), _stream(stream)))
+
+
+def pa_mla_project(rows: int, heads: int, o, o_stride: int, w, w_head_stride: int, out, out_stride: int, workspace,
+                   stream=None):
+    """Latent outputs [rows][heads][512] out of the latent space, [rows][heads][128]
+    (see include/pa.h; w: the first W_v row of head 0)."""
+    _check(lib.pa_mla_project(int(rows), int(heads), _ptr(o), int(o_stride), _ptr(w), int(w_head_stride), _ptr(out),
+                              int(out_stride), _ptr(workspace), _stream(stream)))
+
+
+def pa_mla_expand(rows: int, heads: int, c, c_stride: int, w, w_head_stride: int, k_out, v_out, kv_stride: int,
+                  workspace, stream=None):
+    """Keys and values [rows][heads][128] of every head from latent rows [rows][512]
+    (see include/pa.h)."""
+    _check(lib.pa_mla_expand(int(rows), int(heads), _ptr(c), int(c_stride), _ptr(w), int(w_head_stride), _ptr(k_out),
+                             _ptr(v_out), int(kv_stride), _ptr(workspace), _stream(stream)))
 
 
 def pa_cache_bytes(problem: PaProblem):

@@ -527,6 +527,23 @@ static pa_status make_map_q(CUtensorMap* m, const void* q, uint64_t tokens, uint
   return PA_OK;
 }
 
+// A bf16 tensor of three dims (innermost first; strides in elements, multiples of 8),
+// boxes of 64 x box1 x box2 elements, 128B swizzle.
+static pa_status make_map3(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, int64_t stride1,
+                           int64_t stride2, uint32_t box1, uint32_t box2) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled not available from the driver");
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride2 * 2};
+  const cuuint32_t box[3] = {64, box1, box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed");
+  return PA_OK;
+}
+
 static OutEpilogue epilogue_of(const pa_args& a) {
   OutEpilogue e;
   e.shift = static_cast<const __nv_bfloat16*>(a.shift_bias);
@@ -944,6 +961,78 @@ pa_status pa_cache_read(const pa_plan_t* plan, const pa_args* args, void* k_out,
                                           static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("cache read: ") + cudaGetErrorString(e));
   return PA_OK;
+}
+
+// What the products around latent attention ask of their arguments (widths: dims of a
+// row of x and of the outputs, elements).
+static pa_status check_product(int32_t rows, int32_t heads, const void* x, int64_t x_stride, int64_t x_width,
+                               const void* w, int64_t w_head_stride, int64_t w_width, const void* out,
+                               const void* out2, int64_t out_stride, int64_t out_width, const void* workspace) {
+  if (rows < 0 || heads <= 0) return fail(PA_ERR_INVALID_ARG, "rows must not be negative, heads positive");
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 4)
+    return fail(PA_ERR_INVALID_ARG, "null or misaligned workspace");
+  if (!w || (rows > 0 && (!x || !out || !out2))) return fail(PA_ERR_INVALID_ARG, "null rows, weights or output");
+  if (x_stride < x_width || out_stride < out_width)
+    return fail(PA_ERR_INVALID_ARG, "a row stride smaller than its row");
+  if (w_head_stride < w_width) return fail(PA_ERR_INVALID_ARG, "w_head_stride smaller than a head's weights");
+  if (!rows16(x, x_stride) || !rows16(w, w_head_stride) || !rows16(out, out_stride) || !rows16(out2, out_stride))
+    return fail(PA_ERR_INVALID_ARG, "rows, weights and outputs must be 16-byte aligned, strides multiples of 8");
+  if ((double)x_stride * 2 >= (double)((int64_t)1 << 40) || (double)w_head_stride * 2 >= (double)((int64_t)1 << 40) ||
+      (double)out_stride * 2 >= (double)((int64_t)1 << 40))
+    return fail(PA_ERR_INVALID_ARG, "a stride of 2^40 bytes or more");
+  return PA_OK;
+}
+
+static pa_status run_product(MlaProduct& m, void* stream) {
+  FaultCfg fc;
+  {
+    std::lock_guard<std::mutex> lk(g_fault_mu);
+    fc = g_faults;
+    g_faults.skip_first_load = 0;  // one-shot
+  }
+  const cudaError_t e = launch_mla_product(m, fc, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("product: ") + cudaGetErrorString(e));
+  return PA_OK;
+}
+
+pa_status pa_mla_absorb(int32_t rows, int32_t heads, const void* q, int64_t q_stride, const void* w,
+                        int64_t w_head_stride, void* out, int64_t out_stride, void* workspace, void* stream) {
+  pa_status s = check_product(rows, heads, q, q_stride, (int64_t)heads * 192, w, w_head_stride, 128 * 512, out, out,
+                              out_stride, (int64_t)heads * 576, workspace);
+  if (s != PA_OK || rows == 0) return s;
+  MlaProduct m{0, rows, heads, q, out, q_stride, out_stride, static_cast<int32_t*>(workspace), {}};
+  if ((s = make_map3(&m.tm[0], q, 128, heads, rows, 192, q_stride, 1, 128)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[1], w, 512, 128, heads, 512, w_head_stride, 64, 1)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[2], out, 512, heads, rows, 576, out_stride, 1, 32)) != PA_OK) return s;
+  m.tm[3] = m.tm[2];
+  return run_product(m, stream);
+}
+
+pa_status pa_mla_project(int32_t rows, int32_t heads, const void* o, int64_t o_stride, const void* w,
+                         int64_t w_head_stride, void* out, int64_t out_stride, void* workspace, void* stream) {
+  pa_status s = check_product(rows, heads, o, o_stride, (int64_t)heads * 512, w, w_head_stride, 128 * 512, out, out,
+                              out_stride, (int64_t)heads * 128, workspace);
+  if (s != PA_OK || rows == 0) return s;
+  MlaProduct m{1, rows, heads, o, out, o_stride, out_stride, static_cast<int32_t*>(workspace), {}};
+  if ((s = make_map3(&m.tm[0], o, 512, heads, rows, 512, o_stride, 1, 128)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[1], w, 512, 128, heads, 512, w_head_stride, 128, 1)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[2], out, 128, heads, rows, 128, out_stride, 1, 32)) != PA_OK) return s;
+  m.tm[3] = m.tm[2];
+  return run_product(m, stream);
+}
+
+pa_status pa_mla_expand(int32_t rows, int32_t heads, const void* c, int64_t c_stride, const void* w,
+                        int64_t w_head_stride, void* k_out, void* v_out, int64_t kv_stride, void* workspace,
+                        void* stream) {
+  pa_status s = check_product(rows, heads, c, c_stride, 512, w, w_head_stride, 256 * 512, k_out, v_out, kv_stride,
+                              (int64_t)heads * 128, workspace);
+  if (s != PA_OK || rows == 0) return s;
+  MlaProduct m{2, rows, heads, c, k_out, c_stride, kv_stride, static_cast<int32_t*>(workspace), {}};
+  if ((s = make_map3(&m.tm[0], c, 512, 1, rows, 512, c_stride, 1, 128)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[1], w, 512, 256, heads, 512, w_head_stride, 256, 1)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[2], k_out, 128, heads, rows, 128, kv_stride, 1, 32)) != PA_OK) return s;
+  if ((s = make_map3(&m.tm[3], v_out, 128, heads, rows, 128, kv_stride, 1, 32)) != PA_OK) return s;
+  return run_product(m, stream);
 }
 
 pa_status pa_debug_set_faults(int64_t wait_limit_ns, int32_t skip_first_load) {

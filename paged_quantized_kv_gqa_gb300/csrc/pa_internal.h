@@ -167,6 +167,17 @@ struct AttnParams {
   int32_t part_slots;    // so many slots of partial rows (Plan::part_slots)
 };
 
+// One of the products around latent attention (pa_mla_product.cu): x times the weights.
+struct MlaProduct {
+  int32_t op;              // 0 absorb, 1 project, 2 expand
+  int32_t rows, heads;
+  const void* x;
+  void* out;
+  int64_t x_stride, out_stride;
+  int32_t* status;
+  CUtensorMap tm[4];       // x, weights, output, second output (expand's values)
+};
+
 void set_error(const std::string& msg);
 
 // launchers (return a cudaError_t from the launch)
@@ -192,6 +203,7 @@ cudaError_t launch_append4(const Plan& plan, const AttnParams& p, const void* ck
 cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void* k_new,
                                  const void* v_new, int64_t kv_stride, int32_t* status,
                                  cudaStream_t stream);
+cudaError_t launch_mla_product(const MlaProduct& m, const FaultCfg& fc, cudaStream_t stream);
 // queries rotated, K / V rows rotated (K) and written, every cache
 cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope& rope, const void* q,
                                int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new,
