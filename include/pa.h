@@ -62,11 +62,12 @@ typedef enum pa_status {
   PA_ERR_BAD_POSITION = 7   /* a position outside the rotation's table        */
 } pa_status;
 
-enum { PA_KV_INT8 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT4 = 2, PA_KV_FP4_E2M1 = 3 };
+enum { PA_KV_INT8 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT4 = 2, PA_KV_FP4_E2M1 = 3,
+       PA_KV_BF16 = 4 /* expanded latent rows, no cache */ };
 enum { PA_MASK_FULL = 0, PA_MASK_CAUSAL = 1, PA_MASK_CROSS = 2 };   /* pa_problem.causal */
 enum { PA_SCALE_PER_KV_HEAD = 0, PA_SCALE_PER_CHANNEL = 1, PA_SCALE_GLOBAL = 2 };
-enum { PA_LAYOUT_GQA = 0, PA_LAYOUT_MLA = 1 };
-enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
+enum { PA_LAYOUT_GQA = 0, PA_LAYOUT_MLA = 1, PA_LAYOUT_MLA_EXPANDED = 2 };
+enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2, PA_FAMILY_EXPANDED = 3 };
 
 /*
  * Problem shape (host struct, copied by pa_plan).
@@ -87,6 +88,13 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2 };
  *               real value = code * scale of its 16 dims * k_scale or v_scale.
  *               Bytes of positions outside a sequence may hold anything; the
  *               scales of its positions must be finite.
+ *   MLA_EXPANDED layout: attention to expanded rows (pa_mla_expand) instead of a cache,
+ *               run by pa_mla_prefill.  q_heads = kv_heads (any number, a share of a
+ *               model's), head_dim_qk 192 (128 and 64 rotated ones), head_dim_v 128,
+ *               kv_dtype PA_KV_BF16; block_size (64), max_blocks_per_seq, num_pages and
+ *               scale_kind are not used.  The rows of all sequences follow one another:
+ *               sequence b has kvtot_b of them (its prefix and its new tokens; with
+ *               PA_MASK_CROSS seq_lens_kv[b], the new tokens not among them).
  *   Scales: PER_KV_HEAD  bf16 [kv_heads]              (k_scale and v_scale)
  *           PER_CHANNEL  bf16 [kv_heads * head_dim]   (index kvh * D + d)
  *           GLOBAL       fp32 [1]                     (one value for K and V)
@@ -400,6 +408,27 @@ pa_status pa_mla_project(int32_t rows, int32_t heads, const void* o, int64_t o_s
 pa_status pa_mla_expand(int32_t rows, int32_t heads, const void* c, int64_t c_stride, const void* w,
                         int64_t w_head_stride, void* k_out, void* v_out, int64_t kv_stride, void* workspace,
                         void* stream);
+
+/*
+ * pa_mla_prefill: attention of a plan's new tokens to expanded latent rows, the expanded
+ * form of latent attention (a plan of the MLA_EXPANDED layout).  Row j of sequence b is
+ * row n = kvtot_0 + .. + kvtot_{b-1} + j of
+ *   k_nope, v  bf16, row n at n * kv_stride, head h at h * 128 (pa_mla_expand's outputs)
+ *   k_rope     bf16, row n's 64 rotated dims at n * rope_stride, the same for all heads
+ *              (columns 512 .. 575 of the latent rows: pass their address and stride)
+ *   s_ij = sm_scale * (<q_i[0:128], k_nope_j> + <q_i[128:192], k_rope_j>)
+ * with visibility, out and lse as above.  args: q (head h of a token at h * 192), out, lse
+ * and the output epilogue; the rest is unused.  Rows of a sequence must be finite where
+ * any of its tokens sees them; rows of other sequences may hold anything.
+ *   A plan with chunk_size != 0 may split ranges: call pa_merge afterwards (it also writes
+ * the rows that see nothing).  Ranges of one sequence run by several plans (new tokens
+ * against a cached prefix, cross, and among themselves) are joined by their out and lse.
+ *   q, k_nope, v, k_rope, out 16-byte aligned, strides multiples of 8 elements.
+ * Asynchronous on stream; no allocation.
+ */
+pa_status pa_mla_prefill(const pa_plan_t* plan, const pa_args* args, const void* k_nope, const void* v,
+                         int64_t kv_stride, const void* k_rope, int64_t rope_stride, void* workspace,
+                         void* stream);
 
 /* Bytes of cache_k and of cache_v for a problem's pool (MLA: *v_bytes = 0, V
  * being part of cache_k's rows). */

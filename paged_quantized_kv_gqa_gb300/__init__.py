@@ -29,13 +29,13 @@ LIB_PATH = os.path.join(_HERE, "libpa_gb300_trace.so" if os.environ.get("PA_GB30
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA = 0, 1, 2, 3
 PA_ERR_DEVICE_TIMEOUT, PA_ERR_BAD_PAGE, PA_ERR_BAD_ITEM, PA_ERR_BAD_POSITION = 4, 5, 6, 7
-KV_DTYPES = {"int8": 0, "fp8_e4m3": 1, "int4": 2, "fp4_e2m1": 3}
+KV_DTYPES = {"int8": 0, "fp8_e4m3": 1, "int4": 2, "fp4_e2m1": 3, "bf16": 4}
 MASK_FULL, MASK_CAUSAL, MASK_CROSS = 0, 1, 2
 SCALE_KINDS = {"per_kv_head": 0, "per_channel": 1, "global": 2}
-LAYOUTS = {"gqa": 0, "mla": 1}
+LAYOUTS = {"gqa": 0, "mla": 1, "mla_expanded": 2}
 PA_STATUS_BYTES = 256     # the status block at the start of a workspace
 ROPE_PAIRS = {"halves": 0, "adjacent": 1}
-FAMILIES = {0: "decode", 1: "append", 2: "mla"}
+FAMILIES = {0: "decode", 1: "append", 2: "mla", 3: "expanded"}
 
 
 class PaProblem(ctypes.Structure):
@@ -106,6 +106,7 @@ def _load():
         "pa_mla_absorb": ([i32, i32, vp, i64, vp, i64, vp, i64, vp, vp], i32),
         "pa_mla_project": ([i32, i32, vp, i64, vp, i64, vp, i64, vp, vp], i32),
         "pa_mla_expand": ([i32, i32, vp, i64, vp, i64, vp, vp, i64, vp, vp], i32),
+        "pa_mla_prefill": ([vp, ctypes.POINTER(PaArgs), vp, vp, i64, vp, i64, vp, vp], i32),
         "pa_cache_bytes": ([ctypes.POINTER(PaProblem), ctypes.POINTER(ctypes.c_size_t),
                             ctypes.POINTER(ctypes.c_size_t)], i32),
     }
@@ -172,11 +173,17 @@ def _stream(s) -> Optional[int]:
     return int(s.cuda_stream)
 
 
-def make_problem(*, bsz, q_heads, kv_heads, head_dim_qk, head_dim_v, block_size,
-                 max_blocks_per_seq, num_pages, kv_dtype, scale_kind, layout, causal,
+def make_problem(*, bsz, q_heads, kv_heads, head_dim_qk, head_dim_v, block_size=64,
+                 max_blocks_per_seq=None, num_pages=None, kv_dtype, scale_kind=None, layout, causal,
                  chunk_size, sm_scale, q_stride, cross=False) -> PaProblem:
     """cross=True: cross attention to seq_lens_kv cached states, the query tokens
-    not being in the cache (causal must be False then)."""
+    not being in the cache (causal must be False then).  The "mla_expanded" layout has
+    no cache and needs no max_blocks_per_seq, num_pages and scale_kind."""
+    if layout in ("mla_expanded", LAYOUTS["mla_expanded"]):
+        max_blocks_per_seq, num_pages = max_blocks_per_seq or 1, num_pages or 1
+        scale_kind = "global" if scale_kind is None else scale_kind
+    elif max_blocks_per_seq is None or num_pages is None or scale_kind is None:
+        raise TypeError("a cache needs max_blocks_per_seq, num_pages and scale_kind")
     if cross and causal:
         raise ValueError("cross attention has no causal mask")
     p = PaProblem()
@@ -370,6 +377,14 @@ def pa_mla_expand(rows: int, heads: int, c, c_stride: int, w, w_head_stride: int
     (see include/pa.h)."""
     _check(lib.pa_mla_expand(int(rows), int(heads), _ptr(c), int(c_stride), _ptr(w), int(w_head_stride), _ptr(k_out),
                              _ptr(v_out), int(kv_stride), _ptr(workspace), _stream(stream)))
+
+
+def pa_mla_prefill(plan: Plan, args: PaArgs, k_nope, v, kv_stride: int, k_rope, rope_stride: int, workspace,
+                   stream=None):
+    """Attention of the plan's tokens to expanded latent rows (an "mla_expanded" plan;
+    see include/pa.h); pa_merge joins the ranges of split rows."""
+    _check(lib.pa_mla_prefill(plan.handle, ctypes.byref(args), _ptr(k_nope), _ptr(v), int(kv_stride), _ptr(k_rope),
+                              int(rope_stride), _ptr(workspace), _stream(stream)))
 
 
 def pa_cache_bytes(problem: PaProblem):

@@ -51,12 +51,14 @@ static pa_status check_problem(const pa_problem& p) {
     return fail(PA_ERR_INVALID_ARG, "non-positive shape field in pa_problem");
   if (p.q_heads % p.kv_heads != 0)
     return fail(PA_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
-  if (p.kv_dtype < PA_KV_INT8 || p.kv_dtype > PA_KV_FP4_E2M1)
+  if (p.kv_dtype < PA_KV_INT8 || p.kv_dtype > PA_KV_BF16)
     return fail(PA_ERR_INVALID_ARG, "unknown kv_dtype");
   if (p.scale_kind < PA_SCALE_PER_KV_HEAD || p.scale_kind > PA_SCALE_GLOBAL)
     return fail(PA_ERR_INVALID_ARG, "unknown scale_kind");
-  if (p.layout != PA_LAYOUT_GQA && p.layout != PA_LAYOUT_MLA)
+  if (p.layout < PA_LAYOUT_GQA || p.layout > PA_LAYOUT_MLA_EXPANDED)
     return fail(PA_ERR_INVALID_ARG, "unknown layout");
+  if ((p.kv_dtype == PA_KV_BF16) != (p.layout == PA_LAYOUT_MLA_EXPANDED))
+    return fail(PA_ERR_INVALID_ARG, "bf16 rows go with the MLA_EXPANDED layout, and it with them");
   if (p.causal < PA_MASK_FULL || p.causal > PA_MASK_CROSS)
     return fail(PA_ERR_INVALID_ARG, "causal must be 0, 1 or 2 (PA_MASK_CROSS)");
   if (p.chunk_size < -1) return fail(PA_ERR_INVALID_ARG, "chunk_size must be >= -1");
@@ -68,7 +70,10 @@ static pa_status check_problem(const pa_problem& p) {
     return fail(PA_ERR_INVALID_ARG, "q_stride smaller than q_heads * head_dim_qk");
   if (p.q_stride % 8 != 0)
     return fail(PA_ERR_INVALID_ARG, "q_stride must be a multiple of 8 elements (16 bytes)");
-  if (p.layout == PA_LAYOUT_GQA) {
+  if (p.layout == PA_LAYOUT_MLA_EXPANDED) {
+    if (p.q_heads != p.kv_heads || p.head_dim_qk != 192 || p.head_dim_v != 128 || p.block_size != 64)
+      return fail(PA_ERR_UNSUPPORTED, "expanded latent attention is built for kv_heads = q_heads, 192/128, block_size 64");
+  } else if (p.layout == PA_LAYOUT_GQA) {
     if (p.head_dim_qk != 128 || p.head_dim_v != 128 || p.block_size != 64)
       return fail(PA_ERR_UNSUPPORTED, "GQA kernels are built for head_dim 128, block_size 64");
     if (p.scale_kind == PA_SCALE_GLOBAL && p.kv_dtype == PA_KV_INT8)
@@ -109,11 +114,14 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     if (cu[b + 1] - cu[b] != ql[b])
       return fail(PA_ERR_INVALID_ARG, "cu_seqlens_q is not the prefix sum of seq_lens");
     const int64_t kvtot = (int64_t)slkv[b] + (cross ? 0 : ql[b]);
-    if (ceil_div(kvtot, B) > prob.max_blocks_per_seq)
+    if (!P.expanded() && ceil_div(kvtot, B) > prob.max_blocks_per_seq)
       return fail(PA_ERR_INVALID_ARG, "a sequence needs more pages than max_blocks_per_seq");
     if (kvtot >= (int64_t)1 << 30) return fail(PA_ERR_INVALID_ARG, "sequence too long");
     max_q = std::max(max_q, ql[b]);
+    P.kv_rows += kvtot;
   }
+  if (P.expanded() && P.kv_rows >= (int64_t)1 << 31)
+    return fail(PA_ERR_UNSUPPORTED, "too many rows for 32-bit TMA row coordinates");
   P.total_q = bsz > 0 ? cu[bsz] : 0;
   P.max_q = max_q;
 
@@ -122,6 +130,10 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     P.family = PA_FAMILY_MLA;
     rows_cap = prob.q_heads;
     per_item = 2;
+  } else if (P.expanded()) {
+    P.family = PA_FAMILY_EXPANDED;   // two 128-row query tiles, as for append
+    rows_cap = kAppendRows;
+    per_item = 1;
   } else if ((int64_t)max_q * G <= kDecodeRows) {
     P.family = PA_FAMILY_DECODE;
     rows_cap = kDecodeRows;
@@ -304,8 +316,8 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
           maxlim = std::max(maxlim, t.lim);
         }
         W *= prob.kv_heads;
-        const int64_t target = 4LL * slots;
-        cs = std::max<int64_t>(4LL * B, ceil_div(ceil_div(W, target), B) * B);
+        const int64_t target = 4LL * slots, unit = P.expanded() ? kExpandedTile : B;
+        cs = std::max<int64_t>(4LL * unit, ceil_div(ceil_div(W, target), unit) * unit);
         if (cs >= maxlim) cs = 0;
       }
     }
@@ -337,7 +349,21 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       cost[i] = ceil_div((int64_t)items[i * kItemWords + 6] - items[i * kItemWords + 5], B) + 2;
     std::vector<int> order(n);
     for (int i = 0; i < n; ++i) order[i] = i;
-    std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return cost[a] > cost[b]; });
+    // expanded rows: a step of a 128-row tile is the unit (a tile of few rows costs a
+    // whole one), and heads go by blocks whose rows fit L2, longest first within a block
+    int64_t block_heads = prob.kv_heads;
+    if (P.expanded()) {
+      block_heads = std::max<int64_t>(1, kExpandedBlock / (std::max<int64_t>(P.kv_rows, 1) * 512));
+      for (int i = 0; i < n; ++i) {
+        const int32_t* r = &items[(size_t)i * kItemWords];
+        cost[i] = ceil_div((int64_t)r[6] - r[5], kExpandedTile) * (r[3] > 128 ? 2 : 1) + 3;
+      }
+    }
+    auto head_block = [&](int i) { return items[(size_t)i * kItemWords + 1] / block_heads; };
+    std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
+      const int64_t x = head_block(a), y = head_block(b);
+      return x != y ? x < y : cost[a] > cost[b];
+    });
     using Load = std::pair<int64_t, int>;
     std::priority_queue<Load, std::vector<Load>, std::greater<Load>> heap;
     for (int k = 0; k < P.num_ctas; ++k) heap.push({0, k});
@@ -380,14 +406,14 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     P.fused_merge = P.family == PA_FAMILY_DECODE && P.max_chunks > 1 && !empty_rows && !P.four_bit() &&
                     g_faults.fused_merge;
   }
-  P.off_cnt = align4(P.off_merge + P.merge_tokens.size() * (P.four_bit() ? 4 : 1));
+  P.off_cnt = align4(P.off_merge + P.merge_tokens.size() * (P.compact() ? 4 : 1));
   const size_t words = P.off_cnt + (P.fused_merge ? (size_t)P.total_q * prob.kv_heads : 0);
   static_assert(kStatusBytes % 16 == 0, "plan blob must start 16-byte aligned");
   P.blob.assign(std::max<size_t>(words, 1), 0);
   std::copy(P.work_indptr.begin(), P.work_indptr.end(), P.blob.begin() + P.off_indptr);
   std::copy(P.items.begin(), P.items.end(), P.blob.begin() + P.off_items);
   std::copy(P.nch_token.begin(), P.nch_token.end(), P.blob.begin() + P.off_nch);
-  if (P.four_bit()) {
+  if (P.compact()) {
     // every token's slots: as many as it has chunks (max_chunks for every token, as the
     // 8-bit plans have them, is 1210 MB instead of 13 for one sequence of 131k positions
     // beside 255 of 500: equal shares cut the long one into many)
@@ -403,6 +429,12 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       const int32_t nch = (int32_t)((uint32_t)rec[7] >> 16);
       rec[3] = (int32_t)((uint32_t)rec[3] | (uint32_t)nch << 16);
       rec[7] = nch > 1 ? slot0[rec[2]] + (rec[7] & 0xFFFF) : 0;
+    }
+    if (P.expanded()) {   // in place of the sequence, the row of its first position
+      std::vector<int32_t> row0(bsz + 1, 0);
+      for (int b = 0; b < bsz; ++b) row0[b + 1] = row0[b] + slkv[b] + (cross ? 0 : ql[b]);
+      rec = P.blob.data() + P.off_items;
+      for (size_t i = 0; i < P.items.size(); i += kItemWords, rec += kItemWords) rec[0] = row0[rec[0]];
     }
     int32_t* row = P.blob.data() + P.off_merge;
     for (int c = 0; c < kMergeClasses; ++c) {
@@ -421,14 +453,14 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
   }
   P.plan_bytes = P.blob.size() * sizeof(int32_t);
   size_t off = align_up(kStatusBytes + P.plan_bytes, 256);
-  const size_t slots_part = P.four_bit()         ? (size_t)P.part_slots * prob.q_heads
+  const size_t slots_part = P.compact()          ? (size_t)P.part_slots * prob.q_heads
                             : P.max_chunks == 1 ? 0
                                                 : (size_t)P.total_q * P.max_chunks * prob.q_heads;
   P.part_o_off = off;
-  // partial rows: bf16; fp32 over a 4-bit cache, where a second rounding to bf16
+  // partial rows: bf16; fp32 over a 4-bit cache and expanded rows, where a second rounding to bf16
   // would be the largest error of the result (measured on chunked decode: error
   // against 64 bits 0.0024 with bf16 partial rows, 0.0017 without)
-  off = align_up(off + slots_part * prob.head_dim_v * (P.four_bit() ? sizeof(float) : sizeof(__nv_bfloat16)),
+  off = align_up(off + slots_part * prob.head_dim_v * (P.compact() ? sizeof(float) : sizeof(__nv_bfloat16)),
                  256);
   P.part_m_off = off;
   off = align_up(off + slots_part * sizeof(float), 256);
@@ -446,7 +478,8 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     const double q = ql[b];
     pairs += causal ? q * slkv[b] + q * (q + 1) / 2.0 : q * (double)kvtot;
   }
-  P.kv_bytes = prob.layout == PA_LAYOUT_MLA
+  P.kv_bytes = P.expanded() ? P.kv_rows * 2 * (64 + 256 * (int64_t)prob.kv_heads)
+               : prob.layout == PA_LAYOUT_MLA
                    ? pages * B * prob.head_dim_qk
                : P.four_bit() ? pages * 2 * kSlab4 * (int64_t)prob.kv_heads
                    : pages * B * (int64_t)(prob.head_dim_qk + prob.head_dim_v) * prob.kv_heads;
@@ -579,6 +612,8 @@ static pa_status check_args(const Plan& P, const pa_args* a, bool need_cache) {
   if ((a->shift_bias && reinterpret_cast<uintptr_t>(a->shift_bias) % 2) ||
       (a->smooth_weight && reinterpret_cast<uintptr_t>(a->smooth_weight) % 2))
     return fail(PA_ERR_INVALID_ARG, "shift_bias / smooth_weight must be 2-byte aligned (bf16)");
+  if (need_cache && P.expanded())
+    return fail(PA_ERR_INVALID_ARG, "a plan of expanded rows is run by pa_mla_prefill");
   if (need_cache) {
     if (!a->q || !a->cache_k || !a->cache_v || !a->k_scale || !a->v_scale || !a->block_table)
       return fail(PA_ERR_INVALID_ARG, "null device pointer in pa_args");
@@ -802,7 +837,7 @@ pa_status pa_merge(const pa_plan_t* plan, const pa_args* args, void* workspace, 
   if (!plan || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan or workspace");
   pa_status s = check_args(*plan, args, false);
   if (s != PA_OK) return s;
-  if (plan->family == PA_FAMILY_MLA && reinterpret_cast<uintptr_t>(args->out) % 16)
+  if ((plan->family == PA_FAMILY_MLA || plan->expanded()) && reinterpret_cast<uintptr_t>(args->out) % 16)
     return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
   if (plan->fused_merge || plan->merge_in_run()) return PA_OK;   // pa_run merged the split rows
   return enqueue_merge(*plan, *args, ws_view(*plan, workspace), static_cast<cudaStream_t>(stream));
@@ -843,6 +878,7 @@ pa_status pa_debug_gather(const pa_problem* problem, const pa_args* args, int32_
     return fail(PA_ERR_INVALID_ARG, "null argument to pa_debug_gather");
   if (problem->kv_dtype == PA_KV_INT4 || problem->kv_dtype == PA_KV_FP4_E2M1)
     return fail(PA_ERR_UNSUPPORTED, "pa_debug_gather copies 8-bit caches; use pa_cache_read");
+  if (problem->layout == PA_LAYOUT_MLA_EXPANDED) return fail(PA_ERR_INVALID_ARG, "expanded rows have no cache");
   if (b < 0 || b >= problem->bsz || kv_head < 0 || kv_head >= problem->kv_heads || pos0 < 0 ||
       n < 0 ||
       (int64_t)pos0 + n > (int64_t)problem->max_blocks_per_seq * problem->block_size)
@@ -857,6 +893,7 @@ pa_status pa_cache_bytes(const pa_problem* problem, size_t* k_bytes, size_t* v_b
   if (!problem || !k_bytes || !v_bytes) return fail(PA_ERR_INVALID_ARG, "null argument to pa_cache_bytes");
   pa_status s = check_problem(*problem);
   if (s != PA_OK) return s;
+  if (problem->layout == PA_LAYOUT_MLA_EXPANDED) return fail(PA_ERR_INVALID_ARG, "expanded rows have no cache");
   const size_t n = (size_t)problem->num_pages * problem->kv_heads;
   if (problem->kv_dtype == PA_KV_INT4 || problem->kv_dtype == PA_KV_FP4_E2M1) {
     *k_bytes = *v_bytes = n * kSlab4;
@@ -873,6 +910,7 @@ static pa_status check_rows(const pa_plan_t* plan, const pa_args* args, const vo
   if (!plan || !args || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan, args or workspace");
   const pa_problem& pr = plan->prob;
   const bool mla = pr.layout == PA_LAYOUT_MLA;
+  if (plan->expanded()) return fail(PA_ERR_INVALID_ARG, "a plan of expanded rows has no cache");
   if (pr.causal == PA_MASK_CROSS)
     return fail(PA_ERR_INVALID_ARG, "a cross-attention plan appends no rows: write and read the "
                                     "encoder states with a plan of their own lengths");
@@ -909,6 +947,9 @@ pa_status pa_cache_append(const pa_plan_t* plan, const pa_args* args, const void
 static bool rows16(const void* rows, int64_t stride) {
   return reinterpret_cast<uintptr_t>(rows) % 16 == 0 && stride % 8 == 0;
 }
+
+// A stride (elements of 2 bytes) that a tensor map can hold.
+static bool tma_stride(int64_t stride) { return stride < (int64_t)1 << 39; }
 
 pa_status pa_rope_append(const pa_plan_t* plan, const pa_args* args, const pa_rope* rope,
                          const void* q_new, int64_t q_stride, void* q_out, int64_t q_out_stride,
@@ -977,8 +1018,7 @@ static pa_status check_product(int32_t rows, int32_t heads, const void* x, int64
   if (w_head_stride < w_width) return fail(PA_ERR_INVALID_ARG, "w_head_stride smaller than a head's weights");
   if (!rows16(x, x_stride) || !rows16(w, w_head_stride) || !rows16(out, out_stride) || !rows16(out2, out_stride))
     return fail(PA_ERR_INVALID_ARG, "rows, weights and outputs must be 16-byte aligned, strides multiples of 8");
-  if ((double)x_stride * 2 >= (double)((int64_t)1 << 40) || (double)w_head_stride * 2 >= (double)((int64_t)1 << 40) ||
-      (double)out_stride * 2 >= (double)((int64_t)1 << 40))
+  if (!tma_stride(x_stride) || !tma_stride(w_head_stride) || !tma_stride(out_stride))
     return fail(PA_ERR_INVALID_ARG, "a stride of 2^40 bytes or more");
   return PA_OK;
 }
@@ -1033,6 +1073,66 @@ pa_status pa_mla_expand(int32_t rows, int32_t heads, const void* c, int64_t c_st
   if ((s = make_map3(&m.tm[2], k_out, 128, heads, rows, 128, kv_stride, 1, 32)) != PA_OK) return s;
   if ((s = make_map3(&m.tm[3], v_out, 128, heads, rows, 128, kv_stride, 1, 32)) != PA_OK) return s;
   return run_product(m, stream);
+}
+
+pa_status pa_mla_prefill(const pa_plan_t* plan, const pa_args* args, const void* k_nope, const void* v,
+                         int64_t kv_stride, const void* k_rope, int64_t rope_stride, void* workspace,
+                         void* stream) {
+  if (!plan || !workspace) return fail(PA_ERR_INVALID_ARG, "null plan or workspace");
+  if (!plan->expanded()) return fail(PA_ERR_INVALID_ARG, "pa_mla_prefill runs plans of the MLA_EXPANDED layout");
+  pa_status s = check_args(*plan, args, false);
+  if (s != PA_OK) return s;
+  const pa_problem& pr = plan->prob;
+  if (args->attn_mask) return fail(PA_ERR_UNSUPPORTED, "a tree mask is supported for the decode family only");
+  if (reinterpret_cast<uintptr_t>(args->out) % 16) return fail(PA_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const WsView ws = ws_view(*plan, workspace);
+  if (plan->num_ctas == 0) return plan->merge_in_run() ? enqueue_merge(*plan, *args, ws, st) : PA_OK;
+  if (!args->q || !k_nope || !v || !k_rope) return fail(PA_ERR_INVALID_ARG, "null q, k_nope, v or k_rope");
+  if (kv_stride < (int64_t)pr.kv_heads * 128 || rope_stride < 64)
+    return fail(PA_ERR_INVALID_ARG, "kv_stride or rope_stride smaller than its row");
+  if (!rows16(args->q, pr.q_stride) || !rows16(k_nope, kv_stride) || !rows16(v, kv_stride) || !rows16(k_rope, rope_stride))
+    return fail(PA_ERR_INVALID_ARG, "q, k_nope, v and k_rope must be 16-byte aligned, strides multiples of 8");
+  if (!tma_stride(pr.q_stride) || !tma_stride(kv_stride) || !tma_stride(rope_stride))
+    return fail(PA_ERR_INVALID_ARG, "a stride of 2^40 bytes or more");
+  FaultCfg fc;
+  {
+    std::lock_guard<std::mutex> lk(g_fault_mu);
+    fc = g_faults;
+    g_faults.skip_first_load = 0;  // one-shot
+  }
+  AttnParams p{};
+  p.items = ws.items;
+  p.work_indptr = ws.work_indptr;
+  p.out = static_cast<__nv_bfloat16*>(args->out);
+  p.lse = args->lse;
+  p.part_o = ws.part_o;
+  p.part_m = ws.part_m;
+  p.part_d = ws.part_d;
+  p.status = ws.status;
+  p.wait_limit_ns = fc.wait_limit_ns;
+  p.skip_first_load = fc.skip_first_load;
+  p.q_heads = pr.q_heads;
+  p.kv_heads = pr.kv_heads;
+  p.max_chunks = plan->max_chunks;
+  p.sm_scale_log2 = pr.sm_scale * 1.4426950408889634f;
+  p.ep = epilogue_of(*args);
+  // bounds of the work items (the debug build checks them): an item's first word is a row
+  p.bsz = (int32_t)plan->kv_rows;
+  p.max_blocks = (int32_t)ceil_div(plan->kv_rows, 64);
+  p.total_q = plan->total_q;
+  p.num_items = plan->num_items();
+  p.four_bit = 1;
+  p.part_slots = (int32_t)plan->part_slots;
+  CUtensorMap tq, tk, tr, tv;
+  const uint64_t heads = (uint64_t)pr.q_heads, n = (uint64_t)plan->kv_rows;
+  if ((s = make_map3(&tq, args->q, 192, heads, (uint64_t)plan->total_q, 192, pr.q_stride, 1, 128)) != PA_OK) return s;
+  if ((s = make_map3(&tk, k_nope, 128, heads, n, 128, kv_stride, 1, 128)) != PA_OK) return s;
+  if ((s = make_map3(&tr, k_rope, 64, 1, n, 64, rope_stride, 1, 128)) != PA_OK) return s;
+  if ((s = make_map3(&tv, v, 128, heads, n, 128, kv_stride, 1, 64)) != PA_OK) return s;
+  const cudaError_t e = launch_mla_prefill(*plan, p, tq, tk, tr, tv, st);
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("launch: ") + cudaGetErrorString(e));
+  return plan->merge_in_run() ? enqueue_merge(*plan, *args, ws, st) : PA_OK;
 }
 
 pa_status pa_debug_set_faults(int64_t wait_limit_ns, int32_t skip_first_load) {

@@ -40,6 +40,10 @@ constexpr int kDecode4TileCost = 12;
 // the merge's classes of 4-bit rows: 32, 16, 8, 4, 2, 1 warps a row, for more than 128,
 // 64, 32, 16, 8 chunks and the others
 constexpr int kMergeClasses = 6;
+constexpr int kExpandedTile = 128;   // positions of a step of the expanded form
+// A block of heads that the expanded form's plans keep together: the bytes of its keys and
+// values, so that the tiles of a head find them in L2 (129 MB)
+constexpr int64_t kExpandedBlock = 48ll << 20;
 constexpr int kSlab4 = 4608;         // bytes of one (page, kv head) of a 4-bit K or V cache
 constexpr int kStatusBytes = 256;    // status block at the start of the workspace
 constexpr int64_t kDefaultWaitNs = 2000000000LL;
@@ -86,6 +90,10 @@ struct Plan {
   int32_t merge_class[kMergeClasses + 1] = {};   // first merge entry of each class
   int64_t kv_bytes = 0;
   double flops = 0.0;
+  // rows of split ranges are fp32 in slots numbered without gaps, the merge by classes
+  bool compact() const { return four_bit() || expanded(); }
+  bool expanded() const { return prob.layout == PA_LAYOUT_MLA_EXPANDED; }
+  int64_t kv_rows = 0;   // expanded rows of all sequences
   bool four_bit() const { return prob.kv_dtype == PA_KV_INT4 || prob.kv_dtype == PA_KV_FP4_E2M1; }
   int32_t num_items() const { return (int32_t)(items.size() / kItemWords); }
 };
@@ -163,7 +171,7 @@ struct AttnParams {
   int32_t bsz;           // bounds of the work items (checked by the debug build)
   int32_t total_q;
   int32_t num_items;
-  int32_t four_bit;      // the items are 4-bit records, with
+  int32_t four_bit;      // the items are records of compact slots (item4_from), with
   int32_t part_slots;    // so many slots of partial rows (Plan::part_slots)
 };
 
@@ -203,6 +211,8 @@ cudaError_t launch_append4(const Plan& plan, const AttnParams& p, const void* ck
 cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void* k_new,
                                  const void* v_new, int64_t kv_stride, int32_t* status,
                                  cudaStream_t stream);
+cudaError_t launch_mla_prefill(const Plan& plan, const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                               const CUtensorMap& tm_r, const CUtensorMap& tm_v, cudaStream_t stream);
 cudaError_t launch_mla_product(const MlaProduct& m, const FaultCfg& fc, cudaStream_t stream);
 // queries rotated, K / V rows rotated (K) and written, every cache
 cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope& rope, const void* q,

@@ -3,7 +3,7 @@
 // Merge (FastDeploy append_attention_c8_impl.cuh, merge_multi_chunks_*_kernel
 // launched after the split kernel; the arithmetic is in pa_merge.cuh).
 // 8-bit plans: one warp per (token, query head); the partial states of a token sit
-// at slot (token * max_chunks + c) * q_heads + head.  4-bit plans: one warp per eight
+// at slot (token * max_chunks + c) * q_heads + head.  4-bit and expanded plans: one warp per eight
 // chunks; the states at (first slot of the token + c) * q_heads + head, the
 // slots numbered without gaps.  HBM-bound, CUDA cores: the row reads of all chunks are
 // issued before they are summed.
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256, DV >= 512 ? 5 : 1) merge_kernel(const int
   merge_store<DV, (DV < 512)>(acc[0], M[0], W[0], out, lse, ep, token, head, q_heads, lane);
 }
 
-// Rows whose partial states are fp32 (plans over a 4-bit cache), 128 wide, lane l
+// Rows whose partial states are fp32 (plans over a 4-bit cache or expanded rows), 128 wide, lane l
 // owning dims 4l .. 4l+3 (one 16-byte load per chunk row).  Warp w of a row takes
 // chunks 8 w .. 8 w + 7, then those 8 * (warps of the row) further on; its first eight
 // rows are requested before the weights are known, so that a row of at most eight
@@ -278,7 +278,7 @@ cudaError_t launch_merge(const Plan& plan, const WsView& ws, void* out, float* l
   const __nv_bfloat16* po = ws.part_o;
   const float* pm = ws.part_m;
   const float* pd = ws.part_d;
-  if (plan.four_bit()) {
+  if (plan.compact()) {
     const float* pf = reinterpret_cast<const float*>(po);
     const int32_t* cls = plan.merge_class;
     int longest = 0;   // its class

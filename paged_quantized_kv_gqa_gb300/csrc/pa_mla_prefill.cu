@@ -1,0 +1,447 @@
+// pa_mla_prefill.cu - attention of new tokens to expanded latent rows, bf16, tcgen05 + TMA,
+// sm_103a: keys of 128 dims a head and 64 rotated ones that all heads share, values of 128.
+//
+//   s_ij = sm_scale (<q_i[0:128], k_j> + <q_i[128:192], k_rope_j>), out_i = sum_j softmax(s_i)_j v_j
+//
+// One pass over the keys with a running maximum m and sum l of each row (a row's O is
+// rescaled only when its maximum rises by more than 2^8, which leaves 2^(s - m) exact
+// for the final division by l).
+//
+//   * An item is 256 query tokens of one head, two tiles A and B of 128 rows, against a
+//     range of positions in steps of 128.  TMEM: S_A 0, S_B 128, O_A 256, O_B 384; P
+//     (bf16) takes the place of S and is the A operand of O += P V.
+//   * One warp issues every MMA, in the order PV_A(i) S_A(i+1) PV_B(i) S_B(i+1): while the
+//     softmax of one tile runs, the tensor cores have the other's PV and S.  MMAs of one
+//     thread execute in order, so S_X(i+1) needs no wait for the PV_X(i) that reads P from
+//     its columns, and a finished S_X(i+1) means that O_X holds PV_X(i).  The order runs
+//     on over item boundaries; an item's epilogue overlaps the next one's first S.
+//   * K, V arrive in units of 16 KB through one ring of eight: three of K (128 positions x
+//     64 dims, the third from the shared rotated rows) and two of V (64 positions x 128
+//     dims, an MN-major B operand as it stands).  With Q (two tiles x 192 dims, 96 KB) that
+//     fills shared memory.
+//   * Causal: tile A leaves out the step that only B's rows see.
+//   * Rows of V past the range are zeroed in shared memory before their MMA (they belong to
+//     other sequences and may hold anything; 0 times NaN is NaN), scores by a select.
+// Rounding: P to bf16 (V's type; the MMA takes one type), at most 2^-8 p|v| a position,
+// rows to bf16, partial rows of split ranges in fp32.
+// Bound: the tensor cores, 640 flops per visible (query head, position).
+#include "pa_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTile = 128;                      // positions of a step
+constexpr int kUnit = 16384;                    // bytes of a ring slot
+constexpr int kSlots = 8;
+constexpr int kQTile = 3 * kUnit;               // Q of a tile: three blocks of 64 dims
+constexpr int kThreads = 384;                   // softmax A 0-3, softmax B 4-7, TMA 8, MMA 9
+constexpr int kWarpTma = 8;
+constexpr int kWarpMma = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kTau = 8.0f;                    // lazy-rescale threshold (log2 units)
+
+struct Smem {
+  static constexpr int kQ = 0;                          // [A, B][3][128 rows][128 B]
+  static constexpr int kRing = 2 * kQTile;
+  static constexpr int kBars = kRing + kSlots * kUnit;  // full[S] empty[S] qfull[2] qfree[2] sfull[2] pready[2] odone[2] drain
+  static constexpr int kMisc = kBars + (2 * kSlots + 11) * 8;
+  static constexpr int kTotal = kMisc + 16 + 1024;
+  static_assert(kTotal <= 232448, "shared memory overflow");
+};
+
+constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N) { return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10); }
+
+// A work item and the steps of its two tiles.
+struct Work {
+  Item m;        // m.b: row of the sequence's first position
+  int nt[2];     // steps of tile A, B
+  int n;         // steps of the item
+};
+
+__device__ __forceinline__ Work work_of(const int4 a, const int4 c) {
+  Work w;
+  w.m = item4_from<kTile>(a, c);
+  w.n = w.m.ntiles;
+  const int lim_a = min(w.m.kv1, w.m.cbase + min(w.m.ntok, 128));   // positions that A's rows see
+  w.nt[1] = w.m.ntok > 128 ? w.n : 0;
+  w.nt[0] = w.nt[1] ? max(1, (lim_a - w.m.kv0 + kTile - 1) / kTile) : w.n;   // (a split range may hold none of them)
+  return w;
+}
+
+// (a, b) * c + d in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 c, float2 d) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&c)), "l"(*reinterpret_cast<uint64_t*>(&d)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
+                       const AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using SM = Smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);
+  uint64_t* empty = full + kSlots;
+  uint64_t* qfull = empty + kSlots;   // [tile]
+  uint64_t* qfree = qfull + 2;
+  uint64_t* sfull = qfree + 2;
+  uint64_t* pready = sfull + 2;
+  uint64_t* odone = pready + 2;
+  uint64_t* drain = odone + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
+  volatile int* abort_any = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
+  const uint32_t s_base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int begin = p.work_indptr[blockIdx.x], end = p.work_indptr[blockIdx.x + 1];
+  const uint64_t limit = (uint64_t)p.wait_limit_ns;
+  const int4* recs = reinterpret_cast<const int4*>(p.items);
+  auto work_at = [&](int it) { return work_of(__ldg(recs + 2 * (int64_t)it), __ldg(recs + 2 * (int64_t)it + 1)); };
+  auto raise = [&](int it) {
+    if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, it);
+    *abort_any = 1;
+  };
+
+  PA_DEBUG_PROLOGUE(smem, SM::kTotal - 1024, p, begin, end);
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&qfull[x], 1);
+      mbar_init(&qfree[x], 1);
+      mbar_init(&sfull[x], 1);
+      mbar_init(&pready[x], 4);
+      mbar_init(&odone[x], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_any = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PA_DEBUG_POISON_TMEM(tmem, kTmemCols, warp);
+
+  if (warp == kWarpTma) {
+    // ================================================================ TMA
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_r);
+      tma_prefetch_desc(&tm_v);
+      uint32_t u = 0, nq[2] = {0, 0};   // units, query tiles loaded
+      bool ok = true;
+      // the next slot of the ring, its bytes announced; false when the wait ran out
+      auto slot = [&](uint8_t*& dst, uint64_t*& bar, int it) {
+        const uint32_t s = u % kSlots;
+        if (u >= kSlots && !wait_or_abort(&empty[s], (u / kSlots - 1) & 1, limit, abort_any)) {
+          raise(it);
+          return ok = false;
+        }
+        dst = smem + SM::kRing + s * kUnit;
+        bar = &full[s];
+        mbar_arrive_expect_tx(bar, kUnit);
+        ++u;
+        return true;
+      };
+      auto load_q = [&](int x, const Work& w, int it) {
+        if (nq[x] > 0 && !wait_or_abort(&qfree[x], (nq[x] - 1) & 1, limit, abort_any)) {
+          raise(it);
+          return ok = false;
+        }
+        mbar_arrive_expect_tx(&qfull[x], kQTile);
+        for (int d = 0; d < 3; ++d)
+          tma_load_3d(smem + SM::kQ + x * kQTile + d * kUnit, &tm_q, &qfull[x], 64 * d, w.m.kvh, w.m.tok0 + 128 * x);
+        ++nq[x];
+        return true;
+      };
+      for (int it = begin; it < end && ok; ++it) {
+        const Work w = work_at(it);
+        if (!load_q(0, w, it)) break;
+        for (int i = 0; i < w.n && ok; ++i) {
+          const int row = w.m.b + w.m.kv0 + i * kTile;
+          uint8_t* dst;
+          uint64_t* bar;
+          for (int d = 0; d < 3; ++d) {
+            if (p.skip_first_load && u == 0) {   // failure-detection test hook
+              ok = false;
+              break;
+            }
+            if (!slot(dst, bar, it)) break;
+            if (d < 2) tma_load_3d(dst, &tm_k, bar, 64 * d, w.m.kvh, row);
+            else tma_load_3d(dst, &tm_r, bar, 0, 0, row);
+          }
+          if (ok && i == 0 && w.nt[1] > 0 && !load_q(1, w, it)) break;
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (!slot(dst, bar, it)) break;
+            tma_load_3d(dst, &tm_v, bar, 0, w.m.kvh, row + 64 * h);
+            tma_load_3d(dst + kUnit / 2, &tm_v, bar, 64, w.m.kvh, row + 64 * h);
+          }
+        }
+      }
+      // every issued load lands before the CTA exits
+      for (uint32_t k = u > kSlots ? u - kSlots : 0; k < u; ++k) mbar_wait(&full[k % kSlots], (k / kSlots) & 1, kDrainNs);
+      for (int x = 0; x < 2; ++x)
+        if (nq[x] > 0) mbar_wait(&qfull[x], (nq[x] - 1) & 1, kDrainNs);
+    }
+  } else if (warp == kWarpMma) {
+    // ================================================================ MMA issue
+    // the whole warp runs the loop (warp-uniform operands); one elected lane issues
+    constexpr uint32_t idesc_s = idesc_bf16(128, kTile), idesc_pv = idesc_bf16(128, 128) | (1u << 16);
+    const uint32_t ring = s_base + SM::kRing;
+    uint32_t ns[2] = {0, 0}, np[2] = {0, 0}, nq[2] = {0, 0};   // S, PV steps and items of each tile
+    bool ok = true;
+    auto got = [&](uint32_t u) { return wait_or_abort(&full[u % kSlots], (u / kSlots) & 1, limit, abort_any); };
+    // S_x of step i (units 5 g ..); `fresh`: first use of the step's keys
+    auto issue_s = [&](int x, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
+      if (i == 0) {
+        if (!wait_or_abort(&qfull[x], nq[x] & 1, limit, abort_any)) return ok = false;
+        ++nq[x];
+      }
+      const uint32_t q = s_base + SM::kQ + x * kQTile;
+      for (uint32_t d = 0; d < 3; ++d) {
+        if (fresh && !got(5 * g + d)) return ok = false;
+        tc_fence_after();
+        const uint32_t k = ring + (5 * g + d) % kSlots * kUnit;
+        if (elect_one()) {
+#pragma unroll
+          for (int kq = 0; kq < 4; ++kq)
+            mma_ss(tmem + 128 * x, sdesc_k128(q + d * kUnit + 32 * kq), sdesc_k128(k + 32 * kq), idesc_s, (d | kq) ? 1u : 0u);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) {
+        tc_commit(&sfull[x]);
+        if (i + 1 == w.nt[x]) tc_commit(&qfree[x]);
+        if (last_use)
+          for (uint32_t d = 0; d < 3; ++d) tc_commit(&empty[(5 * g + d) % kSlots]);
+      }
+      __syncwarp();
+      ++ns[x];
+      return true;
+    };
+    auto issue_pv = [&](int x, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
+      if (!wait_or_abort(&pready[x], np[x] & 1, limit, abort_any)) return ok = false;
+      tc_fence_after();
+      for (uint32_t h = 0; h < 2; ++h) {
+        const uint32_t v = ring + (5 * g + 3 + h) % kSlots * kUnit;
+        if (fresh) {
+          if (!got(5 * g + 3 + h)) return ok = false;
+          tc_fence_after();
+          const int nvalid = w.m.kv1 - (w.m.kv0 + i * kTile + 64 * (int)h);
+          if (nvalid < 64) {   // rows past the range: zero, 8 chunks of 16 bytes a row and block
+            for (int r = 8 * max(0, nvalid) + lane; r < 512; r += 32) {
+              st_shared_v4(v + 16 * r, make_uint4(0, 0, 0, 0));
+              st_shared_v4(v + kUnit / 2 + 16 * r, make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (elect_one()) {
+#pragma unroll
+          for (int kq = 0; kq < 4; ++kq)
+            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 32 * h + 8 * kq, sdesc_mn128(v + kq * 2048, kUnit / 2, 1024),
+                   idesc_pv, (i > 0 || h > 0 || kq > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) {
+        if (i + 1 == w.nt[x]) tc_commit(&odone[x]);
+        if (last_use)
+          for (uint32_t h = 0; h < 2; ++h) tc_commit(&empty[(5 * g + 3 + h) % kSlots]);
+      }
+      __syncwarp();
+      ++np[x];
+      return true;
+    };
+    if (begin < end) {
+      int it = begin, i = 0;
+      uint32_t g = 0;
+      Work cur = work_at(it), nxt = cur, ahead = cur;   // ahead: the item behind cur's
+      if (it + 1 < end) ahead = work_at(it + 1);
+      auto first_s = [&](const Work& w, int j, uint32_t gg, int x) {
+        const bool a = j < w.nt[0], b = j < w.nt[1];
+        if (x == 0 ? !a : !b) return true;
+        return issue_s(x, w, j, gg, x == 0 || !a, x == 1 || !b);
+      };
+      ok = first_s(cur, 0, 0, 0) && first_s(cur, 0, 0, 1);
+      while (ok) {
+        int ni = i + 1;
+        bool more = true;
+        if (ni < cur.n) nxt = cur;
+        else if (it + 1 < end) nxt = ahead, ni = 0;
+        else more = false;
+        const bool a = i < cur.nt[0], b = i < cur.nt[1];
+        if (a && !issue_pv(0, cur, i, g, true, !b)) break;
+        if (more && !first_s(nxt, ni, g + 1, 0)) break;
+        if (b && !issue_pv(1, cur, i, g, !a, true)) break;
+        if (more && !first_s(nxt, ni, g + 1, 1)) break;
+        if (!more) break;
+        if (ni == 0) {
+          cur = nxt;
+          if (++it + 1 < end) ahead = work_at(it + 1);
+        }
+        i = ni;
+        ++g;
+      }
+      if (!ok && lane == 0) raise(it);
+    }
+    // drain: every MMA this warp issued completes before TMEM is released
+    if (elect_one()) tc_commit(drain);
+    __syncwarp();
+    mbar_wait(drain, 0, kDrainNs);
+  } else if (warp < 8) {
+    // ================================================================ softmax, thread = row
+    const int x = warp >> 2, rr = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lanes + 128 * x, o_tm = tmem + lanes + 256 + 128 * x;
+    const float c_log2 = p.sm_scale_log2;
+    uint32_t n = 0, items = 0;   // steps, items of this tile
+    bool fail = false;
+    for (int it = begin; it < end && !fail; ++it) {
+      const Work w = work_at(it);
+      const Item& m = w.m;
+      if (w.nt[x] == 0) continue;   // the item has no rows for this tile
+      const int r = 128 * x + rr;
+      const int vis_lim = min(m.kv1, m.cbase + r + 1);   // positions below it are seen
+      float m_run = -INFINITY, l = 0.0f;
+      for (int i = 0; i < w.nt[x]; ++i, ++n) {
+        if (!wait_or_abort(&sfull[x], n & 1, limit, abort_any)) {
+          raise(it);
+          fail = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) tmem_ld16(s_tm + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * c]));
+        tmem_wait_ld();
+        const int nvis = vis_lim - (m.kv0 + i * kTile);
+        if (nvis < kTile) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) v[e] = e < nvis ? v[e] : 0xFF800000u;   // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[e + k]));
+        }
+        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c_log2;
+        const bool need = m_tile > m_run + kTau;
+        float alpha = 1.0f;
+        if (need) {
+          alpha = m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_tile);
+          l *= alpha;
+          m_run = m_tile;
+        }
+        // O holds the PV of the item's earlier steps (they came before this S)
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 2
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_tm + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(o_tm + 16 * c, o);
+          }
+        }
+        // P = 2^(s c - m), bf16, over the first half of S's columns
+        const float neg_m = m_run == -INFINITY ? 0.0f : -m_run;
+        const float2 c2 = make_float2(c_log2, c_log2), m2 = make_float2(neg_m, neg_m);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = 32 * h + 2 * e;
+            float2 t = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, m2);
+            t.x = fast_exp2(t.x);
+            t.y = fast_exp2(t.y);
+            sum[e & 1] = add2(sum[e & 1], t);
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(t.x, t.y);
+            o[e] = *reinterpret_cast<uint32_t*>(&b2);
+          }
+          tmem_st16(s_tm + 16 * h, o);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&pready[x], lane);
+      }
+      if (fail) break;
+      // ---- epilogue: O / l
+      if (!wait_or_abort(&odone[x], items & 1, limit, abort_any)) {
+        raise(it);
+        break;
+      }
+      ++items;
+      tc_fence_after();
+      const float inv_l = l > 0.0f ? __frcp_rn(l) : 0.0f;
+      const bool row_ok = r < m.ntok, final_row = m.nch == 1;
+      const int token = m.tok0 + r;
+      const int64_t row = final_row ? (int64_t)token * p.q_heads + m.kvh
+                                    : ((int64_t)m.chunk + (int64_t)r * m.nch) * p.q_heads + m.kvh;
+#pragma unroll 2
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(o_tm + 16 * c, o);
+        tmem_wait_ld();
+        if (row_ok) {
+          float a[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) a[e] = __uint_as_float(o[e]) * inv_l;
+          if (final_row) ep_store16(p.ep, p.out, row * 128 + 16 * c, m.kvh * 128 + 16 * c, a);
+          else store16_f32(reinterpret_cast<float*>(p.part_o) + row * 128 + 16 * c, a);
+        }
+      }
+      tc_fence_before();   // (the next item's first P, behind which its PV writes O, is announced after this)
+      if (row_ok) {
+        const float ln2 = 0.69314718055994530942f;
+        if (final_row) {
+          if (p.lse != nullptr) p.lse[row] = l > 0.0f ? (m_run + __log2f(l)) * ln2 : -INFINITY;
+        } else {
+          p.part_m[row] = l > 0.0f ? m_run * ln2 : -INFINITY;
+          p.part_d[row] = l;
+        }
+      }
+    }
+  }
+  // (the remaining warps have no role)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();   // the merge grid may be scheduled while the last CTAs finish
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+cudaError_t launch_mla_prefill(const Plan& plan, const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                               const CUtensorMap& tm_r, const CUtensorMap& tm_v, cudaStream_t stream) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kTotal);
+  if (e != cudaSuccess) return e;
+  mla_prefill_kernel<<<plan.num_ctas, kThreads, Smem::kTotal, stream>>>(tm_q, tm_k, tm_r, tm_v, p);
+  return cudaGetLastError();
+}
+
+}  // namespace pa
