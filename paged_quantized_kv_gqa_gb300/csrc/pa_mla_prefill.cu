@@ -25,6 +25,8 @@
 // Rounding: P to bf16 (V's type; the MMA takes one type), at most 2^-8 p|v| a position,
 // rows to bf16, partial rows of split ranges in fp32.
 // Bound: the tensor cores, 640 flops per visible (query head, position).
+#include <type_traits>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -35,6 +37,9 @@ constexpr int kUnit = 16384;                    // bytes of a ring slot
 constexpr int kSlots = 8;
 constexpr int kQTile = 3 * kUnit;               // Q of a tile: three blocks of 64 dims
 constexpr int kThreads = 384;                   // softmax A 0-3, softmax B 4-7, TMA 8, MMA 9
+// registers: 168 a thread at launch, moved to the softmax, whose threads hold a row of scores
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the shares add up to the launch's registers");
 constexpr int kWarpTma = 8;
 constexpr int kWarpMma = 9;
 constexpr uint32_t kTmemCols = 512;
@@ -43,8 +48,8 @@ constexpr float kTau = 8.0f;                    // lazy-rescale threshold (log2 
 struct Smem {
   static constexpr int kQ = 0;                          // [A, B][3][128 rows][128 B]
   static constexpr int kRing = 2 * kQTile;
-  static constexpr int kBars = kRing + kSlots * kUnit;  // full[S] empty[S] qfull[2] qfree[2] sfull[2] pready[2] odone[2] drain
-  static constexpr int kMisc = kBars + (2 * kSlots + 11) * 8;
+  static constexpr int kBars = kRing + kSlots * kUnit;  // kfull kfree vfull vfree qfull qfree sfull pready[2] odone, [2] each, drain
+  static constexpr int kMisc = kBars + 21 * 8;
   static constexpr int kTotal = kMisc + 16 + 1024;
   static_assert(kTotal <= 232448, "shared memory overflow");
 };
@@ -85,6 +90,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&r);
 }
 
+// 64 scores -> 2^(s c - m) as bf16 pairs, and their sum before that rounding
+__device__ __forceinline__ float exp_half(const uint32_t* v, float c, float neg_m, uint32_t (&o)[32]) {
+  const float2 c2 = make_float2(c, c), m2 = make_float2(neg_m, neg_m);
+  float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    float2 t = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, m2);
+    t.x = fast_exp2(t.x);
+    t.y = fast_exp2(t.y);
+    sum[e & 1] = add2(sum[e & 1], t);
+    __nv_bfloat162 b2 = __floats2bfloat162_rn(t.x, t.y);
+    o[e] = *reinterpret_cast<uint32_t*>(&b2);
+  }
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -94,13 +115,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using SM = Smem;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);
-  uint64_t* empty = full + kSlots;
-  uint64_t* qfull = empty + kSlots;   // [tile]
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + SM::kBars);   // [step & 1], as the next three
+  uint64_t* vfull = kfull + 2;
+  uint64_t* kfree = vfull + 2;
+  uint64_t* vfree = kfree + 2;
+  uint64_t* qfull = vfree + 2;        // [tile], as the next four
   uint64_t* qfree = qfull + 2;
   uint64_t* sfull = qfree + 2;
-  uint64_t* pready = sfull + 2;
-  uint64_t* odone = pready + 2;
+  uint64_t* pready = sfull + 2;   // [tile][half of the step's positions]
+  uint64_t* odone = pready + 4;
   uint64_t* drain = odone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_any = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
@@ -117,15 +140,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   PA_DEBUG_PROLOGUE(smem, SM::kTotal - 1024, p, begin, end);
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&kfull[x], 1);
+      mbar_init(&vfull[x], 1);
+      mbar_init(&kfree[x], 1);
+      mbar_init(&vfree[x], 1);
       mbar_init(&qfull[x], 1);
       mbar_init(&qfree[x], 1);
       mbar_init(&sfull[x], 1);
-      mbar_init(&pready[x], 4);
+      mbar_init(&pready[2 * x], 4);
+      mbar_init(&pready[2 * x + 1], 4);
       mbar_init(&odone[x], 1);
     }
     mbar_init(drain, 1);
@@ -139,6 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   PA_DEBUG_POISON_TMEM(tmem, kTmemCols, warp);
 
+  // one instruction for all warps of a warpgroup
+  if (warp >= 8) {
+  regs_down<kRegsOther>();
   if (warp == kWarpTma) {
     // ================================================================ TMA
     if (lane == 0) {
@@ -146,58 +173,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_r);
       tma_prefetch_desc(&tm_v);
-      uint32_t u = 0, nq[2] = {0, 0};   // units, query tiles loaded
+      uint32_t g = 0, nk = 0, nv = 0, nq[2] = {0, 0};   // steps; K, V groups and query tiles begun
       bool ok = true;
-      // the next slot of the ring, its bytes announced; false when the wait ran out
-      auto slot = [&](uint8_t*& dst, uint64_t*& bar, int it) {
-        const uint32_t s = u % kSlots;
-        if (u >= kSlots && !wait_or_abort(&empty[s], (u / kSlots - 1) & 1, limit, abort_any)) {
-          raise(it);
-          return ok = false;
-        }
-        dst = smem + SM::kRing + s * kUnit;
-        bar = &full[s];
-        mbar_arrive_expect_tx(bar, kUnit);
-        ++u;
-        return true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int it) {
+        if (wait_or_abort(bar, parity, limit, abort_any)) return true;
+        raise(it);
+        return ok = false;
       };
       auto load_q = [&](int x, const Work& w, int it) {
-        if (nq[x] > 0 && !wait_or_abort(&qfree[x], (nq[x] - 1) & 1, limit, abort_any)) {
-          raise(it);
-          return ok = false;
-        }
+        if (nq[x] > 0 && !wait(&qfree[x], (nq[x] - 1) & 1, it)) return;
         mbar_arrive_expect_tx(&qfull[x], kQTile);
         for (int d = 0; d < 3; ++d)
           tma_load_3d(smem + SM::kQ + x * kQTile + d * kUnit, &tm_q, &qfull[x], 64 * d, w.m.kvh, w.m.tok0 + 128 * x);
         ++nq[x];
-        return true;
       };
+      auto slot = [&](uint32_t u) { return smem + SM::kRing + u % kSlots * kUnit; };
+      // Unit u takes the slot of unit u - 8: the third of K(g - 2), both of V(g - 2) and the
+      // first two of K(g - 1) for the five units of step g, in this order.
       for (int it = begin; it < end && ok; ++it) {
         const Work w = work_at(it);
-        if (!load_q(0, w, it)) break;
-        for (int i = 0; i < w.n && ok; ++i) {
+        load_q(0, w, it);
+        for (int i = 0; i < w.n && ok; ++i, ++g) {
           const int row = w.m.b + w.m.kv0 + i * kTile;
-          uint8_t* dst;
-          uint64_t* bar;
-          for (int d = 0; d < 3; ++d) {
-            if (p.skip_first_load && u == 0) {   // failure-detection test hook
-              ok = false;
-              break;
-            }
-            if (!slot(dst, bar, it)) break;
-            if (d < 2) tma_load_3d(dst, &tm_k, bar, 64 * d, w.m.kvh, row);
-            else tma_load_3d(dst, &tm_r, bar, 0, 0, row);
+          const uint32_t par2 = ((g - 2) >> 1) & 1;
+          if (g >= 2 && !wait(&kfree[g & 1], par2, it)) break;
+          if (p.skip_first_load && g == 0) {   // failure-detection test hook
+            ok = false;
+            break;
           }
-          if (ok && i == 0 && w.nt[1] > 0 && !load_q(1, w, it)) break;
-          for (int h = 0; h < 2 && ok; ++h) {
-            if (!slot(dst, bar, it)) break;
-            tma_load_3d(dst, &tm_v, bar, 0, w.m.kvh, row + 64 * h);
-            tma_load_3d(dst + kUnit / 2, &tm_v, bar, 64, w.m.kvh, row + 64 * h);
+          uint64_t* bar = &kfull[g & 1];
+          mbar_arrive_expect_tx(bar, 3 * kUnit);
+          ++nk;
+          tma_load_3d(slot(5 * g), &tm_k, bar, 0, w.m.kvh, row);
+          if (g >= 2) wait(&vfree[g & 1], par2, it);   // (loaded all the same: its bytes are announced)
+          tma_load_3d(slot(5 * g + 1), &tm_k, bar, 64, w.m.kvh, row);
+          tma_load_3d(slot(5 * g + 2), &tm_r, bar, 0, 0, row);
+          if (ok && i == 0 && w.nt[1] > 0) load_q(1, w, it);
+          if (!ok || (g >= 1 && !wait(&kfree[(g - 1) & 1], ((g - 1) >> 1) & 1, it))) break;
+          bar = &vfull[g & 1];
+          mbar_arrive_expect_tx(bar, 2 * kUnit);
+          ++nv;
+          for (uint32_t h = 0; h < 2; ++h) {
+            uint8_t* dst = slot(5 * g + 3 + h);
+            tma_load_3d(dst, &tm_v, bar, 0, w.m.kvh, row + 64 * (int)h);
+            tma_load_3d(dst + kUnit / 2, &tm_v, bar, 64, w.m.kvh, row + 64 * (int)h);
           }
         }
       }
       // every issued load lands before the CTA exits
-      for (uint32_t k = u > kSlots ? u - kSlots : 0; k < u; ++k) mbar_wait(&full[k % kSlots], (k / kSlots) & 1, kDrainNs);
+      for (uint32_t k = nk > 2 ? nk - 2 : 0; k < nk; ++k) mbar_wait(&kfull[k & 1], (k >> 1) & 1, kDrainNs);
+      for (uint32_t k = nv > 2 ? nv - 2 : 0; k < nv; ++k) mbar_wait(&vfull[k & 1], (k >> 1) & 1, kDrainNs);
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_wait(&qfull[x], (nq[x] - 1) & 1, kDrainNs);
     }
@@ -206,83 +231,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the whole warp runs the loop (warp-uniform operands); one elected lane issues
     constexpr uint32_t idesc_s = idesc_bf16(128, kTile), idesc_pv = idesc_bf16(128, 128) | (1u << 16);
     const uint32_t ring = s_base + SM::kRing;
-    uint32_t ns[2] = {0, 0}, np[2] = {0, 0}, nq[2] = {0, 0};   // S, PV steps and items of each tile
+    uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // PV steps and items of each tile
     bool ok = true;
-    auto got = [&](uint32_t u) { return wait_or_abort(&full[u % kSlots], (u / kSlots) & 1, limit, abort_any); };
-    // S_x of step i (units 5 g ..); `fresh`: first use of the step's keys
-    auto issue_s = [&](int x, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
-      if (i == 0) {
-        if (!wait_or_abort(&qfull[x], nq[x] & 1, limit, abort_any)) return ok = false;
-        ++nq[x];
-      }
-      const uint32_t q = s_base + SM::kQ + x * kQTile;
-      for (uint32_t d = 0; d < 3; ++d) {
-        if (fresh && !got(5 * g + d)) return ok = false;
-        tc_fence_after();
-        const uint32_t k = ring + (5 * g + d) % kSlots * kUnit;
-        if (elect_one()) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = wait_or_abort(bar, parity, limit, abort_any);
+      tc_fence_after();
+      return ok;
+    };
+    // S_x of step i of an item, step g of the CTA.  fresh: the first use of its keys,
+    // last_use: the last.  All MMAs of a product leave in one elected branch: their issue,
+    // not the tensor cores, was what the kernel waited for with a branch, a wait and a
+    // release per 64 dims (4500 cycles a step, 2560 of them at the MMAs' rate).
+    auto issue_s = [&](auto tile, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
+      constexpr int x = decltype(tile)::value;
+      if (i == 0 && !wait(&qfull[x], nq[x]++ & 1)) return false;
+      if (fresh && !wait(&kfull[g & 1], (g >> 1) & 1)) return false;
+      const uint64_t q = sdesc_k128(s_base + SM::kQ + x * kQTile);
+      if (elect_one()) {
+#pragma unroll
+        for (uint32_t d = 0; d < 3; ++d) {
+          const uint64_t k = sdesc_k128(ring + (5 * g + d) % kSlots * kUnit);
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
-            mma_ss(tmem + 128 * x, sdesc_k128(q + d * kUnit + 32 * kq), sdesc_k128(k + 32 * kq), idesc_s, (d | kq) ? 1u : 0u);
+            mma_ss(tmem + 128 * x, q + ((d * kUnit + 32 * kq) >> 4), k + ((32 * kq) >> 4), idesc_s, (d | kq) ? 1u : 0u);
         }
-        __syncwarp();
-      }
-      if (elect_one()) {
         tc_commit(&sfull[x]);
         if (i + 1 == w.nt[x]) tc_commit(&qfree[x]);
-        if (last_use)
-          for (uint32_t d = 0; d < 3; ++d) tc_commit(&empty[(5 * g + d) % kSlots]);
+        if (last_use) tc_commit(&kfree[g & 1]);
       }
       __syncwarp();
-      ++ns[x];
       return true;
     };
-    auto issue_pv = [&](int x, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
-      if (!wait_or_abort(&pready[x], np[x] & 1, limit, abort_any)) return ok = false;
-      tc_fence_after();
-      for (uint32_t h = 0; h < 2; ++h) {
-        const uint32_t v = ring + (5 * g + 3 + h) % kSlots * kUnit;
-        if (fresh) {
-          if (!got(5 * g + 3 + h)) return ok = false;
-          tc_fence_after();
-          const int nvalid = w.m.kv1 - (w.m.kv0 + i * kTile + 64 * (int)h);
-          if (nvalid < 64) {   // rows past the range: zero, 8 chunks of 16 bytes a row and block
-            for (int r = 8 * max(0, nvalid) + lane; r < 512; r += 32) {
-              st_shared_v4(v + 16 * r, make_uint4(0, 0, 0, 0));
-              st_shared_v4(v + kUnit / 2 + 16 * r, make_uint4(0, 0, 0, 0));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+    auto issue_pv = [&](auto tile, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
+      constexpr int x = decltype(tile)::value;
+      if (fresh) {
+        if (!wait(&vfull[g & 1], (g >> 1) & 1)) return false;
+        const int nvalid = w.m.kv1 - (w.m.kv0 + i * kTile);
+        if (nvalid < kTile) {   // rows past the range: zero, 8 chunks of 16 bytes a row and block
+          for (int r = 8 * nvalid + lane; r < 8 * kTile; r += 32) {
+            const uint32_t v = ring + (5 * g + 3 + (r >> 9)) % kSlots * kUnit + 16 * (r & 511);
+            st_shared_v4(v, make_uint4(0, 0, 0, 0));
+            st_shared_v4(v + kUnit / 2, make_uint4(0, 0, 0, 0));
           }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
+      }
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h) {
+        if (!wait(&pready[2 * x + h], np[x] & 1)) return false;
+        const uint64_t v = sdesc_mn128(ring + (5 * g + 3 + h) % kSlots * kUnit, kUnit / 2, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
-            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 32 * h + 8 * kq, sdesc_mn128(v + kq * 2048, kUnit / 2, 1024),
-                   idesc_pv, (i > 0 || h > 0 || kq > 0) ? 1u : 0u);
+            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 32 * h + 8 * kq, v + ((2048 * kq) >> 4), idesc_pv,
+                   (i > 0 || h > 0 || kq > 0) ? 1u : 0u);
+          if (h == 1) {
+            if (i + 1 == w.nt[x]) tc_commit(&odone[x]);
+            if (last_use) tc_commit(&vfree[g & 1]);
+          }
         }
         __syncwarp();
       }
-      if (elect_one()) {
-        if (i + 1 == w.nt[x]) tc_commit(&odone[x]);
-        if (last_use)
-          for (uint32_t h = 0; h < 2; ++h) tc_commit(&empty[(5 * g + 3 + h) % kSlots]);
-      }
-      __syncwarp();
       ++np[x];
       return true;
     };
+    constexpr std::integral_constant<int, 0> tile_a{};
+    constexpr std::integral_constant<int, 1> tile_b{};
     if (begin < end) {
       int it = begin, i = 0;
       uint32_t g = 0;
       Work cur = work_at(it), nxt = cur, ahead = cur;   // ahead: the item behind cur's
       if (it + 1 < end) ahead = work_at(it + 1);
-      auto first_s = [&](const Work& w, int j, uint32_t gg, int x) {
-        const bool a = j < w.nt[0], b = j < w.nt[1];
-        if (x == 0 ? !a : !b) return true;
-        return issue_s(x, w, j, gg, x == 0 || !a, x == 1 || !b);
+      auto s_a = [&](const Work& w, int j, uint32_t gg) {
+        return j >= w.nt[0] || issue_s(tile_a, w, j, gg, true, j >= w.nt[1]);
       };
-      ok = first_s(cur, 0, 0, 0) && first_s(cur, 0, 0, 1);
+      auto s_b = [&](const Work& w, int j, uint32_t gg) {
+        return j >= w.nt[1] || issue_s(tile_b, w, j, gg, j >= w.nt[0], true);
+      };
+      ok = s_a(cur, 0, 0) && s_b(cur, 0, 0);
       while (ok) {
         int ni = i + 1;
         bool more = true;
@@ -290,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (it + 1 < end) nxt = ahead, ni = 0;
         else more = false;
         const bool a = i < cur.nt[0], b = i < cur.nt[1];
-        if (a && !issue_pv(0, cur, i, g, true, !b)) break;
-        if (more && !first_s(nxt, ni, g + 1, 0)) break;
-        if (b && !issue_pv(1, cur, i, g, !a, true)) break;
-        if (more && !first_s(nxt, ni, g + 1, 1)) break;
+        if (a && !issue_pv(tile_a, cur, i, g, true, !b)) break;
+        if (more && !s_a(nxt, ni, g + 1)) break;
+        if (b && !issue_pv(tile_b, cur, i, g, !a, true)) break;
+        if (more && !s_b(nxt, ni, g + 1)) break;
         if (!more) break;
         if (ni == 0) {
           cur = nxt;
@@ -308,8 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) tc_commit(drain);
     __syncwarp();
     mbar_wait(drain, 0, kDrainNs);
-  } else if (warp < 8) {
+  }
+  // (the remaining warps have no role but to complete the warpgroup)
+  } else {
     // ================================================================ softmax, thread = row
+    regs_up<kRegsSoftmax>();
     const int x = warp >> 2, rr = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lanes + 128 * x, o_tm = tmem + lanes + 256 + 128 * x;
@@ -319,11 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = begin; it < end && !fail; ++it) {
       const Work w = work_at(it);
       const Item& m = w.m;
-      if (w.nt[x] == 0) continue;   // the item has no rows for this tile
+      const int steps = x ? w.nt[1] : w.nt[0];
+      if (steps == 0) continue;   // the item has no rows for this tile
       const int r = 128 * x + rr;
       const int vis_lim = min(m.kv1, m.cbase + r + 1);   // positions below it are seen
       float m_run = -INFINITY, l = 0.0f;
-      for (int i = 0; i < w.nt[x]; ++i, ++n) {
+      for (int i = 0; i < steps; ++i, ++n) {
         if (!wait_or_abort(&sfull[x], n & 1, limit, abort_any)) {
           raise(it);
           fail = true;
@@ -332,62 +363,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t v[128];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) tmem_ld16(s_tm + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * c]));
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v + 32 * c);
         tmem_wait_ld();
         const int nvis = vis_lim - (m.kv0 + i * kTile);
         if (nvis < kTile) {
 #pragma unroll
           for (int e = 0; e < 128; ++e) v[e] = e < nvis ? v[e] : 0xFF800000u;   // -inf
         }
+        // the first half's P against the maximum so far, while the step's maximum is taken
+        uint32_t o[32];
+        float neg_m = m_run == -INFINITY ? 0.0f : -m_run;
+        float sum = exp_half(v, c_log2, neg_m, o);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 128; e += 4) {
+        for (int e = 0; e < 128; e += 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[e + k]));
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(v[e + k])), __uint_as_float(v[e + k + 4]));
         }
         const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c_log2;
         const bool need = m_tile > m_run + kTau;
-        float alpha = 1.0f;
-        if (need) {
-          alpha = m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_tile);
-          l *= alpha;
-          m_run = m_tile;
-        }
-        // O holds the PV of the item's earlier steps (they came before this S)
-        if (i > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 2
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            tmem_ld16(o_tm + 16 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(o_tm + 16 * c, o);
+        if (__any_sync(0xffffffffu, need)) {
+          float alpha = 1.0f;
+          if (need) {
+            alpha = m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_tile);
+            l *= alpha;
+            m_run = m_tile;
           }
-        }
-        // P = 2^(s c - m), bf16, over the first half of S's columns
-        const float neg_m = m_run == -INFINITY ? 0.0f : -m_run;
-        const float2 c2 = make_float2(c_log2, c_log2), m2 = make_float2(neg_m, neg_m);
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          if (i > 0) {   // O holds the PV of the item's earlier steps (they came before this S)
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t t[16];
+              tmem_ld16(o_tm + 16 * c, t);
+              tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t o[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = 32 * h + 2 * e;
-            float2 t = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, m2);
-            t.x = fast_exp2(t.x);
-            t.y = fast_exp2(t.y);
-            sum[e & 1] = add2(sum[e & 1], t);
-            __nv_bfloat162 b2 = __floats2bfloat162_rn(t.x, t.y);
-            o[e] = *reinterpret_cast<uint32_t*>(&b2);
+              for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * alpha);
+              tmem_st16(o_tm + 16 * c, t);
+            }
           }
-          tmem_st16(s_tm + 16 * h, o);
+          neg_m = m_run == -INFINITY ? 0.0f : -m_run;
+          sum = exp_half(v, c_log2, neg_m, o);
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        // P = 2^(s c - m), bf16, over the first half of S's columns; its halves are announced
+        // one by one
+        l += sum;
+        tmem_st32(s_tm, o);
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(&pready[x], lane);
+        warp_arrive(&pready[2 * x], lane);
+        l += exp_half(v + 64, c_log2, neg_m, o);
+        tmem_st32(s_tm + 32, o);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&pready[2 * x + 1], lane);
       }
       if (fail) break;
       // ---- epilogue: O / l
@@ -427,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  // (the remaining warps have no role)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
