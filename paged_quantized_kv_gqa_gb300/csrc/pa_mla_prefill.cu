@@ -10,11 +10,12 @@
 //   * An item is 256 query tokens of one head, two tiles A and B of 128 rows, against a
 //     range of positions in steps of 128.  TMEM: S_A 0, S_B 128, O_A 256, O_B 384; P
 //     (bf16) takes the place of S and is the A operand of O += P V.
-//   * One warp issues every MMA, in the order PV_A(i) S_A(i+1) PV_B(i) S_B(i+1): while the
-//     softmax of one tile runs, the tensor cores have the other's PV and S.  MMAs of one
-//     thread execute in order, so S_X(i+1) needs no wait for the PV_X(i) that reads P from
-//     its columns, and a finished S_X(i+1) means that O_X holds PV_X(i).  The order runs
-//     on over item boundaries; an item's epilogue overlaps the next one's first S.
+//   * A warp per tile issues its MMAs, PV_X(i) then S_X(i+1): while the softmax of one tile
+//     runs, the tensor cores have the other's.  MMAs of one thread execute in order, so
+//     S_X(i+1) needs no wait for the PV_X(i) that reads P from its columns, and a finished
+//     S_X(i+1) means that O_X holds PV_X(i).  The order runs on over item boundaries; an
+//     item's epilogue overlaps the next one's first S.  (What bounded the kernel with one
+//     warp for both tiles was that warp: 4060 cycles a step, of which the MMAs take 2560.)
 //   * K, V arrive in units of 16 KB through one ring of eight: three of K (128 positions x
 //     64 dims, the third from the shared rotated rows) and two of V (64 positions x 128
 //     dims, an MN-major B operand as it stands).  With Q (two tiles x 192 dims, 96 KB) that
@@ -25,8 +26,6 @@
 // Rounding: P to bf16 (V's type; the MMA takes one type), at most 2^-8 p|v| a position,
 // rows to bf16, partial rows of split ranges in fp32.
 // Bound: the tensor cores, 640 flops per visible (query head, position).
-#include <type_traits>
-
 #include "pa_common.cuh"
 
 namespace pa {
@@ -36,7 +35,7 @@ constexpr int kTile = 128;                      // positions of a step
 constexpr int kUnit = 16384;                    // bytes of a ring slot
 constexpr int kSlots = 8;
 constexpr int kQTile = 3 * kUnit;               // Q of a tile: three blocks of 64 dims
-constexpr int kThreads = 384;                   // softmax A 0-3, softmax B 4-7, TMA 8, MMA 9
+constexpr int kThreads = 384;                   // softmax A 0-3, softmax B 4-7, TMA 8, MMA A 9, MMA B 10
 // registers: 168 a thread at launch, moved to the softmax, whose threads hold a row of scores
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the shares add up to the launch's registers");
@@ -48,8 +47,8 @@ constexpr float kTau = 8.0f;                    // lazy-rescale threshold (log2 
 struct Smem {
   static constexpr int kQ = 0;                          // [A, B][3][128 rows][128 B]
   static constexpr int kRing = 2 * kQTile;
-  static constexpr int kBars = kRing + kSlots * kUnit;  // kfull kfree vfull vfree qfull qfree sfull pready[2] odone, [2] each, drain
-  static constexpr int kMisc = kBars + 21 * 8;
+  static constexpr int kBars = kRing + kSlots * kUnit;  // kfull kfree vfull vfree qfull qfree sfull pready[2] odone drain, [2] each
+  static constexpr int kMisc = kBars + 22 * 8;
   static constexpr int kTotal = kMisc + 16 + 1024;
   static_assert(kTotal <= 232448, "shared memory overflow");
 };
@@ -143,16 +142,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&kfull[x], 1);
       mbar_init(&vfull[x], 1);
-      mbar_init(&kfree[x], 1);
-      mbar_init(&vfree[x], 1);
+      mbar_init(&kfree[x], 2);   // a release by each tile
+      mbar_init(&vfree[x], 2);
       mbar_init(&qfull[x], 1);
       mbar_init(&qfree[x], 1);
       mbar_init(&sfull[x], 1);
       mbar_init(&pready[2 * x], 4);
       mbar_init(&pready[2 * x + 1], 4);
       mbar_init(&odone[x], 1);
+      mbar_init(&drain[x], 1);
     }
-    mbar_init(drain, 1);
     *abort_any = 0;
     fence_mbar_init();
   }
@@ -226,115 +225,108 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_wait(&qfull[x], (nq[x] - 1) & 1, kDrainNs);
     }
-  } else if (warp == kWarpMma) {
-    // ================================================================ MMA issue
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ================================================================ MMA issue, a warp per tile
     // the whole warp runs the loop (warp-uniform operands); one elected lane issues
     constexpr uint32_t idesc_s = idesc_bf16(128, kTile), idesc_pv = idesc_bf16(128, 128) | (1u << 16);
-    const uint32_t ring = s_base + SM::kRing;
-    uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // PV steps and items of each tile
+    const int x = warp - kWarpMma;
+    const uint32_t ring = s_base + SM::kRing, s_tm = tmem + 128 * x, o_tm = tmem + 256 + 128 * x;
+    const uint64_t q = sdesc_k128(s_base + SM::kQ + x * kQTile);
+    uint32_t np = 0, nq = 0;   // PV steps and items of this tile
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = wait_or_abort(bar, parity, limit, abort_any);
       tc_fence_after();
       return ok;
     };
-    // S_x of step i of an item, step g of the CTA.  fresh: the first use of its keys,
-    // last_use: the last.  All MMAs of a product leave in one elected branch: their issue,
-    // not the tensor cores, was what the kernel waited for with a branch, a wait and a
-    // release per 64 dims (4500 cycles a step, 2560 of them at the MMAs' rate).
-    auto issue_s = [&](auto tile, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
-      constexpr int x = decltype(tile)::value;
-      if (i == 0 && !wait(&qfull[x], nq[x]++ & 1)) return false;
-      if (fresh && !wait(&kfull[g & 1], (g >> 1) & 1)) return false;
-      const uint64_t q = sdesc_k128(s_base + SM::kQ + x * kQTile);
+    // S of step g; first / last step of the item's.  All MMAs of a product leave in one
+    // elected branch.
+    auto issue_s = [&](uint32_t g, bool first, bool last) {
+      if (first && !wait(&qfull[x], nq++ & 1)) return;
+      if (!wait(&kfull[g & 1], (g >> 1) & 1)) return;
       if (elect_one()) {
 #pragma unroll
         for (uint32_t d = 0; d < 3; ++d) {
           const uint64_t k = sdesc_k128(ring + (5 * g + d) % kSlots * kUnit);
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
-            mma_ss(tmem + 128 * x, q + ((d * kUnit + 32 * kq) >> 4), k + ((32 * kq) >> 4), idesc_s, (d | kq) ? 1u : 0u);
+            mma_ss(s_tm, q + ((d * kUnit + 32 * kq) >> 4), k + ((32 * kq) >> 4), idesc_s, (d | kq) ? 1u : 0u);
         }
         tc_commit(&sfull[x]);
-        if (i + 1 == w.nt[x]) tc_commit(&qfree[x]);
-        if (last_use) tc_commit(&kfree[g & 1]);
+        tc_commit(&kfree[g & 1]);
+        if (last) tc_commit(&qfree[x]);
       }
       __syncwarp();
-      return true;
     };
-    auto issue_pv = [&](auto tile, const Work& w, int i, uint32_t g, bool fresh, bool last_use) {
-      constexpr int x = decltype(tile)::value;
-      if (fresh) {
-        if (!wait(&vfull[g & 1], (g >> 1) & 1)) return false;
-        const int nvalid = w.m.kv1 - (w.m.kv0 + i * kTile);
-        if (nvalid < kTile) {   // rows past the range: zero, 8 chunks of 16 bytes a row and block
-          for (int r = 8 * nvalid + lane; r < 8 * kTile; r += 32) {
-            const uint32_t v = ring + (5 * g + 3 + (r >> 9)) % kSlots * kUnit + 16 * (r & 511);
-            st_shared_v4(v, make_uint4(0, 0, 0, 0));
-            st_shared_v4(v + kUnit / 2, make_uint4(0, 0, 0, 0));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+    auto issue_pv = [&](uint32_t g, int nvalid, bool first, bool last) {
+      if (!wait(&vfull[g & 1], (g >> 1) & 1)) return;
+      if (nvalid < kTile) {
+        // rows past the range: zero, 8 chunks of 16 bytes a row and block (both tiles' warps
+        // do so, each before its own MMAs)
+        for (int r = 8 * nvalid + lane; r < 8 * kTile; r += 32) {
+          const uint32_t v = ring + (5 * g + 3 + (r >> 9)) % kSlots * kUnit + 16 * (r & 511);
+          st_shared_v4(v, make_uint4(0, 0, 0, 0));
+          st_shared_v4(v + kUnit / 2, make_uint4(0, 0, 0, 0));
         }
+        fence_proxy_async_smem();
+        __syncwarp();
       }
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
-        if (!wait(&pready[2 * x + h], np[x] & 1)) return false;
+        if (!wait(&pready[2 * x + h], np & 1)) return;
         const uint64_t v = sdesc_mn128(ring + (5 * g + 3 + h) % kSlots * kUnit, kUnit / 2, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
-            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 32 * h + 8 * kq, v + ((2048 * kq) >> 4), idesc_pv,
-                   (i > 0 || h > 0 || kq > 0) ? 1u : 0u);
+            mma_ts(o_tm, s_tm + 32 * h + 8 * kq, v + ((2048 * kq) >> 4), idesc_pv, (!first || h > 0 || kq > 0) ? 1u : 0u);
           if (h == 1) {
-            if (i + 1 == w.nt[x]) tc_commit(&odone[x]);
-            if (last_use) tc_commit(&vfree[g & 1]);
+            tc_commit(&vfree[g & 1]);
+            if (last) tc_commit(&odone[x]);
           }
         }
         __syncwarp();
       }
-      ++np[x];
-      return true;
+      ++np;
     };
-    constexpr std::integral_constant<int, 0> tile_a{};
-    constexpr std::integral_constant<int, 1> tile_b{};
-    if (begin < end) {
-      int it = begin, i = 0;
-      uint32_t g = 0;
-      Work cur = work_at(it), nxt = cur, ahead = cur;   // ahead: the item behind cur's
-      if (it + 1 < end) ahead = work_at(it + 1);
-      auto s_a = [&](const Work& w, int j, uint32_t gg) {
-        return j >= w.nt[0] || issue_s(tile_a, w, j, gg, true, j >= w.nt[1]);
-      };
-      auto s_b = [&](const Work& w, int j, uint32_t gg) {
-        return j >= w.nt[1] || issue_s(tile_b, w, j, gg, j >= w.nt[0], true);
-      };
-      ok = s_a(cur, 0, 0) && s_b(cur, 0, 0);
-      while (ok) {
-        int ni = i + 1;
-        bool more = true;
-        if (ni < cur.n) nxt = cur;
-        else if (it + 1 < end) nxt = ahead, ni = 0;
-        else more = false;
-        const bool a = i < cur.nt[0], b = i < cur.nt[1];
-        if (a && !issue_pv(tile_a, cur, i, g, true, !b)) break;
-        if (more && !s_a(nxt, ni, g + 1)) break;
-        if (b && !issue_pv(tile_b, cur, i, g, !a, true)) break;
-        if (more && !s_b(nxt, ni, g + 1)) break;
-        if (!more) break;
-        if (ni == 0) {
-          cur = nxt;
-          if (++it + 1 < end) ahead = work_at(it + 1);
+    // S runs one step ahead of PV; the step whose PV is due:
+    uint32_t due_g = 0, g = 0;
+    int due_valid = 0;
+    bool due = false, due_first = false, due_last = false;
+    auto flush = [&]() {
+      if (due) issue_pv(due_g, due_valid, due_first, due_last);
+      due = false;
+    };
+    Work nxt{};
+    if (begin < end) nxt = work_at(begin);
+    for (int it = begin; it < end && ok; ++it) {
+      const Work w = nxt;
+      if (it + 1 < end) nxt = work_at(it + 1);
+      const int steps = x ? w.nt[1] : w.nt[0];
+      for (int i = 0; i < w.n && ok; ++i, ++g) {
+        if (i < steps) {
+          flush();
+          if (ok) issue_s(g, i == 0, i + 1 == steps);
+          due = true;
+          due_g = g;
+          due_valid = w.m.kv1 - (w.m.kv0 + i * kTile);
+          due_first = i == 0;
+          due_last = i + 1 == steps;
+        } else {
+          // the step is the other tile's alone: its operands are free as far as this one goes
+          flush();
+          if (ok && wait(&kfull[g & 1], (g >> 1) & 1) && lane == 0) mbar_arrive(&kfree[g & 1]);
+          if (ok && wait(&vfull[g & 1], (g >> 1) & 1) && lane == 0) mbar_arrive(&vfree[g & 1]);
+          __syncwarp();
         }
-        i = ni;
-        ++g;
       }
       if (!ok && lane == 0) raise(it);
     }
+    if (ok) flush();
+    if (!ok && lane == 0) raise(end - 1);
     // drain: every MMA this warp issued completes before TMEM is released
-    if (elect_one()) tc_commit(drain);
+    if (elect_one()) tc_commit(&drain[x]);
     __syncwarp();
-    mbar_wait(drain, 0, kDrainNs);
+    mbar_wait(&drain[x], 0, kDrainNs);
   }
   // (the remaining warps have no role but to complete the warpgroup)
   } else {
