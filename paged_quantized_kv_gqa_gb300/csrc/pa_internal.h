@@ -161,6 +161,7 @@ struct AttnParams {
   int32_t softmax_wgs;   // decode: softmax warpgroups in use (1 when every item's rows fit in half)
   float sm_scale_log2;   // sm_scale * log2(e)
   OutEpilogue ep;
+  int32_t plain_out;     // expanded rows: no output epilogue, out 32-byte aligned
   const int32_t* cu_seqlens_q;   // device, needed with a tree mask
   const uint8_t* attn_mask;      // [bsz][mask_dim][mask_dim] or null
   int32_t mask_dim;

@@ -37,7 +37,7 @@ constexpr int kSlots = 8;
 constexpr int kQTile = 3 * kUnit;               // Q of a tile: three blocks of 64 dims
 constexpr int kThreads = 384;                   // softmax A 0-3, softmax B 4-7, TMA 8, MMA A 9, MMA B 10
 // registers: 168 a thread at launch, moved to the softmax, whose threads hold a row of scores
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+constexpr int kRegsSoftmax = 192, kRegsOther = 120;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the shares add up to the launch's registers");
 constexpr int kWarpTma = 8;
 constexpr int kWarpMma = 9;
@@ -338,13 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c_log2 = p.sm_scale_log2;
     uint32_t n = 0, items = 0;   // steps, items of this tile
     bool fail = false;
+    const int r = 128 * x + rr;
     for (int it = begin; it < end && !fail; ++it) {
-      const Work w = work_at(it);
-      const Item& m = w.m;
-      const int steps = x ? w.nt[1] : w.nt[0];
+      int steps, seen;   // this tile's; positions that the row sees from the step's first on
+      {
+        const Work w = work_at(it);
+        steps = x ? w.nt[1] : w.nt[0];
+        seen = min(w.m.kv1, w.m.cbase + r + 1) - w.m.kv0;
+      }
+      if (it + 1 < end) prefetch_l1(recs + 2 * (int64_t)(it + 1));
       if (steps == 0) continue;   // the item has no rows for this tile
-      const int r = 128 * x + rr;
-      const int vis_lim = min(m.kv1, m.cbase + r + 1);   // positions below it are seen
       float m_run = -INFINITY, l = 0.0f;
       for (int i = 0; i < steps; ++i, ++n) {
         if (!wait_or_abort(&sfull[x], n & 1, limit, abort_any)) {
@@ -357,11 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v + 32 * c);
         tmem_wait_ld();
-        const int nvis = vis_lim - (m.kv0 + i * kTile);
-        if (nvis < kTile) {
+        if (seen < kTile) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e) v[e] = e < nvis ? v[e] : 0xFF800000u;   // -inf
+          for (int e = 0; e < 128; ++e) v[e] = e < seen ? v[e] : 0xFF800000u;   // -inf
         }
+        seen -= kTile;
         // the first half's P against the maximum so far, while the step's maximum is taken
         uint32_t o[32];
         float neg_m = m_run == -INFINITY ? 0.0f : -m_run;
@@ -409,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&pready[2 * x + 1], lane);
       }
       if (fail) break;
-      // ---- epilogue: O / l
+      // ---- epilogue: O / l (the record again, so that nothing of it lives through the steps)
+      const Item m = work_at(it).m;
       if (!wait_or_abort(&odone[x], items & 1, limit, abort_any)) {
         raise(it);
         break;
@@ -421,17 +425,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int token = m.tok0 + r;
       const int64_t row = final_row ? (int64_t)token * p.q_heads + m.kvh
                                     : ((int64_t)m.chunk + (int64_t)r * m.nch) * p.q_heads + m.kvh;
-#pragma unroll 2
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[16];
-        tmem_ld16(o_tm + 16 * c, o);
-        tmem_wait_ld();
-        if (row_ok) {
-          float a[16];
+      if (final_row && p.plain_out) {
+        // bf16 rows without the steps of the general epilogue, a 32-byte sector a store
+        __nv_bfloat16* dst = p.out + row * 128;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) a[e] = __uint_as_float(o[e]) * inv_l;
-          if (final_row) ep_store16(p.ep, p.out, row * 128 + 16 * c, m.kvh * 128 + 16 * c, a);
-          else store16_f32(reinterpret_cast<float*>(p.part_o) + row * 128 + 16 * c, a);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32], u[16];
+          tmem_ld32(o_tm + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv_l, __uint_as_float(o[2 * e + 1]) * inv_l);
+            u[e] = *reinterpret_cast<uint32_t*>(&b2);
+          }
+          if (row_ok) {
+            st_global_32(dst + 32 * c, u);
+            st_global_32(dst + 32 * c + 16, u + 8);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16];
+          tmem_ld16(o_tm + 16 * c, o);
+          tmem_wait_ld();
+          if (row_ok) {
+            float a[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) a[e] = __uint_as_float(o[e]) * inv_l;
+            if (final_row) {
+              ep_store16(p.ep, p.out, row * 128 + 16 * c, m.kvh * 128 + 16 * c, a);
+            } else {   // (slots are 32-byte aligned)
+              float* dst = reinterpret_cast<float*>(p.part_o) + row * 128 + 16 * c;
+              st_global_32(dst, reinterpret_cast<const uint32_t*>(a));
+              st_global_32(dst + 8, reinterpret_cast<const uint32_t*>(a) + 8);
+            }
+          }
         }
       }
       tc_fence_before();   // (the next item's first P, behind which its PV writes O, is announced after this)
