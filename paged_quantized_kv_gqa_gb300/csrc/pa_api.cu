@@ -98,6 +98,54 @@ static pa_status check_problem(const pa_problem& p) {
 }
 
 // ------------------------------------------------------------------ planner
+// Cost of an item of the expanded form in steps of a 128-row tile: its steps, what an item
+// starts and ends with, and the partial rows of a split one.
+static int64_t expanded_cost(int64_t positions, int rows, bool split) {
+  return ceil_div(positions, kExpandedTile) * (rows > 128 ? 2 : 1) + 3 + (split ? kExpandedSplit : 0);
+}
+
+// Chunk size of the expanded form where the planner chooses: of no split and sizes about
+// 1.4 apart, the one whose items, longest first onto the least loaded CTA, end first
+// (the merge's launch added).  tiles: (positions, rows), each run for every head.
+static int64_t expanded_chunk(const std::vector<std::pair<int64_t, int>>& tiles, int heads, int slots) {
+  auto finish = [&](int64_t cs) -> int64_t {   // of the last CTA; -1: too many items to be worth it
+    std::vector<std::pair<int64_t, int64_t>> costs;   // cost, items
+    int64_t n = 0;
+    bool any = false;
+    for (const auto& t : tiles) {
+      const int64_t chunks = cs > 0 ? std::max<int64_t>(1, ceil_div(t.first, cs)) : 1;
+      for (int64_t c = 0; c < chunks && t.first > 0; ++c) {
+        const int64_t len = chunks > 1 ? std::min(t.first, (c + 1) * cs) - c * cs : t.first;
+        costs.push_back({expanded_cost(len, t.second, chunks > 1), heads});
+      }
+      n += chunks * heads;
+      any = any || chunks > 1;
+      if (n > 24 * (int64_t)slots) return -1;
+    }
+    std::sort(costs.begin(), costs.end(), std::greater<std::pair<int64_t, int64_t>>());
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> load;
+    for (int k = 0; k < slots; ++k) load.push(0);
+    int64_t last = 0;
+    for (const auto& c : costs)
+      for (int64_t k = 0; k < c.second; ++k) {
+        const int64_t l = load.top() + c.first;
+        load.pop();
+        load.push(l);
+        last = std::max(last, l);
+      }
+    return last + (any ? kExpandedMerge : 0);
+  };
+  int64_t best = 0, at = finish(0), longest = 0;
+  for (const auto& t : tiles) longest = std::max(longest, t.first);
+  if (at < 0) return 0;   // many items a CTA: whole ranges
+  // 5, 7, 10, 14, 20 .. steps
+  for (int64_t steps = 5; steps * kExpandedTile < longest; steps = steps % 7 ? steps / 5 * 7 : steps / 7 * 10) {
+    const int64_t cs = steps * kExpandedTile, f = finish(cs);
+    if (f >= 0 && f < at) best = cs, at = f;
+  }
+  return best;
+}
+
 static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int32_t* slkv,
                             const int32_t* cu, int32_t num_sms, Plan& P) {
   P.prob = prob;
@@ -309,6 +357,10 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
     if (cs == -1) {
       if (tiles.empty()) {
         cs = 0;
+      } else if (P.expanded()) {
+        std::vector<std::pair<int64_t, int>> t;
+        for (const auto& x : tiles) t.push_back({x.lim, x.tok1 - x.tok0});
+        cs = expanded_chunk(t, prob.kv_heads, slots);
       } else {
         int64_t W = 0, maxlim = 0;
         for (auto& t : tiles) {
@@ -316,8 +368,8 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
           maxlim = std::max(maxlim, t.lim);
         }
         W *= prob.kv_heads;
-        const int64_t target = 4LL * slots, unit = P.expanded() ? kExpandedTile : B;
-        cs = std::max<int64_t>(4LL * unit, ceil_div(ceil_div(W, target), unit) * unit);
+        const int64_t target = 4LL * slots;
+        cs = std::max<int64_t>(4LL * B, ceil_div(ceil_div(W, target), B) * B);
         if (cs >= maxlim) cs = 0;
       }
     }
@@ -349,19 +401,27 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       cost[i] = ceil_div((int64_t)items[i * kItemWords + 6] - items[i * kItemWords + 5], B) + 2;
     std::vector<int> order(n);
     for (int i = 0; i < n; ++i) order[i] = i;
-    // expanded rows: a step of a 128-row tile is the unit (a tile of few rows costs a
-    // whole one), and heads go by blocks whose rows fit L2, longest first within a block
-    int64_t block_heads = prob.kv_heads;
+    // Expanded rows: a step of a 128-row tile is the unit (a tile of few rows costs a whole
+    // one).  Heads go by blocks whose rows fit L2, longest first within a block; items of
+    // less than a sixteenth of a CTA's share come behind all of them and even out the CTAs
+    // (left in their blocks, the last block's long ones did not: 128 heads of four prompts
+    // of 512-2048, the longest CTA 8 % above the mean, 1 % so).
+    int64_t block_heads = prob.kv_heads, small = 0;
     if (P.expanded()) {
       block_heads = std::max<int64_t>(1, kExpandedBlock / (std::max<int64_t>(P.kv_rows, 1) * 512));
+      int64_t all = 0;
       for (int i = 0; i < n; ++i) {
         const int32_t* r = &items[(size_t)i * kItemWords];
-        cost[i] = ceil_div((int64_t)r[6] - r[5], kExpandedTile) * (r[3] > 128 ? 2 : 1) + 3;
+        cost[i] = expanded_cost((int64_t)r[6] - r[5], r[3], (r[7] >> 16) > 1);
+        all += cost[i];
       }
+      small = all / (16 * (int64_t)slots);
     }
-    auto head_block = [&](int i) { return items[(size_t)i * kItemWords + 1] / block_heads; };
+    auto block_of = [&](int i) -> int64_t {
+      return cost[i] < small ? INT64_MAX : items[(size_t)i * kItemWords + 1] / block_heads;
+    };
     std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
-      const int64_t x = head_block(a), y = head_block(b);
+      const int64_t x = block_of(a), y = block_of(b);
       return x != y ? x < y : cost[a] > cost[b];
     });
     using Load = std::pair<int64_t, int>;

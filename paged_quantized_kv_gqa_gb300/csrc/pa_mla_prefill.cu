@@ -37,7 +37,7 @@ constexpr int kSlots = 8;
 constexpr int kQTile = 3 * kUnit;               // Q of a tile: three blocks of 64 dims
 constexpr int kThreads = 384;                   // softmax A 0-3, softmax B 4-7, TMA 8, MMA A 9, MMA B 10
 // registers: 168 a thread at launch, moved to the softmax, whose threads hold a row of scores
-constexpr int kRegsSoftmax = 192, kRegsOther = 120;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the shares add up to the launch's registers");
 constexpr int kWarpTma = 8;
 constexpr int kWarpMma = 9;
@@ -87,6 +87,26 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=l"(r)
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&r);
+}
+
+// Four pieces of 8 words a lane: lane j of a quad goes from pieces 0 .. 3 of its row to
+// piece j of the quad's rows 0 .. 3.
+__device__ __forceinline__ void quad_transpose(uint32_t (&u)[32], int lane) {
+#pragma unroll
+  for (int b = 1; b <= 2; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & b) continue;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        uint32_t &lo = u[8 * i + w], &hi = u[8 * (i + b) + w];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, b);
+        lo = up ? got : lo;
+        hi = up ? hi : got;
+      }
+    }
+  }
 }
 
 // 64 scores -> 2^(s c - m) as bf16 pairs, and their sum before that rounding
@@ -425,22 +445,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int token = m.tok0 + r;
       const int64_t row = final_row ? (int64_t)token * p.q_heads + m.kvh
                                     : ((int64_t)m.chunk + (int64_t)r * m.nch) * p.q_heads + m.kvh;
-      if (final_row && p.plain_out) {
-        // bf16 rows without the steps of the general epilogue, a 32-byte sector a store
-        __nv_bfloat16* dst = p.out + row * 128;
+      if (p.plain_out || !final_row) {
+        // Rows without an output epilogue: quads of lanes exchange 32-byte pieces, so that a
+        // store instruction writes 8 whole lines (32 sectors of 32 rows each took 4500 cycles
+        // a tile, with what the next loads waited behind them)
+        const int64_t step = final_row ? p.q_heads : (int64_t)m.nch * p.q_heads;   // rows apart
+        const int r4 = r & ~3;
+        const int64_t row4 = row - (r - r4) * step;
+        if (final_row) {
+          uint8_t* dst = reinterpret_cast<uint8_t*>(p.out + row4 * 128) + 32 * (lane & 3);
+#pragma unroll 1   // (code that runs once an item: its fetch is what it costs)
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[64], u[32];
+            tmem_ld32(o_tm + 64 * c, o);
+            tmem_ld32(o_tm + 64 * c + 32, o + 32);
+            tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32], u[16];
-          tmem_ld32(o_tm + 32 * c, o);
-          tmem_wait_ld();
+            for (int k = 0; k < 32; ++k) {
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv_l, __uint_as_float(o[2 * k + 1]) * inv_l);
+              u[k] = *reinterpret_cast<uint32_t*>(&b2);
+            }
+            quad_transpose(u, lane);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv_l, __uint_as_float(o[2 * e + 1]) * inv_l);
-            u[e] = *reinterpret_cast<uint32_t*>(&b2);
+            for (int k = 0; k < 4; ++k)
+              if (r4 + k < m.ntok) st_global_32(dst + k * step * 256 + 128 * c, u + 8 * k);
           }
-          if (row_ok) {
-            st_global_32(dst + 32 * c, u);
-            st_global_32(dst + 32 * c + 16, u + 8);
+        } else {
+          uint8_t* dst = reinterpret_cast<uint8_t*>(reinterpret_cast<float*>(p.part_o) + row4 * 128) + 32 * (lane & 3);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[32];
+            tmem_ld32(o_tm + 32 * c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * inv_l);
+            quad_transpose(u, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (r4 + k < m.ntok) st_global_32(dst + k * step * 512 + 128 * c, u + 8 * k);
           }
         }
       } else {
@@ -453,13 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) a[e] = __uint_as_float(o[e]) * inv_l;
-            if (final_row) {
-              ep_store16(p.ep, p.out, row * 128 + 16 * c, m.kvh * 128 + 16 * c, a);
-            } else {   // (slots are 32-byte aligned)
-              float* dst = reinterpret_cast<float*>(p.part_o) + row * 128 + 16 * c;
-              st_global_32(dst, reinterpret_cast<const uint32_t*>(a));
-              st_global_32(dst + 8, reinterpret_cast<const uint32_t*>(a) + 8);
-            }
+            ep_store16(p.ep, p.out, row * 128 + 16 * c, m.kvh * 128 + 16 * c, a);
           }
         }
       }
