@@ -1083,14 +1083,15 @@ static pa_status check_product(int32_t rows, int32_t heads, const void* x, int64
   return PA_OK;
 }
 
-static pa_status run_product(MlaProduct& m, void* stream) {
+static pa_status run_product(MlaProduct& m, void* stream, int pair_sms = 0) {
   FaultCfg fc;
   {
     std::lock_guard<std::mutex> lk(g_fault_mu);
     fc = g_faults;
     g_faults.skip_first_load = 0;  // one-shot
   }
-  const cudaError_t e = launch_mla_product(m, fc, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = pair_sms ? launch_mla_expand(m, fc, pair_sms, static_cast<cudaStream_t>(stream))
+                                 : launch_mla_product(m, fc, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("product: ") + cudaGetErrorString(e));
   return PA_OK;
 }
@@ -1129,10 +1130,16 @@ pa_status pa_mla_expand(int32_t rows, int32_t heads, const void* c, int64_t c_st
   if (s != PA_OK || rows == 0) return s;
   MlaProduct m{2, rows, heads, c, k_out, c_stride, kv_stride, static_cast<int32_t*>(workspace), {}};
   if ((s = make_map3(&m.tm[0], c, 512, 1, rows, 512, c_stride, 1, 128)) != PA_OK) return s;
-  if ((s = make_map3(&m.tm[1], w, 512, 256, heads, 512, w_head_stride, 256, 1)) != PA_OK) return s;
+  // by CTA pairs where their tiles fill the GPU
+  int sms = 0, dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, std::string("expand: ") + cudaGetErrorString(e));
+  const bool pairs = rows > 128 && ceil_div(rows, 256) * heads >= kExpandPairTiles;
+  if ((s = make_map3(&m.tm[1], w, 512, 256, heads, 512, w_head_stride, pairs ? 128 : 256, 1)) != PA_OK) return s;
   if ((s = make_map3(&m.tm[2], k_out, 128, heads, rows, 128, kv_stride, 1, 32)) != PA_OK) return s;
   if ((s = make_map3(&m.tm[3], v_out, 128, heads, rows, 128, kv_stride, 1, 32)) != PA_OK) return s;
-  return run_product(m, stream);
+  return run_product(m, stream, pairs ? sms : 0);
 }
 
 pa_status pa_mla_prefill(const pa_plan_t* plan, const pa_args* args, const void* k_nope, const void* v,

@@ -40,6 +40,7 @@ constexpr int kDecode4TileCost = 12;
 // the merge's classes of 4-bit rows: 32, 16, 8, 4, 2, 1 warps a row, for more than 128,
 // 64, 32, 16, 8 chunks and the others
 constexpr int kMergeClasses = 6;
+constexpr int kExpandPairTiles = 384;   // tiles of 256 rows from which CTA pairs expand
 constexpr int kExpandedTile = 128;   // positions of a step of the expanded form
 constexpr int kExpandedSplit = 3;    // what the partial rows of a split item cost, in steps
 constexpr int kExpandedMerge = 6;    // and the merge's launch
@@ -217,6 +218,8 @@ cudaError_t launch_cache_append4(const Plan& plan, const pa_args& a, const void*
 cudaError_t launch_mla_prefill(const Plan& plan, const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const CUtensorMap& tm_r, const CUtensorMap& tm_v, cudaStream_t stream);
 cudaError_t launch_mla_product(const MlaProduct& m, const FaultCfg& fc, cudaStream_t stream);
+// expand of many rows, by CTA pairs (its weights' boxes have 128 rows)
+cudaError_t launch_mla_expand(const MlaProduct& m, const FaultCfg& fc, int num_sms, cudaStream_t stream);
 // queries rotated, K / V rows rotated (K) and written, every cache
 cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope& rope, const void* q,
                                int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new,
