@@ -1,4 +1,4 @@
-// pa_rope.cu - the step before attention in one launch: queries rotated by their
+// pa_rope.cu - the step before attention in one launch (two for many rows): queries rotated by their
 // positions, new K / V rows rotated (K), quantised and written into the paged cache.
 //
 // Rotation of a pair (a, b) of dims by the angle whose cos c and sin s the table holds,
@@ -25,7 +25,10 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kWarps = 8;
-constexpr int kRopeUnit = 8;    // positions of a rotation warp's unit
+// positions of a rotation warp's unit: queries alone, and everything else (a warp with all
+// heads of two rows reads their cos and sin once; in units of 8 rows and 2 of 8 heads, to
+// have as many warps, K and V of 35k rows, FP4, took 94 us)
+constexpr int kQUnit = 8, kRopeUnit = 2;
 constexpr int kMlaRow = 576, kMlaLatent = 512, kMlaQ = 192, kMlaNope = 128;
 
 struct RopeParams {
@@ -35,7 +38,7 @@ struct RopeParams {
   const __nv_bfloat16* q;      // or null
   __nv_bfloat16* q_out;
   int64_t q_stride, q_out_stride;
-  RowUnits units;              // units of kRopeUnit positions
+  RowUnits units;              // the rotation's
   uint32_t rot_warps;          // warps of the rotation; the V warps follow
   int32_t groups, group_heads; // head groups of a unit
   int32_t q_heads;             // 0 without queries
@@ -117,16 +120,15 @@ __device__ __forceinline__ bool load_turn(const RopeParams& p, int64_t t, int po
   return true;
 }
 
-// The rotated values of a lane's 8 dims x (bf16), y the 8 dims of the lane that holds
-// the other halves of its pairs.
-__device__ __forceinline__ void turn8(const RopeParams& p, const uint4& x, const uint4& y, const Turn& a, float (&f)[8]) {
+// The rotated values of a lane's 8 dims x (bf16), y the other dims of their pairs, in
+// place.  (As f32x2 instructions, mul.rn and add.rn came out fused now and then: results a
+// last place off.)
+__device__ __forceinline__ void turn8(const uint4& x, const uint4& y, const Turn& a, float (&f)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float lo = bf16_lo(w[k]), hi = bf16_hi(w[k]);
-    const float o_lo = p.adjacent ? hi : bf16_lo(v[k]), o_hi = p.adjacent ? lo : bf16_hi(v[k]);
-    f[2 * k] = __fadd_rn(__fmul_rn(lo, a.c[2 * k]), __fmul_rn(o_lo, a.s[2 * k]));
-    f[2 * k + 1] = __fadd_rn(__fmul_rn(hi, a.c[2 * k + 1]), __fmul_rn(o_hi, a.s[2 * k + 1]));
+    f[2 * k] = __fadd_rn(__fmul_rn(bf16_lo(w[k]), a.c[2 * k]), __fmul_rn(bf16_lo(v[k]), a.s[2 * k]));
+    f[2 * k + 1] = __fadd_rn(__fmul_rn(bf16_hi(w[k]), a.c[2 * k + 1]), __fmul_rn(bf16_hi(v[k]), a.s[2 * k + 1]));
   }
 }
 
@@ -144,6 +146,14 @@ __device__ __forceinline__ uint4 shfl4(const uint4& x, int lane) {
                     __shfl_sync(0xffffffffu, x.z, lane), __shfl_sync(0xffffffffu, x.w, lane));
 }
 
+// The other dims of the pairs of a lane's 8: its own, neighbours swapped, or lane `from`'s.
+__device__ __forceinline__ uint4 partners(const RopeParams& p, const uint4& x, int from) {
+  if (p.adjacent)
+    return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032), __byte_perm(x.z, 0, 0x1032),
+                      __byte_perm(x.w, 0, 0x1032));
+  return shfl4(x, from);
+}
+
 __device__ __forceinline__ uint4 bf16x8_of(const float (&f)[8]) {
   return make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
 }
@@ -151,10 +161,9 @@ __device__ __forceinline__ uint4 bf16x8_of(const float (&f)[8]) {
 template <int KV>
 constexpr bool is_four() { return KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1; }
 
-// One value -> its 8-bit code.
+// A quotient -> its 8-bit code.
 template <int KV>
-__device__ __forceinline__ uint32_t code8(float x, float s) {
-  const float v = __fdiv_rn(x, s);
+__device__ __forceinline__ uint32_t code8(float v) {
   if constexpr (KV == PA_KV_FP8_E4M3) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
@@ -164,39 +173,97 @@ __device__ __forceinline__ uint32_t code8(float x, float s) {
   }
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 1 / s for quot(), or NaN where its short quotients would not do
+__device__ __forceinline__ float short_rcp(float s) {
+  const float a = fabsf(s);
+  return a > 1e-30f && a < 1e30f ? rcp_approx(s) : NAN;
+}
+
+// N values over their scales (r their short_rcp), rounded: by quot(), or by divisions where
+// one of them is not finite or large.
+template <int N, bool PC>
+__device__ __forceinline__ void quotients(const float* x, const float* s, const float* r, float* v) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    v[e] = quot(x[e], s[PC ? e : 0], r[PC ? e : 0]);
+    m = max_nan(m, fabsf(v[e]));
+  }
+  if (!(m < 1e30f)) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __fdiv_rn(x[e], s[PC ? e : 0]);
+  }
+}
+
 // A lane's 8 values of a K row -> its codes (and block scale), in place within the slab.
 // The lanes of a block are neighbours; every lane of the warp calls it, those of rows
 // outside the range with in = false.
 template <int KV, bool PC>
 __device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8], uint8_t* slab, int kvh, int off, int c,
                                         bool in) {
-  float g[8];
+  float g[8], rg[8];
+  if constexpr (PC) {
+    const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(p.a.k_scale) + kvh * kV4Dim + 8 * c;
 #pragma unroll
-  for (int e = 0; e < (PC ? 8 : 1); ++e)
-    g[e] = load_scale(p.a.k_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 8 * c + e : kvh);
+    for (int e = 0; e < 8; ++e) g[e] = __bfloat162float(sc[e]);
+  } else {
+    g[0] = load_scale(p.a.k_scale, p.a.scale_kind, kvh);
+  }
+#pragma unroll
+  for (int e = 0; e < (PC ? 8 : 1); ++e) rg[e] = short_rcp(g[e]);
   if constexpr (!is_four<KV>()) {
+    float v[8];
+    quotients<8, PC>(f, g, rg, v);
     uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(f[e], g[PC ? e : 0]) << (8 * (e & 3));
+    for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(v[e]) << (8 * (e & 3));
     if (in) *reinterpret_cast<uint2*>(slab + off * kV4Dim + 8 * c) = make_uint2(w[0], w[1]);
   } else {
     constexpr int FP4 = KV == PA_KV_FP4_E2M1;
     constexpr float kTop = Fmt<FP4>::kTop;
-    float x[8], a = 0.0f;
+    // the block's maximum of |x / g| by short quotients; a NaN, or a block out of their
+    // range, shows in `fine`
+    float a = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = f[e] != f[e] ? 0.0f : f[e];
-      a = fmaxf(a, PC ? fabsf(__fdiv_rn(x[e], g[e])) : fabsf(x[e]));
-    }
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    if constexpr (!PC) a = fabsf(__fdiv_rn(a, g[0]));   // of the largest: rounding keeps the order
-    const uint32_t sb = block_scale<FP4>(__fdiv_rn(a, kTop));
+    for (int e = 0; e < 8; ++e) a = max_nan(a, PC ? fabsf(quot(f[e], g[e], rg[e])) : fabsf(f[e]));
+    a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    if constexpr (!PC) a = fabsf(quot(a, g[0], rg[0]));   // of the largest: rounding keeps the order
+    uint32_t sb = block_scale<FP4>(quot(a, kTop, 1.0f / kTop));
     const float s = e4m3_to_f32(sb);
-    float q[8];
+    float q[8], low = 1e30f, high = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float step = __fmul_rn(s, g[PC ? e : 0]);
-      q[e] = fminf(fmaxf(step > 0.0f ? __fdiv_rn(x[e], step) : 0.0f, -kTop), kTop);
+    for (int e = 0; e < (PC ? 8 : 1); ++e) {
+      const float st = fabsf(s * g[e]);
+      low = fminf(low, st);
+      high = fmaxf(high, st);
+    }
+    const bool fine = common<FP4>(a, s, low) && high < 1e30f;
+    if (__all_sync(0xffffffffu, fine || !in)) {
+      const float r0 = PC ? 0.0f : rcp_approx(s * g[0]), rs = PC ? rcp_approx(s) : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = quot(f[e], s * g[PC ? e : 0], PC ? rs * rg[e] : r0);
+    } else {
+      float x[8];
+      a = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = f[e] != f[e] ? 0.0f : f[e];
+        a = fmaxf(a, fabsf(__fdiv_rn(x[e], g[PC ? e : 0])));
+      }
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      sb = block_scale<FP4>(__fdiv_rn(a, kTop));
+      const float t = e4m3_to_f32(sb);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float step = __fmul_rn(t, g[PC ? e : 0]);
+        q[e] = fminf(fmaxf(step > 0.0f ? __fdiv_rn(x[e], step) : 0.0f, -kTop), kTop);
+      }
     }
     const uint32_t w = pack8<FP4>(q);
     if (in) {
@@ -214,6 +281,9 @@ __device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat1
 #pragma unroll
   for (int d = 0; d < (PC ? 4 : 1); ++d)
     g[d] = load_scale(p.a.v_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 4 * lane + d : kvh);
+  float rg[4];
+#pragma unroll
+  for (int d = 0; d < (PC ? 4 : 1); ++d) rg[d] = short_rcp(g[d]);
   const __nv_bfloat16* src = rows + 4 * lane - (int64_t)a * p.a.kv_stride;
   uint8_t* dst = slab + 4 * lane * kPage + off0;
 #pragma unroll
@@ -226,9 +296,11 @@ __device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat1
     uint32_t w[4][2] = {};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float v[4] = {bf16_lo(x[j].x), bf16_hi(x[j].x), bf16_lo(x[j].y), bf16_hi(x[j].y)};
+      const float x4[4] = {bf16_lo(x[j].x), bf16_hi(x[j].x), bf16_lo(x[j].y), bf16_hi(x[j].y)};
+      float v[4];
+      quotients<4, PC>(x4, g, rg, v);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) w[d][j >> 2] |= code8<KV>(v[d], g[PC ? d : 0]) << (8 * (j & 3));
+      for (int d = 0; d < 4; ++d) w[d][j >> 2] |= code8<KV>(v[d]) << (8 * (j & 3));
     }
     if (a <= k && k + 8 <= e) {
 #pragma unroll
@@ -274,8 +346,55 @@ __device__ __forceinline__ bool unit_at(const RopeParams& p, const RowUnits& uni
 }
 
 // ---- GQA
+// Queries alone, of many rows: few registers, so that 32 warps an SM have their loads on
+// the way (in one kernel with K's and V's quantisers 16; 35k rows of 32 heads 128 us)
+__global__ void __launch_bounds__(kWarps * 32, 4) rope_q_kernel(const RopeParams p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (id >= p.rot_warps) return;
+  const uint32_t bu = id / (uint32_t)p.groups;
+  const int g0 = (int)(id - bu * p.groups) * p.group_heads, g1 = min(p.q_heads, g0 + p.group_heads);
+  UnitAt m;
+  if (!unit_at<kQUnit>(p, p.units, bu, lane, m)) return;
+  const int c = lane & 15, oct = p.rot / 8;
+  const bool turned = c < oct;
+  const int other = !turned ? lane : (lane & 16) | (c < oct / 2 ? c + oct / 2 : c - oct / 2);
+  for (int r = m.lo; r < m.hi; r += 2) {
+    const int pos = r + (lane >> 4);
+    const bool in = pos < m.hi;
+    const int64_t t = m.row + (pos - m.lo);
+    const __nv_bfloat16* src = p.q + t * p.q_stride + 8 * c;
+    __nv_bfloat16* dst = p.q_out + t * p.q_out_stride + 8 * c;
+    uint4 x[4];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (in && h0 + k < g1) x[k] = *reinterpret_cast<const uint4*>(src + (h0 + k) * kV4Dim);
+      }
+    };
+    load(g0);
+    Turn a;
+    const bool turn = in && turned && load_turn(p, t, pos, c, a);
+    for (int h0 = g0; h0 < g1; h0 += 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (h0 + k >= g1) break;
+        const uint4 y = partners(p, x[k], other);
+        float f[8];
+        if (turn) turn8(x[k], y, a, f);
+        else plain8(x[k], f);
+        if (in) *reinterpret_cast<uint4*>(dst + (h0 + k) * kV4Dim) = bf16x8_of(f);
+      }
+      if (h0 + 4 < g1) load(h0 + 4);
+    }
+  }
+}
+
+// Everything in one launch (U = 8, few rows), or K and V (U = 32).
 template <int KV, bool PC, int U>
-__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 3) rope_append_kernel(const RopeParams p) {
+  constexpr int kBatch = U == 8 ? 4 : 2;   // heads whose rows are on the way at once
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
   constexpr int kSlabBytes = is_four<KV>() ? kV4Slab : kPage * kV4Dim;
@@ -311,17 +430,17 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopePara
   const int c = lane & 15, oct = p.rot / 8;
   const bool turned = c < oct;
   // the lane whose dims are the other halves of this one's pairs
-  const int other = p.adjacent || !turned ? lane : (lane & 16) | (c < oct / 2 ? c + oct / 2 : c - oct / 2);
+  const int other = !turned ? lane : (lane & 16) | (c < oct / 2 ? c + oct / 2 : c - oct / 2);
   for (int r = m.lo; r < m.hi; r += 2) {
     const int pos = r + (lane >> 4);
     const bool in = pos < m.hi;
     const int64_t t = m.row + (pos - m.lo);
     Turn a;
     const bool turn = in && turned && load_turn(p, t, pos, c, a);
-    for (int h0 = g0; h0 < g1; h0 += 4) {
-      uint4 x[4];
+    for (int h0 = g0; h0 < g1; h0 += kBatch) {
+      uint4 x[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kBatch; ++k) {
         const int h = h0 + k;
         x[k] = make_uint4(0, 0, 0, 0);
         if (in && h < g1)
@@ -330,12 +449,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopePara
                             : p.a.k_new + t * p.a.kv_stride + (h - p.q_heads) * kV4Dim + 8 * c);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kBatch; ++k) {
         const int h = h0 + k;
         if (h >= g1) break;
-        const uint4 y = p.adjacent ? x[k] : shfl4(x[k], other);
+        const uint4 y = partners(p, x[k], other);
         float f[8];
-        if (turn) turn8(p, x[k], y, a, f);
+        if (turn) turn8(x[k], y, a, f);
         else plain8(x[k], f);
         if (h < p.q_heads) {
           if (in) *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * kV4Dim + 8 * c) = bf16x8_of(f);
@@ -360,11 +479,11 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
   if (!unit_at<kRopeUnit>(p, p.units, bu, lane, m)) return;
   const int o = lane & 7, oct = p.rot / 8;
   const bool turned = o < oct;
-  const int other = p.adjacent || !turned ? lane : (lane & 24) | (o < oct / 2 ? o + oct / 2 : o - oct / 2);
+  const int other = !turned ? lane : (lane & 24) | (o < oct / 2 ? o + oct / 2 : o - oct / 2);
   if (g0 >= p.q_heads) {   // the rows of the cache
     const int page = page_at(p, m.b, m.u0, lane);
     if (page < 0) return;
-    const float s = load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0);
+    const float s[1] = {load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0)}, rs[1] = {short_rcp(s[0])};
     for (int pos = m.lo; pos < m.hi; ++pos) {
       const int64_t t = m.row + (pos - m.lo);
       const __nv_bfloat16* src = p.a.k_new + t * p.a.kv_stride;
@@ -375,16 +494,18 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
         if (k < 2 || lane < 8) x[k] = *reinterpret_cast<const uint4*>(src + 8 * (lane + 32 * k));
       Turn a;
       const bool turn = lane < 8 && turned && load_turn(p, t, pos, o, a);
-      const uint4 y = p.adjacent ? x[2] : shfl4(x[2], other);
+      const uint4 y = partners(p, x[2], other);
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         if (k == 2 && lane >= 8) break;
         float f[8];
-        if (k == 2 && turn) turn8(p, x[2], y, a, f);
+        if (k == 2 && turn) turn8(x[2], y, a, f);
         else plain8(x[k], f);
         uint32_t w[2] = {0, 0};
+        float v[8];
+        quotients<8, false>(f, s, rs, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(f[e], s) << (8 * (e & 3));
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(v[e]) << (8 * (e & 3));
         *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * k)) = make_uint2(w[0], w[1]);
       }
     }
@@ -398,23 +519,26 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
     __nv_bfloat16* dst = p.q_out + t * p.q_out_stride;
     Turn a;
     const bool turn = turned && load_turn(p, t, pos, o, a);
-    for (int h0 = g0; h0 < g1; h0 += 4) {   // the heads are a multiple of four
-      const int at = (h0 + (lane >> 3)) * kMlaQ + kMlaNope + 8 * o;
-      const int at0 = (h0 + (lane >> 4)) * kMlaQ + 8 * (lane & 15), at1 = at0 + 2 * kMlaQ;
-      const uint4 x = *reinterpret_cast<const uint4*>(src + at);
-      uint4 n0, n1;
+    const int at = (lane >> 3) * kMlaQ + kMlaNope + 8 * o, at0 = (lane >> 4) * kMlaQ + 8 * (lane & 15);
+    for (int h0 = g0; h0 < g1; h0 += 8) {   // the heads are a multiple of eight
+      uint4 x[2], n[4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(src + (h0 + 4 * k) * kMlaQ + at);
       if (copy) {
-        n0 = *reinterpret_cast<const uint4*>(src + at0);
-        n1 = *reinterpret_cast<const uint4*>(src + at1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) n[k] = *reinterpret_cast<const uint4*>(src + (h0 + 2 * k) * kMlaQ + at0);
       }
-      const uint4 y = p.adjacent ? x : shfl4(x, other);
-      float f[8];
-      if (turn) turn8(p, x, y, a, f);
-      else plain8(x, f);
-      *reinterpret_cast<uint4*>(dst + at) = bf16x8_of(f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 y = partners(p, x[k], other);
+        float f[8];
+        if (turn) turn8(x[k], y, a, f);
+        else plain8(x[k], f);
+        *reinterpret_cast<uint4*>(dst + (h0 + 4 * k) * kMlaQ + at) = bf16x8_of(f);
+      }
       if (copy) {
-        *reinterpret_cast<uint4*>(dst + at0) = n0;
-        *reinterpret_cast<uint4*>(dst + at1) = n1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(dst + (h0 + 2 * k) * kMlaQ + at0) = n[k];
       }
     }
   }
@@ -479,27 +603,37 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
     p.pair_axis[i >> 4] |= (uint32_t)(rope.pair_axis[i] & 3) << (2 * (i & 15));
     if (rope.pair_axis[i] != rope.pair_axis[i & ~3]) p.quads = 0;
   }
-  p.units = row_units<kRopeUnit>(pr.bsz, plan.max_q, plan.total_q);
   const bool mla = pr.layout == PA_LAYOUT_MLA;
-  const int heads = p.q_heads + (mla ? 0 : pr.kv_heads);
+  // V's units as pa_cache4.cu takes them, and one launch for all while they are short
+  const bool small = 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms;
   // Heads of a warp: enough to use a row's cos and sin often, few while the warps would
   // not fill the GPU
-  p.group_heads = 16;
-  while (p.group_heads > 4 &&
-         (double)p.units.count * ((heads + p.group_heads - 1) / p.group_heads) < 16.0 * kWarps * plan.num_sms)
-    p.group_heads /= 2;
-  p.groups = (heads + p.group_heads - 1) / p.group_heads + (mla ? 1 : 0);
-  const double rot = (double)p.units.count * p.groups;
-  if (rot > (double)INT32_MAX) return cudaErrorInvalidValue;
-  p.rot_warps = (uint32_t)rot;
+  auto share = [&](int heads, int least) {
+    p.group_heads = 16;
+    while (p.group_heads > least &&
+           (double)p.units.count * ((heads + p.group_heads - 1) / p.group_heads) < 16.0 * kWarps * plan.num_sms)
+      p.group_heads /= 2;
+    p.groups = (heads + p.group_heads - 1) / p.group_heads + (mla ? 1 : 0);
+    const double rot = (double)p.units.count * p.groups;
+    p.rot_warps = rot > (double)INT32_MAX ? 0 : (uint32_t)rot;
+    return p.rot_warps > 0;
+  };
+  if (!mla && q && !small) {
+    p.units = row_units<kQUnit>(pr.bsz, plan.max_q, plan.total_q);
+    if (!share(p.q_heads, 4)) return cudaErrorInvalidValue;
+    rope_q_kernel<<<(p.rot_warps + kWarps - 1) / kWarps, kWarps * 32, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    p.q_heads = 0;
+  }
+  p.units = row_units<kRopeUnit>(pr.bsz, plan.max_q, plan.total_q);
+  if (!share(p.q_heads + (mla ? 0 : pr.kv_heads), mla ? 8 : 4)) return cudaErrorInvalidValue;
   if (mla) {
     const dim3 grid((p.rot_warps + kWarps - 1) / kWarps), block(kWarps * 32);
     if (pr.kv_dtype == PA_KV_FP8_E4M3) rope_latent_kernel<PA_KV_FP8_E4M3><<<grid, block, 0, stream>>>(p);
     else rope_latent_kernel<PA_KV_INT8><<<grid, block, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  // V's units as pa_cache4.cu takes them
-  const bool small = 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms;
   switch (pr.kv_dtype) {
     case PA_KV_INT8: return launch_kv<PA_KV_INT8>(p, plan, small, stream);
     case PA_KV_FP8_E4M3: return launch_kv<PA_KV_FP8_E4M3>(p, plan, small, stream);
