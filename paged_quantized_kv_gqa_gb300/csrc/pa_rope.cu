@@ -44,6 +44,7 @@ struct RopeParams {
   int32_t q_heads;             // 0 without queries
   int32_t table_rows, rot, adjacent, axes, quads;   // quads: four neighbouring pairs share an axis
   int32_t total_q;
+  int32_t k_scale16;           // per-channel K scales are 16-byte aligned
   uint32_t pair_axis[4];       // two bits a pair
 };
 
@@ -161,15 +162,24 @@ __device__ __forceinline__ uint4 bf16x8_of(const float (&f)[8]) {
 template <int KV>
 constexpr bool is_four() { return KV == PA_KV_INT4 || KV == PA_KV_FP4_E2M1; }
 
-// A quotient -> its 8-bit code.
+// Four quotients -> their 8-bit codes, the first in the lowest byte (int8: not NaN).
 template <int KV>
-__device__ __forceinline__ uint32_t code8(float v) {
+__device__ __forceinline__ uint32_t codes4(const float* v) {
   if constexpr (KV == PA_KV_FP8_E4M3) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
-    return r & 0xFFu;
+    uint32_t w;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+    return w;
   } else {
-    return (uint32_t)max(-127, min(127, __float2int_rn(v))) & 0xFFu;
+    // adding 2^23 + 2^22 rounds to an integer, ties to even, and leaves it in the low bits
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = __float_as_uint(fminf(fmaxf(v[k], -127.0f), 127.0f) + 12582912.0f);
+    return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
   }
 }
 
@@ -179,26 +189,31 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// 1 / s for quot(), or NaN where its short quotients would not do
-__device__ __forceinline__ float short_rcp(float s) {
-  const float a = fabsf(s);
-  return a > 1e-30f && a < 1e30f ? rcp_approx(s) : NAN;
+// Whether quot() gives the quotients of values below 2^60 by s.
+__device__ __forceinline__ bool short_by(float s) { return s > 0x1p-60f && s < 0x1p60f; }
+
+// Any quotient, as pa_cache.cu's writer takes it (a NaN counts as 0 for int8).
+template <int KV>
+__device__ __forceinline__ float any_quotient(float x, float s) {
+  const float v = __fdiv_rn(x, s);
+  return KV == PA_KV_INT8 && v != v ? 0.0f : v;
 }
 
-// N values over their scales (r their short_rcp), rounded: by quot(), or by divisions where
-// one of them is not finite or large.
-template <int N, bool PC>
-__device__ __forceinline__ void quotients(const float* x, const float* s, const float* r, float* v) {
-  float m = 0.0f;
+// Eight values over their scales (r = 1 / s; ok: short_by of the scales) -> two words of
+// 8-bit codes.
+template <int KV, bool PC>
+__device__ __forceinline__ uint2 codes8_of(const float (&x)[8], const float* s, const float* r, bool ok) {
+  float v[8], m = 0.0f;
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
+  for (int e = 0; e < 8; ++e) {
+    m = max_nan(m, fabsf(x[e]));
     v[e] = quot(x[e], s[PC ? e : 0], r[PC ? e : 0]);
-    m = max_nan(m, fabsf(v[e]));
   }
-  if (!(m < 1e30f)) {
+  if (!(m < 0x1p60f) || !ok) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = __fdiv_rn(x[e], s[PC ? e : 0]);
+    for (int e = 0; e < 8; ++e) v[e] = any_quotient<KV>(x[e], s[PC ? e : 0]);
   }
+  return make_uint2(codes4<KV>(v), codes4<KV>(v + 4));
 }
 
 // A lane's 8 values of a K row -> its codes (and block scale), in place within the slab.
@@ -208,22 +223,26 @@ template <int KV, bool PC>
 __device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8], uint8_t* slab, int kvh, int off, int c,
                                         bool in) {
   float g[8], rg[8];
+  bool ok = true;
   if constexpr (PC) {
     const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(p.a.k_scale) + kvh * kV4Dim + 8 * c;
+    if (p.k_scale16) {
+      plain8(__ldg(reinterpret_cast<const uint4*>(sc)), g);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = __bfloat162float(sc[e]);
+      for (int e = 0; e < 8; ++e) g[e] = __bfloat162float(sc[e]);
+    }
   } else {
     g[0] = load_scale(p.a.k_scale, p.a.scale_kind, kvh);
   }
 #pragma unroll
-  for (int e = 0; e < (PC ? 8 : 1); ++e) rg[e] = short_rcp(g[e]);
+  for (int e = 0; e < (PC ? 8 : 1); ++e) {
+    rg[e] = rcp_approx(g[e]);
+    ok = ok && short_by(g[e]);
+  }
   if constexpr (!is_four<KV>()) {
-    float v[8];
-    quotients<8, PC>(f, g, rg, v);
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(v[e]) << (8 * (e & 3));
-    if (in) *reinterpret_cast<uint2*>(slab + off * kV4Dim + 8 * c) = make_uint2(w[0], w[1]);
+    const uint2 w = codes8_of<KV, PC>(f, g, rg, ok);
+    if (in) *reinterpret_cast<uint2*>(slab + off * kV4Dim + 8 * c) = w;
   } else {
     constexpr int FP4 = KV == PA_KV_FP4_E2M1;
     constexpr float kTop = Fmt<FP4>::kTop;
@@ -243,7 +262,7 @@ __device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8]
       low = fminf(low, st);
       high = fmaxf(high, st);
     }
-    const bool fine = common<FP4>(a, s, low) && high < 1e30f;
+    const bool fine = ok && common<FP4>(a, s, low) && high < 1e30f;
     if (__all_sync(0xffffffffu, fine || !in)) {
       const float r0 = PC ? 0.0f : rcp_approx(s * g[0]), rs = PC ? rcp_approx(s) : 0.0f;
 #pragma unroll
@@ -282,25 +301,44 @@ __device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat1
   for (int d = 0; d < (PC ? 4 : 1); ++d)
     g[d] = load_scale(p.a.v_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 4 * lane + d : kvh);
   float rg[4];
+  bool ok = true;
 #pragma unroll
-  for (int d = 0; d < (PC ? 4 : 1); ++d) rg[d] = short_rcp(g[d]);
+  for (int d = 0; d < (PC ? 4 : 1); ++d) {
+    rg[d] = rcp_approx(g[d]);
+    ok = ok && short_by(g[d]);
+  }
   const __nv_bfloat16* src = rows + 4 * lane - (int64_t)a * p.a.kv_stride;
   uint8_t* dst = slab + 4 * lane * kPage + off0;
 #pragma unroll
   for (int k = 0; k < U; k += 8) {
     uint2 x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      x[j] = k + j >= a && k + j < e ? __ldg(reinterpret_cast<const uint2*>(src + (int64_t)(k + j) * p.a.kv_stride))
-                                     : make_uint2(0, 0);
-    uint32_t w[4][2] = {};
+    uint32_t top = 0;   // the largest exponents and mantissas
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x4[4] = {bf16_lo(x[j].x), bf16_hi(x[j].x), bf16_lo(x[j].y), bf16_hi(x[j].y)};
-      float v[4];
-      quotients<4, PC>(x4, g, rg, v);
+      x[j] = k + j >= a && k + j < e ? __ldg(reinterpret_cast<const uint2*>(src + (int64_t)(k + j) * p.a.kv_stride))
+                                     : make_uint2(0, 0);
+      top = max_u16x2(top, max_u16x2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu));
+    }
+    // all below 2^60 (bf16 0x5D80)
+    const bool fine = ok && (top & 0xFFFFu) < 0x5D80u && (top >> 16) < 0x5D80u;
+    uint32_t w[4][2];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) w[d][j >> 2] |= code8<KV>(v[d]) << (8 * (j & 3));
+    for (int d = 0; d < 4; ++d) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint2& y = x[4 * h + j];
+          f[j] = d == 0 ? bf16_lo(y.x) : d == 1 ? bf16_hi(y.x) : d == 2 ? bf16_lo(y.y) : bf16_hi(y.y);
+          v[j] = quot(f[j], g[PC ? d : 0], rg[PC ? d : 0]);
+        }
+        if (!fine) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = any_quotient<KV>(f[j], g[PC ? d : 0]);
+        }
+        w[d][h] = codes4<KV>(v);
+      }
     }
     if (a <= k && k + 8 <= e) {
 #pragma unroll
@@ -393,7 +431,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) rope_q_kernel(const RopeParams
 
 // Everything in one launch (U = 8, few rows), or K and V (U = 32).
 template <int KV, bool PC, int U>
-__global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 3) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kernel(const RopeParams p) {
   constexpr int kBatch = U == 8 ? 4 : 2;   // heads whose rows are on the way at once
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
   if (g0 >= p.q_heads) {   // the rows of the cache
     const int page = page_at(p, m.b, m.u0, lane);
     if (page < 0) return;
-    const float s[1] = {load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0)}, rs[1] = {short_rcp(s[0])};
+    const float s[1] = {load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0)}, rs[1] = {rcp_approx(s[0])};
     for (int pos = m.lo; pos < m.hi; ++pos) {
       const int64_t t = m.row + (pos - m.lo);
       const __nv_bfloat16* src = p.a.k_new + t * p.a.kv_stride;
@@ -501,12 +539,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
         float f[8];
         if (k == 2 && turn) turn8(x[2], y, a, f);
         else plain8(x[k], f);
-        uint32_t w[2] = {0, 0};
-        float v[8];
-        quotients<8, false>(f, s, rs, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= code8<KV>(v[e]) << (8 * (e & 3));
-        *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * k)) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * k)) = codes8_of<KV, false>(f, s, rs, short_by(s[0]));
       }
     }
     return;
@@ -586,6 +619,7 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
   p.a.kv_heads = pr.kv_heads;
   p.a.scale_kind = pr.scale_kind;
   p.a.vec = 1;
+  p.k_scale16 = reinterpret_cast<uintptr_t>(a.k_scale) % 16 == 0;
   p.cos_sin = rope.cos_sin;
   p.positions = rope.positions;
   p.q = static_cast<const __nv_bfloat16*>(q);
