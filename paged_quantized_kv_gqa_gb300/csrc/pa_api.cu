@@ -98,10 +98,11 @@ static pa_status check_problem(const pa_problem& p) {
 }
 
 // ------------------------------------------------------------------ planner
-// Cost of an item of the expanded form in steps of a 128-row tile: its steps, what an item
+// Cost of an item of the expanded form in tenths of a microsecond, fitted to 40 plans of
+// five batches (within 15 % of their times): a step of two tiles or of one, what an item
 // starts and ends with, and the partial rows of a split one.
 static int64_t expanded_cost(int64_t positions, int rows, bool split) {
-  return ceil_div(positions, kExpandedTile) * (rows > 128 ? 2 : 1) + 3 + (split ? kExpandedSplit : 0);
+  return ceil_div(positions, kExpandedTile) * (rows > 128 ? 21 : 14) + (split ? 40 : 30);
 }
 
 // Chunk size of the expanded form where the planner chooses: of no split and sizes about
@@ -110,8 +111,7 @@ static int64_t expanded_cost(int64_t positions, int rows, bool split) {
 static int64_t expanded_chunk(const std::vector<std::pair<int64_t, int>>& tiles, int heads, int slots) {
   auto finish = [&](int64_t cs) -> int64_t {   // of the last CTA; -1: too many items to be worth it
     std::vector<std::pair<int64_t, int64_t>> costs;   // cost, items
-    int64_t n = 0;
-    bool any = false;
+    int64_t n = 0, merge = 0;   // (the merge reads 128 KB of partial rows an item)
     for (const auto& t : tiles) {
       const int64_t chunks = cs > 0 ? std::max<int64_t>(1, ceil_div(t.first, cs)) : 1;
       for (int64_t c = 0; c < chunks && t.first > 0; ++c) {
@@ -119,7 +119,7 @@ static int64_t expanded_chunk(const std::vector<std::pair<int64_t, int>>& tiles,
         costs.push_back({expanded_cost(len, t.second, chunks > 1), heads});
       }
       n += chunks * heads;
-      any = any || chunks > 1;
+      if (chunks > 1) merge += chunks * heads * (t.second > 128 ? 30 : 15);
       if (n > 24 * (int64_t)slots) return -1;
     }
     std::sort(costs.begin(), costs.end(), std::greater<std::pair<int64_t, int64_t>>());
@@ -133,7 +133,7 @@ static int64_t expanded_chunk(const std::vector<std::pair<int64_t, int>>& tiles,
         load.push(l);
         last = std::max(last, l);
       }
-    return last + (any ? kExpandedMerge : 0);
+    return last + (merge > 0 ? 41 + merge / 100 : 0);
   };
   int64_t best = 0, at = finish(0), longest = 0;
   for (const auto& t : tiles) longest = std::max(longest, t.first);
@@ -401,14 +401,15 @@ static pa_status build_plan(const pa_problem& prob, const int32_t* ql, const int
       cost[i] = ceil_div((int64_t)items[i * kItemWords + 6] - items[i * kItemWords + 5], B) + 2;
     std::vector<int> order(n);
     for (int i = 0; i < n; ++i) order[i] = i;
-    // Expanded rows: a step of a 128-row tile is the unit (a tile of few rows costs a whole
-    // one).  Heads go by blocks whose rows fit L2, longest first within a block; items of
+    // Expanded rows: heads go by blocks whose rows fit L2, longest first within a block; items of
     // less than a sixteenth of a CTA's share come behind all of them and even out the CTAs
     // (left in their blocks, the last block's long ones did not: 128 heads of four prompts
     // of 512-2048, the longest CTA 8 % above the mean, 1 % so).
     int64_t block_heads = prob.kv_heads, small = 0;
     if (P.expanded()) {
-      block_heads = std::max<int64_t>(1, kExpandedBlock / (std::max<int64_t>(P.kv_rows, 1) * 512));
+      // (few items a CTA: longest first throughout)
+      if (n > 8 * (int64_t)slots)
+        block_heads = std::max<int64_t>(1, kExpandedBlock / (std::max<int64_t>(P.kv_rows, 1) * 512));
       int64_t all = 0;
       for (int i = 0; i < n; ++i) {
         const int32_t* r = &items[(size_t)i * kItemWords];

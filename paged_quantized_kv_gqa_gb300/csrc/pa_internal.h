@@ -42,8 +42,6 @@ constexpr int kDecode4TileCost = 12;
 constexpr int kMergeClasses = 6;
 constexpr int kExpandPairTiles = 384;   // tiles of 256 rows from which CTA pairs expand
 constexpr int kExpandedTile = 128;   // positions of a step of the expanded form
-constexpr int kExpandedSplit = 3;    // what the partial rows of a split item cost, in steps
-constexpr int kExpandedMerge = 6;    // and the merge's launch
 // A block of heads that the expanded form's plans keep together: the bytes of its keys and
 // values, so that the tiles of a head find them in L2 (129 MB)
 constexpr int64_t kExpandedBlock = 48ll << 20;

@@ -57,7 +57,7 @@ def test_plans_are_a_function_of_their_inputs_and_balanced(pa):
     make = lambda: make_plan(pa, [2048, 900, 1700], [0, 0, 300], 128).describe()  # noqa: E731
     a, b = make(), make()
     assert (a["items"] == b["items"]).all() and (a["work_indptr"] == b["work_indptr"]).all()
-    cost = [-(-(k1 - k0) // 128) * (2 if n > 128 else 1) + 3 for _, _, _, n, _, k0, k1, _ in a["items"]]
+    cost = [-(-(k1 - k0) // 128) * (21 if n > 128 else 14) + 30 for _, _, _, n, _, k0, k1, _ in a["items"]]
     load = np.add.reduceat(cost, a["work_indptr"][:-1])
     assert load.max() <= load.mean() + max(cost)
 
