@@ -215,3 +215,34 @@ def test_on_another_stream_and_captured():
     g.replay()
     torch.cuda.synchronize()
     assert (d["cache_k"].cpu().numpy() == rh.expected(p)[1]).all()
+
+
+@pytest.mark.parametrize("kv_dtype", ["int8", "fp4_e2m1"])
+def test_pages_beyond_two_gigabytes(kv_dtype):
+    """The last pages of a pool of 4 GB and more a side: the same stored values as in a
+    small pool."""
+    import paged_quantized_kv_gqa_gb300 as pa
+    p = rh.make(seed=16, seq_lens=[70, 3], seq_lens_kv=[0, 61], q_heads=8, kv_heads=8, kv_dtype=kv_dtype)
+    got = []
+    for pages in (p.num_pages, 140_000 if kv_dtype == "fp4_e2m1" else 70_000):
+        prob = pa.make_problem(bsz=p.bsz, q_heads=8, kv_heads=8, head_dim_qk=128, head_dim_v=128, block_size=64,
+                               max_blocks_per_seq=p.max_blocks_per_seq, num_pages=pages, kv_dtype=kv_dtype,
+                               scale_kind="per_kv_head", layout="gqa", causal=True, chunk_size=0, sm_scale=0.1, q_stride=1024)
+        plan = pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, num_sms())
+        caches = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in pa.pa_cache_bytes(prob)]
+        table = torch.from_numpy(np.where(p.block_table < 0, -1, pages - 1 - p.block_table).astype(np.int32)).cuda()
+        lens = [torch.from_numpy(x).cuda() for x in (p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q)]
+        scales = [dev(p.k_scale), dev(p.v_scale)]
+        args = pa.make_args(q=None, cache_k=caches[0], cache_v=caches[1], k_scale=scales[0], v_scale=scales[1],
+                            block_table=table, out=None, seq_lens=lens[0], seq_lens_kv=lens[1], cu_seqlens_q=lens[2])
+        ws = torch.zeros(max(plan.workspace_size, 256), dtype=torch.uint8, device="cuda")
+        pa.pa_plan_upload(plan, ws)
+        r = pa.make_rope(cos_sin=torch.from_numpy(p.table).cuda(), table_rows=p.table_rows, rot_dim=128)
+        k, v = dev(p.k_new.reshape(p.total_q, -1)), dev(p.v_new.reshape(p.total_q, -1))
+        pa.pa_rope_append(plan, args, r, None, 0, None, 0, k, v, 1024, ws)
+        rows = [torch.zeros(p.total_q, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        pa.pa_cache_read(plan, args, *rows, 1024, ws)
+        assert pa.pa_check(plan, ws)[0] == 0
+        got.append(rows)
+        del caches
+    assert got[1][0].abs().sum() > 0 and all(torch.equal(a, b) for a, b in zip(*got))
