@@ -131,6 +131,14 @@ def _check(status: int):
         raise PaError(status, lib.pa_last_error().decode(errors="replace"))
 
 
+def _i32(x, what: str) -> int:
+    """A number that fits the C argument (ctypes would cut it to 32 bits)."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise OverflowError(f"{what} = {x} does not fit 32 bits")
+    return x
+
+
 def _ptr(x) -> Optional[int]:
     if x is None:
         return None
@@ -340,7 +348,7 @@ def make_rope(*, cos_sin, table_rows, rot_dim, pairs="halves", positions=None, a
         raise ValueError("an axis is a small non-negative number")
     r.tensors = [t for t in (cos_sin, positions) if hasattr(t, "data_ptr")]
     r.cos_sin, r.positions = _ptr(cos_sin), _ptr(positions)
-    r.table_rows, r.rot_dim, r.axes = table_rows, rot_dim, axes
+    r.table_rows, r.rot_dim, r.axes = _i32(table_rows, "table_rows"), _i32(rot_dim, "rot_dim"), _i32(axes, "axes")
     r.pairs = ROPE_PAIRS[pairs] if isinstance(pairs, str) else pairs
     r.pair_axis[:len(pair_axes)] = pair_axes
     return r
@@ -359,24 +367,25 @@ def pa_mla_absorb(rows: int, heads: int, q, q_stride: int, w, w_head_stride: int
                   stream=None):
     """Queries [rows][heads][128 + 64] into the latent space, [rows][heads][512 + 64]
     (see include/pa.h; workspace: a status block of PA_STATUS_BYTES or more)."""
-    _check(lib.pa_mla_absorb(int(rows), int(heads), _ptr(q), int(q_stride), _ptr(w), int(w_head_stride), _ptr(out),
-                             int(out_stride), _ptr(workspace), _stream(stream)))
+    _check(lib.pa_mla_absorb(_i32(rows, "rows"), _i32(heads, "heads"), _ptr(q), int(q_stride), _ptr(w),
+                             int(w_head_stride), _ptr(out), int(out_stride), _ptr(workspace), _stream(stream)))
 
 
 def pa_mla_project(rows: int, heads: int, o, o_stride: int, w, w_head_stride: int, out, out_stride: int, workspace,
                    stream=None):
     """Latent outputs [rows][heads][512] out of the latent space, [rows][heads][128]
     (see include/pa.h; w: the first W_v row of head 0)."""
-    _check(lib.pa_mla_project(int(rows), int(heads), _ptr(o), int(o_stride), _ptr(w), int(w_head_stride), _ptr(out),
-                              int(out_stride), _ptr(workspace), _stream(stream)))
+    _check(lib.pa_mla_project(_i32(rows, "rows"), _i32(heads, "heads"), _ptr(o), int(o_stride), _ptr(w),
+                              int(w_head_stride), _ptr(out), int(out_stride), _ptr(workspace), _stream(stream)))
 
 
 def pa_mla_expand(rows: int, heads: int, c, c_stride: int, w, w_head_stride: int, k_out, v_out, kv_stride: int,
                   workspace, stream=None):
     """Keys and values [rows][heads][128] of every head from latent rows [rows][512]
     (see include/pa.h)."""
-    _check(lib.pa_mla_expand(int(rows), int(heads), _ptr(c), int(c_stride), _ptr(w), int(w_head_stride), _ptr(k_out),
-                             _ptr(v_out), int(kv_stride), _ptr(workspace), _stream(stream)))
+    _check(lib.pa_mla_expand(_i32(rows, "rows"), _i32(heads, "heads"), _ptr(c), int(c_stride), _ptr(w),
+                             int(w_head_stride), _ptr(k_out), _ptr(v_out), int(kv_stride), _ptr(workspace),
+                             _stream(stream)))
 
 
 def pa_mla_prefill(plan: Plan, args: PaArgs, k_nope, v, kv_stride: int, k_rope, rope_stride: int, workspace,

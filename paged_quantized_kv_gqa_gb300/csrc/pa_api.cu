@@ -114,13 +114,13 @@ static int64_t expanded_chunk(const std::vector<std::pair<int64_t, int>>& tiles,
     int64_t n = 0, merge = 0;   // (the merge reads 128 KB of partial rows an item)
     for (const auto& t : tiles) {
       const int64_t chunks = cs > 0 ? std::max<int64_t>(1, ceil_div(t.first, cs)) : 1;
+      n += chunks * heads;
+      if (n > 24 * (int64_t)slots) return -1;
       for (int64_t c = 0; c < chunks && t.first > 0; ++c) {
         const int64_t len = chunks > 1 ? std::min(t.first, (c + 1) * cs) - c * cs : t.first;
         costs.push_back({expanded_cost(len, t.second, chunks > 1), heads});
       }
-      n += chunks * heads;
       if (chunks > 1) merge += chunks * heads * (t.second > 128 ? 30 : 15);
-      if (n > 24 * (int64_t)slots) return -1;
     }
     std::sort(costs.begin(), costs.end(), std::greater<std::pair<int64_t, int64_t>>());
     std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> load;

@@ -40,7 +40,10 @@ constexpr int kDecode4TileCost = 12;
 // the merge's classes of 4-bit rows: 32, 16, 8, 4, 2, 1 warps a row, for more than 128,
 // 64, 32, 16, 8 chunks and the others
 constexpr int kMergeClasses = 6;
-constexpr int kExpandPairTiles = 384;   // tiles of 256 rows from which CTA pairs expand
+// Tiles of 256 rows and a head from which CTA pairs expand (pa_mla_expand.cu; below, a CTA a
+// tile of 128 rows): at 256 tiles (333 rows, 128 heads) 22.8 us against 18.9, at 512 (1024
+// rows, 128 heads; 8192 rows, 16) 33.2 against 43.3 and 31.2 against 41.8
+constexpr int kExpandPairTiles = 384;
 constexpr int kExpandedTile = 128;   // positions of a step of the expanded form
 // A block of heads that the expanded form's plans keep together: the bytes of its keys and
 // values, so that the tiles of a head find them in L2 (129 MB)

@@ -185,10 +185,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (!ok && lane == 0) raise(t);
-      if (elect_one()) tc_commit_pair(drain);   // every MMA issued completes before TMEM is released
+      // every MMA issued completes before TMEM is released (in both CTAs: CTA 1 leaves behind
+      // the cluster barrier)
+      if (elect_one()) tc_commit_pair(drain);
       __syncwarp();
+      mbar_wait(drain, 0, kDrainNs);
     }
-    mbar_wait(drain, 0, kDrainNs + (uint64_t)p.wait_limit_ns);
   } else {
     // ================================================================ epilogue (both CTAs)
     // warps 0-3 the keys' 128 columns, 4-7 the values', 32 rows each (4 warps for all 256

@@ -61,3 +61,10 @@ def test_expand_wants_both_outputs_and_whole_heads(pa):
 @pytest.mark.parametrize("op", ["absorb", "project", "expand"])
 def test_no_rows_is_no_work(pa, op):
     call(pa, op, rows=0, x=None, out=None, out2=None)
+
+
+@pytest.mark.parametrize("op", ["absorb", "project", "expand"])
+@pytest.mark.parametrize("kw", [dict(rows=1 << 32), dict(heads=(1 << 31) + 1)])
+def test_sizes_beyond_the_argument(pa, op, kw):
+    with pytest.raises(OverflowError):
+        call(pa, op, **kw)
