@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = odone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_any = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
+  volatile int* s_done = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8);   // S steps of tile A that are there
   const uint32_t s_base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int begin = p.work_indptr[blockIdx.x], end = p.work_indptr[blockIdx.x + 1];
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&drain[x], 1);
     }
     *abort_any = 0;
+    *s_done = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
@@ -312,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t due_g = 0, g = 0;
     int due_valid = 0;
     bool due = false, due_first = false, due_last = false;
+    int s_of_a = 0;   // S steps of tile A up to this one
     auto flush = [&]() {
       if (due) issue_pv(due_g, due_valid, due_first, due_last);
       due = false;
@@ -323,8 +326,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it + 1 < end) nxt = work_at(it + 1);
       const int steps = x ? w.nt[1] : w.nt[0];
       for (int i = 0; i < w.n && ok; ++i, ++g) {
+        s_of_a += i < w.nt[0];
         if (i < steps) {
           flush();
+          if (x == 1 && i < w.nt[0]) {
+            // Tile B's S of a step behind A's: left to themselves the two warps' MMAs share the
+            // tensor cores in step, both softmaxes wait for them, and then they for both (38
+            // heads of 2048 tokens and 8192 rows 262 us, so 237; taking turns at PV and S both
+            // was slower).  A pace, not a dependence: a count, as a barrier's parity could be
+            // missed.
+            const uint64_t t0 = globaltimer();
+            while (ok && *s_done < s_of_a) ok = !*abort_any && globaltimer() - t0 <= limit;
+          }
           if (ok) issue_s(g, i == 0, i + 1 == steps);
           due = true;
           due_g = g;
@@ -376,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        if (tid == 0) *s_done = (int)n + 1;
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v + 32 * c);
