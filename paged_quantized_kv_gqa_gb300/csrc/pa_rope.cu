@@ -25,9 +25,10 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kWarps = 8;
-// positions of a rotation warp's unit: queries alone, and everything else (a warp with all
-// heads of two rows reads their cos and sin once; in units of 8 rows and 2 of 8 heads, to
-// have as many warps, K and V of 35k rows, FP4, took 94 us)
+// Positions of a rotation warp's unit: of many rows, and of few (and latent rows), where
+// more warps count.  A warp has all heads of a row, or 8, and reads its cos and sin once (K
+// and V of 35k rows, FP4: units of 8 rows and 2 of 8 heads, to have as many warps, 94 us, of
+// 2 rows and all heads 71, of 8 rows and all heads 67).
 constexpr int kQUnit = 8, kRopeUnit = 2;
 constexpr int kMlaRow = 576, kMlaLatent = 512, kMlaQ = 192, kMlaNope = 128;
 
@@ -433,6 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) rope_q_kernel(const RopeParams
 template <int KV, bool PC, int U>
 __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kernel(const RopeParams p) {
   constexpr int kBatch = U == 8 ? 4 : 2;   // heads whose rows are on the way at once
+  constexpr int kUnit = U == 8 ? kRopeUnit : kQUnit;
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
   constexpr int kSlabBytes = is_four<KV>() ? kV4Slab : kPage * kV4Dim;
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kerne
   const uint32_t bu = id / (uint32_t)p.groups;
   const int g0 = (int)(id - bu * p.groups) * p.group_heads;
   const int heads = p.q_heads + p.a.kv_heads, g1 = min(heads, g0 + p.group_heads);
-  if (!unit_at<kRopeUnit>(p, p.units, bu, lane, m)) return;
+  if (!unit_at<kUnit>(p, p.units, bu, lane, m)) return;
   const int page = g1 > p.q_heads ? page_at(p, m.b, m.u0, lane) : -1;
   const int c = lane & 15, oct = p.rot / 8;
   const bool turned = c < oct;
@@ -660,8 +662,9 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
     if (e != cudaSuccess) return e;
     p.q_heads = 0;
   }
-  p.units = row_units<kRopeUnit>(pr.bsz, plan.max_q, plan.total_q);
-  if (!share(p.q_heads + (mla ? 0 : pr.kv_heads), mla ? 8 : 4)) return cudaErrorInvalidValue;
+  p.units = mla || small ? row_units<kRopeUnit>(pr.bsz, plan.max_q, plan.total_q)
+                         : row_units<kQUnit>(pr.bsz, plan.max_q, plan.total_q);
+  if (!share(p.q_heads + (mla ? 0 : pr.kv_heads), mla || !small ? 8 : 4)) return cudaErrorInvalidValue;
   if (mla) {
     const dim3 grid((p.rot_warps + kWarps - 1) / kWarps), block(kWarps * 32);
     if (pr.kv_dtype == PA_KV_FP8_E4M3) rope_latent_kernel<PA_KV_FP8_E4M3><<<grid, block, 0, stream>>>(p);
