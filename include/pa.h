@@ -365,7 +365,8 @@ typedef struct pa_rope {
  * pa_rope_append: the step before pa_run in one launch.  Rotates the new tokens'
  * queries into q_out and does what pa_cache_append does with their keys and values, the
  * keys rotated first: stored K = Q(k' / s) of the rotated binary32 values k' (no rounding
- * to bf16 between), V as pa_cache_append writes it.
+ * to bf16 between), V as pa_cache_append writes it.  A NaN is stored as 0 (int8, 4 bits)
+ * or as E4M3's NaN, infinities saturate.
  *   q_new, q_out: device bf16, token rows q_stride / q_out_stride elements apart, head h
  *   at h * 128 (GQA) or h * 192 (MLA: 128 dims, then 64 of which rot_dim turn) within
  *   a row; q_out == q_new with equal strides rotates in place, other overlaps are not

@@ -16,7 +16,8 @@ def project(o, w):
 
 def expand(c, w):
     """c [n, 512] -> keys and values [n, heads, 128]."""
-    return np.einsum("nc,hdc->nhd", c, w[:, :128]), np.einsum("nc,hdc->nhd", c, w[:, 128:])
+    y = (c @ w.reshape(-1, w.shape[2]).T).reshape(len(c), len(w), 256)
+    return y[..., :128], y[..., 128:]
 
 
 def prefill(q, k, v, k_rope, q_lens, kv_lens, mask, sm_scale):

@@ -15,7 +15,8 @@ from .formats import bf16_to_f64
 
 
 def _fl(x):
-    return x.astype(np.float32).astype(np.float64)
+    with np.errstate(over="ignore"):
+        return x.astype(np.float32).astype(np.float64)
 
 
 def turned(x, first, table, positions, pair_axis, pairs):
@@ -28,14 +29,18 @@ def turned(x, first, table, positions, pair_axis, pairs):
         a, b = (first + i, first + i + n) if pairs == "halves" else (first + 2 * i, first + 2 * i + 1)
         row = table[positions[pair_axis[i]]].astype(np.float64)
         c, s = row[:, i, None], row[:, n + i, None]
-        y[:, :, a] = _fl(_fl(x[:, :, a] * c) - _fl(x[:, :, b] * s))
-        y[:, :, b] = _fl(_fl(x[:, :, b] * c) + _fl(x[:, :, a] * s))
+        with np.errstate(invalid="ignore"):            # infinities of a pair
+            y[:, :, a] = _fl(_fl(x[:, :, a] * c) - _fl(x[:, :, b] * s))
+            y[:, :, b] = _fl(_fl(x[:, :, b] * c) + _fl(x[:, :, a] * s))
     return y
 
 
 def _codes8(x, s, kind):
+    """A NaN becomes E4M3's NaN, and 0 as int8."""
     q = x.astype(np.float32) / s
-    return ca.e4m3_encode(q) if kind == "fp8_e4m3" else ca.int8_encode(q)
+    lost, q = np.isnan(q), np.where(np.isnan(q), np.float32(0), q)
+    codes = ca.e4m3_encode(q) if kind == "fp8_e4m3" else ca.int8_encode(q)
+    return np.where(lost, np.uint8(0x7F if kind == "fp8_e4m3" else 0), codes)
 
 
 def append(p, k, v_bits, cache_k, cache_v):

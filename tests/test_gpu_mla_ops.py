@@ -94,9 +94,21 @@ def test_many_rows(op):
     check(op, 1500, 5, pad=64)
 
 
-@pytest.mark.parametrize("op", ["absorb", "project", "expand"])
-def test_a_rows_nan_stays_its_own(op):
-    heads, rows = 2, 140
+# sizes whose tiles CTA pairs take: blocks of 256 rows, whole and ragged, times heads
+PAIRS = [(257, 192), (300, 200), (769, 96), (1025, 77), (5000, 20), (12300, 8), (33000, 3)]
+
+
+@pytest.mark.parametrize("rows, heads", PAIRS)
+def test_expand_by_pairs(rows, heads):
+    check("expand", rows, heads, pad=8)
+
+
+def test_expand_by_pairs_with_weights_apart():
+    check("expand", 600, 130, w_pad=64, pad=64)
+
+
+@pytest.mark.parametrize("op, rows, heads", [("absorb", 140, 2), ("project", 140, 2), ("expand", 140, 2), ("expand", 300, 192)])
+def test_a_rows_nan_stays_its_own(op, rows, heads):
     shape = {"absorb": (rows, heads, 192), "project": (rows, heads, 512), "expand": (rows, 512)}[op]
     x = randn(5, *shape)
     w = randn(6, heads, 256, 512, scale=0.05)
@@ -110,28 +122,27 @@ def test_a_rows_nan_stays_its_own(op):
         assert torch.equal(a[others], b[others]) and b[7].isnan().any()
 
 
-@pytest.mark.parametrize("op", ["absorb", "project", "expand"])
-def test_the_same_call_gives_the_same_bits_on_any_stream(op):
-    a = run(op, 300, 4)[2]
-    b = run(op, 300, 4, stream=torch.cuda.Stream())[2]
+@pytest.mark.parametrize("op, heads", [("absorb", 4), ("project", 4), ("expand", 4), ("expand", 200)])
+def test_the_same_call_gives_the_same_bits_on_any_stream(op, heads):
+    a = run(op, 300, heads)[2]
+    b = run(op, 300, heads, stream=torch.cuda.Stream())[2]
     assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
-@pytest.mark.parametrize("op", ["absorb", "project", "expand"])
-def test_a_missing_load_is_reported_and_the_next_call_works(op):
+@pytest.mark.parametrize("op, rows, heads", [("absorb", 40, 2), ("project", 40, 2), ("expand", 40, 2), ("expand", 300, 192)])
+def test_a_missing_load_is_reported_and_the_next_call_works(op, rows, heads):
     import paged_quantized_kv_gqa_gb300 as pa
     pa.pa_debug_set_faults(wait_limit_ns=2_000_000, skip_first_load=True)
     try:
-        assert run(op, 40, 2)[3] == pa.PA_ERR_DEVICE_TIMEOUT
+        assert run(op, rows, heads)[3] == pa.PA_ERR_DEVICE_TIMEOUT
     finally:
         pa.pa_debug_set_faults()
-    check(op, 40, 2)
+    check(op, rows, heads)
 
 
-@pytest.mark.parametrize("op", ["absorb", "project", "expand"])
-def test_captured(op):
+@pytest.mark.parametrize("op, rows, heads", [("absorb", 50, 2), ("project", 50, 2), ("expand", 50, 2), ("expand", 300, 192)])
+def test_captured(op, rows, heads):
     import paged_quantized_kv_gqa_gb300 as pa
-    heads, rows = 2, 50
     w = randn(8, heads, 256, 512, scale=0.05).cuda()
     shape = {"absorb": (rows, heads * 192), "project": (rows, heads * 512), "expand": (rows, 512)}[op]
     x = randn(9, *shape).cuda()

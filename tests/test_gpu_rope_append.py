@@ -15,7 +15,7 @@ def dev(bits):
     return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).cuda()
 
 
-def launch(p, *, q=True, in_place=False, packed=False, pad=0, rows=None, stream=None):
+def launch(p, *, q=True, in_place=False, packed=False, pad=0, rows=None, stream=None, sms=None):
     """Runs the call; returns (q_out bits, cache_k, cache_v, status, detail)."""
     import paged_quantized_kv_gqa_gb300 as pa
     T, mla = rows or p.total_q, p.layout == "mla"
@@ -37,7 +37,7 @@ def launch(p, *, q=True, in_place=False, packed=False, pad=0, rows=None, stream=
     prob = pa.make_problem(**{k: getattr(p, k) for k in (
         "bsz", "q_heads", "kv_heads", "head_dim_qk", "head_dim_v", "block_size", "max_blocks_per_seq", "num_pages", "kv_dtype",
         "scale_kind", "layout", "chunk_size", "sm_scale", "q_stride", "causal")})
-    plan = pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, num_sms())
+    plan = pa.pa_plan(prob, p.seq_lens, p.seq_lens_kv, p.cu_seqlens_q, sms or num_sms())
     ws = torch.zeros(max(plan.workspace_size, 256), dtype=torch.uint8, device="cuda")
     pa.pa_plan_upload(plan, ws)
     args = pa.make_args(q=None, cache_k=d["cache_k"], cache_v=d["cache_v"], k_scale=d["k_scale"], v_scale=d["v_scale"],
@@ -123,11 +123,53 @@ def test_far_values(kv_dtype, spread):
     check(rh.make(seed=8, seq_lens=[12], seq_lens_kv=[60], kv_dtype=kv_dtype, scale_kind="per_channel", spread=spread))
 
 
+# A plan for few SMs takes the launches of large calls (queries by themselves, units of 8
+# rows of K and 32 positions of V) at sizes that the oracle can follow
 @pytest.mark.parametrize("kv_dtype", rh.FORMATS)
-def test_many_rows(kv_dtype):
-    """Enough rows for the launch of large calls (units of 32 positions of V, groups of 16 heads)."""
-    p = rh.make(seed=9, seq_lens=[700, 1, 350], seq_lens_kv=[13, 64, 0], q_heads=28, kv_heads=14, kv_dtype=kv_dtype)
-    check(p)
+@pytest.mark.parametrize("scale_kind", ["per_kv_head", "per_channel", "global"])
+def test_many_rows(kv_dtype, scale_kind):
+    check(rh.make(seed=9, seq_lens=[170, 1, 0, 75], seq_lens_kv=[13, 64, 3, 0], q_heads=28, kv_heads=14, kv_dtype=kv_dtype,
+                  scale_kind=scale_kind), sms=2)
+
+
+@pytest.mark.parametrize("pairs", ["halves", "adjacent"])
+@pytest.mark.parametrize("rot, axes", [(128, 1), (80, 3), (64, 2)])
+def test_many_rows_of_several_axes(rot, axes, pairs):
+    check(rh.make(seed=20, seq_lens=[99, 40], seq_lens_kv=[60, 1], q_heads=21, kv_heads=3, kv_dtype="int4", rot=rot, axes=axes,
+                  pairs=pairs, table_rows=400), sms=1)
+
+
+@pytest.mark.parametrize("kw", [dict(q=False), dict(in_place=True), dict(packed=True, pad=16), dict(packed=True, in_place=True)])
+def test_many_rows_in_place_packed_or_without_queries(kw):
+    check(rh.make(seed=21, seq_lens=[130, 7], seq_lens_kv=[31, 0], q_heads=10, kv_heads=5, kv_dtype="int8"), sms=1, **kw)
+
+
+@pytest.mark.parametrize("kv_dtype", rh.FORMATS)
+@pytest.mark.parametrize("spread", [1e-3, 30.0, 1e30])
+def test_many_rows_of_far_values(kv_dtype, spread):
+    check(rh.make(seed=22, seq_lens=[150], seq_lens_kv=[60], kv_heads=4, kv_dtype=kv_dtype, scale_kind="per_channel",
+                  spread=spread), sms=1)
+
+
+@pytest.mark.parametrize("sms", [None, 1])
+@pytest.mark.parametrize("kv_dtype", rh.FORMATS)
+def test_not_numbers(kv_dtype, sms):
+    """NaN and infinities in rows: every other block, and row, as without them; int8 and 4 bits
+    store a NaN as 0, E4M3 as its NaN (0x7F), and infinities saturate."""
+    import paged_quantized_kv_gqa_gb300 as pa
+    p = rh.make(seed=23, seq_lens=[140], seq_lens_kv=[3], q_heads=2, kv_heads=2, kv_dtype=kv_dtype)
+    p.k_new, p.v_new, p.q_new = p.k_new.copy(), p.v_new.copy(), p.q_new.copy()
+    clean = launch(p, sms=sms)
+    for x in (p.k_new, p.v_new, p.q_new):
+        x[5, 0, 3] = 0x7FC0
+        x[77, 1, 100] = 0x7F80
+        x[78, 1, 101] = 0xFF80
+    got = launch(p, sms=sms)
+    assert got[3] == pa.PA_OK
+    rows = [r for r in range(140) if r not in (5, 77, 78)]
+    assert (got[0][rows] == clean[0][rows]).all()
+    q, want_k, want_v = rh.expected(p)
+    assert (got[1] == want_k).all() and (got[2] == want_v).all()
 
 
 def test_many_latent_rows():
