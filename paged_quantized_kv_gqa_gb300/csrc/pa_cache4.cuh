@@ -27,9 +27,9 @@
 // not a normal E4M3 number or is saturated, infinities, NaN) go position by
 // position with divisions.  Where the range covers a unit in part, the nibbles of
 // other positions stay (one warp owns a unit, so nobody else writes its bytes).
-// What bounds it: 2.56 bytes per element against 13 instructions per element and
-// lane: 31k rows of 8 heads in 40.4 us (int4) or 38.4 (FP4), 4.0 and 4.2 TB/s; with
-// per-channel scales 64.  (Requesting the next rows before the current ones are worked
+// What bounds it: 2.56 bytes per element against the quantiser's instructions (quotients by
+// pairs): 31k rows of 8 heads in 40.3 us (int4) or 37.1 (FP4), 4.0 and 4.4 TB/s; with
+// per-channel scales 69 and 62.  (Requesting the next rows before the current ones are worked
 // on spills, and gained nothing.)  That is for blocks of the common range.  A block whose
 // max |x / g| is below M / 64 (its scale is subnormal, or 0 for a block of zeros) sends
 // the four K rows or the V unit that hold it through the divisions: the same rows times
@@ -83,8 +83,41 @@ __device__ __forceinline__ float quot(float x, float d, float r) {
   return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
 }
 
+// Pairs of binary32 numbers, an operation of each rounded by itself.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// quot() of a pair
+__device__ __forceinline__ float2 quot2(float2 x, float2 d, float2 r) {
+  const float2 q = mul2(x, r);
+  return fma2(fma2(q, make_float2(-d.x, -d.y), x), r, q);
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ float2 bf16_2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
 template <int FP4>
 struct Fmt {
@@ -236,7 +269,10 @@ __device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloa
         for (int i = 0; i < 2; ++i) {
           y[i] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[i] = fmaxf(y[i], fabsf(quot(f[i][e], g[e], rg[e])));
+          for (int e = 0; e < 8; e += 2) {
+            const float2 v = quot2(make_float2(f[i][e], f[i][e + 1]), make_float2(g[e], g[e + 1]), make_float2(rg[e], rg[e + 1]));
+            y[i] = fmaxf(y[i], fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
         }
         const float t = (lane & 1) ? y[0] : y[1];
         a = fmaxf((lane & 1) ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, t, 1));
@@ -253,7 +289,13 @@ __device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloa
           const float ri = __shfl_sync(0xffffffffu, rs, (lane & ~1) | i);
           float q[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q[e] = PC ? quot(f[i][e], si * g[e], ri * rg[e]) : quot(f[i][e], si, ri);
+          for (int e = 0; e < 8; e += 2) {
+            const float2 s2 = make_float2(si, si), r2 = make_float2(ri, ri);
+            const float2 v = quot2(make_float2(f[i][e], f[i][e + 1]), PC ? mul2(s2, make_float2(g[e], g[e + 1])) : s2,
+                                   PC ? mul2(r2, make_float2(rg[e], rg[e + 1])) : r2);
+            q[e] = v.x;
+            q[e + 1] = v.y;
+          }
           if (in(base + 4 * h + 2 * i + r0))
             *reinterpret_cast<uint32_t*>(codes + (base + 4 * h + 2 * i) * (kV4Dim / 2)) = pack8<FP4>(q);
         }
@@ -320,7 +362,10 @@ __device__ __forceinline__ void write_v(const Append4Params& p, const __nv_bfloa
         for (int j = 0; j < 4; ++j) {
           y[j] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[j] = fmaxf(y[j], fabsf(quot(f[j][e], g[e], rg[e])));
+          for (int e = 0; e < 4; e += 2) {
+            const float2 v = quot2(make_float2(f[j][e], f[j][e + 1]), make_float2(g[e], g[e + 1]), make_float2(rg[e], rg[e + 1]));
+            y[j] = fmaxf(y[j], fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
           y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 1));
           y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 2));
         }
@@ -337,9 +382,14 @@ __device__ __forceinline__ void write_v(const Append4Params& p, const __nv_bfloa
       for (int j = 0; j < 4; ++j) {
         const float sj = __shfl_sync(0xffffffffu, st, (lane & ~3) | j);
         const float rj = __shfl_sync(0xffffffffu, rs, (lane & ~3) | j);
+        const float2 s2 = make_float2(sj, sj), r2 = make_float2(rj, rj);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          q[e][4 * h + j] = PC ? quot(f[j][e], sj * g[e], rj * rg[e]) : quot(f[j][e], sj, rj);
+        for (int e = 0; e < 4; e += 2) {
+          const float2 v = quot2(make_float2(f[j][e], f[j][e + 1]), PC ? mul2(s2, make_float2(g[e], g[e + 1])) : s2,
+                                 PC ? mul2(r2, make_float2(rg[e], rg[e + 1])) : r2);
+          q[e][4 * h + j] = v.x;
+          q[e + 1][4 * h + j] = v.y;
+        }
       }
       if (mine_in) scales[8 * k + 4 * h] = (uint8_t)sb;
     }

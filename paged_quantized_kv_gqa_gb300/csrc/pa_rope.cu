@@ -18,6 +18,9 @@
 // dims of all the unit's positions, whose bytes gather in registers.
 // MLA: 8 lanes hold the 64 rotated dims of a head, 4 query heads a step; a latent row is
 // one warp's.
+#include <algorithm>
+#include <cmath>
+
 #include "pa_cache4.cuh"
 
 namespace pa {
@@ -26,11 +29,13 @@ namespace {
 constexpr int kPage = 64;
 constexpr int kWarps = 8;
 // Positions of a rotation warp's unit: of many rows, and of few (and latent rows), where
-// more warps count.  A warp has all heads of a row, or 8, and reads its cos and sin once (K
-// and V of 35k rows, FP4: units of 8 rows and 2 of 8 heads, to have as many warps, 94 us, of
-// 2 rows and all heads 71, of 8 rows and all heads 67).
+// more warps count.  A warp has all heads of a row, or 8 to 16, and reads its cos and sin
+// once (K and V of 35k rows, FP4: units of 8 rows and 2 of 8 heads, to have as many warps,
+// 94 us, of 2 rows and all heads 66, of 4 62, of 8 60; K's warps among V's instead of before
+// them 76: theirs are the long ones).
 constexpr int kQUnit = 8, kRopeUnit = 2;
-constexpr int kMlaRow = 576, kMlaLatent = 512, kMlaQ = 192, kMlaNope = 128;
+constexpr int kQCtas = 4;   // CTAs an SM of the queries' kernel
+constexpr int kMlaRow = 576, kMlaQ = 192, kMlaNope = 128;
 
 struct RopeParams {
   Append4Params a;             // the rows, cache, scales and lengths (units, total: the V warps')
@@ -45,8 +50,9 @@ struct RopeParams {
   int32_t q_heads;             // 0 without queries
   int32_t table_rows, rot, adjacent, axes, quads;   // quads: four neighbouring pairs share an axis
   int32_t total_q;
-  int32_t k_scale16;           // per-channel K scales are 16-byte aligned
+  int32_t k_scale16, v32;      // per-channel K scales are 16-byte, cache_v 32-byte aligned
   uint32_t pair_axis[4];       // two bits a pair
+  float neg_zero;              // -0, unknown to the compiler (turn8)
 };
 
 __device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
@@ -56,7 +62,7 @@ __device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
 
 // cos and sin (signed for its place in the pair) of a lane's 8 dims
 struct Turn {
-  float c[8], s[8];
+  float2 c[4], s[4];
 };
 
 // Fills `a` for dims 8 o .. 8 o + 7 of a rotated width of p.rot in row t at position
@@ -107,40 +113,33 @@ __device__ __forceinline__ bool load_turn(const RopeParams& p, int64_t t, int po
   }
   if (p.adjacent) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a.c[e] = c[e >> 1];
-      a.s[e] = (e & 1) ? s[e >> 1] : -s[e >> 1];
+    for (int e = 0; e < 4; ++e) {
+      a.c[e] = make_float2(c[e], c[e]);
+      a.s[e] = make_float2(-s[e], s[e]);
     }
   } else {
     const bool lower = 8 * o < half;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a.c[e] = c[e];
-      a.s[e] = lower ? -s[e] : s[e];
+    for (int e = 0; e < 4; ++e) {
+      a.c[e] = make_float2(c[2 * e], c[2 * e + 1]);
+      a.s[e] = make_float2(lower ? -s[2 * e] : s[2 * e], lower ? -s[2 * e + 1] : s[2 * e + 1]);
     }
   }
   return true;
 }
 
-// The rotated values of a lane's 8 dims x (bf16), y the other dims of their pairs, in
-// place.  (As f32x2 instructions, mul.rn and add.rn came out fused now and then: results a
-// last place off.)
-__device__ __forceinline__ void turn8(const uint4& x, const uint4& y, const Turn& a, float (&f)[8]) {
+// The rotated values of a lane's 8 dims x (bf16), y the other dims of their pairs.  The
+// products are multiply-adds of p.neg_zero, -0: mul.rn.f32x2 and add.rn.f32x2 came out fused
+// now and then, results a last place off.
+__device__ __forceinline__ void turn8(const RopeParams& p, const uint4& x, const uint4& y, const Turn& a, float2 (&f)[4]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+  const float2 nz = make_float2(p.neg_zero, p.neg_zero);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __fadd_rn(__fmul_rn(bf16_lo(w[k]), a.c[2 * k]), __fmul_rn(bf16_lo(v[k]), a.s[2 * k]));
-    f[2 * k + 1] = __fadd_rn(__fmul_rn(bf16_hi(w[k]), a.c[2 * k + 1]), __fmul_rn(bf16_hi(v[k]), a.s[2 * k + 1]));
-  }
+  for (int k = 0; k < 4; ++k) f[k] = add2(fma2(bf16_2(w[k]), a.c[k], nz), fma2(bf16_2(v[k]), a.s[k], nz));
 }
 
-__device__ __forceinline__ void plain8(const uint4& x, float (&f)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = bf16_lo(w[k]);
-    f[2 * k + 1] = bf16_hi(w[k]);
-  }
+__device__ __forceinline__ void plain8(const uint4& x, float2 (&f)[4]) {
+  f[0] = bf16_2(x.x), f[1] = bf16_2(x.y), f[2] = bf16_2(x.z), f[3] = bf16_2(x.w);
 }
 
 __device__ __forceinline__ uint4 shfl4(const uint4& x, int lane) {
@@ -156,8 +155,9 @@ __device__ __forceinline__ uint4 partners(const RopeParams& p, const uint4& x, i
   return shfl4(x, from);
 }
 
-__device__ __forceinline__ uint4 bf16x8_of(const float (&f)[8]) {
-  return make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
+__device__ __forceinline__ uint4 bf16x8_of(const float2 (&f)[4]) {
+  return make_uint4(bf16x2_of(f[0].x, f[0].y), bf16x2_of(f[1].x, f[1].y), bf16x2_of(f[2].x, f[2].y),
+                    bf16x2_of(f[3].x, f[3].y));
 }
 
 template <int KV>
@@ -190,6 +190,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// max |x|, NaN if there is one
+__device__ __forceinline__ float max_abs8(const float2 (&x)[4]) {
+  return max3_abs_nan(max3_abs_nan(x[0].x, x[0].y, x[1].x), max3_abs_nan(x[1].y, x[2].x, x[2].y),
+                      max3_abs_nan(x[3].x, x[3].y, 0.0f));
+}
+
 // Whether quot() gives the quotients of values below 2^60 by s.
 __device__ __forceinline__ bool short_by(float s) { return s > 0x1p-60f && s < 0x1p60f; }
 
@@ -203,27 +215,59 @@ __device__ __forceinline__ float any_quotient(float x, float s) {
 // Eight values over their scales (r = 1 / s; ok: short_by of the scales) -> two words of
 // 8-bit codes.
 template <int KV, bool PC>
-__device__ __forceinline__ uint2 codes8_of(const float (&x)[8], const float* s, const float* r, bool ok) {
-  float v[8], m = 0.0f;
+__device__ __forceinline__ uint2 codes8_of(const float2 (&x)[4], const float2* s, const float2* r, bool ok) {
+  float2 v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = quot2(x[e], s[PC ? e : 0], r[PC ? e : 0]);
+  if (!(max_abs8(x) < 0x1p60f) || !ok) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 d = s[PC ? e : 0];
+      v[e] = make_float2(any_quotient<KV>(x[e].x, d.x), any_quotient<KV>(x[e].y, d.y));
+    }
+  }
+  return make_uint2(codes4<KV>(&v[0].x), codes4<KV>(&v[2].x));
+}
+
+// A K row's 8 values of a lane, 4 bits, by divisions: codes and the block's scale.
+template <int FP4, bool PC>
+__device__ __forceinline__ void any_k4(const float2 (&f)[4], const float2* g, uint8_t* slab, int off, int c, bool in) {
+  constexpr float kTop = Fmt<FP4>::kTop;
+  float x[8], a = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    m = max_nan(m, fabsf(x[e]));
-    v[e] = quot(x[e], s[PC ? e : 0], r[PC ? e : 0]);
+    x[e] = e & 1 ? f[e >> 1].y : f[e >> 1].x;
+    if (x[e] != x[e]) x[e] = 0.0f;
+    a = fmaxf(a, fabsf(__fdiv_rn(x[e], PC && (e & 1) ? g[e >> 1].y : g[PC ? e >> 1 : 0].x)));
   }
-  if (!(m < 0x1p60f) || !ok) {
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  const uint32_t sb = block_scale<FP4>(__fdiv_rn(a, kTop));
+  const float t = e4m3_to_f32(sb);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = any_quotient<KV>(x[e], s[PC ? e : 0]);
+  for (int e = 0; e < 8; ++e) {
+    const float step = __fmul_rn(t, PC && (e & 1) ? g[e >> 1].y : g[PC ? e >> 1 : 0].x);
+    x[e] = fminf(fmaxf(step > 0.0f ? __fdiv_rn(x[e], step) : 0.0f, -kTop), kTop);
   }
-  return make_uint2(codes4<KV>(v), codes4<KV>(v + 4));
+  const uint32_t w = pack8<FP4>(x);
+  if (in) {
+    *reinterpret_cast<uint32_t*>(slab + k4_code_off(off, 8 * c)) = w;
+    if ((c & 1) == 0) slab[k4_scale_off(off, c >> 1)] = (uint8_t)sb;
+  }
+}
+
+template <int FP4>
+__device__ __forceinline__ uint32_t pack4x2(const float2 (&q)[4]) {
+  const float v[8] = {q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
+  return pack8<FP4>(v);
 }
 
 // A lane's 8 values of a K row -> its codes (and block scale), in place within the slab.
 // The lanes of a block are neighbours; every lane of the warp calls it, those of rows
-// outside the range with in = false.
+// outside the range with in = false.  (4 bits: per-channel scales, store_k4 has the others.)
 template <int KV, bool PC>
-__device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8], uint8_t* slab, int kvh, int off, int c,
+__device__ __forceinline__ void store_k(const RopeParams& p, const float2 (&f)[4], uint8_t* slab, int kvh, int off, int c,
                                         bool in) {
-  float g[8], rg[8];
+  float2 g[4], rg[4];
   bool ok = true;
   if constexpr (PC) {
     const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(p.a.k_scale) + kvh * kV4Dim + 8 * c;
@@ -231,15 +275,16 @@ __device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8]
       plain8(__ldg(reinterpret_cast<const uint4*>(sc)), g);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = __bfloat162float(sc[e]);
+      for (int e = 0; e < 4; ++e) g[e] = make_float2(__bfloat162float(sc[2 * e]), __bfloat162float(sc[2 * e + 1]));
     }
   } else {
-    g[0] = load_scale(p.a.k_scale, p.a.scale_kind, kvh);
+    g[0].x = g[0].y = load_scale(p.a.k_scale, p.a.scale_kind, kvh);
   }
 #pragma unroll
-  for (int e = 0; e < (PC ? 8 : 1); ++e) {
-    rg[e] = rcp_approx(g[e]);
-    ok = ok && short_by(g[e]);
+  for (int e = 0; e < (PC ? 4 : 1); ++e) {
+    rg[e].x = rcp_approx(g[e].x);
+    rg[e].y = PC ? rcp_approx(g[e].y) : rg[e].x;
+    ok = ok && short_by(g[e].x) && short_by(g[e].y);
   }
   if constexpr (!is_four<KV>()) {
     const uint2 w = codes8_of<KV, PC>(f, g, rg, ok);
@@ -249,108 +294,156 @@ __device__ __forceinline__ void store_k(const RopeParams& p, const float (&f)[8]
     constexpr float kTop = Fmt<FP4>::kTop;
     // the block's maximum of |x / g| by short quotients; a NaN, or a block out of their
     // range, shows in `fine`
-    float a = 0.0f;
+    float2 q[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = max_nan(a, PC ? fabsf(quot(f[e], g[e], rg[e])) : fabsf(f[e]));
+    for (int e = 0; e < 4; ++e) q[e] = quot2(f[e], g[e], rg[e]);
+    float a = max_abs8(q);
     a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    if constexpr (!PC) a = fabsf(quot(a, g[0], rg[0]));   // of the largest: rounding keeps the order
-    uint32_t sb = block_scale<FP4>(quot(a, kTop, 1.0f / kTop));
-    const float s = e4m3_to_f32(sb);
-    float q[8], low = 1e30f, high = 0.0f;
+    const uint32_t sb = block_scale<FP4>(quot(a, kTop, 1.0f / kTop));
+    const float s = e4m3_to_f32(sb), rs = rcp_approx(s);
+    const float2 s2 = make_float2(s, s), rs2 = make_float2(rs, rs);
+    float low = 1e30f, high = 0.0f;
 #pragma unroll
-    for (int e = 0; e < (PC ? 8 : 1); ++e) {
-      const float st = fabsf(s * g[e]);
-      low = fminf(low, st);
-      high = fmaxf(high, st);
+    for (int e = 0; e < 4; ++e) {
+      const float2 st = mul2(s2, g[e]);
+      low = fminf(low, fminf(fabsf(st.x), fabsf(st.y)));
+      high = fmaxf(high, fmaxf(fabsf(st.x), fabsf(st.y)));
+      q[e] = quot2(f[e], st, mul2(rs2, rg[e]));
     }
     const bool fine = ok && common<FP4>(a, s, low) && high < 1e30f;
     if (__all_sync(0xffffffffu, fine || !in)) {
-      const float r0 = PC ? 0.0f : rcp_approx(s * g[0]), rs = PC ? rcp_approx(s) : 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = quot(f[e], s * g[PC ? e : 0], PC ? rs * rg[e] : r0);
+      const uint32_t w = pack4x2<FP4>(q);
+      if (in) {
+        *reinterpret_cast<uint32_t*>(slab + k4_code_off(off, 8 * c)) = w;
+        if ((c & 1) == 0) slab[k4_scale_off(off, c >> 1)] = (uint8_t)sb;
+      }
     } else {
-      float x[8];
-      a = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = f[e] != f[e] ? 0.0f : f[e];
-        a = fmaxf(a, fabsf(__fdiv_rn(x[e], g[PC ? e : 0])));
-      }
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      sb = block_scale<FP4>(__fdiv_rn(a, kTop));
-      const float t = e4m3_to_f32(sb);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float step = __fmul_rn(t, g[PC ? e : 0]);
-        q[e] = fminf(fmaxf(step > 0.0f ? __fdiv_rn(x[e], step) : 0.0f, -kTop), kTop);
-      }
-    }
-    const uint32_t w = pack8<FP4>(q);
-    if (in) {
-      *reinterpret_cast<uint32_t*>(slab + k4_code_off(off, 8 * c)) = w;
-      if ((c & 1) == 0) slab[k4_scale_off(off, c >> 1)] = (uint8_t)sb;
+      any_k4<FP4, true>(f, g, slab, off, c, in);
     }
   }
 }
 
-// V of an 8-bit cache: the unit's positions [a, e) of U, lane = 4 dims.
-template <int KV, bool PC, int U>
+// The K rows of two neighbouring heads, kvh and kvh + 1, 4 bits, a scale a head or for all:
+// a lane of a block works out the scale of one of them.  `slab` is head kvh's; in0, in1:
+// whether the row is to be written (kvh may be -1, or the last head, with the other's false).
+template <int KV>
+__device__ __forceinline__ void store_k4(const RopeParams& p, const float2 (&f)[2][4], uint8_t* slab, int kvh, int off, int c,
+                                         bool in0, bool in1) {
+  constexpr int FP4 = KV == PA_KV_FP4_E2M1;
+  constexpr float kTop = Fmt<FP4>::kTop;
+  const bool odd = c & 1;
+  const int mine = kvh + (odd ? 1 : 0);
+  const float g = load_scale(p.a.k_scale, p.a.scale_kind, min(max(mine, 0), p.a.kv_heads - 1));
+  const float a0 = max_abs8(f[0]), a1 = max_abs8(f[1]);
+  const float m = max_nan(odd ? a1 : a0, __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1));
+  // of the largest: rounding keeps the order
+  const float a = fabsf(quot(m, g, rcp_approx(g)));
+  const uint32_t sb = block_scale<FP4>(quot(a, kTop, 1.0f / kTop));
+  const float s = e4m3_to_f32(sb), st = s * g, rs = rcp_approx(st);
+  const bool in = odd ? in1 : in0, fine = short_by(g) && common<FP4>(a, s, fabsf(st));
+  uint8_t* codes = slab + k4_code_off(off, 8 * c);
+  if (__all_sync(0xffffffffu, fine || !in)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int from = (threadIdx.x & 30) | i;
+      const float si = __shfl_sync(0xffffffffu, st, from), ri = __shfl_sync(0xffffffffu, rs, from);
+      const float2 s2 = make_float2(si, si), r2 = make_float2(ri, ri);
+      float2 q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = quot2(f[i][e], s2, r2);
+      const uint32_t w = pack4x2<FP4>(q);
+      if (i ? in1 : in0) *reinterpret_cast<uint32_t*>(codes + i * kV4Slab) = w;
+    }
+    if (in) slab[(odd ? kV4Slab : 0) + k4_scale_off(off, c >> 1)] = (uint8_t)sb;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float gi = __shfl_sync(0xffffffffu, g, (threadIdx.x & 30) | i);
+      const float2 g2[1] = {make_float2(gi, gi)};
+      any_k4<FP4, false>(f[i], g2, slab + i * kV4Slab, off, c, i ? in1 : in0);
+    }
+  }
+}
+
+// V of an 8-bit cache: the unit's positions [a, e) of U (FULL: all), lane = 4 dims.
+template <int KV, bool PC, int U, bool FULL>
 __device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat16* rows, uint8_t* slab, int kvh, int off0,
                                          int a, int e, int lane) {
-  float g[4];
+  float2 g[2], rg[2];
 #pragma unroll
-  for (int d = 0; d < (PC ? 4 : 1); ++d)
-    g[d] = load_scale(p.a.v_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 4 * lane + d : kvh);
-  float rg[4];
+  for (int d = 0; d < (PC ? 2 : 1); ++d) {
+    g[d].x = load_scale(p.a.v_scale, p.a.scale_kind, PC ? kvh * kV4Dim + 4 * lane + 2 * d : kvh);
+    g[d].y = PC ? load_scale(p.a.v_scale, p.a.scale_kind, kvh * kV4Dim + 4 * lane + 2 * d + 1) : g[d].x;
+  }
   bool ok = true;
 #pragma unroll
-  for (int d = 0; d < (PC ? 4 : 1); ++d) {
-    rg[d] = rcp_approx(g[d]);
-    ok = ok && short_by(g[d]);
+  for (int d = 0; d < (PC ? 2 : 1); ++d) {
+    rg[d] = make_float2(rcp_approx(g[d].x), rcp_approx(g[d].y));
+    ok = ok && short_by(g[d].x) && short_by(g[d].y);
   }
-  const __nv_bfloat16* src = rows + 4 * lane - (int64_t)a * p.a.kv_stride;
+  const __nv_bfloat16* src = rows + 4 * lane - (FULL ? 0 : (int64_t)a * p.a.kv_stride);
   uint8_t* dst = slab + 4 * lane * kPage + off0;
+  uint32_t w[4][U / 4];
 #pragma unroll
   for (int k = 0; k < U; k += 8) {
     uint2 x[8];
     uint32_t top = 0;   // the largest exponents and mantissas
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = k + j >= a && k + j < e ? __ldg(reinterpret_cast<const uint2*>(src + (int64_t)(k + j) * p.a.kv_stride))
-                                     : make_uint2(0, 0);
+    for (int j = 0; j < 8; ++j, src += p.a.kv_stride) {
+      x[j] = FULL || (k + j >= a && k + j < e) ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
       top = max_u16x2(top, max_u16x2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu));
     }
     // all below 2^60 (bf16 0x5D80)
     const bool fine = ok && (top & 0xFFFFu) < 0x5D80u && (top >> 16) < 0x5D80u;
-    uint32_t w[4][2];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
+    for (int d = 0; d < 4; d += 2) {
+      const float2 gd = g[PC ? d / 2 : 0], rd = rg[PC ? d / 2 : 0];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float f[4], v[4];
+        float v0[4], v1[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint2& y = x[4 * h + j];
-          f[j] = d == 0 ? bf16_lo(y.x) : d == 1 ? bf16_hi(y.x) : d == 2 ? bf16_lo(y.y) : bf16_hi(y.y);
-          v[j] = quot(f[j], g[PC ? d : 0], rg[PC ? d : 0]);
+          const float2 v = quot2(bf16_2(d ? x[4 * h + j].y : x[4 * h + j].x), gd, rd);
+          v0[j] = v.x;
+          v1[j] = v.y;
         }
         if (!fine) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = any_quotient<KV>(f[j], g[PC ? d : 0]);
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = bf16_2(d ? x[4 * h + j].y : x[4 * h + j].x);
+            v0[j] = any_quotient<KV>(f.x, gd.x);
+            v1[j] = any_quotient<KV>(f.y, gd.y);
+          }
         }
-        w[d][h] = codes4<KV>(v);
+        w[d][k / 4 + h] = codes4<KV>(v0);
+        w[d + 1][k / 4 + h] = codes4<KV>(v1);
       }
     }
-    if (a <= k && k + 8 <= e) {
+  }
 #pragma unroll
-      for (int d = 0; d < 4; ++d) *reinterpret_cast<uint2*>(dst + d * kPage + k) = make_uint2(w[d][0], w[d][1]);
+  for (int d = 0; d < 4; ++d) {
+    uint8_t* to = dst + d * kPage;
+    if constexpr (FULL && U == 32) {   // whole sectors
+      if (p.v32) {
+        st_global_32(to, w[d]);
+      } else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[d][0], w[d][1], w[d][2], w[d][3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[d][4], w[d][5], w[d][6], w[d][7]);
+      }
+    } else if constexpr (FULL) {
+#pragma unroll
+      for (int k = 0; k < U; k += 8) *reinterpret_cast<uint2*>(to + k) = make_uint2(w[d][k / 4], w[d][k / 4 + 1]);
     } else {   // only the range's own positions
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (k + j >= a && k + j < e) {
+      for (int k = 0; k < U; k += 8) {
+        if (a <= k && k + 8 <= e) {
+          *reinterpret_cast<uint2*>(to + k) = make_uint2(w[d][k / 4], w[d][k / 4 + 1]);
+        } else {
 #pragma unroll
-          for (int d = 0; d < 4; ++d) dst[d * kPage + k + j] = (uint8_t)(w[d][j >> 2] >> (8 * (j & 3)));
+          for (int j = k; j < k + 8; ++j)
+            if (j >= a && j < e) to[j] = (uint8_t)(w[d][j >> 2] >> (8 * (j & 3)));
         }
+      }
     }
   }
 }
@@ -387,7 +480,7 @@ __device__ __forceinline__ bool unit_at(const RopeParams& p, const RowUnits& uni
 // ---- GQA
 // Queries alone, of many rows: few registers, so that 32 warps an SM have their loads on
 // the way (in one kernel with K's and V's quantisers 16; 35k rows of 32 heads 128 us)
-__global__ void __launch_bounds__(kWarps * 32, 4) rope_q_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kQCtas) rope_q_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (id >= p.rot_warps) return;
@@ -420,8 +513,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) rope_q_kernel(const RopeParams
       for (int k = 0; k < 4; ++k) {
         if (h0 + k >= g1) break;
         const uint4 y = partners(p, x[k], other);
-        float f[8];
-        if (turn) turn8(x[k], y, a, f);
+        float2 f[4];
+        if (turn) turn8(p, x[k], y, a, f);
         else plain8(x[k], f);
         if (in) *reinterpret_cast<uint4*>(dst + (h0 + k) * kV4Dim) = bf16x8_of(f);
       }
@@ -430,9 +523,13 @@ __global__ void __launch_bounds__(kWarps * 32, 4) rope_q_kernel(const RopeParams
   }
 }
 
-// Everything in one launch (U = 8, few rows), or K and V (U = 32).
+// Everything in one launch (U = 8, few rows), or K and V (U = 32; 35k rows of 8 heads: FP4
+// 60 us, int8 67, their bytes 27 and 33; per-channel scales 91 and 83, 5 less than with 32
+// warps an SM, which spill more).  K alone takes 45 and V 23 (FP4): instructions (47 % of the
+// issue slots at 32 % of the warps) and loads in turn; the next heads' rows requested ahead
+// 62 to 70, 4 heads at once 60 to 68.
 template <int KV, bool PC, int U>
-__global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : PC ? 3 : 4) rope_append_kernel(const RopeParams p) {
   constexpr int kBatch = U == 8 ? 4 : 2;   // heads whose rows are on the way at once
   constexpr int kUnit = U == 8 ? kRopeUnit : kQUnit;
   const int lane = threadIdx.x & 31;
@@ -457,7 +554,8 @@ __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kerne
       e - a == U ? write_v<FP4, PC, U, true>(p.a, rows, half, kvh, first, a, e, lane)
                  : write_v<FP4, PC, U, false>(p.a, rows, half, kvh, first, a, e, lane);
     } else {
-      store_v8<KV, PC, U>(p, rows, slab, kvh, m.u0 % kPage, a, e, lane);
+      e - a == U ? store_v8<KV, PC, U, true>(p, rows, slab, kvh, m.u0 % kPage, a, e, lane)
+                 : store_v8<KV, PC, U, false>(p, rows, slab, kvh, m.u0 % kPage, a, e, lane);
     }
     return;
   }
@@ -477,30 +575,40 @@ __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kerne
     const int64_t t = m.row + (pos - m.lo);
     Turn a;
     const bool turn = in && turned && load_turn(p, t, pos, c, a);
+    const __nv_bfloat16* q_row = p.q + t * p.q_stride + 8 * c;
+    const __nv_bfloat16* k_row = p.a.k_new + t * p.a.kv_stride - p.q_heads * kV4Dim + 8 * c;   // of head h: + h * 128
+    __nv_bfloat16* q_to = p.q_out + t * p.q_out_stride + 8 * c;
+    uint8_t* slabs = p.a.cache_k + (int64_t)page * p.a.kv_heads * kSlabBytes;
     for (int h0 = g0; h0 < g1; h0 += kBatch) {
       uint4 x[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int h = h0 + k;
         x[k] = make_uint4(0, 0, 0, 0);
-        if (in && h < g1)
-          x[k] = *reinterpret_cast<const uint4*>(
-              h < p.q_heads ? p.q + t * p.q_stride + h * kV4Dim + 8 * c
-                            : p.a.k_new + t * p.a.kv_stride + (h - p.q_heads) * kV4Dim + 8 * c);
+        if (in && h < g1) x[k] = *reinterpret_cast<const uint4*>((h < p.q_heads ? q_row : k_row) + h * kV4Dim);
       }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int h = h0 + k;
-        if (h >= g1) break;
+      // the rotated values of head h0 + k; a query's are written
+      auto rotate = [&](int k, float2 (&f)[4]) {
         const uint4 y = partners(p, x[k], other);
-        float f[8];
-        if (turn) turn8(x[k], y, a, f);
+        if (turn) turn8(p, x[k], y, a, f);
         else plain8(x[k], f);
-        if (h < p.q_heads) {
-          if (in) *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * kV4Dim + 8 * c) = bf16x8_of(f);
-        } else if (page >= 0) {
-          const int kvh = h - p.q_heads;
-          store_k<KV, PC>(p, f, p.a.cache_k + ((int64_t)page * p.a.kv_heads + kvh) * kSlabBytes, kvh, pos % kPage, c, in);
+        if (in && h0 + k < min(g1, p.q_heads)) *reinterpret_cast<uint4*>(q_to + (h0 + k) * kV4Dim) = bf16x8_of(f);
+      };
+      constexpr int kStep = is_four<KV>() && !PC ? 2 : 1;
+#pragma unroll
+      for (int k = 0; k < kBatch; k += kStep) {
+        const int h = h0 + k, kvh = h - p.q_heads;
+        if (h >= g1) break;
+        uint8_t* slab = slabs + (int64_t)kvh * kSlabBytes;
+        if constexpr (kStep == 2) {
+          float2 f[2][4];
+          rotate(k, f[0]);
+          rotate(k + 1, f[1]);
+          if (page >= 0 && kvh + 1 >= 0) store_k4<KV>(p, f, slab, kvh, pos % kPage, c, in && kvh >= 0, in && h + 1 < g1);
+        } else {
+          float2 f[4];
+          rotate(k, f);
+          if (page >= 0 && kvh >= 0) store_k<KV, PC>(p, f, slab, kvh, pos % kPage, c, in);
         }
       }
     }
@@ -509,7 +617,7 @@ __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : 4) rope_append_kerne
 
 // ---- MLA: groups of query heads, and one more for the latent row
 template <int KV>
-__global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_latent_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (id >= p.rot_warps) return;
@@ -523,7 +631,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
   if (g0 >= p.q_heads) {   // the rows of the cache
     const int page = page_at(p, m.b, m.u0, lane);
     if (page < 0) return;
-    const float s[1] = {load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0)}, rs[1] = {rcp_approx(s[0])};
+    const float scale = load_scale(p.a.k_scale, PA_SCALE_GLOBAL, 0), rcp = rcp_approx(scale);
+    const float2 s[1] = {make_float2(scale, scale)}, rs[1] = {make_float2(rcp, rcp)};
     for (int pos = m.lo; pos < m.hi; ++pos) {
       const int64_t t = m.row + (pos - m.lo);
       const __nv_bfloat16* src = p.a.k_new + t * p.a.kv_stride;
@@ -538,10 +647,10 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         if (k == 2 && lane >= 8) break;
-        float f[8];
-        if (k == 2 && turn) turn8(x[2], y, a, f);
+        float2 f[4];
+        if (k == 2 && turn) turn8(p, x[2], y, a, f);
         else plain8(x[k], f);
-        *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * k)) = codes8_of<KV, false>(f, s, rs, short_by(s[0]));
+        *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * k)) = codes8_of<KV, false>(f, s, rs, short_by(scale));
       }
     }
     return;
@@ -566,8 +675,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_latent_kernel(const RopePara
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint4 y = partners(p, x[k], other);
-        float f[8];
-        if (turn) turn8(x[k], y, a, f);
+        float2 f[4];
+        if (turn) turn8(p, x[k], y, a, f);
         else plain8(x[k], f);
         *reinterpret_cast<uint4*>(dst + (h0 + 4 * k) * kMlaQ + at) = bf16x8_of(f);
       }
@@ -622,6 +731,7 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
   p.a.scale_kind = pr.scale_kind;
   p.a.vec = 1;
   p.k_scale16 = reinterpret_cast<uintptr_t>(a.k_scale) % 16 == 0;
+  p.v32 = reinterpret_cast<uintptr_t>(a.cache_v) % 32 == 0;
   p.cos_sin = rope.cos_sin;
   p.positions = rope.positions;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -634,6 +744,7 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
   p.adjacent = rope.pairs == PA_ROPE_ADJACENT;
   p.axes = rope.axes;
   p.total_q = plan.total_q;
+  p.neg_zero = -0.0f;
   p.quads = 1;
   for (int i = 0; i < rope.rot_dim / 2; ++i) {
     p.pair_axis[i >> 4] |= (uint32_t)(rope.pair_axis[i] & 3) << (2 * (i & 15));
@@ -644,8 +755,8 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
   const bool small = 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms;
   // Heads of a warp: enough to use a row's cos and sin often, few while the warps would
   // not fill the GPU
-  auto share = [&](int heads, int least) {
-    p.group_heads = 16;
+  auto share = [&](int heads, int least, int most = 16) {
+    p.group_heads = most;
     while (p.group_heads > least &&
            (double)p.units.count * ((heads + p.group_heads - 1) / p.group_heads) < 16.0 * kWarps * plan.num_sms)
       p.group_heads /= 2;
@@ -656,7 +767,14 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
   };
   if (!mla && q && !small) {
     p.units = row_units<kQUnit>(pr.bsz, plan.max_q, plan.total_q);
-    if (!share(p.q_heads, 4)) return cudaErrorInvalidValue;
+    // 8 or 16 heads, by the time of the waves of warps (24k rows of 32 heads: 16 in 1.24 waves
+    // 59 us, 8 in 2.47 50; 35k: 16 in 1.81 waves 94, 8 in 3.63 98)
+    auto waves = [&](int g) {
+      const double warps = ((double)plan.total_q / kQUnit + pr.bsz) * ((p.q_heads + g - 1) / g);   // that have rows
+      return std::ceil(warps / (kQCtas * kWarps * plan.num_sms)) * (std::min(g, p.q_heads) + 2);
+    };
+    const int g = waves(8) < waves(16) ? 8 : 16;
+    if (!share(p.q_heads, g, g)) return cudaErrorInvalidValue;
     rope_q_kernel<<<(p.rot_warps + kWarps - 1) / kWarps, kWarps * 32, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -15,13 +15,18 @@ def dev(bits):
     return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).cuda()
 
 
-def launch(p, *, q=True, in_place=False, packed=False, pad=0, rows=None, stream=None, sms=None):
-    """Runs the call; returns (q_out bits, cache_k, cache_v, status, detail)."""
+def launch(p, *, q=True, in_place=False, packed=False, pad=0, rows=None, stream=None, sms=None, cache_at=0):
+    """Runs the call (the values' cache cache_at bytes into its buffer); returns (q_out bits,
+    cache_k, cache_v, status, detail)."""
     import paged_quantized_kv_gqa_gb300 as pa
     T, mla = rows or p.total_q, p.layout == "mla"
     d = {n: torch.from_numpy(getattr(p, n).copy()).cuda() for n in ("block_table", "seq_lens", "seq_lens_kv", "cu_seqlens_q",
                                                                      "cache_k")}
-    d["cache_v"] = d["cache_k"] if mla else torch.from_numpy(p.cache_v.copy()).cuda()
+    if mla:
+        d["cache_v"] = d["cache_k"]
+    else:
+        d["cache_v"] = torch.zeros(p.cache_v.size + cache_at, dtype=torch.uint8, device="cuda")[cache_at:].view(p.cache_v.shape)
+        d["cache_v"].copy_(torch.from_numpy(p.cache_v))
     for w in "kv":
         s = getattr(p, w + "_scale")
         d[w + "_scale"] = torch.from_numpy(s).cuda() if p.scale_kind == "global" else dev(s)
@@ -149,6 +154,27 @@ def test_many_rows_in_place_packed_or_without_queries(kw):
 def test_many_rows_of_far_values(kv_dtype, spread):
     check(rh.make(seed=22, seq_lens=[150], seq_lens_kv=[60], kv_heads=4, kv_dtype=kv_dtype, scale_kind="per_channel",
                   spread=spread), sms=1)
+
+
+@pytest.mark.parametrize("sms", [None, 1])
+@pytest.mark.parametrize("kv_dtype", ["int4", "fp4_e2m1"])
+@pytest.mark.parametrize("q_heads, kv_heads", [(1, 1), (3, 3), (5, 1), (15, 5), (9, 3), (18, 9)])
+def test_odd_heads_of_four_bits(kv_dtype, q_heads, kv_heads, sms):
+    check(rh.make(seed=24, seq_lens=[67, 2], seq_lens_kv=[31, 64], q_heads=q_heads, kv_heads=kv_heads, kv_dtype=kv_dtype), sms=sms)
+
+
+@pytest.mark.parametrize("sms", [None, 1])
+@pytest.mark.parametrize("scale_kind", ["per_kv_head", "global"])
+@pytest.mark.parametrize("kv_dtype", rh.FORMATS)
+@pytest.mark.parametrize("spread", [1e-3, 30.0, 1e30])
+def test_far_values_of_odd_heads(kv_dtype, scale_kind, spread, sms):
+    check(rh.make(seed=25, seq_lens=[70], seq_lens_kv=[60], q_heads=3, kv_heads=3, kv_dtype=kv_dtype, scale_kind=scale_kind,
+                  spread=spread), sms=sms)
+
+
+@pytest.mark.parametrize("kv_dtype", rh.FORMATS)
+def test_a_cache_on_a_boundary_of_16_bytes(kv_dtype):
+    check(rh.make(seed=26, seq_lens=[130], seq_lens_kv=[31], kv_dtype=kv_dtype), sms=1, cache_at=16)
 
 
 @pytest.mark.parametrize("sms", [None, 1])
