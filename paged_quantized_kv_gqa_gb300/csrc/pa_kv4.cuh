@@ -85,23 +85,27 @@ struct RowUnits {
   int64_t count;     // numbers given out
 };
 
-template <int U>
-inline RowUnits row_units(int bsz, int max_q, int64_t total_q) {
+inline RowUnits row_units_of(int U, int bsz, int max_q, int64_t total_q) {
   const int per_seq = (max_q + U - 2) / U + 1;   // touched at most by a range of max_q rows
   const int64_t rect = (int64_t)bsz * per_seq, by_rows = total_q / U + 2 * (int64_t)bsz;
   return rect <= 2 * by_rows ? RowUnits{per_seq, bsz, rect} : RowUnits{0, bsz, by_rows};
 }
 
-// Unit number n -> sequence and unit of its range (a number may be past the range's
-// last unit); the whole warp calls it.
 template <int U>
-__device__ __forceinline__ void find_unit(const RowUnits& ru, const int32_t* cu, uint32_t n, int lane, int& b, int& u) {
+inline RowUnits row_units(int bsz, int max_q, int64_t total_q) {
+  return row_units_of(U, bsz, max_q, total_q);
+}
+
+// Unit number n -> sequence and unit of its range (a number may be past the range's
+// last unit); the whole warp calls it.  Units of 1 << shift.
+__device__ __forceinline__ void find_unit_of(int shift, const RowUnits& ru, const int32_t* cu, uint32_t n, int lane, int& b,
+                                             int& u) {
   if (ru.per_seq > 0) {
     b = (int)(n / (uint32_t)ru.per_seq);
     u = (int)(n - (uint32_t)b * (uint32_t)ru.per_seq);
     return;
   }
-  auto first = [&](int k) { return (uint32_t)cu[k] / U + 2u * (uint32_t)k; };
+  auto first = [&](int k) { return ((uint32_t)cu[k] >> shift) + 2u * (uint32_t)k; };
   int lo = 0, hi = ru.bsz;   // first(lo) <= n < first(hi)
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, k = lo + lane * step;
@@ -111,6 +115,14 @@ __device__ __forceinline__ void find_unit(const RowUnits& ru, const int32_t* cu,
   }
   b = lo;
   u = (int)(n - first(lo));
+}
+
+template <int U>
+__device__ __forceinline__ void find_unit(const RowUnits& ru, const int32_t* cu, uint32_t n, int lane, int& b, int& u) {
+  static_assert((U & (U - 1)) == 0, "a power of two");
+  constexpr int shift = U == 1 ? 0 : U == 2 ? 1 : U == 4 ? 2 : U == 8 ? 3 : U == 16 ? 4 : U == 32 ? 5 : 6;
+  static_assert(1 << shift == U, "up to 64");
+  find_unit_of(shift, ru, cu, n, lane, b, u);
 }
 
 // Eight codes of a word -> four fp16x2 words, in the order `codes8` defines:

@@ -13,7 +13,7 @@
 //
 // GQA: lane = 8 dims of a row, two rows a step, so that a lane's cos and sin are read
 // once for all heads of its row; the other dim of a pair comes by a shuffle (halves) or
-// is the lane's own (adjacent).  A warp takes a unit of 8 positions and a group of the
+// is the lane's own (adjacent).  A warp takes a unit of 2 to 8 positions and a group of the
 // heads, the queries' first, K's behind them.  V: a warp per (unit, kv head), lane = 4
 // dims of all the unit's positions, whose bytes gather in registers.
 // MLA: 8 lanes hold the 64 rotated dims of a head, 4 query heads a step; a latent row is
@@ -28,12 +28,6 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kWarps = 8;
-// Positions of a rotation warp's unit: of many rows, and of few (and latent rows), where
-// more warps count.  A warp has all heads of a row, or 8 to 16, and reads its cos and sin
-// once (K and V of 35k rows, FP4: units of 8 rows and 2 of 8 heads, to have as many warps,
-// 94 us, of 2 rows and all heads 66, of 4 62, of 8 60; K's warps among V's instead of before
-// them 76: theirs are the long ones).
-constexpr int kQUnit = 8, kRopeUnit = 2;
 constexpr int kQCtas = 4;   // CTAs an SM of the queries' kernel
 constexpr int kMlaRow = 576, kMlaQ = 192, kMlaNope = 128;
 
@@ -44,7 +38,8 @@ struct RopeParams {
   const __nv_bfloat16* q;      // or null
   __nv_bfloat16* q_out;
   int64_t q_stride, q_out_stride;
-  RowUnits units;              // the rotation's
+  RowUnits units;              // the rotation's, of 1 << unit_shift positions
+  int32_t unit_shift;
   uint32_t rot_warps;          // warps of the rotation; the V warps follow
   int32_t groups, group_heads; // head groups of a unit
   int32_t q_heads;             // 0 without queries
@@ -457,22 +452,22 @@ __device__ __forceinline__ int page_at(const RopeParams& p, int b, int pos, int 
   return -1;
 }
 
-// A unit of U positions: sequence, first position, and the range's part [lo, hi) of it.
+// A unit of positions: sequence, first position, and the range's part [lo, hi) of it.
 struct UnitAt {
   int b, u0, lo, hi;
   int64_t row;   // token row of position lo
 };
 
-template <int U>
-__device__ __forceinline__ bool unit_at(const RopeParams& p, const RowUnits& units, uint32_t n, int lane, UnitAt& m) {
+__device__ __forceinline__ bool unit_at(const RopeParams& p, int shift, const RowUnits& units, uint32_t n, int lane,
+                                        UnitAt& m) {
   int u;
-  find_unit<U>(units, p.a.cu_seqlens_q, n, lane, m.b, u);
+  find_unit_of(shift, units, p.a.cu_seqlens_q, n, lane, m.b, u);
   const int q = p.a.seq_lens[m.b];
   if (q <= 0) return false;
   const int start = p.a.seq_lens_kv[m.b], end = start + q;
-  m.u0 = (start / U + u) * U;
+  m.u0 = ((start >> shift) + u) << shift;
   m.lo = max(m.u0, start);
-  m.hi = min(m.u0 + U, end);
+  m.hi = min(m.u0 + (1 << shift), end);
   m.row = (int64_t)p.a.cu_seqlens_q[m.b] + (m.lo - start);
   return m.lo < m.hi;
 }
@@ -487,7 +482,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQCtas) rope_q_kernel(const RopeP
   const uint32_t bu = id / (uint32_t)p.groups;
   const int g0 = (int)(id - bu * p.groups) * p.group_heads, g1 = min(p.q_heads, g0 + p.group_heads);
   UnitAt m;
-  if (!unit_at<kQUnit>(p, p.units, bu, lane, m)) return;
+  if (!unit_at(p, p.unit_shift, p.units, bu, lane, m)) return;
   const int c = lane & 15, oct = p.rot / 8;
   const bool turned = c < oct;
   const int other = !turned ? lane : (lane & 16) | (c < oct / 2 ? c + oct / 2 : c - oct / 2);
@@ -531,7 +526,6 @@ __global__ void __launch_bounds__(kWarps * 32, kQCtas) rope_q_kernel(const RopeP
 template <int KV, bool PC, int U>
 __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : PC ? 3 : 4) rope_append_kernel(const RopeParams p) {
   constexpr int kBatch = U == 8 ? 4 : 2;   // heads whose rows are on the way at once
-  constexpr int kUnit = U == 8 ? kRopeUnit : kQUnit;
   const int lane = threadIdx.x & 31;
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
   constexpr int kSlabBytes = is_four<KV>() ? kV4Slab : kPage * kV4Dim;
@@ -541,7 +535,7 @@ __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : PC ? 3 : 4) rope_app
     if (n >= p.a.total) return;
     const uint32_t bu = n / (uint32_t)p.a.kv_heads;
     const int kvh = (int)(n - bu * p.a.kv_heads);
-    if (!unit_at<U>(p, p.a.units, bu, lane, m)) return;
+    if (!unit_at(p, U == 8 ? 3 : 5, p.a.units, bu, lane, m)) return;
     const int page = page_at(p, m.b, m.u0, lane);
     if (page < 0) return;
     const __nv_bfloat16* rows = p.a.v_new + m.row * p.a.kv_stride + (int64_t)kvh * kV4Dim;
@@ -563,7 +557,7 @@ __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : PC ? 3 : 4) rope_app
   const uint32_t bu = id / (uint32_t)p.groups;
   const int g0 = (int)(id - bu * p.groups) * p.group_heads;
   const int heads = p.q_heads + p.a.kv_heads, g1 = min(heads, g0 + p.group_heads);
-  if (!unit_at<kUnit>(p, p.units, bu, lane, m)) return;
+  if (!unit_at(p, p.unit_shift, p.units, bu, lane, m)) return;
   const int page = g1 > p.q_heads ? page_at(p, m.b, m.u0, lane) : -1;
   const int c = lane & 15, oct = p.rot / 8;
   const bool turned = c < oct;
@@ -624,7 +618,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_latent_kernel(const RopeP
   const uint32_t bu = id / (uint32_t)p.groups;
   const int g0 = (int)(id - bu * p.groups) * p.group_heads;
   UnitAt m;
-  if (!unit_at<kRopeUnit>(p, p.units, bu, lane, m)) return;
+  if (!unit_at(p, p.unit_shift, p.units, bu, lane, m)) return;
   const int o = lane & 7, oct = p.rot / 8;
   const bool turned = o < oct;
   const int other = !turned ? lane : (lane & 24) | (o < oct / 2 ? o + oct / 2 : o - oct / 2);
@@ -751,8 +745,22 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
     if (rope.pair_axis[i] != rope.pair_axis[i & ~3]) p.quads = 0;
   }
   const bool mla = pr.layout == PA_LAYOUT_MLA;
-  // V's units as pa_cache4.cu takes them, and one launch for all while they are short
-  const bool small = 2.0 * plan.total_q * pr.kv_heads / 32 < 4.0 * kWarps * plan.num_sms;
+  // One launch for all while rows are few, V by units of 8; then the queries by themselves
+  // and V by units of 32.  Rows of all heads an SM, us in one launch and in two, FP4: 2048
+  // rows of 40 heads 20.7 and 20.4, 1024 12.7 and 18.7, 4096 35.6 and 29.0; 4096 rows of 18
+  // 17.6 and 20.3, 6144 23.0 and 21.5; without queries, where both are one launch, 2048
+  // rows of 8 heads 10.6 and 10.6, 1024 8.2 and 10.4, 4096 14.7 and 12.7.
+  const bool small = (double)plan.total_q * (p.q_heads + pr.kv_heads) < (q ? 560.0 : 150.0) * plan.num_sms;
+  // Positions of a rotation warp's unit: a warp has all heads of a row, or 8 to 16, and reads
+  // its cos and sin once; with many rows 8, so that what a unit begins with is shared, with
+  // fewer 4 or 2, so that there are 16 units an SM.  Units of 2, 4 and 8, us (40 heads, FP4):
+  // 6144 rows 39, 44, 56, 12800 66, 66, 78, 16384 84, 82, 88, 35200 157, 155, 153.  (K and V of
+  // 35k rows by units of 8 and 2 of 8 heads, to have as many warps, 94 us, all heads 60; K's
+  // warps among V's instead of before them 76: theirs are the long ones.)
+  p.unit_shift = 1;
+  if (!mla && !small)
+    while (p.unit_shift < 3 && plan.total_q >= (16 << (p.unit_shift + 1)) * (int64_t)plan.num_sms) ++p.unit_shift;
+  p.units = row_units_of(1 << p.unit_shift, pr.bsz, plan.max_q, plan.total_q);
   // Heads of a warp: enough to use a row's cos and sin often, few while the warps would
   // not fill the GPU
   auto share = [&](int heads, int least, int most = 16) {
@@ -766,11 +774,10 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
     return p.rot_warps > 0;
   };
   if (!mla && q && !small) {
-    p.units = row_units<kQUnit>(pr.bsz, plan.max_q, plan.total_q);
     // 8 or 16 heads, by the time of the waves of warps (24k rows of 32 heads: 16 in 1.24 waves
     // 59 us, 8 in 2.47 50; 35k: 16 in 1.81 waves 94, 8 in 3.63 98)
     auto waves = [&](int g) {
-      const double warps = ((double)plan.total_q / kQUnit + pr.bsz) * ((p.q_heads + g - 1) / g);   // that have rows
+      const double warps = ((double)plan.total_q / (1 << p.unit_shift) + pr.bsz) * ((p.q_heads + g - 1) / g);   // that have rows
       return std::ceil(warps / (kQCtas * kWarps * plan.num_sms)) * (std::min(g, p.q_heads) + 2);
     };
     const int g = waves(8) < waves(16) ? 8 : 16;
@@ -780,8 +787,6 @@ cudaError_t launch_rope_append(const Plan& plan, const pa_args& a, const pa_rope
     if (e != cudaSuccess) return e;
     p.q_heads = 0;
   }
-  p.units = mla || small ? row_units<kRopeUnit>(pr.bsz, plan.max_q, plan.total_q)
-                         : row_units<kQUnit>(pr.bsz, plan.max_q, plan.total_q);
   if (!share(p.q_heads + (mla ? 0 : pr.kv_heads), mla || !small ? 8 : 4)) return cudaErrorInvalidValue;
   if (mla) {
     const dim3 grid((p.rot_warps + kWarps - 1) / kWarps), block(kWarps * 32);

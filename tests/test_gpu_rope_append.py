@@ -160,7 +160,7 @@ def test_many_rows_of_far_values(kv_dtype, spread):
 @pytest.mark.parametrize("kv_dtype", ["int4", "fp4_e2m1"])
 @pytest.mark.parametrize("q_heads, kv_heads", [(1, 1), (3, 3), (5, 1), (15, 5), (9, 3), (18, 9)])
 def test_odd_heads_of_four_bits(kv_dtype, q_heads, kv_heads, sms):
-    check(rh.make(seed=24, seq_lens=[67, 2], seq_lens_kv=[31, 64], q_heads=q_heads, kv_heads=kv_heads, kv_dtype=kv_dtype), sms=sms)
+    check(rh.make(seed=24, seq_lens=[300, 2], seq_lens_kv=[31, 64], q_heads=q_heads, kv_heads=kv_heads, kv_dtype=kv_dtype), sms=sms)
 
 
 @pytest.mark.parametrize("sms", [None, 1])
@@ -168,8 +168,16 @@ def test_odd_heads_of_four_bits(kv_dtype, q_heads, kv_heads, sms):
 @pytest.mark.parametrize("kv_dtype", rh.FORMATS)
 @pytest.mark.parametrize("spread", [1e-3, 30.0, 1e30])
 def test_far_values_of_odd_heads(kv_dtype, scale_kind, spread, sms):
-    check(rh.make(seed=25, seq_lens=[70], seq_lens_kv=[60], q_heads=3, kv_heads=3, kv_dtype=kv_dtype, scale_kind=scale_kind,
+    check(rh.make(seed=25, seq_lens=[160], seq_lens_kv=[60], q_heads=3, kv_heads=3, kv_dtype=kv_dtype, scale_kind=scale_kind,
                   spread=spread), sms=sms)
+
+
+@pytest.mark.parametrize("kv_dtype", rh.FORMATS)
+@pytest.mark.parametrize("q", [True, False])
+@pytest.mark.parametrize("sms", [1, 2, 4])
+def test_units_of_many_rows(kv_dtype, sms, q):
+    check(rh.make(seed=27, seq_lens=[77, 3, 0, 166], seq_lens_kv=[13, 63, 3, 7], q_heads=28, kv_heads=14, kv_dtype=kv_dtype),
+          sms=sms, q=q)
 
 
 @pytest.mark.parametrize("kv_dtype", rh.FORMATS)
