@@ -136,11 +136,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!wait_or_abort(&empty[k % kStages], (k / kStages) & 1, limit, abort_any)) ok = false;
         if (!ok) raise(end);
       }
-      if (!ok) {   // loads may be on their way, counted in the other CTA: a time that they all take
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 1000000ull) {
-        }
-      }
     }
   } else if (warp == 9) {
     // ================================================================ MMA (CTA 0, for both)
@@ -165,7 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (d >= 2 && !wait(&dfree[d & 1], ((d >> 1) - 1) & 1)) break;
         const uint32_t acc = tmem + 256 * (d & 1);
-        const bool last_of_head = t + 1 == end || (t + 1) / p.blocks != head;
+        const bool head_follows = t + 1 < end && (t + 1) / p.blocks != head;
         for (int kb = 0; kb < kKBlocks; ++kb, ++n) {
           const uint32_t s = n % kStages;
           if (!wait(&full[s], (n / kStages) & 1)) break;
@@ -177,7 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_commit_pair(&empty[s]);
             if (kb + 1 == kKBlocks) {
               tc_commit_pair(&dfull[d & 1]);
-              if (last_of_head) tc_commit_pair(bfree);
+              if (head_follows) tc_commit_pair(bfree);
             }
           }
           __syncwarp();
@@ -185,8 +180,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (!ok && lane == 0) raise(t);
-      // every MMA issued completes before TMEM is released (in both CTAs: CTA 1 leaves behind
-      // the cluster barrier)
+      // every MMA issued completes before TMEM is released (in both CTAs: CTA 1 comes to that
+      // behind the cluster barrier)
       if (elect_one()) tc_commit_pair(drain);
       __syncwarp();
       mbar_wait(drain, 0, kDrainNs);
@@ -243,6 +238,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   cluster_sync();   // no CTA leaves while its peer may still signal or read it
+  // nor before the MMAs' own signals have come, which the barrier above does not order.  drain's
+  // is the last of them; roles that gave up did not wait for theirs, nor for loads counted in the
+  // other CTA: a time that they all take.
+  if (warp == 9) {
+    mbar_wait(drain, 0, kDrainNs);
+    if (*abort_any) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) {
+      }
+    }
+  }
   if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
