@@ -40,6 +40,19 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
   }
 }
 
+// The same for a whole warp, whose lanes all get one answer: lanes that poll by themselves may
+// give up at different times, and elected issues and tensor-memory accesses are for all of them.
+enum WholeWarp { whole_warp };
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                              volatile int* abort_any, WholeWarp) {
+  if (mbar_try_wait_warp(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (mbar_try_wait_warp(bar, parity)) return true;
+    if (__any_sync(0xffffffffu, *abort_any || globaltimer() - t0 > limit_ns)) return false;
+  }
+}
+
 // ---------------------------------------------------------------- debug build
 // The debug library (libpa_gb300_debug.so, compiled with PA_DEBUG) adds, in
 // every attention kernel:

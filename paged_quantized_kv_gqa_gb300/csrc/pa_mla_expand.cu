@@ -146,7 +146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int64_t loaded = -1;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = wait_or_abort(bar, parity, limit, abort_any);
+        ok = wait_or_abort(bar, parity, limit, abort_any, whole_warp);
         tc_fence_after();
         return ok;
       };
@@ -199,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int64_t t = begin; t < end; ++t, ++d) {
       const int head = (int)(t / p.blocks);
       const int r0 = (int)(t - (int64_t)head * p.blocks) * 2 * kRows + (int)rank * kRows + row;
-      if (!wait_or_abort(&dfull[d & 1], (d >> 1) & 1, limit, abort_any)) {
+      if (!wait_or_abort(&dfull[d & 1], (d >> 1) & 1, limit, abort_any, whole_warp)) {
         if (lane == 0) raise(t);
         break;
       }

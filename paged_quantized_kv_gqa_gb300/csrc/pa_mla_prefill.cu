@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t np = 0, nq = 0;   // PV steps and items of this tile
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = wait_or_abort(bar, parity, limit, abort_any);
+      ok = wait_or_abort(bar, parity, limit, abort_any, whole_warp);
       tc_fence_after();
       return ok;
     };
@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // was slower).  A pace, not a dependence: a count, as a barrier's parity could be
             // missed.
             const uint64_t t0 = globaltimer();
-            while (ok && *s_done < s_of_a) ok = !*abort_any && globaltimer() - t0 <= limit;
+            while (ok && __any_sync(0xffffffffu, *s_done < s_of_a))
+              ok = !__any_sync(0xffffffffu, *abort_any || globaltimer() - t0 > limit);
           }
           if (ok) issue_s(g, i == 0, i + 1 == steps);
           due = true;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (steps == 0) continue;   // the item has no rows for this tile
       float m_run = -INFINITY, l = 0.0f;
       for (int i = 0; i < steps; ++i, ++n) {
-        if (!wait_or_abort(&sfull[x], n & 1, limit, abort_any)) {
+        if (!wait_or_abort(&sfull[x], n & 1, limit, abort_any, whole_warp)) {
           raise(it);
           fail = true;
           break;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (fail) break;
       // ---- epilogue: O / l (the record again, so that nothing of it lives through the steps)
       const Item m = work_at(it).m;
-      if (!wait_or_abort(&odone[x], items & 1, limit, abort_any)) {
+      if (!wait_or_abort(&odone[x], items & 1, limit, abort_any, whole_warp)) {
         raise(it);
         break;
       }

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     constexpr uint32_t idesc = idesc_bf16(kRows, kN) | (kBmn ? 1u << 16 : 0u);
     for (int kb = 0; kb < kKBlocks; ++kb) {
       const int s = kb % kStages;
-      if (!wait_or_abort(&full[s], (kb / kStages) & 1, limit, abort_any)) {
+      if (!wait_or_abort(&full[s], (kb / kStages) & 1, limit, abort_any, whole_warp)) {
         if (lane == 0) {
           if (!*abort_any) record_status(p.status, PA_ERR_DEVICE_TIMEOUT, (int)blockIdx.x);
           *abort_any = 1;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
               __ldg(reinterpret_cast<const uint4*>(p.src + row * p.src_stride + so));
       }
     }
-    const bool ok = wait_or_abort(done, 0, limit, abort_any) && !*abort_any;
+    const bool ok = wait_or_abort(done, 0, limit, abort_any, whole_warp) && !__any_sync(0xffffffffu, *abort_any);
     tc_fence_after();
     const int r0 = row0 + 32 * warp;
     if (ok && r0 < p.rows) {
