@@ -28,12 +28,12 @@
 // position with divisions.  Where the range covers a unit in part, the nibbles of
 // other positions stay (one warp owns a unit, so nobody else writes its bytes).
 // What bounds it: 2.56 bytes per element against the quantiser's instructions (quotients by
-// pairs): 31k rows of 8 heads in 40.3 us (int4) or 37.1 (FP4), 4.0 and 4.4 TB/s; with
-// per-channel scales 69 and 62.  (Requesting the next rows before the current ones are worked
+// pairs): 31k rows of 8 heads in 37.6 us (int4) or 34.6 (FP4), 4.3 and 4.7 TB/s; with
+// per-channel scales 63 and 57.  (Requesting the next rows before the current ones are worked
 // on spills, and gained nothing.)  That is for blocks of the common range.  A block whose
 // max |x / g| is below M / 64 (its scale is subnormal, or 0 for a block of zeros) sends
 // the four K rows or the V unit that hold it through the divisions: the same rows times
-// 0.03 with g = 1 took 316 us, rows of which every 16th is 0 315.
+// 0.03 with g = 1 took 317 us, rows of which every 16th is 0 315.
 #pragma once
 
 #include "pa_common.cuh"
@@ -112,6 +112,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 quot2(float2 x, float2 d, float2 r) {
   const float2 q = mul2(x, r);
   return fma2(fma2(q, make_float2(-d.x, -d.y), x), r, q);
+}
+
+// The quotients of two neighbouring dims, as a pair or one by one.
+template <bool PAIRS>
+__device__ __forceinline__ float2 quot_dims(float2 x, float2 d, float2 r) {
+  if constexpr (PAIRS) return quot2(x, d, r);
+  else return make_float2(quot(x.x, d.x, r.x), quot(x.y, d.y, r.y));
+}
+
+template <bool PAIRS>
+__device__ __forceinline__ float2 mul_dims(float2 a, float2 b) {
+  if constexpr (PAIRS) return mul2(a, b);
+  else return make_float2(a.x * b.x, a.y * b.y);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -217,7 +230,7 @@ __device__ __noinline__ void write_any(const __nv_bfloat16* src, int64_t stride,
 
 // ---- K, positions [lo, hi) of the unit of U that starts at `first` of the half
 // page (FULL: all of them); rows: the row of position lo
-template <int FP4, bool PC, int U, bool FULL>
+template <int FP4, bool PC, int U, bool FULL, bool PAIRS = true>
 __device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloat16* rows, uint8_t* half, int kvh,
                                         int first, int lo, int hi, int lane) {
   auto in = [&](int r) { return FULL || (r >= lo && r < hi); };
@@ -270,8 +283,8 @@ __device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloa
           y[i] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const float2 v = quot2(make_float2(f[i][e], f[i][e + 1]), make_float2(g[e], g[e + 1]), make_float2(rg[e], rg[e + 1]));
-            y[i] = fmaxf(y[i], fmaxf(fabsf(v.x), fabsf(v.y)));
+            const float2 v = quot_dims<PAIRS>(make_float2(f[i][e], f[i][e + 1]), make_float2(g[e], g[e + 1]), make_float2(rg[e], rg[e + 1]));
+            y[i] = fmaxf(fmaxf(y[i], fabsf(v.x)), fabsf(v.y));
           }
         }
         const float t = (lane & 1) ? y[0] : y[1];
@@ -291,8 +304,9 @@ __device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloa
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float2 s2 = make_float2(si, si), r2 = make_float2(ri, ri);
-            const float2 v = quot2(make_float2(f[i][e], f[i][e + 1]), PC ? mul2(s2, make_float2(g[e], g[e + 1])) : s2,
-                                   PC ? mul2(r2, make_float2(rg[e], rg[e + 1])) : r2);
+            const float2 v = quot_dims<PAIRS>(make_float2(f[i][e], f[i][e + 1]),
+                                              PC ? mul_dims<PAIRS>(s2, make_float2(g[e], g[e + 1])) : s2,
+                                              PC ? mul_dims<PAIRS>(r2, make_float2(rg[e], rg[e + 1])) : r2);
             q[e] = v.x;
             q[e + 1] = v.y;
           }
@@ -310,7 +324,7 @@ __device__ __forceinline__ void write_k(const Append4Params& p, const __nv_bfloa
 }
 
 // ---- V, the same: four dims of every position per lane
-template <int FP4, bool PC, int U, bool FULL>
+template <int FP4, bool PC, int U, bool FULL, bool PAIRS = true>
 __device__ __forceinline__ void write_v(const Append4Params& p, const __nv_bfloat16* rows, uint8_t* half, int kvh,
                                         int first, int lo, int hi, int lane) {
   auto in = [&](int r) { return FULL || (r >= lo && r < hi); };
@@ -363,8 +377,8 @@ __device__ __forceinline__ void write_v(const Append4Params& p, const __nv_bfloa
           y[j] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            const float2 v = quot2(make_float2(f[j][e], f[j][e + 1]), make_float2(g[e], g[e + 1]), make_float2(rg[e], rg[e + 1]));
-            y[j] = fmaxf(y[j], fmaxf(fabsf(v.x), fabsf(v.y)));
+            const float2 v = quot_dims<PAIRS>(make_float2(f[j][e], f[j][e + 1]), make_float2(g[e], g[e + 1]), make_float2(rg[e], rg[e + 1]));
+            y[j] = fmaxf(fmaxf(y[j], fabsf(v.x)), fabsf(v.y));
           }
           y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 1));
           y[j] = fmaxf(y[j], __shfl_xor_sync(0xffffffffu, y[j], 2));
@@ -385,8 +399,9 @@ __device__ __forceinline__ void write_v(const Append4Params& p, const __nv_bfloa
         const float2 s2 = make_float2(sj, sj), r2 = make_float2(rj, rj);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          const float2 v = quot2(make_float2(f[j][e], f[j][e + 1]), PC ? mul2(s2, make_float2(g[e], g[e + 1])) : s2,
-                                 PC ? mul2(r2, make_float2(rg[e], rg[e + 1])) : r2);
+          const float2 v = quot_dims<PAIRS>(make_float2(f[j][e], f[j][e + 1]),
+                                            PC ? mul_dims<PAIRS>(s2, make_float2(g[e], g[e + 1])) : s2,
+                                            PC ? mul_dims<PAIRS>(r2, make_float2(rg[e], rg[e + 1])) : r2);
           q[e][4 * h + j] = v.x;
           q[e + 1][4 * h + j] = v.y;
         }
