@@ -207,21 +207,39 @@ __device__ __forceinline__ float any_quotient(float x, float s) {
   return KV == PA_KV_INT8 && v != v ? 0.0f : v;
 }
 
+// The quotients that codes4 takes where short_by holds.  E4M3 keeps a zero's sign and quot2 makes
+// every zero +0, so there it is -x / d by the same steps, whose zeros' signs are turned too, and
+// `kTurn` turns the codes' signs back.
+template <int KV>
+constexpr uint32_t kTurn = KV == PA_KV_FP8_E4M3 ? 0x80808080u : 0u;
+
+template <int KV>
+__device__ __forceinline__ float2 short_quotients(float2 x, float2 d, float2 r) {
+  if constexpr (KV == PA_KV_FP8_E4M3) {
+    const float2 nr = make_float2(-r.x, -r.y), n = mul2(x, nr);
+    return fma2(fma2(n, d, x), nr, n);
+  } else {
+    return quot2(x, d, r);
+  }
+}
+
 // Eight values over their scales (r = 1 / s; ok: short_by of the scales) -> two words of
 // 8-bit codes.
 template <int KV, bool PC>
 __device__ __forceinline__ uint2 codes8_of(const float2 (&x)[4], const float2* s, const float2* r, bool ok) {
   float2 v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = quot2(x[e], s[PC ? e : 0], r[PC ? e : 0]);
+  for (int e = 0; e < 4; ++e) v[e] = short_quotients<KV>(x[e], s[PC ? e : 0], r[PC ? e : 0]);
+  uint32_t turn = kTurn<KV>;
   if (!(max_abs8(x) < 0x1p60f) || !ok) {
+    turn = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 d = s[PC ? e : 0];
       v[e] = make_float2(any_quotient<KV>(x[e].x, d.x), any_quotient<KV>(x[e].y, d.y));
     }
   }
-  return make_uint2(codes4<KV>(&v[0].x), codes4<KV>(&v[2].x));
+  return make_uint2(codes4<KV>(&v[0].x) ^ turn, codes4<KV>(&v[2].x) ^ turn);
 }
 
 // A K row's 8 values of a lane, 4 bits, by divisions: codes and the block's scale.
@@ -398,7 +416,7 @@ __device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat1
         float v0[4], v1[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 v = quot2(bf16_2(d ? x[4 * h + j].y : x[4 * h + j].x), gd, rd);
+          const float2 v = short_quotients<KV>(bf16_2(d ? x[4 * h + j].y : x[4 * h + j].x), gd, rd);
           v0[j] = v.x;
           v1[j] = v.y;
         }
@@ -410,8 +428,8 @@ __device__ __forceinline__ void store_v8(const RopeParams& p, const __nv_bfloat1
             v1[j] = any_quotient<KV>(f.y, gd.y);
           }
         }
-        w[d][k / 4 + h] = codes4<KV>(v0);
-        w[d + 1][k / 4 + h] = codes4<KV>(v1);
+        w[d][k / 4 + h] = codes4<KV>(v0) ^ (fine ? kTurn<KV> : 0);
+        w[d + 1][k / 4 + h] = codes4<KV>(v1) ^ (fine ? kTurn<KV> : 0);
       }
     }
   }
