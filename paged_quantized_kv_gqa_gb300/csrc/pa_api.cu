@@ -1188,7 +1188,6 @@ pa_status pa_mla_prefill(const pa_plan_t* plan, const pa_args* args, const void*
   p.plain_out = !p.ep.shift && !p.ep.smooth && !p.ep.int8_out && reinterpret_cast<uintptr_t>(args->out) % 32 == 0;
   // bounds of the work items (the debug build checks them): an item's first word is a row
   p.bsz = (int32_t)plan->kv_rows;
-  p.max_blocks = (int32_t)ceil_div(plan->kv_rows, 64);
   p.total_q = plan->total_q;
   p.num_items = plan->num_items();
   p.four_bit = 1;

@@ -166,9 +166,12 @@ static __device__ __noinline__ bool debug_items_ok(const AttnParams& p, int begi
       const bool slots = m.nch == 1 || (m.chunk >= 0 && (int64_t)m.chunk + (int64_t)(m.ntok - 1) * m.nch < p.part_slots);
       m.chunk = slots ? 0 : -1;
     }
+    // expanded rows have no block table: m.b is the sequence's first row, and its range ends
+    // within the p.bsz rows
+    const int64_t held = p.block_table ? (int64_t)p.max_blocks * kDebugPage : (int64_t)p.bsz - m.b;
     const bool ok = m.b >= 0 && m.b < p.bsz && m.kvh >= 0 && m.kvh < p.kv_heads && m.tok0 >= 0 &&
                     m.ntok >= 1 && m.tok0 + m.ntok <= p.total_q && m.cbase >= 0 && m.kv0 >= 0 &&
-                    m.kv0 <= m.kv1 && (int64_t)m.kv1 <= (int64_t)p.max_blocks * kDebugPage &&
+                    m.kv0 <= m.kv1 && m.kv1 <= held &&
                     m.nch >= 1 && m.chunk >= 0 && m.chunk < m.nch &&
                     (m.nch == 1 || m.nch <= p.max_chunks);
     if (!ok) {
