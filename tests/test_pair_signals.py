@@ -6,7 +6,7 @@ kernel is read as text: every barrier that such a commit names has a wait that b
 reach, and none is signalled once more than it is waited for."""
 import re
 
-from test_tmem_order import source
+from test_tmem_order import commit_barriers, source, unfenced
 
 WAIT = re.compile(r"\b(?:wait_or_abort\w*|mbar_wait|wait)\(\s*&?(\w+)")
 
@@ -50,3 +50,10 @@ def test_a_wait_of_one_cta_is_seen():
     text = "if (rank == 0) { tc_commit_pair(drain); mbar_wait(drain, 0, 1); }"
     assert unwaited(text) == {"drain"}
     assert not unwaited(text + " mbar_wait(drain, 0, 1);")
+
+
+def test_every_wait_for_mmas_is_followed_by_the_fence():
+    """As in the other kernels of latent attention (test_abi_mla_prefill.py)."""
+    text = source("pa_mla_expand.cu")
+    assert {"drain", "dfull", "empty", "bfree"} <= commit_barriers(text) and not unfenced(text)
+    assert unfenced(text.replace("tc_fence_after();", ";"))
