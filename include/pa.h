@@ -91,8 +91,8 @@ enum { PA_FAMILY_DECODE = 0, PA_FAMILY_APPEND = 1, PA_FAMILY_MLA = 2, PA_FAMILY_
  *   MLA_EXPANDED layout: attention to expanded rows (pa_mla_expand) instead of a cache,
  *               run by pa_mla_prefill.  q_heads = kv_heads (any number, a share of a
  *               model's), head_dim_qk 192 (128 and 64 rotated ones), head_dim_v 128,
- *               kv_dtype PA_KV_BF16; block_size (64), max_blocks_per_seq, num_pages and
- *               scale_kind are not used.  The rows of all sequences follow one another:
+ *               kv_dtype PA_KV_BF16, block_size 64; max_blocks_per_seq, num_pages and
+ *               scale_kind are not used and may hold anything.  The rows of all sequences follow one another:
  *               sequence b has kvtot_b of them (its prefix and its new tokens; with
  *               PA_MASK_CROSS seq_lens_kv[b], the new tokens not among them).
  *   Scales: PER_KV_HEAD  bf16 [kv_heads]              (k_scale and v_scale)

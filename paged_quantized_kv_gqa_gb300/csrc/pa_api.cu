@@ -46,14 +46,15 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------------ checks
 static pa_status check_problem(const pa_problem& p) {
+  const bool cache = p.layout != PA_LAYOUT_MLA_EXPANDED;
   if (p.bsz < 0 || p.q_heads <= 0 || p.kv_heads <= 0 || p.head_dim_qk <= 0 ||
-      p.head_dim_v <= 0 || p.block_size <= 0 || p.max_blocks_per_seq <= 0 || p.num_pages <= 0)
+      p.head_dim_v <= 0 || p.block_size <= 0 || (cache && (p.max_blocks_per_seq <= 0 || p.num_pages <= 0)))
     return fail(PA_ERR_INVALID_ARG, "non-positive shape field in pa_problem");
   if (p.q_heads % p.kv_heads != 0)
     return fail(PA_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
   if (p.kv_dtype < PA_KV_INT8 || p.kv_dtype > PA_KV_BF16)
     return fail(PA_ERR_INVALID_ARG, "unknown kv_dtype");
-  if (p.scale_kind < PA_SCALE_PER_KV_HEAD || p.scale_kind > PA_SCALE_GLOBAL)
+  if (cache && (p.scale_kind < PA_SCALE_PER_KV_HEAD || p.scale_kind > PA_SCALE_GLOBAL))
     return fail(PA_ERR_INVALID_ARG, "unknown scale_kind");
   if (p.layout < PA_LAYOUT_GQA || p.layout > PA_LAYOUT_MLA_EXPANDED)
     return fail(PA_ERR_INVALID_ARG, "unknown layout");
