@@ -53,6 +53,9 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
   }
 }
 
+// Whether all lanes of the (whole) warp say so.
+__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // ---------------------------------------------------------------- debug build
 // The debug library (libpa_gb300_debug.so, compiled with PA_DEBUG) adds, in
 // every attention kernel:
