@@ -262,16 +262,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMma || warp == kWarpMma + 1) {
     // ================================================================ MMA issue, a warp per tile
-    // the whole warp runs the loop (warp-uniform operands); one elected lane issues
+    // the whole warp runs the loop (warp-uniform operands)
     constexpr uint32_t idesc_s = idesc_bf16(128, kTile), idesc_pv = idesc_bf16(128, 128) | (1u << 16);
     const int x = warp - kWarpMma;
     const uint32_t ring = s_base + SM::kRing, s_tm = tmem + 128 * x, o_tm = tmem + 256 + 128 * x;
     const uint64_t q = sdesc_k128(s_base + SM::kQ + x * kQTile);
     uint32_t np = 0, nq = 0;   // PV steps and items of this tile
-    // Each lane waits for itself, and a wait that ran out is its own affair up to the vote behind
-    // the step's S, which all branches on `ok` follow; the elected lane issues if its own waits
-    // have come true.  (A vote in every wait, between P or S and the MMA behind it, took 4 % more
-    // of one CTA of 400 steps, and 1 % more of prompts.)
+    // One lane issues everything (MMAs of one thread execute in order, its commits cover them),
+    // if its own waits have come true.  Each lane waits for itself, and a wait that ran out is its
+    // own affair up to the vote behind the step's S, which all branches on `ok` follow.  (A vote
+    // in every wait, between P or S and the MMA behind it: one CTA of 400 steps 686 us of 665.)
+    const bool leader = elect_one();
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && wait_or_abort(bar, parity, limit, abort_any);
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue_s = [&](uint32_t g, bool first, bool last) {
       if (first) wait(&qfull[x], nq++ & 1);
       wait(&kfull[g & 1], (g >> 1) & 1);
-      if (elect_one() && ok) {
+      if (leader && ok) {
 #pragma unroll
         for (uint32_t d = 0; d < 3; ++d) {
           const uint64_t k = sdesc_k128(ring + (5 * g + d) % kSlots * kUnit);
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t h = 0; h < 2; ++h) {
         wait(&pready[2 * x + h], np & 1);
         const uint64_t v = sdesc_mn128(ring + (5 * g + 3 + h) % kSlots * kUnit, kUnit / 2, 1024);
-        if (elect_one() && ok) {
+        if (leader && ok) {
 #pragma unroll
           for (int kq = 0; kq < 4; ++kq)
             mma_ts(o_tm, s_tm + 32 * h + 8 * kq, v + ((2048 * kq) >> 4), idesc_pv, (!first || h > 0 || kq > 0) ? 1u : 0u);
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = warp_all(ok);
     if (!ok && lane == 0) raise(end - 1);
     // drain: every MMA this warp issued completes before TMEM is released
-    if (elect_one()) tc_commit(&drain[x]);
+    if (leader) tc_commit(&drain[x]);
     __syncwarp();
     mbar_wait(&drain[x], 0, kDrainNs);
   }

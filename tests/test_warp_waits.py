@@ -5,8 +5,8 @@ different times, and an elected issue, tensor-memory access or __syncwarp asks f
 them.  The kernels are read as text.  Outside the branches of a single lane a wait is either
 the one for whole warps, whose lanes get one answer, or it goes into the lane's own `ok`
 (`ok = ok && wait_or_abort(..)`): then no branch hangs on a wait, MMAs are issued under
-`elect_one() && ok` with the warp together again behind them, and the lanes vote on ok before
-the warp branches on it."""
+`leader && ok` by a lane elected once, with the warp together again behind them, and the lanes
+vote on ok before the warp branches on it."""
 import re
 
 import pytest
@@ -35,10 +35,10 @@ def unvoted(text):
             bad.append(m.start())
     if own_ok:
         bad += [m.start() for m in re.finditer(r"(?:!|&& |return )wait\(", text) if not any(a <= m.start() < b for a, b in single)]
-        for m in re.finditer(r"if \(elect_one\(\)[^{;]*(?=\{)", text):
+        for m in re.finditer(r"if \((?:elect_one\(\)|leader)[^{;]*(?=\{)", text):
             end = block(text, m.end())
             if "mma_" in text[m.end():end]:
-                if m.group() != "if (elect_one() && ok) " or not re.match(r"\s*(?:ok = warp_all\(ok\)|__syncwarp\(\));", text[end:]):
+                if m.group() != "if (leader && ok) " or "bool leader = elect_one();" not in text or not re.match(r"\s*(?:ok = warp_all\(ok\)|__syncwarp\(\));", text[end:]):
                     bad.append(m.start())
     return sorted({text.count("\n", 0, at) + 1 for at in bad if not any(a <= at < b for a, b in single)})
 
@@ -70,9 +70,10 @@ def test_lanes_that_part_are_seen():
     assert unvoted("const bool ok = f() && !*abort_any;") == [1]
     assert not unvoted("ok = !__any_sync(0xffffffffu, *abort_any || late);")
     assert not unvoted("if (!*abort_any) record_status(a, b, c);\n*abort_any = 1;")
-    own = f" ok = ok && {call});\n"
-    issue = "if (elect_one() && ok) { mma_ss(d); }\n"
+    own = f"const bool leader = elect_one(); ok = ok && {call});\n"
+    issue = "if (leader && ok) { mma_ss(d); }\n"
     assert not unvoted(own + issue + " ok = warp_all(ok);")
     assert unvoted(own + issue) == [2]
-    assert unvoted(own + "if (elect_one()) { mma_ss(d); }\n ok = warp_all(ok);") == [2]
+    assert unvoted(own + "if (elect_one() && ok) { mma_ss(d); }\n ok = warp_all(ok);") == [2]
+    assert unvoted(own + "if (leader) { mma_ss(d); }\n ok = warp_all(ok);") == [2]
     assert unvoted(own + "if (!wait(bar)) return;") == [2]
