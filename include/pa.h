@@ -362,7 +362,7 @@ typedef struct pa_rope {
 } pa_rope;
 
 /*
- * pa_rope_append: the step before pa_run in one launch.  Rotates the new tokens'
+ * pa_rope_append: the step before pa_run in one call (a launch, two for many rows).  Rotates the new tokens'
  * queries into q_out and does what pa_cache_append does with their keys and values, the
  * keys rotated first: stored K = Q(k' / s) of the rotated binary32 values k' (no rounding
  * to bf16 between), V as pa_cache_append writes it.  A NaN is stored as 0 (int8, 4 bits)
@@ -422,8 +422,9 @@ pa_status pa_mla_expand(int32_t rows, int32_t heads, const void* c, int64_t c_st
  * and the output epilogue; the rest is unused.  Rows of a sequence must be finite where
  * any of its tokens sees them; rows of other sequences may hold anything.
  *   A plan with chunk_size != 0 may split ranges: call pa_merge afterwards (it also writes
- * the rows that see nothing).  Ranges of one sequence run by several plans (new tokens
- * against a cached prefix, cross, and among themselves) are joined by their out and lse.
+ * the rows that see nothing).  pa_merge joins the ranges of one plan.  Ranges of a sequence run
+ * by several plans (new tokens against a cached prefix, cross, and among themselves) are the
+ * caller's to join: lse = log(e^lse1 + e^lse2), out = e^(lse1 - lse) out1 + e^(lse2 - lse) out2.
  *   q, k_nope, v, k_rope, out 16-byte aligned, strides multiples of 8 elements.
  * Asynchronous on stream; no allocation.
  */

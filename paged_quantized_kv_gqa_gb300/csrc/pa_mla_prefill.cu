@@ -26,7 +26,7 @@
 // Rounding: P to bf16 (V's type; the MMA takes one type), at most 2^-8 p|v| a position,
 // rows to bf16, partial rows of split ranges in fp32.
 // Bound: the tensor cores, 640 flops per visible (query head, position); 38 heads of 2048 tokens
-// against 8192 rows in 234 us, 1742 TFLOP/s, 8192 tokens of 32 heads, causal, 1684.  A step of both
+// against 8192 rows in 236 us, 1730 TFLOP/s, 8192 tokens of 32 heads, causal, 1670.  A step of both
 // tiles takes 3150 cycles, its MMAs 2560; the rest is the chain S -> softmax -> PV of each tile.
 #include "pa_common.cuh"
 

@@ -537,10 +537,13 @@ __global__ void __launch_bounds__(kWarps * 32, kQCtas) rope_q_kernel(const RopeP
 }
 
 // Everything in one launch (U = 8, few rows), or K and V (U = 32; 35k rows of 8 heads: FP4
-// 60 us, int8 67, their bytes 27 and 33; per-channel scales 91 and 83, 5 less than with 32
-// warps an SM, which spill more).  K alone takes 45 and V 23 (FP4): instructions (47 % of the
-// issue slots at 32 % of the warps) and loads in turn; the next heads' rows requested ahead
-// 62 to 70, 4 heads at once 60 to 68.
+// 58 us, int4 61, int8 67, E4M3 63, their bytes 27 and 33; per-channel scales 88, 99, 80 and 78,
+// 5 less than with 32 warps an SM, which spill more; on three axes 4 to 6 more).  K alone takes
+// 45 and V 23 (FP4): instructions (47 % of the issue slots at 32 % of the warps) and loads in
+// turn; the next heads' rows requested ahead 62 to 70, 4 heads at once 60 to 68.  4-bit blocks
+// below E4M3's normal range go by divisions, and with one of them all of a K step or V unit: the
+// same rows on three axes times 0.03 with scales of 1 353 us (FP4; int4 356) of 63 (65), every
+// 16th row 0 338 (340).
 template <int KV, bool PC, int U>
 __global__ void __launch_bounds__(kWarps * 32, U == 8 ? 2 : PC ? 3 : 4) rope_append_kernel(const RopeParams p) {
   constexpr int kBatch = U == 8 ? 4 : 2;   // heads whose rows are on the way at once
